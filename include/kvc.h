@@ -137,6 +137,32 @@ typedef struct kvc_params {
                               trees.  0 = binary trees only (byte 7 must be 0).*/
 } kvc_params;
 
+/* ---- chunk calls ------------------------------------------------------------- */
+/* kvc_chunk_attn, kvc_chunk_mass and kvc_mass_evict (no counterpart on the
+ * pages: the calls a server makes after compression, when more than one token
+ * arrives at once or the cache has to stay within a budget while it grows).
+ * One block per call, passed by const pointer, owned by the caller (host). */
+typedef struct kvc_chunk {
+  int32_t T;            /* token rows per (b, head) of q, k_new, v_new, out and lse,
+                           1..65536                                               */
+  int32_t layer_begin;  /* the call covers layers [layer_begin, layer_end):       */
+  int32_t layer_end;    /* 0 <= layer_begin < layer_end <= L                      */
+  int32_t page_rows;    /* 0: the entries of (b,l,h) are the contiguous rows from
+                           off_lh on.  Else a power of two in 16..1024: entry e is
+                           row page_table[b,l,h, e / page_rows] * page_rows + e %
+                           page_rows, and off_lh is not read (it may be NULL)     */
+  int32_t max_pages;    /* columns of page_table (page_rows > 0)                  */
+  float   softcap;      /* > 0: scores pass cap * tanh(s / cap); 0 = off          */
+  float   window;       /* > 0: a token sees the entries with pos_token - pos_e <
+                           window only; 0 = off                                   */
+  const int32_t* page_table; /* device [B, L, H, max_pages] page numbers; entries
+                           past the last used page are not read                   */
+  const int32_t* n_new; /* device [B]: new tokens of each sequence, 0..T; NULL =
+                           T for every sequence                                   */
+  const float* slopes;  /* device [H*G]: head h adds -slopes[h] * (pos_token -
+                           pos_e) to its scores; NULL = off                       */
+} kvc_chunk;
+
 /* Human-readable name of a status code (static string). */
 const char* kvc_status_string(int status);
 
@@ -415,6 +441,92 @@ int kvc_partition(const kvc_params* p, const int32_t* ctx_len, const void* hidde
 int kvc_tree_cuts(const kvc_params* p, const int32_t* ctx_len, const void* K,
                   const float* rope_cos, const float* rope_sin, const int32_t* slot_bounds,
                   const int32_t* n_slots, float* kappa, uint8_t* cuts, void* stream);
+
+/* Attention of a chunk of new tokens over the packed cache: the follow-up turn
+ * of a conversation, a piece of a long prompt, drafted tokens to verify, or one
+ * token per sequence (T = 1).  The n_b = n_new[b] tokens of sequence b become
+ * entries len_lh .. len_lh + n_b - 1 of every (b,l,h) of the layer range (log m
+ * = 0, pos = pos_new[b] + t), and token t attends over the entries e <= len_lh
+ * + t that its window leaves it.  For query head g of the group:
+ *   s_e = q_t . k_e / sqrt(d);  s_e = softcap * tanh(s_e / softcap);
+ *   s_e += logm_e - slope_g * (pos_t - pos_e);
+ *   out = sum_e softmax_e(s) v_e,  lse = log2 sum_e 2^(s_e log2 e)
+ * with fp32 statistics (bf16: the softmax numerators are rounded to bf16 for
+ * the product with V, the sum is of the unrounded ones).  A row whose scores
+ * are all -inf gets out = 0 and lse = -inf.
+ *   q, out        [B, Lr, H*G, T, d], Lr = layer_end - layer_begin
+ *   k_new, v_new  [B, Lr, H, T, d]
+ *   lse           [B, Lr, H*G, T] f32, or NULL
+ *   pos_new       [B] f32: position of each sequence's first new token
+ *   len_lh, cap_lh, off_lh, len_out  whole [B, L, H] arrays (only the range's
+ *                 entries are read or written)
+ * Rows t >= n_b of out and lse are left as they were, and rows of the cache at
+ * or beyond an (l,h)'s entries are never used, whatever they hold.
+ * len_out receives len_lh + n_b; it may be len_lh itself, another array (a
+ * caller that verifies drafts keeps the old lengths until it knows how many
+ * tokens stand), or NULL.  Positions must be multiples of 1/2 below 2^23.
+ * Every value the rows in use hold must be finite, except that log m may be
+ * -inf (the entry is never seen).  Pages may be shared between (b,l,h) as
+ * long as the rows appended by a call belong to one only.
+ * p->packed_rows must be the extent of Kp, Vp, logm and pos (1 .. 2^31 - 1).
+ * An (l,h) with a length or n_b out of range, a page number or row range
+ * outside the extent, or too few page_table columns is skipped and reported as
+ * KVC_EDEVICE; one with len + n_b > cap_lh as KVC_ECAPACITY (nothing is
+ * appended, its out, lse and length stay).  The workspace needs no
+ * initialisation; calls that overlap must not share one.
+ * Errors: KVC_EINVAL (also q, k_new, v_new, Kp, Vp or out off a 16-byte
+ * boundary), KVC_EWORKSPACE, KVC_ECUDA. */
+int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const void* q, const void* k_new,
+                   const void* v_new, const float* pos_new, void* Kp, void* Vp, float* logm,
+                   float* pos, const int32_t* len_lh, const int32_t* cap_lh,
+                   const int64_t* off_lh, void* out, float* lse, int32_t* len_out,
+                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of kvc_chunk_attn and kvc_chunk_mass (one buffer may serve
+ * both, call after call; 256-byte aligned device memory, no initialisation
+ * needed); 0 for invalid arguments.  Depends on p, T and the layer range. */
+size_t kvc_chunk_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk* c /* host */);
+
+/* The attention weight every entry received from the chunk, accumulated:
+ *   mass_e = decay * mass_e + sum_{g, t < n_b} 2^(s_e log2 e - lse_{g,t})
+ * over the entries token t sees, with s as in kvc_chunk_attn (same c, q and
+ * pos_new) and lse [B, Lr, H*G, T] of that call (for T = 1 also the lse_out of
+ * kvc_decode_attn_lse).  len_lh are the lengths BEFORE the chunk; entries
+ * len_lh .. len_lh + n_b - 1 are the chunk's own, already in the cache, and
+ * start from 0 (what mass held there is not read).  A row with lse = -inf adds
+ * nothing.  mass: f32 laid out like logm ([packed_rows]).  0 <= decay <= 1.
+ * Sums run in a fixed order: the same call gives the same bits.  Checks and
+ * skipped (l,h) as in kvc_chunk_attn (no capacity is involved).  Errors:
+ * KVC_EINVAL, KVC_EWORKSPACE, KVC_ECUDA. */
+int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const void* q, const void* Kp,
+                   const float* logm, const float* pos, const float* pos_new,
+                   const int32_t* len_lh, const int64_t* off_lh, const float* lse, float decay,
+                   float* mass, void* workspace, size_t ws_bytes, void* stream);
+
+/* Eviction by accumulated mass, each (l,h) by itself: an entry is protected
+ * when pos_e >= pos_next[b] - recent; B = min(len_lh, max(keep_lh, protected
+ * entries)) entries stay: the protected ones, then those of largest mass (ties
+ * to the lower entry index; NaN below everything).  In place, as in
+ * kvc_evict_topb: the staying entries at index >= B move, in index order, into
+ * the evicted entries below B (K, V, log m, pos and mass alike); entries at
+ * index >= B keep what they held.  len_out (required, may be len_lh itself)
+ * receives B; with pages, the pages wholly at or beyond B are free.
+ * keep_lh [B, L, H] int32 (negative counts as 0), pos_next [B] f32 the
+ * position the next token will have, recent >= 0.  max_len bounds len_lh; an
+ * (l,h) beyond it, or with a row range or page outside p->packed_rows, is
+ * skipped (len_out = len_lh) and reported as KVC_EDEVICE.  c gives the layer
+ * range and the pages (its other members are not read, but must be valid).
+ * Two (b,l,h) of one call must not share the pages that it changes.
+ * Errors: KVC_EINVAL, KVC_EWORKSPACE, KVC_ECUDA. */
+int kvc_mass_evict(const kvc_params* p, const kvc_chunk* c, float* mass, const int32_t* keep_lh,
+                   int32_t recent, const float* pos_next, void* Kp, void* Vp, float* logm,
+                   float* pos, const int32_t* len_lh, const int64_t* off_lh, int32_t* len_out,
+                   int32_t max_len, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of kvc_mass_evict (256-byte aligned device memory, no
+ * initialisation needed); 0 for invalid arguments. */
+size_t kvc_mass_evict_workspace_bytes(const kvc_params* p /* host */,
+                                      const kvc_chunk* c /* host */, int32_t max_len);
 
 #ifdef __cplusplus
 }

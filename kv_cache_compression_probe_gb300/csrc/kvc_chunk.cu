@@ -1,0 +1,703 @@
+// kvc_chunk_attn and kvc_chunk_mass: attention of a chunk of new tokens over the
+// packed cache, and the attention weight every entry received from it.  This
+// file holds the host entries, the prepare and combine kernels, and the fp32
+// kernels.
+//
+// fp32 kernels: 256 threads hold a tile of 64 (or, for few rows, 16) query rows
+// and 64 entries.  Query rows, entries' keys and values are staged in shared
+// memory as fp32; thread (ty, tx) forms the scores of rows ty*R.. and entries
+// tx + 16 j, so the 16 lanes of a row share its maximum and sum by shuffles.
+// fp32 has no tensor-core form of full precision; the bound is the FFMA rate.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kvc_chunk.cuh"
+#include "kvc_internal.h"
+
+namespace {
+
+using kvc::ChunkArgs;
+using kvc::ChunkSeg;
+using kvc::ChunkUnit;
+
+constexpr int kKeys = 64;              // entries per tile of the fp32 kernels
+constexpr int kSimtThreads = 256;
+
+// ---------------------------------------------------------------- prepare
+// One warp per (unit, group of 16 new tokens): checks the unit, appends the
+// group's keys and values (kAppend) and writes the unit's record.  Bound by the
+// bytes of the chunk's keys and values, or by latency for one token.
+constexpr int kPrepTok = 16;
+constexpr int kPrepWarps = 4;
+
+template <typename T, int D, bool kAppend>
+__global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArgs a, int groups) {
+  kvcd::pdl_trigger();
+  kvcd::pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kPrepWarps + (threadIdx.x >> 5);
+  const int64_t u = w / groups;
+  const int g = (int)(w - u * groups);
+  if (u >= a.units) return;
+  const int b = (int)(u / a.per_seq);
+  const int64_t gu = kvcd::unit_global(a, u);
+  const int len = a.len_lh[gu];
+  const int n = a.n_new ? a.n_new[b] : a.T;
+  const int64_t off = a.page_table ? 0 : a.off_lh[gu];
+  int bad = KVC_OK;
+  if (len < 0 || n < 0 || n > a.T || off < 0 || (int64_t)len + n > a.packed_rows) bad = KVC_EDEVICE;
+  else if (!a.page_table && off + len + n > a.packed_rows) bad = KVC_EDEVICE;
+  else if (kAppend && (int64_t)len + n > a.cap_lh[gu]) bad = KVC_ECAPACITY;
+  else if (a.page_table) {
+    const int need = (int)(((int64_t)len + n + (1 << a.page_shift) - 1) >> a.page_shift);
+    if (need > a.max_pages) {
+      bad = KVC_EDEVICE;
+    } else {
+      const int32_t* tab = a.page_table + gu * a.max_pages;
+      const int64_t pages = a.packed_rows >> a.page_shift;
+      bool ok = true;
+      for (int i = lane; i < need; i += 32) ok &= tab[i] >= 0 && tab[i] < pages;
+      if (!__all_sync(KVC_FULL_MASK, ok)) bad = KVC_EDEVICE;
+    }
+  }
+  if (g == 0 && lane == 0) {
+    if (bad != KVC_OK) kvcd::record_error(a.err, bad);
+    ChunkUnit r;
+    r.len = bad == KVC_OK ? len : 0;
+    r.n = bad == KVC_OK ? n : 0;
+    r.off = off;
+    a.rec[u] = r;
+  }
+  if (!kAppend || bad != KVC_OK) return;
+  constexpr int kVec = D * (int)sizeof(T) / 16;        // 16-byte vectors of a row
+  const kvcd::RowMap rows = kvcd::row_map(a, u, off);
+  const int t0 = g * kPrepTok, t1 = min(n, t0 + kPrepTok);
+  const uint4* kn = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_new) + u * a.T * D);
+  const uint4* vn = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_new) + u * a.T * D);
+  for (int i = lane; i < (t1 - t0) * kVec; i += 32) {
+    const int t = t0 + i / kVec, v = i % kVec;
+    const int64_t row = rows(len + t);
+    reinterpret_cast<uint4*>(static_cast<T*>(a.Kp) + row * D)[v] = kn[t * kVec + v];
+    reinterpret_cast<uint4*>(static_cast<T*>(a.Vp) + row * D)[v] = vn[t * kVec + v];
+  }
+  for (int t = t0 + lane; t < t1; t += 32) {
+    const int64_t row = rows(len + t);
+    a.logm[row] = 0.f;
+    a.pos[row] = a.pos_new[b] + (float)t;
+  }
+}
+
+// ---------------------------------------------------------------- fp32 score tile
+template <int D, int MR>
+struct SimtSmem {
+  float q[MR][D + 4];
+  float k[kKeys][D + 4];               // then the numerators [MR][kKeys + 4]
+  float v[kKeys][D];
+  float lm[kKeys], rel[kKeys];
+  kvcd::LocateSmem loc;
+};
+
+// Rows [first, first + count) of a [.., D] array given by `row`, as fp32 in
+// shared memory; rows past `count` are zeroed.
+template <typename T, int D, int kRows, int kStride, class RowFn>
+__device__ __forceinline__ void stage_rows(float* dst, const T* src, int count, RowFn row) {
+  constexpr int kE = 16 / (int)sizeof(T);
+  constexpr int kVec = D / kE;
+  for (int i = threadIdx.x; i < kRows * kVec; i += kSimtThreads) {
+    const int r = i / kVec, v = i % kVec;
+    float x[kE];
+    if (r < count) {
+      const uint4 w = *reinterpret_cast<const uint4*>(src + row(r) * D + v * kE);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(ws[e] << 16);
+          x[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(ws[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kE; e += 4)
+      *reinterpret_cast<float4*>(dst + r * kStride + v * kE + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+  }
+}
+
+// Products of this thread's R rows and 4 entries (tx + 16 j).
+template <int D, int R>
+__device__ __forceinline__ void score_tile(const float* q, const float* k, int ty, int tx, float (&s)[R][4]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int f = 0; f < D; f += 4) {
+    float4 kv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(k + (tx + 16 * j) * (D + 4) + f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float4 qv = *reinterpret_cast<const float4*>(q + (ty * R + i) * (D + 4) + f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+    }
+  }
+}
+
+// Base-2 score from the raw product; sees: whether the row may look at all.
+__device__ __forceinline__ float score_of(const ChunkArgs& a, float dot, float lm2, float rel,
+                                          float slope2, int t, bool sees) {
+  float x = dot * a.scale;
+  if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+  x = fmaf(x, kvcd::kLog2eC, lm2);
+  if (a.slopes) x = fmaf(slope2, rel - (float)t, x);   // pos_e - pos_token
+  if (a.window > 0.f && !(rel > (float)t - a.window)) sees = false;
+  return sees ? x : -INFINITY;
+}
+
+// ln m (base 2) and position relative to the chunk's first token of a tile's
+// entries.
+__device__ __forceinline__ void stage_bias(const ChunkArgs& a, float* lm, float* rel, int e0, int count,
+                                           const kvcd::RowMap& rows, float pos0) {
+  for (int c = threadIdx.x; c < kKeys; c += kSimtThreads) {
+    lm[c] = c < count ? a.logm[rows(e0 + c)] * kvcd::kLog2eC : 0.f;
+    rel[c] = c < count && (a.slopes || a.window > 0.f) ? a.pos[rows(e0 + c)] - pos0 : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- fp32 attention
+template <typename T, int D, int MR>
+__global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkArgs a) {
+  constexpr int R = MR / 16, C = D / 64;               // rows and 4-feature groups per thread
+  extern __shared__ __align__(16) unsigned char simt_raw[];
+  auto& sm = *reinterpret_cast<SimtSmem<D, MR>*>(simt_raw);
+  float* P = &sm.k[0][0];
+  kvcd::pdl_trigger();
+  kvcd::pdl_wait();
+  const kvcd::AttnCost<kKeys> cost{a};
+  const kvcd::Piece piece = kvcd::locate_piece<kSimtThreads>(cost, sm.loc);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  if (tid == 0) a.seg[blockIdx.x] = ChunkSeg{piece.item, piece.item >= 0 && piece.lo > piece.start};
+  if (a.len_out)
+    for (int64_t u = (int64_t)blockIdx.x * kSimtThreads + tid; u < a.units; u += (int64_t)gridDim.x * kSimtThreads) {
+      const ChunkUnit r = kvcd::load_unit(a.rec, u);
+      const int64_t gu = kvcd::unit_global(a, u);
+      a.len_out[gu] = r.n > 0 ? r.len + r.n : a.len_lh[gu];
+    }
+  for (kvcd::Walk<kvcd::AttnCost<kKeys>> w(cost, piece); w.next();) {
+    const int64_t u = w.item / a.rp;
+    const int t0 = (int)(w.item - u * a.rp) * a.tpb;
+    const int h = (int)(u % a.H);
+    const float pos0 = a.pos_new[u / a.per_seq];
+    const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
+    const int used = a.G * a.tt;                       // rows of the block in use
+    __syncthreads();
+    stage_rows<T, D, MR, D + 4>(&sm.q[0][0], static_cast<const T*>(a.q), used, [&](int r) {
+      return (u * a.G + r / a.tt) * a.T + min(a.T - 1, t0 + r % a.tt);
+    });
+    int tok[R], lim[R];
+    float slope2[R], m[R], l[R], o[R][C][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = ty * R + i;
+      tok[i] = t0 + r % a.tt;
+      const bool live = r < used && tok[i] < w.r.n;
+      lim[i] = live ? w.r.len + tok[i] + 1 : 0;
+      slope2[i] = a.slopes && live ? a.slopes[h * a.G + r / a.tt] * kvcd::kLog2eC : 0.f;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
+    }
+    const int total = w.r.len + w.r.n;
+    for (int tile = w.tb; tile < w.te; ++tile) {
+      const int e0 = tile * kKeys, cnt = min(kKeys, total - e0);
+      __syncthreads();
+      auto row = [&](int r) { return rows(e0 + r); };
+      stage_rows<T, D, kKeys, D + 4>(&sm.k[0][0], static_cast<const T*>(a.Kp), cnt, row);
+      stage_rows<T, D, kKeys, D>(&sm.v[0][0], static_cast<const T*>(a.Vp), cnt, row);
+      stage_bias(a, sm.lm, sm.rel, e0, cnt, rows, pos0);
+      __syncthreads();
+      float s[R][4];
+      score_tile<D, R>(&sm.q[0][0], &sm.k[0][0], ty, tx, s);
+      __syncthreads();                                 // the keys' place holds the numerators next
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float mx = m[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = tx + 16 * j;
+          s[i][j] = score_of(a, s[i][j], sm.lm[c], sm.rel[c], slope2[i], tok[i], e0 + c < lim[i]);
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(KVC_FULL_MASK, mx, x));
+        const float base = mx == -INFINITY ? 0.f : mx;
+        const float f = exp2f(m[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(s[i][j] - base);
+          sum += p;
+          P[(ty * R + i) * (kKeys + 4) + tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(KVC_FULL_MASK, sum, x);
+        l[i] = fmaf(l[i], f, sum);
+        m[i] = mx;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][c][e] *= f;
+      }
+      __syncwarp();                                    // a row's numerators come from its own warp
+#pragma unroll 2
+      for (int kk = 0; kk < kKeys; kk += 4) {
+        float p[R][4];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(P + (ty * R + i) * (kKeys + 4) + kk);
+          p[i][0] = v.x; p[i][1] = v.y; p[i][2] = v.z; p[i][3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.v[kk + e][c * 64 + tx * 4]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              o[i][c][0] = fmaf(p[i][e], v.x, o[i][c][0]);
+              o[i][c][1] = fmaf(p[i][e], v.y, o[i][c][1]);
+              o[i][c][2] = fmaf(p[i][e], v.z, o[i][c][2]);
+              o[i][c][3] = fmaf(p[i][e], v.w, o[i][c][3]);
+            }
+          }
+      }
+    }
+    const bool whole = w.whole();
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = ty * R + i;
+      if (lim[i] == 0) continue;
+      if (whole) {
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const int64_t orow = (u * a.G + r / a.tt) * a.T + tok[i];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            static_cast<T*>(a.out)[orow * D + c * 64 + tx * 4 + e] = kvcd::from_f<T>(o[i][c][e] * inv);
+        if (a.lse && tx == 0) a.lse[orow] = l[i] > 0.f ? m[i] + log2f(l[i]) : -INFINITY;
+      } else {
+        const int64_t prow = slot * MR + r;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          *reinterpret_cast<float4*>(a.part + prow * D + c * 64 + tx * 4) =
+              make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+        if (tx == 0) { a.part_ml[prow * 2] = m[i]; a.part_ml[prow * 2 + 1] = l[i]; }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine
+// Block x joins the partial results of the item that the cut before CTA x
+// splits, if that is the item's first cut: the head piece lies in slot 2(x-1)+1,
+// the following pieces in slots 2x, 2(x+1), ...  blockIdx.y takes a group of
+// rows, a warp a row.
+template <typename T, int D, int kRowsBlock>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkArgs a, int grid) {
+  kvcd::pdl_trigger();
+  kvcd::pdl_wait();
+  const int x = blockIdx.x + 1;
+  const ChunkSeg s = a.seg[x], before = a.seg[x - 1];
+  if (!s.mid || (before.mid && before.item == s.item)) return;
+  int y1 = x + 1;                                      // pieces x .. y1 - 1 follow the head
+  while (y1 < grid && a.seg[y1].mid && a.seg[y1].item == s.item) ++y1;
+  const int64_t u = s.item / a.rp;
+  const int t0 = (int)(s.item - u * a.rp) * a.tpb;
+  const ChunkUnit rec = kvcd::load_unit(a.rec, u);
+  const int lane = threadIdx.x & 31;
+  constexpr int C = D / 32;
+  const int rows_tile = a.G * a.tt;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < kRowsBlock; r += gridDim.y * 8) {
+    const int tile = kRowsBlock > 128 ? r >> 7 : 0, rt = kRowsBlock > 128 ? r & 127 : r;
+    const int t = t0 + tile * a.tt + rt % a.tt;
+    if (rt >= rows_tile || t >= rec.n || tile * a.tt >= a.tpb) continue;
+    float M = -INFINITY, l = 0.f, o[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = 0.f;
+    for (int y = x - 1; y < y1; ++y) {
+      const int64_t prow = ((int64_t)y * 2 + (y == x - 1 ? 1 : 0)) * kRowsBlock + r;
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + prow * 2);
+      float pv[C];
+      const float* po = a.part + prow * D + lane * C;
+      if constexpr (C == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(po);
+        pv[0] = v.x; pv[1] = v.y; pv[2] = v.z; pv[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(po);
+        pv[0] = v.x; pv[1] = v.y;
+      }
+      const float Mn = fmaxf(M, ml.x);
+      if (Mn == -INFINITY) continue;                   // nothing seen so far
+      const float f0 = exp2f(M - Mn), f1 = exp2f(ml.x - Mn);
+      l = fmaf(l, f0, ml.y * f1);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = f1 == 0.f ? o[c] * f0 : fmaf(o[c], f0, pv[c] * f1);
+      M = Mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t orow = (u * a.G + rt / a.tt) * a.T + t;
+    T* op = static_cast<T*>(a.out) + orow * D + lane * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) op[c] = kvcd::from_f<T>(o[c] * inv);
+    if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? M + log2f(l) : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------- fp32 mass
+// Items are a unit's key tiles, steps their row tiles.  The line is located by
+// unit (tiles x row tiles); inside a unit the division gives tile and row tile.
+template <int kTile>
+struct MassCost {
+  const ChunkArgs& a;
+  __device__ __forceinline__ int64_t items() const { return a.units; }
+  __device__ __forceinline__ int row_tiles(const ChunkUnit& r) const { return max(1, (r.n + a.tt - 1) / a.tt); }
+  __device__ __forceinline__ int64_t operator()(int64_t u, ChunkUnit& r) const {
+    r = kvcd::load_unit(a.rec, u);
+    return (int64_t)((r.len + r.n + kTile - 1) / kTile) * row_tiles(r);
+  }
+};
+// for (MassWalk w(cost, piece); w.next(); ): row tiles [w.tb, w.te) of key tile
+// w.tile of unit w.u.
+template <int kTile>
+struct MassWalk {
+  const MassCost<kTile>& cost;
+  long long f, hi, start;
+  int64_t steps;
+  int64_t u;
+  ChunkUnit r;
+  int rs, tile, tb, te;
+  __device__ __forceinline__ MassWalk(const MassCost<kTile>& c, const kvcd::Piece& p)
+      : cost(c), f(p.lo), hi(p.item >= 0 ? p.hi : p.lo), start(p.start), u(p.item), rs(0) {}
+  __device__ __forceinline__ bool next() {
+    if (rs > 0) f += te - tb;
+    if (f >= hi) return false;
+    if (rs == 0) steps = cost(u, r);
+    while (f - start >= steps) {                       // a step follows: f < hi <= all steps
+      start += steps;
+      steps = cost(++u, r);
+    }
+    rs = cost.row_tiles(r);
+    tile = (int)((f - start) / rs);
+    tb = (int)((f - start) - (int64_t)tile * rs);
+    te = (int)min((long long)rs, tb + (hi - f));
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return tb == 0 && te == rs; }
+};
+// The item and offset at which a piece starts.
+template <int kTile>
+__device__ __forceinline__ ChunkSeg mass_seg(const MassCost<kTile>& cost, const kvcd::Piece& p) {
+  if (p.item < 0) return ChunkSeg{-1, 0};
+  ChunkUnit r;
+  cost(p.item, r);
+  const int rs = cost.row_tiles(r);
+  const long long at = p.lo - p.start;
+  return ChunkSeg{((int64_t)p.item << 32) | (at / rs), at % rs > 0};
+}
+
+__device__ __forceinline__ void mass_store(const ChunkArgs& a, const ChunkUnit& r, const kvcd::RowMap& rows, int e, float sum) {
+  const int64_t row = rows(e);
+  a.mass[row] = e < r.len ? fmaf(a.decay, a.mass[row], sum) : sum;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkArgs a) {
+  constexpr int MR = 64, R = 4;
+  extern __shared__ __align__(16) unsigned char simt_raw[];
+  auto& sm = *reinterpret_cast<SimtSmem<D, MR>*>(simt_raw);
+  float* red = &sm.v[0][0];                            // [16][kKeys] column sums by row group
+  kvcd::pdl_trigger();
+  kvcd::pdl_wait();
+  const MassCost<kKeys> cost{a};
+  const kvcd::Piece piece = kvcd::locate_piece<kSimtThreads>(cost, sm.loc);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  if (tid == 0) a.seg[blockIdx.x] = mass_seg(cost, piece);
+  for (MassWalk<kKeys> w(cost, piece); w.next();) {
+    const int64_t u = w.u;
+    const int e0 = w.tile * kKeys;
+    const int h = (int)(u % a.H);
+    const float pos0 = a.pos_new[u / a.per_seq];
+    const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
+    const int cnt = min(kKeys, w.r.len + w.r.n - e0);
+    const int used = a.G * a.tt;
+    __syncthreads();
+    stage_rows<T, D, kKeys, D + 4>(&sm.k[0][0], static_cast<const T*>(a.Kp), cnt, [&](int r) { return rows(e0 + r); });
+    stage_bias(a, sm.lm, sm.rel, e0, cnt, rows, pos0);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int rt = w.tb; rt < w.te; ++rt) {
+      const int t0 = rt * a.tt;
+      __syncthreads();
+      stage_rows<T, D, MR, D + 4>(&sm.q[0][0], static_cast<const T*>(a.q), used, [&](int r) {
+        return (u * a.G + r / a.tt) * a.T + min(a.T - 1, t0 + r % a.tt);
+      });
+      __syncthreads();
+      float s[R][4];
+      score_tile<D, R>(&sm.q[0][0], &sm.k[0][0], ty, tx, s);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = ty * R + i, t = t0 + r % a.tt;
+        if (r >= used || t >= w.r.n) continue;
+        const int g = r / a.tt;
+        const float lse = a.lse[(u * a.G + g) * a.T + t];
+        if (lse == -INFINITY) continue;
+        const float slope2 = a.slopes ? a.slopes[h * a.G + g] * kvcd::kLog2eC : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = tx + 16 * j;
+          acc[j] += exp2f(score_of(a, s[i][j], sm.lm[c], sm.rel[c], slope2, t,
+                                   c < cnt && e0 + c <= w.r.len + t) - lse);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[ty * kKeys + tx + 16 * j] = acc[j];
+    __syncthreads();
+    if (tid < cnt) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum += red[i * kKeys + tid];
+      if (w.whole()) mass_store(a, w.r, rows, e0 + tid, sum);
+      else a.part[((int64_t)blockIdx.x * 2 + (w.tb == 0 ? 1 : 0)) * kKeys + tid] = sum;
+    }
+  }
+}
+
+// Joins the partial column sums of a key tile that a cut splits (as
+// chunk_combine_kernel).
+template <int kTile>
+__global__ void __launch_bounds__(kTile) chunk_mass_combine_kernel(ChunkArgs a, int grid) {
+  kvcd::pdl_trigger();
+  kvcd::pdl_wait();
+  const int x = blockIdx.x + 1;
+  const ChunkSeg s = a.seg[x], before = a.seg[x - 1];
+  if (!s.mid || (before.mid && before.item == s.item)) return;
+  const int64_t u = s.item >> 32;
+  const int e = (int)(s.item & 0xffffffff) * kTile + threadIdx.x;
+  const ChunkUnit r = kvcd::load_unit(a.rec, u);
+  if (e >= r.len + r.n) return;
+  float sum = a.part[((int64_t)(x - 1) * 2 + 1) * kTile + threadIdx.x];
+  for (int y = x; y < grid && a.seg[y].mid && a.seg[y].item == s.item; ++y)
+    sum += a.part[(int64_t)y * 2 * kTile + threadIdx.x];
+  mass_store(a, r, kvcd::row_map(a, u, r.off), e, sum);
+}
+
+// ---------------------------------------------------------------- host side
+struct ChunkLayout {
+  size_t rec, seg, part, ml, total;
+};
+
+constexpr int kMaxRowsBlock = 256;     // rows of one partial result at most
+constexpr int kCtaPerSm = 2;           // pieces per SM at most
+
+ChunkLayout chunk_layout(const kvc_params* p, const kvc_chunk* c) {
+  const size_t units = (size_t)p->B * p->H * (c->layer_end - c->layer_begin);
+  const size_t ctas = (size_t)kCtaPerSm * std::max(kvc::sm_count(), 1);
+  ChunkLayout w;
+  w.rec = 0;
+  w.seg = kvc::align256(units * sizeof(ChunkUnit));
+  w.part = w.seg + kvc::align256(ctas * sizeof(ChunkSeg));
+  w.ml = w.part + kvc::align256(ctas * 2 * kMaxRowsBlock * p->d * sizeof(float));
+  w.total = w.ml + kvc::align256(ctas * 2 * kMaxRowsBlock * 2 * sizeof(float));
+  return w;
+}
+
+bool misaligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) != 0; }
+
+template <typename T, int D>
+cudaError_t launch_prepare(const ChunkArgs& a, cudaStream_t s) {
+  const int groups = a.cap_lh ? (a.T + kPrepTok - 1) / kPrepTok : 1;
+  const int64_t warps = a.units * groups;
+  const dim3 grid((unsigned)((warps + kPrepWarps - 1) / kPrepWarps)), block(32 * kPrepWarps);
+  kvc::count_launch();
+  if (a.cap_lh) return kvc::chunk_launch(chunk_prepare_kernel<T, D, true>, grid, block, 0, s, a, groups);
+  return kvc::chunk_launch(chunk_prepare_kernel<T, D, false>, grid, block, 0, s, a, groups);
+}
+
+template <typename T, int D, int MR>
+cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
+  a.tt = std::min(MR / a.G, a.T);
+  a.tpb = a.tt;
+  a.rp = (a.T + a.tpb - 1) / a.tpb;
+  const size_t smem = sizeof(SimtSmem<D, MR>);
+  cudaError_t e = cudaFuncSetAttribute(chunk_attn_simt_kernel<T, D, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sms;
+  e = kvc::chunk_launch(chunk_attn_simt_kernel<T, D, MR>, dim3(grid), dim3(kSimtThreads), smem, s, a);
+  if (e != cudaSuccess) return e;
+  kvc::count_launch(2);
+  return kvc::chunk_launch(chunk_combine_kernel<T, D, MR>, dim3(grid - 1, MR / 16), dim3(256), 0, s, a, grid);
+}
+
+template <typename T, int D>
+cudaError_t launch_attn(ChunkArgs& a, int sms, cudaStream_t s) {
+  cudaError_t e = launch_prepare<T, D>(a, s);
+  if (e != cudaSuccess) return e;
+  if (a.G * a.T <= 16) return launch_attn_simt<T, D, 16>(a, sms, s);
+  return launch_attn_simt<T, D, 64>(a, sms, s);
+}
+
+template <typename T, int D>
+cudaError_t launch_mass(ChunkArgs& a, int sms, cudaStream_t s) {
+  cudaError_t e = launch_prepare<T, D>(a, s);
+  if (e != cudaSuccess) return e;
+  a.tt = std::min(64 / a.G, a.T);
+  const size_t smem = sizeof(SimtSmem<D, 64>);
+  e = cudaFuncSetAttribute(chunk_mass_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sms;
+  e = kvc::chunk_launch(chunk_mass_simt_kernel<T, D>, dim3(grid), dim3(kSimtThreads), smem, s, a);
+  if (e != cudaSuccess) return e;
+  kvc::count_launch(2);
+  return kvc::chunk_launch(chunk_mass_combine_kernel<kKeys>, dim3(grid - 1), dim3(kKeys), 0, s, a, grid);
+}
+
+}  // namespace
+
+namespace kvc {
+
+int chunk_check(const kvc_params* p, const kvc_chunk* c) {
+  const int st = check_params(p);
+  if (st != KVC_OK) return st;
+  if (!c || c->T < 1 || c->T > 65536) return KVC_EINVAL;
+  if (c->layer_begin < 0 || c->layer_begin >= c->layer_end || c->layer_end > p->L) return KVC_EINVAL;
+  if (p->packed_rows < 1 || p->packed_rows >= (1LL << 31)) return KVC_EINVAL;
+  if (c->page_rows != 0) {
+    if (c->page_rows < 16 || c->page_rows > 1024 || (c->page_rows & (c->page_rows - 1))) return KVC_EINVAL;
+    if (!c->page_table || c->max_pages < 1 || p->packed_rows < c->page_rows) return KVC_EINVAL;
+  }
+  if (!(c->softcap >= 0.f && c->softcap < INFINITY && c->window >= 0.f && c->window < INFINITY)) return KVC_EINVAL;
+  // units times row blocks, and the prepare kernel's grid, stay below 2^31
+  const int64_t units = (int64_t)p->B * p->H * (c->layer_end - c->layer_begin);
+  if (units > (1 << 24) || units * ((c->T + 1) / 2) >= (1LL << 31)) return KVC_EINVAL;
+  return KVC_OK;
+}
+
+void chunk_fill(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c) {
+  const int Lr = c->layer_end - c->layer_begin;
+  a.page_table = c->page_rows ? c->page_table : nullptr;
+  a.n_new = c->n_new;
+  a.slopes = c->slopes;
+  a.packed_rows = p->packed_rows;
+  a.units = (int64_t)p->B * Lr * p->H;
+  a.lh_span = (int64_t)Lr * p->H;
+  a.lh_gap = (int64_t)(p->L - Lr) * p->H;
+  a.lh_base = (int64_t)c->layer_begin * p->H;
+  a.T = c->T;
+  a.H = p->H;
+  a.G = p->G;
+  a.per_seq = Lr * p->H;
+  a.max_pages = c->max_pages;
+  a.page_shift = 0;
+  while (c->page_rows >> (a.page_shift + 1)) ++a.page_shift;
+  a.scale = 1.f / sqrtf((float)p->d);
+  a.scale_log2 = a.scale * kvcd::kLog2eC;
+  a.softcap = c->softcap;
+  a.window = c->window;
+  a.wait_ns = wait_limit_ns();
+  a.withhold = withhold_copies();
+}
+
+static int chunk_workspace(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c, void* workspace, size_t ws_bytes) {
+  const ChunkLayout w = chunk_layout(p, c);
+  if (!workspace || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return KVC_EWORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  a.rec = reinterpret_cast<ChunkUnit*>(ws + w.rec);
+  a.seg = reinterpret_cast<ChunkSeg*>(ws + w.seg);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  return KVC_OK;
+}
+
+}  // namespace kvc
+
+extern "C" size_t kvc_chunk_workspace_bytes(const kvc_params* p, const kvc_chunk* c) {
+  if (kvc::chunk_check(p, c) != KVC_OK) return 0;
+  return chunk_layout(p, c).total;
+}
+
+extern "C" int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const void* q, const void* k_new,
+                              const void* v_new, const float* pos_new, void* Kp, void* Vp, float* logm,
+                              float* pos, const int32_t* len_lh, const int32_t* cap_lh,
+                              const int64_t* off_lh, void* out, float* lse, int32_t* len_out,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  int st = kvc::chunk_check(p, c);
+  if (st != KVC_OK) return st;
+  if (!q || !k_new || !v_new || !pos_new || !Kp || !Vp || !logm || !pos || !len_lh || !cap_lh || !out ||
+      (!off_lh && c->page_rows == 0))
+    return KVC_EINVAL;
+  if (misaligned16(q) || misaligned16(k_new) || misaligned16(v_new) || misaligned16(Kp) || misaligned16(Vp) ||
+      misaligned16(out))
+    return KVC_EINVAL;
+  ChunkArgs a = {};
+  kvc::chunk_fill(a, p, c);
+  st = kvc::chunk_workspace(a, p, c, workspace, ws_bytes);
+  if (st != KVC_OK) return st;
+  a.err = kvc::err_word();
+  const int sms = kvc::sm_count();
+  if (!a.err || sms <= 0) return KVC_ECUDA;
+  a.q = q; a.k_new = k_new; a.v_new = v_new; a.pos_new = pos_new;
+  a.Kp = Kp; a.Vp = Vp; a.logm = logm; a.pos = pos;
+  a.len_lh = len_lh; a.cap_lh = cap_lh; a.off_lh = off_lh;
+  a.out = out; a.lse = lse; a.len_out = len_out;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (p->dtype == KVC_BF16)
+    e = p->d == 128 ? launch_attn<__nv_bfloat16, 128>(a, sms, s) : launch_attn<__nv_bfloat16, 64>(a, sms, s);
+  else
+    e = p->d == 128 ? launch_attn<float, 128>(a, sms, s) : launch_attn<float, 64>(a, sms, s);
+  return kvc::cuda_status(e);
+}
+
+extern "C" int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const void* q, const void* Kp,
+                              const float* logm, const float* pos, const float* pos_new,
+                              const int32_t* len_lh, const int64_t* off_lh, const float* lse, float decay,
+                              float* mass, void* workspace, size_t ws_bytes, void* stream) {
+  int st = kvc::chunk_check(p, c);
+  if (st != KVC_OK) return st;
+  if (!q || !Kp || !logm || !pos || !pos_new || !len_lh || !lse || !mass || (!off_lh && c->page_rows == 0) ||
+      !(decay >= 0.f && decay <= 1.f))
+    return KVC_EINVAL;
+  if (misaligned16(q) || misaligned16(Kp)) return KVC_EINVAL;
+  ChunkArgs a = {};
+  kvc::chunk_fill(a, p, c);
+  st = kvc::chunk_workspace(a, p, c, workspace, ws_bytes);
+  if (st != KVC_OK) return st;
+  a.err = kvc::err_word();
+  const int sms = kvc::sm_count();
+  if (!a.err || sms <= 0) return KVC_ECUDA;
+  a.q = q; a.Kp = const_cast<void*>(Kp); a.logm = const_cast<float*>(logm); a.pos = const_cast<float*>(pos);
+  a.pos_new = pos_new; a.len_lh = len_lh; a.off_lh = off_lh; a.lse = const_cast<float*>(lse);
+  a.decay = decay; a.mass = mass;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (p->dtype == KVC_BF16)
+    e = p->d == 128 ? launch_mass<__nv_bfloat16, 128>(a, sms, s) : launch_mass<__nv_bfloat16, 64>(a, sms, s);
+  else
+    e = p->d == 128 ? launch_mass<float, 128>(a, sms, s) : launch_mass<float, 64>(a, sms, s);
+  return kvc::cuda_status(e);
+}

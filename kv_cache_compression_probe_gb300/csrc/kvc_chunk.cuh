@@ -1,0 +1,220 @@
+// What the chunk kernels share (kvc_chunk_attn, kvc_chunk_mass, kvc_mass_evict):
+// the argument block, row addressing of contiguous and paged caches, and the
+// split of the work over the CTAs.
+//
+// A unit is one (b,l,h) of the layer range; its record (entries before the
+// chunk, new tokens, first row) is written by the prepare kernel, with n = 0 for
+// a unit that is skipped.  An item is one unit's row block (attention) or key
+// tile (mass); it costs as many steps as it has key tiles (row tiles).  The
+// steps of all items lie on one line, which is cut into equal pieces, one per
+// CTA: every CTA has the same work to within one step whatever the lengths are,
+// and an item that crosses a cut leaves one partial result per CTA, which a
+// combine kernel joins in CTA order (so results do not depend on timing).
+#pragma once
+#include <utility>
+
+#include "kvc_common.cuh"
+
+namespace kvc {
+
+struct ChunkUnit {                     // 16 bytes
+  int32_t len, n;                      // entries before the chunk, new tokens (0: skipped)
+  int64_t off;                         // first row (contiguous cache)
+};
+
+// Where a CTA's piece of the step line starts: the item, and whether inside it.
+struct ChunkSeg {
+  int64_t item, mid;
+};
+
+struct ChunkArgs {
+  const void* q;
+  const void* k_new;
+  const void* v_new;
+  const float* pos_new;
+  void* Kp;
+  void* Vp;
+  float* logm;
+  float* pos;
+  const int32_t* len_lh;
+  const int32_t* cap_lh;               // null: no append (mass)
+  const int64_t* off_lh;
+  void* out;
+  float* lse;                          // attention: written when not null; mass: read
+  int32_t* len_out;
+  float* mass;
+  const int32_t* page_table;           // null: contiguous
+  const int32_t* n_new;                // null: T
+  const float* slopes;
+  // workspace
+  ChunkUnit* rec;                      // [units]
+  ChunkSeg* seg;                       // [grid]
+  float* part;                         // per CTA two slots (kvc_chunk.cu)
+  float* part_ml;
+  int32_t* err;
+  int64_t packed_rows, units;
+  int64_t lh_span, lh_gap, lh_base;    // layer range, as lh_global
+  int T, H, G, per_seq;                // per_seq: units of one sequence
+  int max_pages, page_shift;
+  int tt, tpb, rp;                     // tokens per row tile, tokens per row block, row blocks per unit
+  float scale, scale_log2, softcap, window, decay;
+  uint64_t wait_ns;
+  int withhold;
+};
+
+}  // namespace kvc
+
+namespace kvcd {
+
+constexpr float kLog2eC = 1.4426950408889634f;
+
+__device__ __forceinline__ int64_t unit_global(const kvc::ChunkArgs& a, int64_t u) {
+  return u + (u / a.lh_span) * a.lh_gap + a.lh_base;
+}
+
+// Row of entry e of a unit.
+struct RowMap {
+  const int32_t* table;
+  int64_t off;
+  int shift;
+  __device__ __forceinline__ int64_t operator()(int e) const {
+    if (!table) return off + e;
+    return ((int64_t)__ldg(table + (e >> shift)) << shift) + (e & ((1 << shift) - 1));
+  }
+};
+__device__ __forceinline__ RowMap row_map(const kvc::ChunkArgs& a, int64_t u, int64_t off) {
+  RowMap m;
+  m.table = a.page_table ? a.page_table + unit_global(a, u) * a.max_pages : nullptr;
+  m.off = off;
+  m.shift = a.page_shift;
+  return m;
+}
+
+__device__ __forceinline__ kvc::ChunkUnit load_unit(const kvc::ChunkUnit* rec, int64_t u) {
+  const int4 v = __ldcg(reinterpret_cast<const int4*>(rec) + u);
+  kvc::ChunkUnit r;
+  r.len = v.x;
+  r.n = v.y;
+  r.off = ((int64_t)(uint32_t)v.z) | ((int64_t)v.w << 32);
+  return r;
+}
+
+// Steps of attention item i: key tiles of kTile entries that the row block's
+// last token sees; 0 past the unit's tokens.
+template <int kTile>
+struct AttnCost {
+  const kvc::ChunkArgs& a;
+  __device__ __forceinline__ int64_t items() const { return a.units * a.rp; }
+  __device__ __forceinline__ int operator()(int64_t i, kvc::ChunkUnit& r) const {
+    const int64_t u = i / a.rp;
+    const int t0 = (int)(i - u * a.rp) * a.tpb;
+    r = load_unit(a.rec, u);
+    if (t0 >= r.n) return 0;
+    return (r.len + min(r.n, t0 + a.tpb) + kTile - 1) / kTile;
+  }
+};
+
+// Block-wide: this CTA's piece [lo, hi) of the step line and the item that holds
+// step lo, with that item's first step.  item = -1 for an empty piece.
+struct Piece {
+  long long lo, hi, start;
+  int item;
+};
+struct LocateSmem {
+  long long warp[32];
+  Piece piece;
+};
+template <int kThreads, class Cost>
+__device__ Piece locate_piece(const Cost& cost, LocateSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t n = cost.items();
+  const int64_t per = (n + kThreads - 1) / kThreads;
+  const int64_t i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  kvc::ChunkUnit r;
+  long long mine = 0;
+  for (int64_t i = i0; i < i1; ++i) mine += cost(i, r);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(KVC_FULL_MASK, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm.warp[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.warp[w];
+    total += sm.warp[w];
+  }
+  const long long q = (total + gridDim.x - 1) / gridDim.x;
+  const long long lo = min(total, (long long)blockIdx.x * q), hi = min(total, lo + q);
+  long long at = before + incl - mine;
+  if (lo >= hi) {
+    if (tid == 0) sm.piece = Piece{lo, hi, 0, -1};
+  } else if (at <= lo && lo < at + mine) {
+    for (int64_t i = i0; i < i1; ++i) {
+      const int c = cost(i, r);
+      if (lo < at + c) {
+        sm.piece = Piece{lo, hi, at, (int)i};
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+  return sm.piece;
+}
+
+// Walks the items of a piece: for (Walk w(cost, piece); w.next(); ) visits the
+// steps [w.tb, w.te) of item w.item, of its w.tiles.
+template <class Cost>
+struct Walk {
+  const Cost& cost;
+  Piece p;
+  kvc::ChunkUnit r;
+  int item, tb, te, tiles;
+  bool first;
+  __device__ __forceinline__ Walk(const Cost& c, const Piece& pc) : cost(c), p(pc), item(pc.item), first(true) {}
+  __device__ __forceinline__ bool next() {
+    if (!first) {
+      p.start += tiles;
+      ++item;
+    }
+    if (p.item < 0 || p.start >= p.hi) return false;
+    while ((tiles = cost(item, r)) == 0) ++item;      // a step follows: p.start < p.hi <= all steps
+    tb = first ? (int)(p.lo - p.start) : 0;
+    te = (int)min((long long)tiles, p.hi - p.start);
+    first = false;
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return tb == 0 && te == tiles; }
+};
+
+}  // namespace kvcd
+
+namespace kvc {
+
+// Launch with programmatic stream serialization: the kernel calls pdl_wait
+// before it reads what its predecessor writes.
+template <typename... Params, typename... Args>
+cudaError_t chunk_launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Argument checks shared by the calls (p, c and the page table), and the fields
+// of the argument block that come from them.
+int chunk_check(const kvc_params* p, const kvc_chunk* c);
+void chunk_fill(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c);
+
+}  // namespace kvc

@@ -26,7 +26,9 @@ EXPORTED = ("kvc_status_string", "kvc_last_cuda_error", "kvc_device_error", "kvc
             "kvc_rope_table", "kvc_score", "kvc_select", "kvc_merge_pack", "kvc_decode_attn",
             "kvc_partition", "kvc_decode_attn_noalloc", "kvc_decode_attn_lse", "kvc_token_alpha",
             "kvc_evict_workspace_bytes", "kvc_evict_topb", "kvc_set_phase_timing",
-            "kvc_score_phase_ms", "kvc_decode_attn_layers", "kvc_tree_cuts", "kvc_set_wait_limit")
+            "kvc_score_phase_ms", "kvc_decode_attn_layers", "kvc_tree_cuts", "kvc_set_wait_limit",
+            "kvc_chunk_attn", "kvc_chunk_workspace_bytes", "kvc_chunk_mass", "kvc_mass_evict",
+            "kvc_mass_evict_workspace_bytes")
 
 
 class kvc_params(ctypes.Structure):
@@ -45,6 +47,15 @@ class kvc_params(ctypes.Structure):
     ]
 
 
+class kvc_chunk(ctypes.Structure):
+    _fields_ = [
+        ("T", c_int32), ("layer_begin", c_int32), ("layer_end", c_int32),
+        ("page_rows", c_int32), ("max_pages", c_int32), ("softcap", c_float),
+        ("window", c_float), ("page_table", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+        ("slopes", ctypes.c_void_p),
+    ]
+
+
 class KvcError(RuntimeError):
     def __init__(self, status: int, what: str):
         msg = f"{what}: {kvc_status_string(status)} ({status})"
@@ -56,6 +67,7 @@ class KvcError(RuntimeError):
 
 _lib = None
 _P = ctypes.POINTER(kvc_params)
+_C = ctypes.POINTER(kvc_chunk)
 
 
 def lib():
@@ -100,6 +112,16 @@ def lib():
         L.kvc_partition.restype = c_int
         L.kvc_tree_cuts.argtypes = [_P] + [vp] * 9
         L.kvc_tree_cuts.restype = c_int
+        L.kvc_chunk_attn.argtypes = [_P, _C] + [vp] * 15 + [c_size_t, vp]
+        L.kvc_chunk_attn.restype = c_int
+        L.kvc_chunk_workspace_bytes.argtypes = [_P, _C]
+        L.kvc_chunk_workspace_bytes.restype = c_size_t
+        L.kvc_chunk_mass.argtypes = [_P, _C] + [vp] * 8 + [c_float, vp, vp, c_size_t, vp]
+        L.kvc_chunk_mass.restype = c_int
+        L.kvc_mass_evict.argtypes = [_P, _C, vp, vp, c_int32] + [vp] * 8 + [c_int32, vp, c_size_t, vp]
+        L.kvc_mass_evict.restype = c_int
+        L.kvc_mass_evict_workspace_bytes.argtypes = [_P, _C, c_int32]
+        L.kvc_mass_evict_workspace_bytes.restype = c_size_t
         _lib = L
     return _lib
 
@@ -141,6 +163,25 @@ def make_params(**kw) -> kvc_params:
     for k, v in defaults.items():
         setattr(p, k, v)
     return p
+
+
+def make_chunk(T, layer_begin=0, layer_end=1, page_rows=0, page_table=None, n_new=None,
+               softcap=0.0, window=0.0, slopes=None) -> kvc_chunk:
+    """A kvc_chunk block; page_table ([B, L, H, max_pages] or [B*L*H, max_pages]
+    int32), n_new ([B] int32) and slopes ([H*G] f32) are CUDA tensors that the
+    block keeps alive."""
+    c = kvc_chunk()
+    c.T, c.layer_begin, c.layer_end = int(T), int(layer_begin), int(layer_end)
+    c.page_rows = int(page_rows)
+    c.max_pages = page_table.shape[-1] if page_table is not None else 0
+    c.softcap, c.window = float(softcap), float(window)
+    for name, t, dt in (("page_table", page_table, torch.int32), ("n_new", n_new, torch.int32),
+                        ("slopes", slopes, torch.float32)):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}")
+        setattr(c, name, _ptr(t))
+    c._keep = (page_table, n_new, slopes)
+    return c
 
 
 # ------------------------------------------------------------------ calls
@@ -286,6 +327,47 @@ def kvc_tree_cuts(p, ctx_len, K, rope_cos, rope_sin, slot_bounds, n_slots, kappa
     _check(lib().kvc_tree_cuts(ctypes.byref(p), _ptr(ctx_len), _ptr(K), _ptr(rope_cos),
                                _ptr(rope_sin), _ptr(slot_bounds), _ptr(n_slots), _ptr(kappa),
                                _ptr(cuts), _stream(stream)), "kvc_tree_cuts")
+
+
+def kvc_chunk_workspace_bytes(p, c) -> int:
+    return int(lib().kvc_chunk_workspace_bytes(ctypes.byref(p), ctypes.byref(c)))
+
+
+def kvc_chunk_attn(p, c, q, k_new, v_new, pos_new, Kp, Vp, logm, pos, len_lh, cap_lh, off_lh, out,
+                   lse, len_out, workspace, stream=None):
+    """Attention of a chunk of new tokens over the packed cache (contiguous rows
+    or pages); lse, len_out and, with pages, off_lh may be None."""
+    w, wb = _ws(workspace)
+    _check(lib().kvc_chunk_attn(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(k_new),
+                                _ptr(v_new), _ptr(pos_new), _ptr(Kp), _ptr(Vp), _ptr(logm),
+                                _ptr(pos), _ptr(len_lh), _ptr(cap_lh), _ptr(off_lh), _ptr(out),
+                                _ptr(lse), _ptr(len_out), w, wb, _stream(stream)),
+           "kvc_chunk_attn")
+
+
+def kvc_chunk_mass(p, c, q, Kp, logm, pos, pos_new, len_lh, off_lh, lse, decay, mass, workspace,
+                   stream=None):
+    """mass = decay * mass + the attention weight every entry received from the
+    chunk (len_lh: the lengths before it)."""
+    w, wb = _ws(workspace)
+    _check(lib().kvc_chunk_mass(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(Kp), _ptr(logm),
+                                _ptr(pos), _ptr(pos_new), _ptr(len_lh), _ptr(off_lh), _ptr(lse),
+                                float(decay), _ptr(mass), w, wb, _stream(stream)),
+           "kvc_chunk_mass")
+
+
+def kvc_mass_evict_workspace_bytes(p, c, max_len: int) -> int:
+    return int(lib().kvc_mass_evict_workspace_bytes(ctypes.byref(p), ctypes.byref(c), int(max_len)))
+
+
+def kvc_mass_evict(p, c, mass, keep_lh, recent, pos_next, Kp, Vp, logm, pos, len_lh, off_lh,
+                   len_out, max_len, workspace, stream=None):
+    """Per-(b, l, h) eviction down to keep_lh entries by mass, in place."""
+    w, wb = _ws(workspace)
+    _check(lib().kvc_mass_evict(ctypes.byref(p), ctypes.byref(c), _ptr(mass), _ptr(keep_lh),
+                                int(recent), _ptr(pos_next), _ptr(Kp), _ptr(Vp), _ptr(logm),
+                                _ptr(pos), _ptr(len_lh), _ptr(off_lh), _ptr(len_out),
+                                int(max_len), w, wb, _stream(stream)), "kvc_mass_evict")
 
 
 def workspace(which: int, p: kvc_params, device="cuda", zero=False) -> torch.Tensor:

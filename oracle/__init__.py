@@ -6,3 +6,4 @@ anything in this package.  The product path (the C-ABI library and its Python
 binding) never imports it, and this package imports nothing from the product.
 """
 from .kvc_oracle import *  # noqa: F401,F403
+from .chunk_oracle import *  # noqa: F401,F403
