@@ -12,7 +12,7 @@
 
 #include <algorithm>
 
-#include "kvc_chunk.cuh"
+#include "kvc_chunk_tc.cuh"
 #include "kvc_internal.h"
 
 namespace {
@@ -538,6 +538,19 @@ cudaError_t launch_prepare(const ChunkArgs& a, cudaStream_t s) {
   return kvc::chunk_launch(chunk_prepare_kernel<T, D, false>, grid, block, 0, s, a, groups);
 }
 
+template <typename T, int D>
+cudaError_t launch_combine(const ChunkArgs& a, int rows_block, int grid, cudaStream_t s) {
+  if (grid < 2) return cudaSuccess;
+  kvc::count_launch();
+  const dim3 g(grid - 1, rows_block / 16);
+  switch (rows_block) {
+    case 16: return kvc::chunk_launch(chunk_combine_kernel<T, D, 16>, g, dim3(256), 0, s, a, grid);
+    case 64: return kvc::chunk_launch(chunk_combine_kernel<T, D, 64>, g, dim3(256), 0, s, a, grid);
+    case 128: return kvc::chunk_launch(chunk_combine_kernel<T, D, 128>, g, dim3(256), 0, s, a, grid);
+    default: return kvc::chunk_launch(chunk_combine_kernel<T, D, 256>, g, dim3(256), 0, s, a, grid);
+  }
+}
+
 template <typename T, int D, int MR>
 cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
   a.tt = std::min(MR / a.G, a.T);
@@ -549,8 +562,16 @@ cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
   const int grid = 2 * sms;
   e = kvc::chunk_launch(chunk_attn_simt_kernel<T, D, MR>, dim3(grid), dim3(kSimtThreads), smem, s, a);
   if (e != cudaSuccess) return e;
-  kvc::count_launch(2);
-  return kvc::chunk_launch(chunk_combine_kernel<T, D, MR>, dim3(grid - 1, MR / 16), dim3(256), 0, s, a, grid);
+  kvc::count_launch();
+  return launch_combine<T, D>(a, MR, grid, s);
+}
+
+template <int D>
+cudaError_t launch_attn_bf16(ChunkArgs& a, int sms, int page_rows, cudaStream_t s) {
+  cudaError_t e = launch_prepare<__nv_bfloat16, D>(a, s);
+  if (e == cudaSuccess) e = kvc::chunk_attn_tc_launch(a, D, sms, page_rows, s);
+  if (e != cudaSuccess) return e;
+  return launch_combine<__nv_bfloat16, D>(a, a.T > a.tt ? 256 : 128, sms, s);
 }
 
 template <typename T, int D>
@@ -659,7 +680,7 @@ extern "C" int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const voi
   if (st != KVC_OK) return st;
   a.err = kvc::err_word();
   const int sms = kvc::sm_count();
-  if (!a.err || sms <= 0) return KVC_ECUDA;
+  if (!a.err || sms <= 0 || !kvc::chunk_tc_available()) return KVC_ECUDA;
   a.q = q; a.k_new = k_new; a.v_new = v_new; a.pos_new = pos_new;
   a.Kp = Kp; a.Vp = Vp; a.logm = logm; a.pos = pos;
   a.len_lh = len_lh; a.cap_lh = cap_lh; a.off_lh = off_lh;
@@ -667,7 +688,7 @@ extern "C" int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (p->dtype == KVC_BF16)
-    e = p->d == 128 ? launch_attn<__nv_bfloat16, 128>(a, sms, s) : launch_attn<__nv_bfloat16, 64>(a, sms, s);
+    e = p->d == 128 ? launch_attn_bf16<128>(a, sms, c->page_rows, s) : launch_attn_bf16<64>(a, sms, c->page_rows, s);
   else
     e = p->d == 128 ? launch_attn<float, 128>(a, sms, s) : launch_attn<float, 64>(a, sms, s);
   return kvc::cuda_status(e);

@@ -1,0 +1,636 @@
+// kvc_chunk_attn in bf16 on the tensor cores.
+//
+// A query row tile is up to 128 rows: tt tokens x G heads of one (b,l,h), so the
+// K and V of a KV head are read once for its whole group.  Per 128-entry tile
+//   S[128 rows x 128 entries] = Q K^T    (tcgen05, both operands from shared memory)
+//   P = 2^(s - m)                        (one thread per row, fp32, in registers)
+//   O[128 rows x d] += P V               (P as the TMEM operand, V MN-major)
+// with the running maximum m and sum l of each row in one thread.  O is rescaled
+// only when the maximum has grown by more than 2^8 since the last time, which
+// leaves P below 2^8 and the result unchanged.
+//
+// Two streams of S, P and O alternate, so that the tensor cores work on one
+// while the softmax of the other runs:
+//   kRowStreams  two row tiles over the same K and V tiles (many rows: the bound
+//                is the tensor rate, or the softmax's issue slots);
+//   else         one row tile over alternate K/V tiles, joined at the end (few
+//                rows: the bound is HBM, and the two streams halve the latency
+//                of a tile's chain).
+// Warps: 0 copies (TMA), 1 issues the products, 2 and 3 fetch ln m and positions
+// of alternate tiles, 4..7 and 8..11 are the softmax of the two streams.  The
+// work is cut as kvc_chunk.cuh says; persistent, one CTA per SM (512 TMEM
+// columns: S, S, O, O; P lies in S's place).
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "kvc_chunk_tc.cuh"
+
+namespace {
+
+using kvc::ChunkArgs;
+using kvc::ChunkSeg;
+using kvc::ChunkUnit;
+using namespace kvctc;
+
+constexpr int kThreads = 384;
+constexpr int kBias = 4;               // bias tiles in flight
+constexpr float kLazy = 8.f;           // rescale O when the maximum grew by more (base 2)
+constexpr int kCols = 512;             // TMEM columns
+
+template <int D>
+struct AttnSmem {
+  static constexpr int kStages = D == 128 ? 4 : 8;     // K or V tiles in flight: 128 KB
+  static constexpr uint32_t kTileBytes = 128 * D * 2;
+  alignas(1024) unsigned char q[2][kTileBytes];
+  alignas(1024) unsigned char ring[kStages][kTileBytes];
+  alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - first new position
+  float m1[128], l1[128];                              // stream 1's statistics (entry streams)
+  uint64_t full[kStages], empty[kStages], q_full[2], q_empty[2], bias_full[kBias], bias_empty[kBias];
+  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  kvcd::LocateSmem loc;
+  uint32_t tmem;
+  int abort;
+};
+
+// Where a load or product stands in the ring.
+struct Ring {
+  int slot, phase;
+  __device__ __forceinline__ Ring() : slot(0), phase(0) {}
+  template <int N> __device__ __forceinline__ void step() {
+    if (++slot == N) { slot = 0; phase ^= 1; }
+  }
+};
+
+// Base-2 scores of one row over a 128-entry tile, in place of the raw products.
+template <bool kCap, bool kPos>
+__device__ __forceinline__ float scores(const ChunkArgs& a, uint32_t (&s)[128], const float* lm, const float* rel,
+                                        float slope2, float tok, int lim) {
+  const uint64_t sc = pk(a.scale_log2, a.scale_log2), slope = pk(slope2, slope2), mtok = pk(-tok, -tok);
+  const float edge = kPos && a.window > 0.f ? tok - a.window : -INFINITY;   // sees rel > edge
+  const float cap_in = kCap ? a.scale / a.softcap : 0.f, cap_out = kCap ? a.softcap * kvcd::kLog2eC : 0.f;
+#pragma unroll
+  for (int c = 0; c < 128; c += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(lm + c);
+    uint64_t x0, x1;
+    if constexpr (kCap) {
+      x0 = pk(fmaf(tanh_f(__uint_as_float(s[c]) * cap_in), cap_out, b.x),
+              fmaf(tanh_f(__uint_as_float(s[c + 1]) * cap_in), cap_out, b.y));
+      x1 = pk(fmaf(tanh_f(__uint_as_float(s[c + 2]) * cap_in), cap_out, b.z),
+              fmaf(tanh_f(__uint_as_float(s[c + 3]) * cap_in), cap_out, b.w));
+    } else {
+      x0 = fma2(pk(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, pk(b.x, b.y));
+      x1 = fma2(pk(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, pk(b.z, b.w));
+    }
+    if constexpr (kPos) {
+      const float4 r = *reinterpret_cast<const float4*>(rel + c);
+      x0 = fma2(slope, add2(pk(r.x, r.y), mtok), x0);
+      x1 = fma2(slope, add2(pk(r.z, r.w), mtok), x1);
+    }
+    float f0, f1, f2, f3;
+    upk(x0, f0, f1);
+    upk(x1, f2, f3);
+    if constexpr (kPos) {
+      const float4 r = *reinterpret_cast<const float4*>(rel + c);
+      f0 = r.x > edge ? f0 : -INFINITY;
+      f1 = r.y > edge ? f1 : -INFINITY;
+      f2 = r.z > edge ? f2 : -INFINITY;
+      f3 = r.w > edge ? f3 : -INFINITY;
+    }
+    s[c] = __float_as_uint(f0); s[c + 1] = __float_as_uint(f1);
+    s[c + 2] = __float_as_uint(f2); s[c + 3] = __float_as_uint(f3);
+  }
+  if (__any_sync(KVC_FULL_MASK, lim < 128)) {          // the chunk's own tokens, or the last entries
+#pragma unroll
+    for (int c = 0; c < 128; ++c)
+      if (c >= lim) s[c] = 0xff800000u;
+  }
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 128; c += 4) {
+    m0 = kvcd::fmax3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    m1 = kvcd::fmax3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+  }
+  return fmaxf(m0, m1);
+}
+
+template <int D, bool kRowStreams, bool kCap, bool kPos>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ChunkArgs a) {
+  using Smem = AttnSmem<D>;
+  constexpr int kStages = Smem::kStages;
+  constexpr int kBlocks = D / 64;
+  extern __shared__ __align__(1024) unsigned char attn_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(attn_raw) + 1023) & ~uintptr_t(1023));
+  kvcd::pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) { kvcd::mbar_init(&sm.full[i], 1); kvcd::mbar_init(&sm.empty[i], 1); }
+    for (int i = 0; i < kBias; ++i) {
+      kvcd::mbar_init(&sm.bias_full[i], 1);
+      kvcd::mbar_init(&sm.bias_empty[i], kRowStreams ? 8 : 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      kvcd::mbar_init(&sm.q_full[i], 1);
+      kvcd::mbar_init(&sm.q_empty[i], 1);
+      kvcd::mbar_init(&sm.s_full[i], 1);
+      kvcd::mbar_init(&sm.p_full[i], 4);
+      kvcd::mbar_init(&sm.o_done[i], 1);
+    }
+    kvcd::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    kvcd::fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kvcd::smem_u32(&sm.tmem)),
+                 "r"((uint32_t)kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  kvcd::pdl_wait();                                    // the prepare kernel's records and appended rows
+  const kvcd::AttnCost<128> cost{a};
+  const kvcd::Piece piece = kvcd::locate_piece<kThreads>(cost, sm.loc);
+  if (tid == 0) a.seg[blockIdx.x] = ChunkSeg{piece.item, piece.item >= 0 && piece.lo > piece.start};
+  if (a.len_out)
+    for (int64_t u = (int64_t)blockIdx.x * kThreads + tid; u < a.units; u += (int64_t)gridDim.x * kThreads) {
+      const ChunkUnit r = kvcd::load_unit(a.rec, u);
+      const int64_t gu = kvcd::unit_global(a, u);
+      a.len_out[gu] = r.n > 0 ? r.len + r.n : a.len_lh[gu];
+    }
+  const uint32_t tmem = sm.tmem;
+  volatile int* abort_flag = &sm.abort;
+  const uint64_t ns = a.wait_ns;
+  // outstanding copies, for the drain after a give-up: bit i of these = slot i's (or query
+  // buffer i's) last copy was issued in phase 0 / 1
+  uint32_t issued = 0, issued_phase = 0, q_issued = 0, q_phase = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    fence_proxy_async_all();
+    Ring ring;
+    int li = 0;
+    bool ok = true;
+    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next(); ++li) {
+      const int64_t u = w.item / a.rp;
+      const int t0 = (int)(w.item - u * a.rp) * a.tpb;
+      const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
+      const int total = w.r.len + w.r.n, nt = w.te - w.tb;
+      const bool two = kRowStreams && t0 + a.tt < w.r.n;
+      const int qb = kRowStreams ? 0 : li & 1, use = kRowStreams ? li : li >> 1;
+      // the query rows: their buffer is free once the products before have read it
+      if (use > 0) ok = warp_wait(&sm.q_empty[qb], (uint32_t)((use - 1) & 1), ns, abort_flag);
+      if (!ok) break;
+      if (lane == 0 && !a.withhold) {
+        const uint32_t bytes = (uint32_t)(a.G * a.tt * 128 * kBlocks);
+        kvcd::mbar_arrive_expect_tx(&sm.q_full[qb], two ? 2 * bytes : bytes);
+        for (int i = 0; i < (two ? 2 : 1); ++i)
+#pragma unroll
+          for (int h = 0; h < kBlocks; ++h)
+            tma3d(kvcd::smem_u32(sm.q[kRowStreams ? i : qb]) + h * kHalf, &qmap, h * 64, t0 + i * a.tt, (int)(u * a.G),
+                  &sm.q_full[qb]);
+        q_issued |= 1u << qb;
+        q_phase = (q_phase & ~(1u << qb)) | ((uint32_t)(use & 1) << qb);
+      }
+      // K and V tiles in the order the products take them: K runs one tile (row
+      // streams) or two (entry streams) ahead of V
+      constexpr int kAhead = kRowStreams ? 1 : 2;
+      for (int i = 0; ok && i < nt + kAhead; ++i) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {                  // v = 0: V of tile i - kAhead; 1: K of tile i
+          const int t = v ? i : i - kAhead;
+          if (t < 0 || t >= nt) continue;
+          ok = warp_wait(&sm.empty[ring.slot], (uint32_t)(ring.phase ^ 1), ns, abort_flag);
+          if (!ok) break;
+          if (!a.withhold) {
+            copy_tile<D>(a, rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]), (w.tb + t) * 128, total,
+                         &sm.full[ring.slot], lane);
+            issued |= 1u << ring.slot;
+            issued_phase = (issued_phase & ~(1u << ring.slot)) | ((uint32_t)ring.phase << ring.slot);
+          }
+          ring.step<kStages>();
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products (lane 0 issues)
+    Ring ring;
+    int li = 0;
+    uint32_t pphase = 0;                               // bit s: parity of stream s's next P
+    bool ok = true;
+    auto take = [&](int& slot) {                       // the next K or V tile
+      ok = ok && warp_wait(&sm.full[ring.slot], (uint32_t)ring.phase, ns, abort_flag);
+      slot = ring.slot;
+      ring.step<kStages>();
+      fence_after();
+      return ok;
+    };
+    auto qk = [&](int s, int slot, int qtile) {        // S_s = Q K^T
+      if (lane == 0) {
+        const uint32_t kb = kvcd::smem_u32(sm.ring[slot]), qb = kvcd::smem_u32(sm.q[qtile]);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + s * 128, desc_k(qb + (k >> 2) * kHalf + (k & 3) * 32),
+                 desc_k(kb + (k >> 2) * kHalf + (k & 3) * 32), idesc(128, false), k > 0);
+        commit(&sm.s_full[s]);
+      }
+      __syncwarp();
+    };
+    auto wait_p = [&](int s) {
+      ok = ok && warp_wait(&sm.p_full[s], (pphase >> s) & 1, ns, abort_flag);
+      pphase ^= 1u << s;
+      fence_after();
+      return ok;
+    };
+    auto pv = [&](int s, int slot, bool first, bool last) {  // O_s += P_s V
+      if (lane == 0) {
+        const uint32_t vb = kvcd::smem_u32(sm.ring[slot]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8, desc_mn(vb + k * 2048, kHalf), idesc(D, true),
+                 !(first && k == 0));
+        if (last) commit(&sm.o_done[s]);
+      }
+      __syncwarp();
+    };
+    auto release = [&](int slot) {
+      if (lane == 0) commit(&sm.empty[slot]);
+      __syncwarp();
+    };
+    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next(); ++li) {
+      const int64_t u = w.item / a.rp;
+      const int t0 = (int)(w.item - u * a.rp) * a.tpb;
+      const int total = w.r.len + w.r.n, nt = w.te - w.tb;
+      const int ns2 = kRowStreams && t0 + a.tt < w.r.n ? 2 : 1;
+      const int qb = kRowStreams ? 0 : li & 1, use = kRowStreams ? li : li >> 1;
+      ok = warp_wait(&sm.q_full[qb], (uint32_t)(use & 1), ns, abort_flag);
+      if (!ok) break;
+      // rows past the last entry: V zero (P is 0 there, but they may hold anything)
+      auto clear_tail = [&](int slot, int tile) {
+        const int valid = total - (w.tb + tile) * 128;
+        if (valid >= 128) return;
+        for (int z = lane; z < (128 - valid) * 8 * kBlocks; z += 32) {
+          const int r = valid + z / (8 * kBlocks), h = (z >> 3) & (kBlocks - 1), c = z & 7;
+          *reinterpret_cast<uint4*>(sm.ring[slot] + h * kHalf + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        kvcd::fence_proxy_async_smem();
+        __syncwarp();
+      };
+      int slot;
+      if constexpr (kRowStreams) {
+        if (!take(slot)) break;
+        for (int s = 0; s < ns2; ++s) qk(s, slot, s);
+        release(slot);
+        if (nt == 1 && lane == 0) commit(&sm.q_empty[qb]);
+        for (int i = 0; ok && i < nt; ++i) {
+          int vs = 0, ks = 0;
+          for (int s = 0; s < ns2; ++s) {
+            if (!wait_p(s)) break;
+            if (s == 0) {
+              if (!take(vs)) break;
+              clear_tail(vs, i);
+            }
+            pv(s, vs, i == 0, i + 1 == nt);
+            if (s + 1 == ns2) release(vs);
+            if (i + 1 < nt) {
+              if (s == 0 && !take(ks)) break;
+              qk(s, ks, s);
+              if (s + 1 == ns2) {
+                release(ks);
+                if (i + 2 == nt && lane == 0) commit(&sm.q_empty[qb]);
+              }
+            }
+          }
+        }
+      } else {
+        for (int j = 0; ok && j < min(2, nt); ++j) {
+          if (!take(slot)) break;
+          qk(j, slot, qb);
+          release(slot);
+          if (j + 1 == nt && lane == 0) commit(&sm.q_empty[qb]);
+        }
+        for (int j = 0; ok && j < nt; ++j) {
+          const int s = j & 1;
+          if (!wait_p(s)) break;
+          if (!take(slot)) break;
+          clear_tail(slot, j);
+          pv(s, slot, j < 2, j + 2 >= nt);
+          release(slot);
+          if (j + 2 < nt) {
+            if (!take(slot)) break;
+            qk(s, slot, qb);
+            release(slot);
+            if (j + 3 == nt && lane == 0) commit(&sm.q_empty[qb]);
+          }
+        }
+      }
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ ln m and positions
+    int cnt = 0;                                       // tiles so far; this warp takes every other one
+    bool ok = true;
+    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next();) {
+      const int64_t u = w.item / a.rp;
+      const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
+      const int total = w.r.len + w.r.n;
+      const float pos0 = kPos ? a.pos_new[u / a.per_seq] : 0.f;
+      for (int t = w.tb; ok && t < w.te; ++t, ++cnt) {
+        if ((cnt & 1) != (warp & 1)) continue;
+        float lm[4], rel[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = t * 128 + lane + 32 * j;
+          lm[j] = rel[j] = 0.f;
+          if (e < total) {
+            const int64_t row = rows(e);
+            lm[j] = __ldcg(a.logm + row) * kvcd::kLog2eC;
+            if (kPos) rel[j] = __ldcg(a.pos + row) - pos0;
+          }
+        }
+        const int b = cnt % kBias, use = cnt / kBias;
+        if (use > 0) ok = warp_wait(&sm.bias_empty[b], (uint32_t)((use - 1) & 1), ns, abort_flag);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sm.lm[b][lane + 32 * j] = lm[j];
+          if (kPos) sm.rel[b][lane + 32 * j] = rel[j];
+        }
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.bias_full[b]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int st = (warp - 4) >> 2, q4 = warp & 3;     // stream; TMEM lane quarter
+    const int row = q4 * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t ts = tl + st * 128, to = tl + 256 + st * D;
+    uint32_t sphase = 0, ophase[2] = {0, 0};
+    int cnt = 0;                                       // bias tiles so far
+    bool joined = false;                               // entry streams: stream 1's results may be in use
+    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); w.next();) {
+      const int64_t u = w.item / a.rp;
+      const int t0 = (int)(w.item - u * a.rp) * a.tpb + (kRowStreams ? st * a.tt : 0);
+      const int tok = t0 + row % a.tt, g = row / a.tt;
+      const bool live = g < a.G && tok < w.r.n;
+      const bool busy = __any_sync(KVC_FULL_MASK, live);
+      const int see = live ? w.r.len + tok + 1 : 0;    // entries this row sees
+      const float slope2 = kPos && a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
+      const int nt = w.te - w.tb;
+      const bool mine = !kRowStreams || st == 0 || t0 < w.r.n;     // this stream has work
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < nt; ++i, ++cnt) {
+        if (!kRowStreams && (i & 1) != st) continue;
+        const int b = cnt % kBias;
+        wait_or_abort(&sm.bias_full[b], (uint32_t)((cnt / kBias) & 1), ns, abort_flag);
+        if (!mine) {
+          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          continue;
+        }
+        wait_or_abort(&sm.s_full[st], sphase, ns, abort_flag);
+        sphase ^= 1;
+        fence_after();
+        if (busy) {
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tld32(ts + c * 32, s + c * 32);
+          wait_ld();
+          const float mx = scores<kCap, kPos>(a, s, sm.lm[b], sm.rel[b], slope2, (float)tok, see - (w.tb + i) * 128);
+          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          // the first entries of the stream set the maximum; later ones move it only when
+          // they exceed it by more than 2^kLazy
+          const bool first = kRowStreams ? i == 0 : i < 2;
+          if (__any_sync(KVC_FULL_MASK, mx > m + (first ? 0.f : kLazy))) {
+            const float mn = fmaxf(m, mx);
+            const float f = m == -INFINITY ? 0.f : kvcd::ex2(m - mn);
+            if (!first) {                              // S is ready, so the product before has ended
+              l *= f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tld16(to + c, o);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tst16(to + c, o);
+              }
+            }
+            m = mn;
+          }
+          if (!kRowStreams && st == 1 && joined) {     // stream 0 has read the results before
+            named_sync(2, 256);
+            joined = false;
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          const uint64_t mb = pk(-base, -base);
+          uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float x0, x1, x2, x3;
+              upk(add2(pk(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), mb), x0, x1);
+              upk(add2(pk(__uint_as_float(s[c + e + 2]), __uint_as_float(s[c + e + 3])), mb), x2, x3);
+              x0 = kvcd::ex2(x0); x1 = kvcd::ex2(x1); x2 = kvcd::ex2(x2); x3 = kvcd::ex2(x3);
+              sum0 = add2(sum0, pk(x0, x1));
+              sum1 = add2(sum1, pk(x2, x3));
+              p[e / 2] = bf16x2(x0, x1);
+              p[e / 2 + 1] = bf16x2(x2, x3);
+            }
+            tst16(ts + c / 2, p);
+          }
+          float a0, a1;
+          upk(add2(sum0, sum1), a0, a1);
+          l += a0 + a1;
+          wait_st();
+        } else {
+          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          if (!kRowStreams && st == 1 && joined) {
+            named_sync(2, 256);
+            joined = false;
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.p_full[st]);
+      }
+      // ---- this piece's result
+      const bool whole = w.whole();
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (w.tb == 0 ? 1 : 0)) * (kRowStreams ? 256 : 128) +
+                           (kRowStreams ? st * 128 : 0) + row;
+      const int64_t orow = (u * a.G + g) * a.T + tok;
+      float f0 = 1.f, f1 = 0.f;
+      if constexpr (!kRowStreams) {
+        if (nt > 1) {
+          if (st == 1) {                               // hand m and l over; stream 0 writes the result
+            sm.m1[row] = m;
+            sm.l1[row] = l;
+            named_arrive(1, 256);
+            joined = true;
+            ophase[1] ^= 1;
+            continue;
+          }
+          wait_or_abort(&sm.o_done[0], ophase[0], ns, abort_flag);
+          wait_or_abort(&sm.o_done[1], ophase[1], ns, abort_flag);
+          ophase[0] ^= 1;
+          ophase[1] ^= 1;
+          named_sync(1, 256);
+          const float mb = sm.m1[row], lb = sm.l1[row];
+          const float mn = fmaxf(m, mb);
+          f0 = m == -INFINITY ? 0.f : kvcd::ex2(m - mn);
+          f1 = mb == -INFINITY ? 0.f : kvcd::ex2(mb - mn);
+          l = fmaf(l, f0, lb * f1);
+          m = mn;
+        } else {
+          if (st == 1) continue;
+          wait_or_abort(&sm.o_done[0], ophase[0], ns, abort_flag);
+          ophase[0] ^= 1;
+        }
+      } else {
+        if (!mine) continue;
+        wait_or_abort(&sm.o_done[st], ophase[0], ns, abort_flag);
+        ophase[0] ^= 1;
+      }
+      fence_after();
+      const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      f0 *= inv;
+      f1 *= inv;
+      if (busy) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tld16(to + c, o);
+          wait_ld();
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * f0;
+          if (!kRowStreams && nt > 1) {
+            tld16(to + D + c, o);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
+          }
+          if (live && whole) {
+            uint4* op = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c);
+            op[0] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+            op[1] = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
+          } else if (live) {
+            float4* pp = reinterpret_cast<float4*>(a.part + slot * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pp[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        }
+        if (live && whole && a.lse) a.lse[orow] = l > 0.f ? m + log2f(l) : -INFINITY;
+        if (live && !whole) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, l);
+      }
+      fence_before();
+      if (!kRowStreams && nt > 1) named_arrive(2, 256);
+    }
+    if (!kRowStreams && st == 1 && joined) named_sync(2, 256);
+  }
+
+  fence_before();
+  __syncthreads();
+  if (*abort_flag) {                                   // a bounded wait gave up
+    if (warp == 0 && lane == 0) {                      // copies still in flight land first
+      for (int i = 0; i < kStages; ++i)
+        if ((issued >> i) & 1) kvcd::mbar_wait(&sm.full[i], (issued_phase >> i) & 1);
+      for (int i = 0; i < 2; ++i)
+        if ((q_issued >> i) & 1) kvcd::mbar_wait(&sm.q_full[i], (q_phase >> i) & 1);
+    }
+    if (warp == 1 && lane == 0) {                      // and every issued product ends
+      commit(&sm.drain);
+      kvcd::mbar_wait(&sm.drain, 0);
+    }
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)kCols) : "memory");
+  if (*abort_flag && tid == 0) kvcd::record_error(a.err, KVC_ETIMEOUT);
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
+std::once_flag g_enc_once;
+PFN_cuTensorMapEncodeTiled_v12000 enc_fn() {
+  std::call_once(g_enc_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_enc;
+}
+
+template <int D, bool kRowStreams, bool kCap, bool kPos>
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a, int sms,
+                   cudaStream_t s) {
+  const size_t smem = sizeof(AttnSmem<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(chunk_attn_tc_kernel<D, kRowStreams, kCap, kPos>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kvc::count_launch();
+  return kvc::chunk_launch(chunk_attn_tc_kernel<D, kRowStreams, kCap, kPos>, dim3(sms), dim3(kThreads), smem, s, km, vm,
+                           qm, a);
+}
+
+template <int D, bool kRowStreams>
+cudaError_t launch_mods(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a,
+                        int sms, cudaStream_t s) {
+  const bool cap = a.softcap > 0.f, pos = a.slopes || a.window > 0.f;
+  if (cap) return pos ? launch<D, kRowStreams, true, true>(km, vm, qm, a, sms, s)
+                      : launch<D, kRowStreams, true, false>(km, vm, qm, a, sms, s);
+  return pos ? launch<D, kRowStreams, false, true>(km, vm, qm, a, sms, s)
+             : launch<D, kRowStreams, false, false>(km, vm, qm, a, sms, s);
+}
+
+}  // namespace
+
+namespace kvc {
+
+bool chunk_tc_available() { return enc_fn() != nullptr; }
+
+bool chunk_encode_rows(CUtensorMap* m, const void* base, int64_t rows, int d, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool chunk_encode_q(CUtensorMap* m, const void* base, int64_t heads, int T, int d, int tt, int G) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)T * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)tt, (cuuint32_t)G};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row tiles of up to 128 rows; a unit with more than one goes by row streams.
+cudaError_t chunk_attn_tc_launch(ChunkArgs& a, int d, int sms, int page_rows, cudaStream_t s) {
+  a.tt = std::min(128 / a.G, a.T);
+  const bool row_streams = a.T > a.tt;
+  a.tpb = row_streams ? 2 * a.tt : a.tt;
+  a.rp = (a.T + a.tpb - 1) / a.tpb;
+  const int box = page_rows ? std::min(page_rows, 128) : 128;
+  CUtensorMap km, vm, qm;
+  if (!chunk_encode_rows(&km, a.Kp, a.packed_rows, d, box) || !chunk_encode_rows(&vm, a.Vp, a.packed_rows, d, box) ||
+      !chunk_encode_q(&qm, a.q, a.units * a.G, a.T, d, a.tt, a.G))
+    return cudaErrorInvalidValue;
+  if (d == 128)
+    return row_streams ? launch_mods<128, true>(km, vm, qm, a, sms, s) : launch_mods<128, false>(km, vm, qm, a, sms, s);
+  return row_streams ? launch_mods<64, true>(km, vm, qm, a, sms, s) : launch_mods<64, false>(km, vm, qm, a, sms, s);
+}
+
+}  // namespace kvc

@@ -1,0 +1,195 @@
+// Tensor-core building blocks of the bf16 chunk kernels: tcgen05 descriptors and
+// instructions, TMEM moves, tensor-map copies, packed fp32 arithmetic and the
+// score function.
+#pragma once
+#include <cuda.h>
+
+#include "kvc_chunk.cuh"
+
+namespace kvctc {
+
+constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows x 64 features (one swizzled block)
+
+// 128-byte-swizzled operand descriptors: K-major, and MN-major with `lbo` bytes
+// between 64-feature blocks.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// bf16 x bf16 -> fp32, M = 128; b_mn: the B operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24) | (b_mn ? 1u << 16 : 0u);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+// A operand from TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   kvcd::smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Earlier generic writes to global memory (another kernel's) before async-proxy reads.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+#define KVC_R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
+#define KVC_R16(a, i) KVC_R4(a, i), KVC_R4(a, i + 4), KVC_R4(a, i + 8), KVC_R4(a, i + 12)
+#define KVC_I4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+#define KVC_I16(a, i) KVC_I4(a, i), KVC_I4(a, i + 4), KVC_I4(a, i + 8), KVC_I4(a, i + 12)
+
+// 16 or 32 consecutive TMEM columns of this thread's lane (no wait).
+__device__ __forceinline__ void tld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : KVC_R16(r, 0)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : KVC_R16(r, 0), KVC_R16(r, 16)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tst16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      KVC_I16(r, 0)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(kvcd::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(kvcd::smem_u32(bar))
+      : "memory");
+}
+
+// Packed pairs of fp32.
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// (bf16(lo), bf16(hi)) in one register, each rounded to nearest.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// tanh(y) in fp32: y times a degree-5 polynomial in y^2 below y^2 = 1/2 (least
+// squares of the relative error over that range; off by at most 9e-8 of the
+// value), 1 - 2 / (1 + e^2y) above, where nothing cancels.
+__device__ __forceinline__ float tanh_f(float y) {
+  const float z = y * y;
+  float p = fmaf(z, -0.005034883506596088f, 0.019964737817645073f);
+  p = fmaf(z, p, -0.053502924740314484f);
+  p = fmaf(z, p, 0.13328056037425995f);
+  p = fmaf(z, p, -0.3333311080932617f);
+  p = fmaf(y * z, p, y);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + kvcd::ex2(y * 2.885390081777927f)));
+  return z < 0.5f ? p : fmaf(-2.f, r, 1.f);
+}
+
+// Waits for a phase; gives up when another role has, or after `ns` nanoseconds.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
+  if (*abort) return false;
+  if (kvcd::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = kvcd::global_timer_ns();
+  while (!kvcd::mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (kvcd::global_timer_ns() - t0 > ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same for a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
+  return __all_sync(KVC_FULL_MASK, wait_or_abort(bar, parity, ns, abort));
+}
+
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void named_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// Copies of one 128-entry tile of K or V, issued by a whole warp: entries from
+// e0 on, of `total` in all, into `dst` (64-feature blocks kHalf apart),
+// completing on `bar`.  Contiguous: one box per block, rows past the last
+// entry included.  Paged: one box per page (or part of one); boxes with no entry
+// are not copied.  The caller's lane 0 has not yet announced the bytes.
+template <int D>
+__device__ __forceinline__ void copy_tile(const kvc::ChunkArgs& a, const kvcd::RowMap& rows, const CUtensorMap* map,
+                                          uint32_t dst, int e0, int total, uint64_t* bar, int lane) {
+  constexpr int kBlocks = D / 64;
+  if (!rows.table) {
+    if (lane == 0) {
+      kvcd::mbar_arrive_expect_tx(bar, kBlocks * kHalf);
+#pragma unroll
+      for (int h = 0; h < kBlocks; ++h) tma2d(dst + h * kHalf, map, h * 64, (int)(rows.off + e0), bar);
+    }
+    return;
+  }
+  const int box = min(1 << rows.shift, 128);
+  const int n = (min(128, total - e0) + box - 1) / box;          // boxes with entries
+  int y = 0;
+  if (lane < n) y = (int)rows(e0 + lane * box);
+  if (lane == 0) kvcd::mbar_arrive_expect_tx(bar, n * box * 128 * kBlocks);
+  __syncwarp();
+  if (lane < n)
+#pragma unroll
+    for (int h = 0; h < kBlocks; ++h) tma2d(dst + h * kHalf + lane * box * 128, map, h * 64, y, bar);
+}
+
+}  // namespace kvctc
+
+namespace kvc {
+// bf16 [rows, d] in 128-byte-swizzled boxes of 64 features x box_rows rows; and
+// the query array [units * G, T, d] in boxes of 64 x tt x G.
+bool chunk_encode_rows(CUtensorMap* m, const void* base, int64_t rows, int d, int box_rows);
+bool chunk_encode_q(CUtensorMap* m, const void* base, int64_t heads, int T, int d, int tt, int G);
+bool chunk_tc_available();
+cudaError_t chunk_attn_tc_launch(ChunkArgs& a, int d, int sms, int page_rows, cudaStream_t s);
+}  // namespace kvc
