@@ -368,62 +368,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkArgs a, int gri
 }
 
 // ---------------------------------------------------------------- fp32 mass
-// Items are a unit's key tiles, steps their row tiles.  The line is located by
-// unit (tiles x row tiles); inside a unit the division gives tile and row tile.
-template <int kTile>
-struct MassCost {
-  const ChunkArgs& a;
-  __device__ __forceinline__ int64_t items() const { return a.units; }
-  __device__ __forceinline__ int row_tiles(const ChunkUnit& r) const { return max(1, (r.n + a.tt - 1) / a.tt); }
-  __device__ __forceinline__ int64_t operator()(int64_t u, ChunkUnit& r) const {
-    r = kvcd::load_unit(a.rec, u);
-    return (int64_t)((r.len + r.n + kTile - 1) / kTile) * row_tiles(r);
-  }
-};
-// for (MassWalk w(cost, piece); w.next(); ): row tiles [w.tb, w.te) of key tile
-// w.tile of unit w.u.
-template <int kTile>
-struct MassWalk {
-  const MassCost<kTile>& cost;
-  long long f, hi, start;
-  int64_t steps;
-  int64_t u;
-  ChunkUnit r;
-  int rs, tile, tb, te;
-  __device__ __forceinline__ MassWalk(const MassCost<kTile>& c, const kvcd::Piece& p)
-      : cost(c), f(p.lo), hi(p.item >= 0 ? p.hi : p.lo), start(p.start), u(p.item), rs(0) {}
-  __device__ __forceinline__ bool next() {
-    if (rs > 0) f += te - tb;
-    if (f >= hi) return false;
-    if (rs == 0) steps = cost(u, r);
-    while (f - start >= steps) {                       // a step follows: f < hi <= all steps
-      start += steps;
-      steps = cost(++u, r);
-    }
-    rs = cost.row_tiles(r);
-    tile = (int)((f - start) / rs);
-    tb = (int)((f - start) - (int64_t)tile * rs);
-    te = (int)min((long long)rs, tb + (hi - f));
-    return true;
-  }
-  __device__ __forceinline__ bool whole() const { return tb == 0 && te == rs; }
-};
-// The item and offset at which a piece starts.
-template <int kTile>
-__device__ __forceinline__ ChunkSeg mass_seg(const MassCost<kTile>& cost, const kvcd::Piece& p) {
-  if (p.item < 0) return ChunkSeg{-1, 0};
-  ChunkUnit r;
-  cost(p.item, r);
-  const int rs = cost.row_tiles(r);
-  const long long at = p.lo - p.start;
-  return ChunkSeg{((int64_t)p.item << 32) | (at / rs), at % rs > 0};
-}
-
-__device__ __forceinline__ void mass_store(const ChunkArgs& a, const ChunkUnit& r, const kvcd::RowMap& rows, int e, float sum) {
-  const int64_t row = rows(e);
-  a.mass[row] = e < r.len ? fmaf(a.decay, a.mass[row], sum) : sum;
-}
-
+// The tile's keys stay in shared memory while the query rows pass.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkArgs a) {
   constexpr int MR = 64, R = 4;
@@ -432,11 +377,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkA
   float* red = &sm.v[0][0];                            // [16][kKeys] column sums by row group
   kvcd::pdl_trigger();
   kvcd::pdl_wait();
-  const MassCost<kKeys> cost{a};
+  const kvcd::MassCost<kKeys> cost{a};
   const kvcd::Piece piece = kvcd::locate_piece<kSimtThreads>(cost, sm.loc);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  if (tid == 0) a.seg[blockIdx.x] = mass_seg(cost, piece);
-  for (MassWalk<kKeys> w(cost, piece); w.next();) {
+  if (tid == 0) a.seg[blockIdx.x] = kvcd::mass_seg(cost, piece);
+  for (kvcd::MassWalk<kKeys> w(cost, piece); w.next();) {
     const int64_t u = w.u;
     const int e0 = w.tile * kKeys;
     const int h = (int)(u % a.H);
@@ -481,7 +426,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkA
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) sum += red[i * kKeys + tid];
-      if (w.whole()) mass_store(a, w.r, rows, e0 + tid, sum);
+      if (w.whole()) kvcd::mass_store(a, w.r, rows, e0 + tid, sum);
       else a.part[((int64_t)blockIdx.x * 2 + (w.tb == 0 ? 1 : 0)) * kKeys + tid] = sum;
     }
   }
@@ -503,7 +448,7 @@ __global__ void __launch_bounds__(kTile) chunk_mass_combine_kernel(ChunkArgs a, 
   float sum = a.part[((int64_t)(x - 1) * 2 + 1) * kTile + threadIdx.x];
   for (int y = x; y < grid && a.seg[y].mid && a.seg[y].item == s.item; ++y)
     sum += a.part[(int64_t)y * 2 * kTile + threadIdx.x];
-  mass_store(a, r, kvcd::row_map(a, u, r.off), e, sum);
+  kvcd::mass_store(a, r, kvcd::row_map(a, u, r.off), e, sum);
 }
 
 // ---------------------------------------------------------------- host side
@@ -582,6 +527,21 @@ cudaError_t launch_attn(ChunkArgs& a, int sms, cudaStream_t s) {
   return launch_attn_simt<T, D, 64>(a, sms, s);
 }
 
+template <int kTile>
+cudaError_t launch_mass_combine(const ChunkArgs& a, int grid, cudaStream_t s) {
+  if (grid < 2) return cudaSuccess;
+  kvc::count_launch();
+  return kvc::chunk_launch(chunk_mass_combine_kernel<kTile>, dim3(grid - 1), dim3(kTile), 0, s, a, grid);
+}
+
+template <int D>
+cudaError_t launch_mass_bf16(ChunkArgs& a, int sms, int page_rows, cudaStream_t s) {
+  cudaError_t e = launch_prepare<__nv_bfloat16, D>(a, s);
+  if (e == cudaSuccess) e = kvc::chunk_mass_tc_launch(a, D, sms, page_rows, s);
+  if (e != cudaSuccess) return e;
+  return launch_mass_combine<128>(a, sms, s);
+}
+
 template <typename T, int D>
 cudaError_t launch_mass(ChunkArgs& a, int sms, cudaStream_t s) {
   cudaError_t e = launch_prepare<T, D>(a, s);
@@ -593,8 +553,8 @@ cudaError_t launch_mass(ChunkArgs& a, int sms, cudaStream_t s) {
   const int grid = 2 * sms;
   e = kvc::chunk_launch(chunk_mass_simt_kernel<T, D>, dim3(grid), dim3(kSimtThreads), smem, s, a);
   if (e != cudaSuccess) return e;
-  kvc::count_launch(2);
-  return kvc::chunk_launch(chunk_mass_combine_kernel<kKeys>, dim3(grid - 1), dim3(kKeys), 0, s, a, grid);
+  kvc::count_launch();
+  return launch_mass_combine<kKeys>(a, grid, s);
 }
 
 }  // namespace
@@ -710,14 +670,14 @@ extern "C" int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const voi
   if (st != KVC_OK) return st;
   a.err = kvc::err_word();
   const int sms = kvc::sm_count();
-  if (!a.err || sms <= 0) return KVC_ECUDA;
+  if (!a.err || sms <= 0 || !kvc::chunk_tc_available()) return KVC_ECUDA;
   a.q = q; a.Kp = const_cast<void*>(Kp); a.logm = const_cast<float*>(logm); a.pos = const_cast<float*>(pos);
   a.pos_new = pos_new; a.len_lh = len_lh; a.off_lh = off_lh; a.lse = const_cast<float*>(lse);
   a.decay = decay; a.mass = mass;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (p->dtype == KVC_BF16)
-    e = p->d == 128 ? launch_mass<__nv_bfloat16, 128>(a, sms, s) : launch_mass<__nv_bfloat16, 64>(a, sms, s);
+    e = p->d == 128 ? launch_mass_bf16<128>(a, sms, c->page_rows, s) : launch_mass_bf16<64>(a, sms, c->page_rows, s);
   else
     e = p->d == 128 ? launch_mass<float, 128>(a, sms, s) : launch_mass<float, 64>(a, sms, s);
   return kvc::cuda_status(e);

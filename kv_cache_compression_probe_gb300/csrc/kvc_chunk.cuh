@@ -190,6 +190,74 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return tb == 0 && te == tiles; }
 };
 
+// Mass: the items of a unit are its key tiles, their steps the unit's row tiles.
+// The line is located by unit; inside a unit the division gives tile and row tile.
+template <int kTile>
+struct MassCost {
+  const kvc::ChunkArgs& a;
+  __device__ __forceinline__ int64_t items() const { return a.units; }
+  __device__ __forceinline__ int row_tiles(const kvc::ChunkUnit& r) const { return max(1, (r.n + a.tt - 1) / a.tt); }
+  __device__ __forceinline__ int key_tiles(const kvc::ChunkUnit& r) const { return (r.len + r.n + kTile - 1) / kTile; }
+  __device__ __forceinline__ int64_t operator()(int64_t u, kvc::ChunkUnit& r) const {
+    r = load_unit(a.rec, u);
+    return (int64_t)key_tiles(r) * row_tiles(r);
+  }
+};
+
+// for (MassWalk w(cost, piece); w.next(); ): row tiles [w.tb, w.te) of the w.rs of
+// key tile w.tile of unit w.u.
+template <int kTile>
+struct MassWalk {
+  const MassCost<kTile>& cost;
+  long long left;                      // steps of the piece still to come
+  int64_t u;
+  kvc::ChunkUnit r;
+  int rs, tile, tiles, tb, te;
+  long long at;
+  __device__ __forceinline__ MassWalk(const MassCost<kTile>& c, const Piece& p)
+      : cost(c), left(p.item >= 0 ? p.hi - p.lo : 0), u(p.item), rs(0), at(p.lo - p.start) {}
+  __device__ __forceinline__ bool next() {
+    if (rs > 0) left -= te - tb;
+    if (left <= 0) return false;
+    if (rs == 0) {                                     // the piece's first item
+      cost(u, r);
+      rs = cost.row_tiles(r);
+      tiles = cost.key_tiles(r);
+      tile = (int)(at / rs);
+      tb = (int)(at - (long long)tile * rs);
+    } else {
+      tb = 0;
+      ++tile;
+      while (tile >= tiles) {                          // a step follows, so a unit with tiles does
+        cost(++u, r);
+        rs = cost.row_tiles(r);
+        tiles = cost.key_tiles(r);
+        tile = 0;
+      }
+    }
+    te = (int)min((long long)rs, tb + left);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return tb == 0 && te == rs; }
+};
+
+// The item and offset at which a piece starts.
+template <int kTile>
+__device__ __forceinline__ kvc::ChunkSeg mass_seg(const MassCost<kTile>& cost, const Piece& p) {
+  if (p.item < 0) return kvc::ChunkSeg{-1, 0};
+  kvc::ChunkUnit r;
+  cost(p.item, r);
+  const int rs = cost.row_tiles(r);
+  const long long at = p.lo - p.start;
+  return kvc::ChunkSeg{((int64_t)p.item << 32) | (at / rs), at % rs > 0};
+}
+
+__device__ __forceinline__ void mass_store(const kvc::ChunkArgs& a, const kvc::ChunkUnit& r, const RowMap& rows, int e,
+                                           float sum) {
+  const int64_t row = rows(e);
+  a.mass[row] = e < r.len ? fmaf(a.decay, a.mass[row], sum) : sum;
+}
+
 }  // namespace kvcd
 
 namespace kvc {

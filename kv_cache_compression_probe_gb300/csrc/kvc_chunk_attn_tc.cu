@@ -48,7 +48,7 @@ struct AttnSmem {
   alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - first new position
   float m1[128], l1[128];                              // stream 1's statistics (entry streams)
   uint64_t full[kStages], empty[kStages], q_full[2], q_empty[2], bias_full[kBias], bias_empty[kBias];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint64_t s_full[2], p_full[2], o_done[2], j_full, j_free, drain;
   kvcd::LocateSmem loc;
   uint32_t tmem;
   int abort;
@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       kvcd::mbar_init(&sm.p_full[i], 4);
       kvcd::mbar_init(&sm.o_done[i], 1);
     }
+    kvcd::mbar_init(&sm.j_full, 4);
+    kvcd::mbar_init(&sm.j_free, 4);
     kvcd::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     kvcd::fence_mbar_init();
@@ -371,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tl + st * 128, to = tl + 256 + st * D;
     uint32_t sphase = 0, ophase[2] = {0, 0};
     int cnt = 0;                                       // bias tiles so far
-    bool joined = false;                               // entry streams: stream 1's results may be in use
+    // entry streams: stream 1 hands m and l over (j_full) and touches its output again only
+    // when stream 0 has read it (j_free); both complete once per joined piece
+    uint32_t joins = 0;
+    bool joined = false;
     for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); w.next();) {
       const int64_t u = w.item / a.rp;
       const int t0 = (int)(w.item - u * a.rp) * a.tpb + (kRowStreams ? st * a.tt : 0);
@@ -386,12 +391,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < nt; ++i, ++cnt) {
         if (!kRowStreams && (i & 1) != st) continue;
         const int b = cnt % kBias;
-        wait_or_abort(&sm.bias_full[b], (uint32_t)((cnt / kBias) & 1), ns, abort_flag);
+        warp_wait(&sm.bias_full[b], (uint32_t)((cnt / kBias) & 1), ns, abort_flag);
         if (!mine) {
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           continue;
         }
-        wait_or_abort(&sm.s_full[st], sphase, ns, abort_flag);
+        warp_wait(&sm.s_full[st], sphase, ns, abort_flag);
         sphase ^= 1;
         fence_after();
         if (busy) {
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mn;
           }
           if (!kRowStreams && st == 1 && joined) {     // stream 0 has read the results before
-            named_sync(2, 256);
+            warp_wait(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
             joined = false;
           }
           const float base = m == -INFINITY ? 0.f : m;
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           if (!kRowStreams && st == 1 && joined) {
-            named_sync(2, 256);
+            warp_wait(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
             joined = false;
           }
         }
@@ -470,16 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (st == 1) {                               // hand m and l over; stream 0 writes the result
             sm.m1[row] = m;
             sm.l1[row] = l;
-            named_arrive(1, 256);
+            __syncwarp();
+            if (lane == 0) kvcd::mbar_arrive(&sm.j_full);
+            ++joins;
             joined = true;
             ophase[1] ^= 1;
             continue;
           }
-          wait_or_abort(&sm.o_done[0], ophase[0], ns, abort_flag);
-          wait_or_abort(&sm.o_done[1], ophase[1], ns, abort_flag);
+          warp_wait(&sm.o_done[0], ophase[0], ns, abort_flag);
+          warp_wait(&sm.o_done[1], ophase[1], ns, abort_flag);
           ophase[0] ^= 1;
           ophase[1] ^= 1;
-          named_sync(1, 256);
+          warp_wait(&sm.j_full, joins & 1, ns, abort_flag);
           const float mb = sm.m1[row], lb = sm.l1[row];
           const float mn = fmaxf(m, mb);
           f0 = m == -INFINITY ? 0.f : kvcd::ex2(m - mn);
@@ -488,12 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mn;
         } else {
           if (st == 1) continue;
-          wait_or_abort(&sm.o_done[0], ophase[0], ns, abort_flag);
+          warp_wait(&sm.o_done[0], ophase[0], ns, abort_flag);
           ophase[0] ^= 1;
         }
       } else {
         if (!mine) continue;
-        wait_or_abort(&sm.o_done[st], ophase[0], ns, abort_flag);
+        warp_wait(&sm.o_done[st], ophase[0], ns, abort_flag);
         ophase[0] ^= 1;
       }
       fence_after();
@@ -529,9 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && !whole) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, l);
       }
       fence_before();
-      if (!kRowStreams && nt > 1) named_arrive(2, 256);
+      if (!kRowStreams && nt > 1) {
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.j_free);
+        ++joins;
+      }
     }
-    if (!kRowStreams && st == 1 && joined) named_sync(2, 256);
   }
 
   fence_before();

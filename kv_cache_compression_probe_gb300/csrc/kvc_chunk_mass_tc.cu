@@ -1,0 +1,353 @@
+// kvc_chunk_mass in bf16 on the tensor cores.
+//
+// Transposed products, S^T[128 entries x N query rows] = K Q^T: an entry is a
+// TMEM lane, so the thread that owns it adds 2^(s - lse) over its columns with
+// no exchange, and the sum stays in one register.  A key tile is loaded once and
+// the query row tiles (128 rows: tt tokens x G heads; fewer, rounded up to 16,
+// when the chunk is smaller) pass it.  Four groups of four warps take the steps
+// in turn, each with its own TMEM buffer, which hides the latency of a step's
+// chain; a key tile with several steps is joined through shared memory in group
+// order.  Few rows: HBM is the bound (K is read once); many rows: the exponential
+// unit (one exponential a score), just above the tensor cores' own time.
+// Warps: 0 copies (TMA), 1 issues the products, 2 and 3 fetch the row statistics
+// of alternate steps, 4..19 are the four groups.
+#include <algorithm>
+
+#include "kvc_chunk_tc.cuh"
+
+namespace {
+
+using kvc::ChunkArgs;
+using kvc::ChunkUnit;
+using namespace kvctc;
+
+constexpr int kGroups = 4;
+constexpr int kThreads = 128 + kGroups * 128;
+constexpr int kCols = 512;             // a 128-column buffer per group
+
+template <int D>
+struct MassSmem {
+  static constexpr int kK = 4, kQ = 2; // key and query tiles in flight
+  static constexpr uint32_t kTileBytes = 128 * D * 2;
+  alignas(1024) unsigned char k[kK][kTileBytes];
+  alignas(1024) unsigned char q[kQ][kTileBytes];
+  alignas(16) float nl[kGroups][128];                  // -lse of a row, -inf for rows that add nothing
+  alignas(16) float slope[kGroups][128], tok[kGroups][128];
+  float hand[kGroups][128];
+  uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ];
+  uint64_t r_full[kGroups], r_empty[kGroups], s_full[kGroups], s_empty[kGroups];
+  uint64_t hand_full, hand_empty, drain;
+  kvcd::LocateSmem loc;
+  uint32_t tmem;
+  int abort;
+};
+
+// Sum over 16 columns of one entry's 2^(s - lse).  kEdge: some row adds nothing
+// or does not see some entry of the tile.
+template <bool kCap, bool kPos, bool kEdge>
+__device__ __forceinline__ void add16(const ChunkArgs& a, const uint32_t (&s)[16], const float* nl, const float* slope,
+                                      const float* tok, float lm, float rel, float first_tok, uint64_t& sum0,
+                                      uint64_t& sum1) {
+  const uint64_t sc = pk(a.scale_log2, a.scale_log2), lm2 = pk(lm, lm), rel2 = pk(rel, rel);
+  const float cap_in = kCap ? a.scale / a.softcap : 0.f, cap_out = kCap ? a.softcap * kvcd::kLog2eC : 0.f;
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    const float4 n = *reinterpret_cast<const float4*>(nl + c);
+    uint64_t x0 = add2(pk(n.x, n.y), lm2), x1 = add2(pk(n.z, n.w), lm2);
+    if constexpr (kCap) {
+      const uint64_t co = pk(cap_out, cap_out);
+      x0 = fma2(pk(tanh_f(__uint_as_float(s[c]) * cap_in), tanh_f(__uint_as_float(s[c + 1]) * cap_in)), co, x0);
+      x1 = fma2(pk(tanh_f(__uint_as_float(s[c + 2]) * cap_in), tanh_f(__uint_as_float(s[c + 3]) * cap_in)), co, x1);
+    } else {
+      x0 = fma2(pk(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, x0);
+      x1 = fma2(pk(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, x1);
+    }
+    float4 t;
+    if constexpr (kPos || kEdge) t = *reinterpret_cast<const float4*>(tok + c);
+    if constexpr (kPos) {
+      const float4 sl = *reinterpret_cast<const float4*>(slope + c);
+      x0 = fma2(pk(sl.x, sl.y), add2(rel2, pk(-t.x, -t.y)), x0);
+      x1 = fma2(pk(sl.z, sl.w), add2(rel2, pk(-t.z, -t.w)), x1);
+    }
+    float f[4];
+    upk(x0, f[0], f[1]);
+    upk(x1, f[2], f[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = kvcd::ex2(f[e]);
+    if constexpr (kEdge) {
+      const float nn[4] = {n.x, n.y, n.z, n.w}, tt[4] = {t.x, t.y, t.z, t.w};
+      const float w = kPos && a.window > 0.f ? a.window : INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        bool sees = nn[e] != -INFINITY && tt[e] >= first_tok;
+        if constexpr (kPos) sees = sees && rel > tt[e] - w;
+        f[e] = sees ? f[e] : 0.f;
+      }
+    }
+    sum0 = add2(sum0, pk(f[0], f[1]));
+    sum1 = add2(sum1, pk(f[2], f[3]));
+  }
+}
+
+template <int D, bool kCap, bool kPos>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_mass_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ ChunkArgs a) {
+  using Smem = MassSmem<D>;
+  constexpr int kBlocks = D / 64, kK = Smem::kK, kQ = Smem::kQ;
+  extern __shared__ __align__(1024) unsigned char mass_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(mass_raw) + 1023) & ~uintptr_t(1023));
+  kvcd::pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kK; ++i) { kvcd::mbar_init(&sm.k_full[i], 1); kvcd::mbar_init(&sm.k_empty[i], 1); }
+    for (int i = 0; i < kQ; ++i) { kvcd::mbar_init(&sm.q_full[i], 1); kvcd::mbar_init(&sm.q_empty[i], 1); }
+    for (int i = 0; i < kGroups; ++i) {
+      kvcd::mbar_init(&sm.r_full[i], 1);
+      kvcd::mbar_init(&sm.r_empty[i], 4);
+      kvcd::mbar_init(&sm.s_full[i], 1);
+      kvcd::mbar_init(&sm.s_empty[i], 4);
+    }
+    kvcd::mbar_init(&sm.hand_full, 4 * kGroups);
+    kvcd::mbar_init(&sm.hand_empty, 4);
+    kvcd::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    kvcd::fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kvcd::smem_u32(&sm.tmem)),
+                 "r"((uint32_t)kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  kvcd::pdl_wait();                                    // the prepare kernel's records
+  const kvcd::MassCost<128> cost{a};
+  const kvcd::Piece piece = kvcd::locate_piece<kThreads>(cost, sm.loc);
+  if (tid == 0) a.seg[blockIdx.x] = kvcd::mass_seg(cost, piece);
+  const uint32_t tmem = sm.tmem;
+  volatile int* abort_flag = &sm.abort;
+  const uint64_t ns = a.wait_ns;
+  const int used = a.G * a.tt, cols = (used + 15) & ~15;         // rows of a row tile; columns of S^T
+  int k_loads = 0, q_loads = 0;                        // copies issued (for the drain after a give-up)
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    fence_proxy_async_all();
+    int nk = 0, nq = 0;
+    bool ok = true;
+    for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
+      const kvcd::RowMap rows = kvcd::row_map(a, w.u, w.r.off);
+      const int ks = nk % kK;
+      if (nk >= kK) ok = warp_wait(&sm.k_empty[ks], (uint32_t)((nk / kK - 1) & 1), ns, abort_flag);
+      if (!ok) break;
+      if (!a.withhold) {
+        copy_tile<D>(a, rows, &kmap, kvcd::smem_u32(sm.k[ks]), w.tile * 128, w.r.len + w.r.n, &sm.k_full[ks], lane);
+        k_loads = nk + 1;
+      }
+      for (int rt = w.tb; rt < w.te; ++rt, ++nq) {
+        const int qs = nq % kQ;
+        if (nq >= kQ) ok = warp_wait(&sm.q_empty[qs], (uint32_t)((nq / kQ - 1) & 1), ns, abort_flag);
+        if (!ok) break;
+        if (lane == 0 && !a.withhold) {
+          kvcd::mbar_arrive_expect_tx(&sm.q_full[qs], (uint32_t)(used * 128 * kBlocks));
+#pragma unroll
+          for (int h = 0; h < kBlocks; ++h)
+            tma3d(kvcd::smem_u32(sm.q[qs]) + h * kHalf, &qmap, h * 64, rt * a.tt, (int)(w.u * a.G), &sm.q_full[qs]);
+        }
+        if (!a.withhold) q_loads = nq + 1;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products (lane 0 issues)
+    int nk = 0, nq = 0;
+    bool ok = true;
+    for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
+      const int ks = nk % kK;
+      ok = warp_wait(&sm.k_full[ks], (uint32_t)((nk / kK) & 1), ns, abort_flag);
+      for (int rt = w.tb; ok && rt < w.te; ++rt, ++nq) {
+        const int qs = nq % kQ, sb = nq % kGroups;
+        ok = warp_wait(&sm.q_full[qs], (uint32_t)((nq / kQ) & 1), ns, abort_flag);
+        if (ok && nq >= kGroups)
+          ok = warp_wait(&sm.s_empty[sb], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
+        if (!ok) break;
+        fence_after();
+        if (lane == 0) {
+          const uint32_t kb = kvcd::smem_u32(sm.k[ks]), qb = kvcd::smem_u32(sm.q[qs]);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + sb * 128, desc_k(kb + (k >> 2) * kHalf + (k & 3) * 32),
+                   desc_k(qb + (k >> 2) * kHalf + (k & 3) * 32), idesc(cols, false), k > 0);
+          commit(&sm.s_full[sb]);
+          commit(&sm.q_empty[qs]);
+          if (rt + 1 == w.te) commit(&sm.k_empty[ks]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ row statistics
+    int nq = 0;
+    bool ok = true;
+    for (kvcd::MassWalk<128> w(cost, piece); ok && w.next();) {
+      for (int rt = w.tb; ok && rt < w.te; ++rt, ++nq) {
+        if ((nq & 1) != (warp & 1)) continue;
+        float nl[4], sl[4], tk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = lane + 32 * j, g = r / a.tt, t = rt * a.tt + r % a.tt;
+          nl[j] = -INFINITY;
+          sl[j] = 0.f;
+          tk[j] = (float)t;
+          if (r < used && t < w.r.n) {
+            const float lse = __ldcg(a.lse + (w.u * a.G + g) * a.T + t);
+            if (lse != -INFINITY) nl[j] = -lse;
+            if (kPos && a.slopes) sl[j] = a.slopes[(w.u % a.H) * a.G + g] * kvcd::kLog2eC;
+          }
+        }
+        const int b = nq % kGroups;
+        if (nq >= kGroups) ok = warp_wait(&sm.r_empty[b], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = lane + 32 * j;
+          sm.nl[b][r] = nl[j];
+          sm.tok[b][r] = tk[j];
+          if (kPos) sm.slope[b][r] = sl[j];
+        }
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.r_full[b]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ weights of the entries
+    const int grp = (warp - 4) >> 2, q4 = warp & 3;
+    const int key = q4 * 32 + lane;
+    const uint32_t ts = tmem + ((uint32_t)(q4 * 32) << 16) + grp * 128;
+    int nq = 0;
+    uint32_t phase = 0;
+    uint32_t joins = 0;                                // key tiles joined so far
+    for (kvcd::MassWalk<128> w(cost, piece); w.next();) {
+      const int steps = w.te - w.tb;
+      const int taker = (nq + steps - 1) % kGroups;    // the group of the last step writes the result
+      const int mine = (grp - nq % kGroups + kGroups) % kGroups;   // this group's first step of the item
+      const int e = w.tile * 128 + key, total = w.r.len + w.r.n;
+      float lm = 0.f, rel = 0.f, old = 0.f, acc = 0.f;
+      int64_t row = 0;
+      if (mine < steps || taker == grp) {
+        if (e < total) {
+          row = kvcd::row_map(a, w.u, w.r.off)(e);
+          lm = __ldcg(a.logm + row) * kvcd::kLog2eC;
+          if (kPos) rel = __ldcg(a.pos + row) - a.pos_new[w.u / a.per_seq];
+          if (taker == grp && e < w.r.len) old = a.mass[row];
+        }
+        uint64_t sum0 = 0, sum1 = 0;
+        const float first_tok = (float)(e - w.r.len);  // tokens from this one on see the entry
+        for (int i = mine; i < steps; i += kGroups) {
+          const int t0 = (w.tb + i) * a.tt;
+          warp_wait(&sm.r_full[grp], phase, ns, abort_flag);
+          warp_wait(&sm.s_full[grp], phase, ns, abort_flag);
+          phase ^= 1;
+          fence_after();
+          const bool edge = used < 128 || t0 + a.tt > w.r.n || w.tile * 128 + 127 > w.r.len + t0 || a.window > 0.f;
+          for (int c = 0; c < cols; c += 32) {         // the second half's columns may be stale: cols is a
+            uint32_t s0[16], s1[16];                   // multiple of 16 and they are skipped below
+            tld16(ts + c, s0);
+            if (c + 16 < cols) tld16(ts + c + 16, s1);
+            wait_ld();
+            const float *nl = sm.nl[grp] + c, *sl = sm.slope[grp] + c, *tk = sm.tok[grp] + c;
+            if (edge) {
+              add16<kCap, kPos, true>(a, s0, nl, sl, tk, lm, rel, first_tok, sum0, sum1);
+              if (c + 16 < cols) add16<kCap, kPos, true>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel, first_tok, sum0, sum1);
+            } else {
+              add16<kCap, kPos, false>(a, s0, nl, sl, tk, lm, rel, first_tok, sum0, sum1);
+              add16<kCap, kPos, false>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel, first_tok, sum0, sum1);
+            }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            kvcd::mbar_arrive(&sm.s_empty[grp]);
+            kvcd::mbar_arrive(&sm.r_empty[grp]);
+          }
+        }
+        float a0, a1;
+        upk(add2(sum0, sum1), a0, a1);
+        acc = a0 + a1;
+      }
+      if (steps > 1) {                                 // join the groups' sums in group order
+        // every warp announces its sums of join j only after the sums of join j - 1 are read,
+        // and the taker reads once all have, so neither barrier can run two phases ahead
+        if (joins > 0) warp_wait(&sm.hand_empty, (joins - 1) & 1, ns, abort_flag);
+        sm.hand[grp][key] = mine < steps ? acc : 0.f;
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.hand_full);
+        if (grp == taker) {
+          warp_wait(&sm.hand_full, joins & 1, ns, abort_flag);
+          acc = 0.f;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) acc += sm.hand[g][key];
+          __syncwarp();
+          if (lane == 0) kvcd::mbar_arrive(&sm.hand_empty);
+        }
+        ++joins;
+      }
+      if (grp == taker && e < total) {
+        if (w.whole()) a.mass[row] = e < w.r.len ? fmaf(a.decay, old, acc) : acc;
+        else a.part[((int64_t)blockIdx.x * 2 + (w.tb == 0 ? 1 : 0)) * 128 + key] = acc;
+      }
+      nq += steps;
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  if (*abort_flag) {                                   // a bounded wait gave up
+    if (warp == 0 && lane == 0) {                      // copies still in flight land first
+      for (int i = max(0, k_loads - kK); i < k_loads; ++i) kvcd::mbar_wait(&sm.k_full[i % kK], (uint32_t)((i / kK) & 1));
+      for (int i = max(0, q_loads - kQ); i < q_loads; ++i) kvcd::mbar_wait(&sm.q_full[i % kQ], (uint32_t)((i / kQ) & 1));
+    }
+    if (warp == 1 && lane == 0) {                      // and every issued product ends
+      commit(&sm.drain);
+      kvcd::mbar_wait(&sm.drain, 0);
+    }
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)kCols) : "memory");
+  if (*abort_flag && tid == 0) kvcd::record_error(a.err, KVC_ETIMEOUT);
+}
+
+template <int D, bool kCap, bool kPos>
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& qm, const ChunkArgs& a, int sms, cudaStream_t s) {
+  const size_t smem = sizeof(MassSmem<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(chunk_mass_tc_kernel<D, kCap, kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kvc::count_launch();
+  return kvc::chunk_launch(chunk_mass_tc_kernel<D, kCap, kPos>, dim3(sms), dim3(kThreads), smem, s, km, qm, a);
+}
+
+template <int D>
+cudaError_t launch_mods(const CUtensorMap& km, const CUtensorMap& qm, const ChunkArgs& a, int sms, cudaStream_t s) {
+  const bool cap = a.softcap > 0.f, pos = a.slopes || a.window > 0.f;
+  if (cap) return pos ? launch<D, true, true>(km, qm, a, sms, s) : launch<D, true, false>(km, qm, a, sms, s);
+  return pos ? launch<D, false, true>(km, qm, a, sms, s) : launch<D, false, false>(km, qm, a, sms, s);
+}
+
+}  // namespace
+
+namespace kvc {
+
+cudaError_t chunk_mass_tc_launch(ChunkArgs& a, int d, int sms, int page_rows, cudaStream_t s) {
+  a.tt = std::min(128 / a.G, a.T);
+  CUtensorMap km, qm;
+  if (!chunk_encode_rows(&km, a.Kp, a.packed_rows, d, page_rows ? std::min(page_rows, 128) : 128) ||
+      !chunk_encode_q(&qm, a.q, a.units * a.G, a.T, d, a.tt, a.G))
+    return cudaErrorInvalidValue;
+  return d == 128 ? launch_mods<128>(km, qm, a, sms, s) : launch_mods<64>(km, qm, a, sms, s);
+}
+
+}  // namespace kvc

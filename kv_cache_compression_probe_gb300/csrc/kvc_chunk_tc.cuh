@@ -152,9 +152,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
   return __all_sync(KVC_FULL_MASK, wait_or_abort(bar, parity, ns, abort));
 }
 
-__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void named_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
 // Copies of one 128-entry tile of K or V, issued by a whole warp: entries from
 // e0 on, of `total` in all, into `dst` (64-feature blocks kHalf apart),
 // completing on `bar`.  Contiguous: one box per block, rows past the last
@@ -191,5 +188,6 @@ namespace kvc {
 bool chunk_encode_rows(CUtensorMap* m, const void* base, int64_t rows, int d, int box_rows);
 bool chunk_encode_q(CUtensorMap* m, const void* base, int64_t heads, int T, int d, int tt, int G);
 bool chunk_tc_available();
+cudaError_t chunk_mass_tc_launch(ChunkArgs& a, int d, int sms, int page_rows, cudaStream_t s);
 cudaError_t chunk_attn_tc_launch(ChunkArgs& a, int d, int sms, int page_rows, cudaStream_t s);
 }  // namespace kvc

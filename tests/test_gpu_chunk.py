@@ -40,6 +40,8 @@ CASES = {
     "long chunk, G 1": dict(lens=[100], n_new=[700], G=1),
     "long chunk, G 2, d 64": dict(lens=[100, 0], n_new=[300], H=2, G=2, d=64),
     "many units": dict(lens=np.arange(7 * 3 * 16) * 3 % 211, n_new=[1, 2, 3, 4, 5, 6, 7], B=7, L=3, H=16, G=2),
+    "row tiles of every count": dict(lens=np.arange(24) * 97 % 1500 + 300, n_new=[1, 65, 129, 194], B=4, L=3, H=2,
+                                     G=2, d=64, page=64, softcap=30.0),
     "layer range": dict(lens=[5, 70, 200, 130, 64, 9, 1, 300], n_new=[9, 20], B=2, L=4, layers=(1, 3)),
     "no n_new": dict(lens=[5, 70], n_new=[9, 9], B=2, pass_n_new=False),
     # scores
@@ -242,3 +244,28 @@ def test_mass_is_deterministic(kvc):
         got.append((s["mass"].clone(), s["out"].clone()))
     for m, o in got[1:]:
         assert torch.equal(m.view(torch.int32), got[0][0].view(torch.int32)) and torch.equal(o, got[0][1])
+
+
+def test_waits_give_up_and_the_next_call_is_right(kvc):
+    """Copies withheld: every consumer's wait can only end by its limit.  The calls
+    report it, and the same calls are right afterwards."""
+    kvc.kvc_device_error()
+    for kw in (dict(lens=[700, 90, 1300, 64], n_new=[40, 21], B=2, H=2),
+               dict(lens=[700, 90, 1300, 64], n_new=[1, 1], B=2, H=2, page=64)):
+        ch = Chunk(kvc, **kw)
+        kvc.kvc_set_wait_limit(200_000, True)           # 0.2 ms
+        try:
+            for call in (ch.attn, lambda s: ch.run_mass(s, 0.5)):
+                s = ch.upload()
+                call(s)
+                torch.cuda.synchronize()
+                assert kvc.kvc_device_error() == kvc.KVC_ETIMEOUT
+        finally:
+            kvc.kvc_set_wait_limit(2_000_000_000, False)
+        s = ch.upload()
+        ch.attn(s)
+        ch.run_mass(s, 0.5)
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_error() == 0
+        ch.check_attn(s)
+        ch.check_mass(s, s["lse"].cpu().numpy(), 0.5)
