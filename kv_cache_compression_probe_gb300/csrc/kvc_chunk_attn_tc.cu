@@ -3,11 +3,14 @@
 // A query row tile is up to 128 rows: tt tokens x G heads of one (b,l,h), so the
 // K and V of a KV head are read once for its whole group.  Per 128-entry tile
 //   S[128 rows x 128 entries] = Q K^T    (tcgen05, both operands from shared memory)
-//   P = 2^(s - m)                        (one thread per row, fp32, in registers)
+//   P = 2^(s - m)                        (two threads per row, fp32)
 //   O[128 rows x d] += P V               (P as the TMEM operand, V MN-major)
-// with the running maximum m and sum l of each row in one thread.  O is rescaled
-// only when the maximum has grown by more than 2^8 since the last time, which
-// leaves P below 2^8 and the result unchanged.
+// with the reference m and the sum l of each row in registers.  m need not be
+// the maximum, only near enough that nothing over- or underflows: fp32 and bf16
+// have the same exponent range, so a reference off by up to 2^60 costs nothing.
+// It starts at 0, a tile takes one pass, and only a row whose maximum lies further
+// away has its tile done again and O rescaled.  Tiles go from the newest entries to
+// the oldest, so with a distance bias the first tile holds the largest scores.
 //
 // Two streams of S, P and O alternate, so that the tensor cores work on one
 // while the softmax of the other runs:
@@ -17,7 +20,7 @@
 //                rows: the bound is HBM, and the two streams halve the latency
 //                of a tile's chain).
 // Warps: 0 copies (TMA), 1 issues the products, 2 and 3 fetch ln m and positions
-// of alternate tiles, 4..7 and 8..11 are the softmax of the two streams.  The
+// of alternate tiles, 4..11 and 12..19 are the softmax of the two streams.  The
 // work is cut as kvc_chunk.cuh says; persistent, one CTA per SM (512 TMEM
 // columns: S, S, O, O; P lies in S's place).
 #include <cudaTypedefs.h>
@@ -34,9 +37,9 @@ using kvc::ChunkSeg;
 using kvc::ChunkUnit;
 using namespace kvctc;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kBias = 4;               // bias tiles in flight
-constexpr float kLazy = 8.f;           // rescale O when the maximum grew by more (base 2)
+constexpr float kFar = 60.f;           // a row's reference may be off its maximum by this much (base 2)
 constexpr int kCols = 512;             // TMEM columns
 
 template <int D>
@@ -46,6 +49,7 @@ struct AttnSmem {
   alignas(1024) unsigned char q[2][kTileBytes];
   alignas(1024) unsigned char ring[kStages][kTileBytes];
   alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - first new position
+  float xtop[2][2][128], xl[2][2][128];                // what the two halves of a row tell each other
   float m1[128], l1[128];                              // stream 1's statistics (entry streams)
   uint64_t full[kStages], empty[kStages], q_full[2], q_empty[2], bias_full[kBias], bias_empty[kBias];
   uint64_t s_full[2], p_full[2], o_done[2], j_full, j_free, drain;
@@ -63,56 +67,83 @@ struct Ring {
   }
 };
 
-// Base-2 scores of one row over a 128-entry tile, in place of the raw products.
-template <bool kCap, bool kPos>
-__device__ __forceinline__ float scores(const ChunkArgs& a, uint32_t (&s)[128], const float* lm, const float* rel,
-                                        float slope2, float tok, int lim) {
-  const uint64_t sc = pk(a.scale_log2, a.scale_log2), slope = pk(slope2, slope2), mtok = pk(-tok, -tok);
-  const float edge = kPos && a.window > 0.f ? tok - a.window : -INFINITY;   // sees rel > edge
-  const float cap_in = kCap ? a.scale / a.softcap : 0.f, cap_out = kCap ? a.softcap * kvcd::kLog2eC : 0.f;
-#pragma unroll
-  for (int c = 0; c < 128; c += 4) {
-    const float4 b = *reinterpret_cast<const float4*>(lm + c);
-    uint64_t x0, x1;
-    if constexpr (kCap) {
-      x0 = pk(fmaf(tanh_f(__uint_as_float(s[c]) * cap_in), cap_out, b.x),
-              fmaf(tanh_f(__uint_as_float(s[c + 1]) * cap_in), cap_out, b.y));
-      x1 = pk(fmaf(tanh_f(__uint_as_float(s[c + 2]) * cap_in), cap_out, b.z),
-              fmaf(tanh_f(__uint_as_float(s[c + 3]) * cap_in), cap_out, b.w));
-    } else {
-      x0 = fma2(pk(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, pk(b.x, b.y));
-      x1 = fma2(pk(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, pk(b.z, b.w));
-    }
-    if constexpr (kPos) {
-      const float4 r = *reinterpret_cast<const float4*>(rel + c);
-      x0 = fma2(slope, add2(pk(r.x, r.y), mtok), x0);
-      x1 = fma2(slope, add2(pk(r.z, r.w), mtok), x1);
-    }
-    float f0, f1, f2, f3;
-    upk(x0, f0, f1);
-    upk(x1, f2, f3);
-    if constexpr (kPos) {
-      const float4 r = *reinterpret_cast<const float4*>(rel + c);
-      f0 = r.x > edge ? f0 : -INFINITY;
-      f1 = r.y > edge ? f1 : -INFINITY;
-      f2 = r.z > edge ? f2 : -INFINITY;
-      f3 = r.w > edge ? f3 : -INFINITY;
-    }
-    s[c] = __float_as_uint(f0); s[c + 1] = __float_as_uint(f1);
-    s[c + 2] = __float_as_uint(f2); s[c + 3] = __float_as_uint(f3);
+// What a thread needs to turn the products of its row into base-2 scores.
+struct RowScore {
+  float scale, cap_in, cap_out;        // s log2 e = scale dot, or cap_out tanh(cap_in dot)
+  float slope, tok, edge;              // bias slope (rel - tok); sees rel > edge
+};
+
+// Scores (less `base`) of four entries c .. c + 3 of a tile.  kCut: the row sees
+// only the first `lim` entries of the tile.
+template <bool kCap, bool kPos, bool kCut>
+__device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, const float* lm, const float* rel, int c,
+                                        uint64_t mbase, int lim, float (&f)[4]) {
+  const float4 b = *reinterpret_cast<const float4*>(lm + c);
+  uint64_t x0 = add2(pk(b.x, b.y), mbase), x1 = add2(pk(b.z, b.w), mbase);
+  if constexpr (kCap) {
+    const uint64_t co = pk(r.cap_out, r.cap_out);
+    x0 = fma2(pk(tanh_f(__uint_as_float(s[0]) * r.cap_in), tanh_f(__uint_as_float(s[1]) * r.cap_in)), co, x0);
+    x1 = fma2(pk(tanh_f(__uint_as_float(s[2]) * r.cap_in), tanh_f(__uint_as_float(s[3]) * r.cap_in)), co, x1);
+  } else {
+    const uint64_t sc = pk(r.scale, r.scale);
+    x0 = fma2(pk(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, x0);
+    x1 = fma2(pk(__uint_as_float(s[2]), __uint_as_float(s[3])), sc, x1);
   }
-  if (__any_sync(KVC_FULL_MASK, lim < 128)) {          // the chunk's own tokens, or the last entries
-#pragma unroll
-    for (int c = 0; c < 128; ++c)
-      if (c >= lim) s[c] = 0xff800000u;
+  if constexpr (kPos) {
+    const float4 d = *reinterpret_cast<const float4*>(rel + c);
+    const uint64_t sl = pk(r.slope, r.slope), mt = pk(-r.tok, -r.tok);
+    x0 = fma2(sl, add2(pk(d.x, d.y), mt), x0);
+    x1 = fma2(sl, add2(pk(d.z, d.w), mt), x1);
+    upk(x0, f[0], f[1]);
+    upk(x1, f[2], f[3]);
+    f[0] = d.x > r.edge ? f[0] : -INFINITY;
+    f[1] = d.y > r.edge ? f[1] : -INFINITY;
+    f[2] = d.z > r.edge ? f[2] : -INFINITY;
+    f[3] = d.w > r.edge ? f[3] : -INFINITY;
+  } else {
+    upk(x0, f[0], f[1]);
+    upk(x1, f[2], f[3]);
   }
-  float m0 = -INFINITY, m1 = -INFINITY;
+  if constexpr (kCut) {
 #pragma unroll
-  for (int c = 0; c < 128; c += 4) {
-    m0 = kvcd::fmax3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-    m1 = kvcd::fmax3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+    for (int e = 0; e < 4; ++e) f[e] = c + e < lim ? f[e] : -INFINITY;
   }
-  return fmaxf(m0, m1);
+}
+
+// Numerators 2^(s - base) of a row over 64 entries of a tile, packed as bf16 pairs;
+// their sum in fp32 and the largest s - base.  All products are fetched first: one
+// long stretch of independent work hides the latencies that blocks of 16 showed
+// (250 cycles a block for 80 instructions).
+template <bool kCap, bool kPos, bool kCut>
+__device__ __forceinline__ void numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel, float base,
+                                           int lim, uint32_t (&p)[32], float& top, float& sum) {
+  const uint64_t mb = pk(-base, -base);
+  uint64_t s0 = 0, s1 = 0;
+  float t0 = -INFINITY, t1 = -INFINITY;
+  uint32_t s[2][16];
+  tld16(ts, s[0]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    wait_ld(s[q & 1]);
+    if (q < 3) tld16(ts + (q + 1) * 16, s[(q + 1) & 1]);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float f[4];
+      scores4<kCap, kPos, kCut>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
+      t0 = kvcd::fmax3(t0, f[0], f[1]);
+      t1 = kvcd::fmax3(t1, f[2], f[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = kvcd::ex2(f[i]);
+      s0 = add2(s0, pk(f[0], f[1]));
+      s1 = add2(s1, pk(f[2], f[3]));
+      p[q * 8 + e / 2] = bf16x2(f[0], f[1]);
+      p[q * 8 + e / 2 + 1] = bf16x2(f[2], f[3]);
+    }
+  }
+  top = fmaxf(t0, t1);
+  float a0, a1;
+  upk(add2(s0, s1), a0, a1);
+  sum = a0 + a1;
 }
 
 template <int D, bool kRowStreams, bool kCap, bool kPos>
@@ -130,17 +161,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) { kvcd::mbar_init(&sm.full[i], 1); kvcd::mbar_init(&sm.empty[i], 1); }
     for (int i = 0; i < kBias; ++i) {
       kvcd::mbar_init(&sm.bias_full[i], 1);
-      kvcd::mbar_init(&sm.bias_empty[i], kRowStreams ? 8 : 4);
+      kvcd::mbar_init(&sm.bias_empty[i], kRowStreams ? 16 : 8);
     }
     for (int i = 0; i < 2; ++i) {
       kvcd::mbar_init(&sm.q_full[i], 1);
       kvcd::mbar_init(&sm.q_empty[i], 1);
       kvcd::mbar_init(&sm.s_full[i], 1);
-      kvcd::mbar_init(&sm.p_full[i], 4);
+      kvcd::mbar_init(&sm.p_full[i], 8);
       kvcd::mbar_init(&sm.o_done[i], 1);
     }
     kvcd::mbar_init(&sm.j_full, 4);
-    kvcd::mbar_init(&sm.j_free, 4);
+    kvcd::mbar_init(&sm.j_free, 8);
     kvcd::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     kvcd::fence_mbar_init();
@@ -209,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&sm.empty[ring.slot], (uint32_t)(ring.phase ^ 1), ns, abort_flag);
           if (!ok) break;
           if (!a.withhold) {
-            copy_tile<D>(a, rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]), (w.tb + t) * 128, total,
+            copy_tile<D>(a, rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]), (w.te - 1 - t) * 128, total,
                          &sm.full[ring.slot], lane);
             issued |= 1u << ring.slot;
             issued_phase = (issued_phase & ~(1u << ring.slot)) | ((uint32_t)ring.phase << ring.slot);
@@ -219,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ products (lane 0 issues)
+    // ------------------------------------------------------------ products (one lane issues)
     Ring ring;
     int li = 0;
     uint32_t pphase = 0;                               // bit s: parity of stream s's next P
@@ -231,14 +262,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after();
       return ok;
     };
-    auto qk = [&](int s, int slot, int qtile) {        // S_s = Q K^T
-      if (lane == 0) {
-        const uint32_t kb = kvcd::smem_u32(sm.ring[slot]), qb = kvcd::smem_u32(sm.q[qtile]);
+    const uint32_t q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK), k_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboK);
+    const uint32_t v_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboMN);
+    constexpr uint32_t kTile16 = Smem::kTileBytes >> 4;          // tile stride in descriptor units
+    auto qk = [&](int s, int slot, int qtile, bool last_q, uint64_t* q_done) {  // S_s = Q K^T
+      const uint32_t qb = q_lo + qtile * kTile16, kb = k_lo + slot * kTile16, d = tmem + s * 128;
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + s * 128, desc_k(qb + (k >> 2) * kHalf + (k & 3) * 32),
-                 desc_k(kb + (k >> 2) * kHalf + (k & 3) * 32), idesc(128, false), k > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+          mma_ss(d, desc(qb + at), desc(kb + at), idesc(128, false), k > 0);
+        }
         commit(&sm.s_full[s]);
+        if (last_q) commit(q_done);
       }
       __syncwarp();
     };
@@ -249,18 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       return ok;
     };
     auto pv = [&](int s, int slot, bool first, bool last) {  // O_s += P_s V
-      if (lane == 0) {
-        const uint32_t vb = kvcd::smem_u32(sm.ring[slot]);
+      const uint32_t vb = v_lo + slot * kTile16, d = tmem + 256 + s * D, p = tmem + s * 128;
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8, desc_mn(vb + k * 2048, kHalf), idesc(D, true),
-                 !(first && k == 0));
+        for (int k = 0; k < 8; ++k) mma_ts(d, p + (k >> 2) * 64 + (k & 3) * 8, desc(vb + k * 128), idesc(D, true), !(first && k == 0));
         if (last) commit(&sm.o_done[s]);
       }
       __syncwarp();
     };
     auto release = [&](int slot) {
-      if (lane == 0) commit(&sm.empty[slot]);
+      if (elect_one()) commit(&sm.empty[slot]);
       __syncwarp();
     };
     for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next(); ++li) {
@@ -273,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // rows past the last entry: V zero (P is 0 there, but they may hold anything)
       auto clear_tail = [&](int slot, int tile) {
-        const int valid = total - (w.tb + tile) * 128;
+        const int valid = total - (w.te - 1 - tile) * 128;
         if (valid >= 128) return;
         for (int z = lane; z < (128 - valid) * 8 * kBlocks; z += 32) {
           const int r = valid + z / (8 * kBlocks), h = (z >> 3) & (kBlocks - 1), c = z & 7;
@@ -285,48 +319,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot;
       if constexpr (kRowStreams) {
         if (!take(slot)) break;
-        for (int s = 0; s < ns2; ++s) qk(s, slot, s);
+        for (int s = 0; s < ns2; ++s) qk(s, slot, s, nt == 1 && s + 1 == ns2, &sm.q_empty[qb]);
         release(slot);
-        if (nt == 1 && lane == 0) commit(&sm.q_empty[qb]);
         for (int i = 0; ok && i < nt; ++i) {
           int vs = 0, ks = 0;
+          if (!take(vs)) break;                        // usually there already: waited for before P
+          clear_tail(vs, i);
+          if (i + 1 < nt && !take(ks)) break;
           for (int s = 0; s < ns2; ++s) {
             if (!wait_p(s)) break;
-            if (s == 0) {
-              if (!take(vs)) break;
-              clear_tail(vs, i);
-            }
             pv(s, vs, i == 0, i + 1 == nt);
             if (s + 1 == ns2) release(vs);
             if (i + 1 < nt) {
-              if (s == 0 && !take(ks)) break;
-              qk(s, ks, s);
-              if (s + 1 == ns2) {
-                release(ks);
-                if (i + 2 == nt && lane == 0) commit(&sm.q_empty[qb]);
-              }
+              qk(s, ks, s, i + 2 == nt && s + 1 == ns2, &sm.q_empty[qb]);
+              if (s + 1 == ns2) release(ks);
             }
           }
         }
       } else {
         for (int j = 0; ok && j < min(2, nt); ++j) {
           if (!take(slot)) break;
-          qk(j, slot, qb);
+          qk(j, slot, qb, j + 1 == nt, &sm.q_empty[qb]);
           release(slot);
-          if (j + 1 == nt && lane == 0) commit(&sm.q_empty[qb]);
         }
         for (int j = 0; ok && j < nt; ++j) {
           const int s = j & 1;
-          if (!wait_p(s)) break;
+          int ks = 0;
           if (!take(slot)) break;
           clear_tail(slot, j);
+          if (j + 2 < nt && !take(ks)) break;
+          if (!wait_p(s)) break;
           pv(s, slot, j < 2, j + 2 >= nt);
           release(slot);
           if (j + 2 < nt) {
-            if (!take(slot)) break;
-            qk(s, slot, qb);
-            release(slot);
-            if (j + 3 == nt && lane == 0) commit(&sm.q_empty[qb]);
+            qk(s, ks, qb, j + 3 == nt, &sm.q_empty[qb]);
+            release(ks);
           }
         }
       }
@@ -340,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
       const int total = w.r.len + w.r.n;
       const float pos0 = kPos ? a.pos_new[u / a.per_seq] : 0.f;
-      for (int t = w.tb; ok && t < w.te; ++t, ++cnt) {
+      for (int t = w.te - 1; ok && t >= w.tb; --t, ++cnt) {
         if ((cnt & 1) != (warp & 1)) continue;
         float lm[4], rel[4];
 #pragma unroll
@@ -367,10 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and output
-    const int st = (warp - 4) >> 2, q4 = warp & 3;     // stream; TMEM lane quarter
-    const int row = q4 * 32 + lane;
+    // Warps 4..11 and 12..19 are the two streams.  A row belongs to two threads, one for each
+    // half of a tile's entries (and of the output's features); their warps meet once a tile at
+    // a named barrier of 64 threads.
+    const int sw = warp - 4, st = sw >> 3, half = (sw >> 2) & 1, q4 = warp & 3;   // q4: TMEM lane quarter
+    const int row = q4 * 32 + lane, pair = 1 + st * 4 + q4;
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t ts = tl + st * 128, to = tl + 256 + st * D;
+    const uint32_t ts = tl + st * 128 + half * 64, to = tl + 256 + st * D + half * (D / 2);
     uint32_t sphase = 0, ophase[2] = {0, 0};
     int cnt = 0;                                       // bias tiles so far
     // entry streams: stream 1 hands m and l over (j_full) and touches its output again only
@@ -384,13 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = g < a.G && tok < w.r.n;
       const bool busy = __any_sync(KVC_FULL_MASK, live);
       const int see = live ? w.r.len + tok + 1 : 0;    // entries this row sees
-      const float slope2 = kPos && a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
+      RowScore rs;
+      rs.scale = a.scale_log2;
+      rs.cap_in = kCap ? a.scale / a.softcap : 0.f;
+      rs.cap_out = kCap ? a.softcap * kvcd::kLog2eC : 0.f;
+      rs.slope = kPos && a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
+      rs.tok = (float)tok;
+      rs.edge = kPos && a.window > 0.f ? rs.tok - a.window : -INFINITY;
       const int nt = w.te - w.tb;
       const bool mine = !kRowStreams || st == 0 || t0 < w.r.n;     // this stream has work
-      float m = -INFINITY, l = 0.f;
+      float m = 0.f, l = 0.f;                          // the row's reference, and this half's sum
       for (int i = 0; i < nt; ++i, ++cnt) {
         if (!kRowStreams && (i & 1) != st) continue;
-        const int b = cnt % kBias;
+        const int b = cnt % kBias, tile = w.te - 1 - i;
         warp_wait(&sm.bias_full[b], (uint32_t)((cnt / kBias) & 1), ns, abort_flag);
         if (!mine) {
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
@@ -400,58 +436,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         sphase ^= 1;
         fence_after();
         if (busy) {
-          uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tld32(ts + c * 32, s + c * 32);
-          wait_ld();
-          const float mx = scores<kCap, kPos>(a, s, sm.lm[b], sm.rel[b], slope2, (float)tok, see - (w.tb + i) * 128);
-          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
-          // the first entries of the stream set the maximum; later ones move it only when
-          // they exceed it by more than 2^kLazy
-          const bool first = kRowStreams ? i == 0 : i < 2;
-          if (__any_sync(KVC_FULL_MASK, mx > m + (first ? 0.f : kLazy))) {
-            const float mn = fmaxf(m, mx);
-            const float f = m == -INFINITY ? 0.f : kvcd::ex2(m - mn);
-            if (!first) {                              // S is ready, so the product before has ended
-              l *= f;
+          // The numerators are taken relative to m at once; if the row's largest score turns
+          // out more than 2^kFar away (only ever for its first entries, or after a leap), both
+          // halves agree on a new m, rescale O and do the tile again.
+          const int lim = live ? see - tile * 128 - half * 64 : 64;
+          const float *lm = sm.lm[b] + half * 64, *rel = sm.rel[b] + half * 64;
+          const bool cut = __any_sync(KVC_FULL_MASK, lim < 64);
+          uint32_t p[32];
+          float top, sum;
+          if (cut) numerators<kCap, kPos, true>(rs, ts, lm, rel, m, lim, p, top, sum);
+          else numerators<kCap, kPos, false>(rs, ts, lm, rel, m, lim, p, top, sum);
+          const bool seen = l > 0.f;
+          const bool far = live && (top > kFar || (!seen && top < -kFar && top > -INFINITY));
+          if (named_or(pair, 64, far)) {
+            sm.xtop[st][half][row] = top;
+            sm.xl[st][half][row] = l;
+            named_or(pair, 64, false);
+            const float t = fmaxf(top, sm.xtop[st][half ^ 1][row]);
+            const bool any_seen = seen || sm.xl[st][half ^ 1][row] > 0.f;
+            const bool move = live && (t > kFar || (!any_seen && t < -kFar && t > -INFINITY));
+            const float f = move ? kvcd::ex2(-t) : 1.f;
+            l = move ? (any_seen ? l * f : 0.f) : l;
+            // S is ready, so the product before has ended and O is at rest
+            if ((kRowStreams ? i > 0 : i > 1) && __any_sync(KVC_FULL_MASK, move && any_seen)) {
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
+              for (int c = 0; c < D / 2; c += 16) {
                 uint32_t o[16];
                 tld16(to + c, o);
-                wait_ld();
+                wait_ld(o);
+                const float g2 = move && any_seen ? f : 1.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g2);
                 tst16(to + c, o);
               }
             }
-            m = mn;
+            if (move) m += t;
+            if (__any_sync(KVC_FULL_MASK, move)) numerators<kCap, kPos, true>(rs, ts, lm, rel, m, lim, p, top, sum);
+            named_or(pair, 64, false);                 // xtop and xl may be written again
           }
+          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          l += sum;
           if (!kRowStreams && st == 1 && joined) {     // stream 0 has read the results before
             warp_wait(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
             joined = false;
           }
-          const float base = m == -INFINITY ? 0.f : m;
-          const uint64_t mb = pk(-base, -base);
-          uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float x0, x1, x2, x3;
-              upk(add2(pk(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), mb), x0, x1);
-              upk(add2(pk(__uint_as_float(s[c + e + 2]), __uint_as_float(s[c + e + 3])), mb), x2, x3);
-              x0 = kvcd::ex2(x0); x1 = kvcd::ex2(x1); x2 = kvcd::ex2(x2); x3 = kvcd::ex2(x3);
-              sum0 = add2(sum0, pk(x0, x1));
-              sum1 = add2(sum1, pk(x2, x3));
-              p[e / 2] = bf16x2(x0, x1);
-              p[e / 2 + 1] = bf16x2(x2, x3);
-            }
-            tst16(ts + c / 2, p);
-          }
-          float a0, a1;
-          upk(add2(sum0, sum1), a0, a1);
-          l += a0 + a1;
+          tst16(ts, reinterpret_cast<const uint32_t(&)[16]>(p[0]));
+          tst16(ts + 16, reinterpret_cast<const uint32_t(&)[16]>(p[16]));
           wait_st();
         } else {
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
@@ -469,17 +499,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t slot = ((int64_t)blockIdx.x * 2 + (w.tb == 0 ? 1 : 0)) * (kRowStreams ? 256 : 128) +
                            (kRowStreams ? st * 128 : 0) + row;
       const int64_t orow = (u * a.G + g) * a.T + tok;
+      if (kRowStreams ? !mine : (st == 1 && nt == 1)) continue;
+      if (busy) {                                      // the row's sum (the halves in order)
+        sm.xl[st][half][row] = l;
+        named_or(pair, 64, false);
+        l = sm.xl[st][0][row] + sm.xl[st][1][row];
+        named_or(pair, 64, false);
+      }
+      if (!(l > 0.f)) m = -INFINITY;
       float f0 = 1.f, f1 = 0.f;
       if constexpr (!kRowStreams) {
         if (nt > 1) {
           if (st == 1) {                               // hand m and l over; stream 0 writes the result
-            sm.m1[row] = m;
-            sm.l1[row] = l;
-            __syncwarp();
-            if (lane == 0) kvcd::mbar_arrive(&sm.j_full);
+            if (half == 0) {
+              sm.m1[row] = m;
+              sm.l1[row] = l;
+              __syncwarp();
+              if (lane == 0) kvcd::mbar_arrive(&sm.j_full);
+            }
             ++joins;
             joined = true;
-            ophase[1] ^= 1;
             continue;
           }
           warp_wait(&sm.o_done[0], ophase[0], ns, abort_flag);
@@ -494,12 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = fmaf(l, f0, lb * f1);
           m = mn;
         } else {
-          if (st == 1) continue;
           warp_wait(&sm.o_done[0], ophase[0], ns, abort_flag);
           ophase[0] ^= 1;
         }
       } else {
-        if (!mine) continue;
         warp_wait(&sm.o_done[st], ophase[0], ns, abort_flag);
         ophase[0] ^= 1;
       }
@@ -509,31 +546,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       f1 *= inv;
       if (busy) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = 0; c < D / 2; c += 16) {
           uint32_t o[16];
           tld16(to + c, o);
-          wait_ld();
+          wait_ld(o);
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * f0;
           if (!kRowStreams && nt > 1) {
             tld16(to + D + c, o);
-            wait_ld();
+            wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
           }
+          const int at = half * (D / 2) + c;
           if (live && whole) {
-            uint4* op = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c);
+            uint4* op = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + at);
             op[0] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
             op[1] = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
           } else if (live) {
-            float4* pp = reinterpret_cast<float4*>(a.part + slot * D + c);
+            float4* pp = reinterpret_cast<float4*>(a.part + slot * D + at);
 #pragma unroll
             for (int e = 0; e < 4; ++e) pp[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
         }
-        if (live && whole && a.lse) a.lse[orow] = l > 0.f ? m + log2f(l) : -INFINITY;
-        if (live && !whole) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, l);
+        if (half == 0 && live && whole && a.lse) a.lse[orow] = l > 0.f ? m + log2f(l) : -INFINITY;
+        if (half == 0 && live && !whole) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, l);
       }
       fence_before();
       if (!kRowStreams && nt > 1) {

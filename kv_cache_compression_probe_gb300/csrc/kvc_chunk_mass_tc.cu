@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ products (lane 0 issues)
+    // ------------------------------------------------------------ products (one lane issues)
     int nk = 0, nq = 0;
     bool ok = true;
+    const uint32_t k_lo = desc_lo(kvcd::smem_u32(sm.k[0]), kLboK), q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK);
+    const uint32_t id = idesc(cols, false);
     for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
       const int ks = nk % kK;
       ok = warp_wait(&sm.k_full[ks], (uint32_t)((nk / kK) & 1), ns, abort_flag);
@@ -174,12 +176,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&sm.s_empty[sb], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
         if (!ok) break;
         fence_after();
-        if (lane == 0) {
-          const uint32_t kb = kvcd::smem_u32(sm.k[ks]), qb = kvcd::smem_u32(sm.q[qs]);
+        const uint32_t kb = k_lo + ks * (Smem::kTileBytes >> 4), qb = q_lo + qs * (Smem::kTileBytes >> 4);
+        const uint32_t d = tmem + sb * 128;
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + sb * 128, desc_k(kb + (k >> 2) * kHalf + (k & 3) * 32),
-                   desc_k(qb + (k >> 2) * kHalf + (k & 3) * 32), idesc(cols, false), k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+            mma_ss(d, desc(kb + at), desc(qb + at), id, k > 0);
+          }
           commit(&sm.s_full[sb]);
           commit(&sm.q_empty[qs]);
           if (rt + 1 == w.te) commit(&sm.k_empty[ks]);
@@ -256,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s0[16], s1[16];                   // multiple of 16 and they are skipped below
             tld16(ts + c, s0);
             if (c + 16 < cols) tld16(ts + c + 16, s1);
-            wait_ld();
+            wait_ld(s0);
+            wait_ld(s1);
             const float *nl = sm.nl[grp] + c, *sl = sm.slope[grp] + c, *tk = sm.tok[grp] + c;
             if (edge) {
               add16<kCap, kPos, true>(a, s0, nl, sl, tk, lm, rel, first_tok, sum0, sum1);

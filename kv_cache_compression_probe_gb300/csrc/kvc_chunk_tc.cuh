@@ -10,16 +10,14 @@ namespace kvctc {
 
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows x 64 features (one swizzled block)
 
-// 128-byte-swizzled operand descriptors: K-major, and MN-major with `lbo` bytes
-// between 64-feature blocks.
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// 128-byte-swizzled operand descriptors.  The high word is the same for all; the
+// low word is the address in 16-byte units and, for an MN-major operand, the
+// distance between 64-feature blocks.  Steps inside a tile add to the low word, so
+// the issuing warp keeps them in uniform registers.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo << 16); }
+constexpr uint32_t kLboK = 1, kLboMN = kHalf >> 4;
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 // bf16 x bf16 -> fp32, M = 128; b_mn: the B operand is MN-major.
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24) | (b_mn ? 1u << 16 : 0u);
@@ -37,6 +35,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(acc));
 }
+// One lane of a converged warp; the compiler knows that what it uses is uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    kvcd::smem_u32(bar))
@@ -44,7 +48,6 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Earlier generic writes to global memory (another kernel's) before async-proxy reads.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -54,6 +57,16 @@ __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.pr
 #define KVC_I4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
 #define KVC_I16(a, i) KVC_I4(a, i), KVC_I4(a, i + 4), KVC_I4(a, i + 8), KVC_I4(a, i + 12)
 
+// Waits for the TMEM loads so far; the loaded registers pass through, so nothing that
+// uses them moves up.
+#define KVC_P4(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3])
+#define KVC_P16(a, i) KVC_P4(a, i), KVC_P4(a, i + 4), KVC_P4(a, i + 8), KVC_P4(a, i + 12)
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KVC_P16(r, 0));
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KVC_P16(r, 0), KVC_P16(r, 16));
+}
 // 16 or 32 consecutive TMEM columns of this thread's lane (no wait).
 __device__ __forceinline__ void tld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
@@ -61,7 +74,7 @@ __device__ __forceinline__ void tld16(uint32_t addr, uint32_t (&r)[16]) {
       : KVC_R16(r, 0)
       : "r"(addr));
 }
-__device__ __forceinline__ void tld32(uint32_t addr, uint32_t* r) {
+__device__ __forceinline__ void tld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
       "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -150,6 +163,18 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
 // The same for a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
   return __all_sync(KVC_FULL_MASK, wait_or_abort(bar, parity, ns, abort));
+}
+
+// Or of a predicate over the `n` threads of named barrier `id` (whole warps, converged),
+// which also orders their shared-memory accesses.
+__device__ __forceinline__ bool named_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
 }
 
 // Copies of one 128-entry tile of K or V, issued by a whole warp: entries from
