@@ -8,6 +8,7 @@
 // memory as fp32; thread (ty, tx) forms the scores of rows ty*R.. and entries
 // tx + 16 j, so the 16 lanes of a row share its maximum and sum by shuffles.
 // fp32 has no tensor-core form of full precision; the bound is the FFMA rate.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -63,11 +64,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
   }
   if (g == 0 && lane == 0) {
     if (bad != KVC_OK) kvcd::record_error(a.err, bad);
-    ChunkUnit r;
-    r.len = bad == KVC_OK ? len : 0;
-    r.n = bad == KVC_OK ? n : 0;
-    r.off = off;
-    a.rec[u] = r;
+    kvcd::store_unit(a, u, bad == KVC_OK ? len : 0, bad == KVC_OK ? n : 0, off);
   }
   if (!kAppend || bad != KVC_OK) return;
   constexpr int kVec = D * (int)sizeof(T) / 16;        // 16-byte vectors of a row
@@ -86,6 +83,35 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
     a.logm[row] = 0.f;
     a.pos[row] = a.pos_new[b] + (float)t;
   }
+}
+
+// ---------------------------------------------------------------- window
+// One CTA per unit of a call with a window: the first 128-entry tile that holds an
+// entry inside the first token's window (the widest).  Tiles before it are seen by
+// no token: attention leaves them out, and the mass of their entries only decays.
+// In a cache in position order these are all the tiles outside the window.
+constexpr int kWinThreads = 512;
+__global__ void __launch_bounds__(kWinThreads) chunk_window_kernel(ChunkArgs a) {
+  __shared__ int s_first;
+  kvcd::pdl_trigger();
+  if (threadIdx.x == 0) s_first = INT_MAX;
+  __syncthreads();
+  kvcd::pdl_wait();
+  const int64_t u = blockIdx.x;
+  const int4 v = __ldcg(a.rec + u);                     // the prepare kernel's record
+  const int len = v.x;
+  const kvcd::RowMap rows = kvcd::row_map(a, u, ((int64_t)(uint32_t)v.z) | ((int64_t)v.w << 32));
+  const float edge = a.pos_new[u / a.per_seq] - a.window;
+  int mine = len;                                       // the chunk's own entries are always live
+  for (int e = threadIdx.x; e < len && mine == len; e += kWinThreads)
+    if (a.pos[rows(e)] > edge) mine = e;
+  mine = __reduce_min_sync(KVC_FULL_MASK, mine);
+  if ((threadIdx.x & 31) == 0) atomicMin(&s_first, mine);
+  __syncthreads();
+  const int first = s_first & ~127;
+  if (threadIdx.x == 0) a.first[u] = first;
+  if (a.mass)
+    for (int e = threadIdx.x; e < min(len, first); e += kWinThreads) a.mass[rows(e)] *= a.decay;
 }
 
 // ---------------------------------------------------------------- fp32 score tile
@@ -188,7 +214,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkA
   if (tid == 0) a.seg[blockIdx.x] = ChunkSeg{piece.item, piece.item >= 0 && piece.lo > piece.start};
   if (a.len_out)
     for (int64_t u = (int64_t)blockIdx.x * kSimtThreads + tid; u < a.units; u += (int64_t)gridDim.x * kSimtThreads) {
-      const ChunkUnit r = kvcd::load_unit(a.rec, u);
+      const ChunkUnit r = kvcd::load_unit(a, u);
       const int64_t gu = kvcd::unit_global(a, u);
       a.len_out[gu] = r.n > 0 ? r.len + r.n : a.len_lh[gu];
     }
@@ -221,7 +247,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkA
     }
     const int total = w.r.len + w.r.n;
     for (int tile = w.tb; tile < w.te; ++tile) {
-      const int e0 = tile * kKeys, cnt = min(kKeys, total - e0);
+      const int e0 = w.r.first + tile * kKeys, cnt = min(kKeys, total - e0);
       __syncthreads();
       auto row = [&](int r) { return rows(e0 + r); };
       stage_rows<T, D, kKeys, D + 4>(&sm.k[0][0], static_cast<const T*>(a.Kp), cnt, row);
@@ -327,7 +353,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkArgs a, int gri
   while (y1 < grid && a.seg[y1].mid && a.seg[y1].item == s.item) ++y1;
   const int64_t u = s.item / a.rp;
   const int t0 = (int)(s.item - u * a.rp) * a.tpb;
-  const ChunkUnit rec = kvcd::load_unit(a.rec, u);
+  const ChunkUnit rec = kvcd::load_unit(a, u);
   const int lane = threadIdx.x & 31;
   constexpr int C = D / 32;
   const int rows_tile = a.G * a.tt;
@@ -383,7 +409,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkA
   if (tid == 0) a.seg[blockIdx.x] = kvcd::mass_seg(cost, piece);
   for (kvcd::MassWalk<kKeys> w(cost, piece); w.next();) {
     const int64_t u = w.u;
-    const int e0 = w.tile * kKeys;
+    const int e0 = w.r.first + w.tile * kKeys;
     const int h = (int)(u % a.H);
     const float pos0 = a.pos_new[u / a.per_seq];
     const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
@@ -442,8 +468,8 @@ __global__ void __launch_bounds__(kTile) chunk_mass_combine_kernel(ChunkArgs a, 
   const ChunkSeg s = a.seg[x], before = a.seg[x - 1];
   if (!s.mid || (before.mid && before.item == s.item)) return;
   const int64_t u = s.item >> 32;
-  const int e = (int)(s.item & 0xffffffff) * kTile + threadIdx.x;
-  const ChunkUnit r = kvcd::load_unit(a.rec, u);
+  const ChunkUnit r = kvcd::load_unit(a, u);
+  const int e = r.first + (int)(s.item & 0xffffffff) * kTile + threadIdx.x;
   if (e >= r.len + r.n) return;
   float sum = a.part[((int64_t)(x - 1) * 2 + 1) * kTile + threadIdx.x];
   for (int y = x; y < grid && a.seg[y].mid && a.seg[y].item == s.item; ++y)
@@ -453,7 +479,7 @@ __global__ void __launch_bounds__(kTile) chunk_mass_combine_kernel(ChunkArgs a, 
 
 // ---------------------------------------------------------------- host side
 struct ChunkLayout {
-  size_t rec, seg, part, ml, total;
+  size_t rec, first, seg, part, ml, total;
 };
 
 constexpr int kMaxRowsBlock = 256;     // rows of one partial result at most
@@ -464,7 +490,8 @@ ChunkLayout chunk_layout(const kvc_params* p, const kvc_chunk* c) {
   const size_t ctas = (size_t)kCtaPerSm * std::max(kvc::sm_count(), 1);
   ChunkLayout w;
   w.rec = 0;
-  w.seg = kvc::align256(units * sizeof(ChunkUnit));
+  w.first = kvc::align256(units * sizeof(int4));
+  w.seg = w.first + kvc::align256(units * sizeof(int32_t));
   w.part = w.seg + kvc::align256(ctas * sizeof(ChunkSeg));
   w.ml = w.part + kvc::align256(ctas * 2 * kMaxRowsBlock * p->d * sizeof(float));
   w.total = w.ml + kvc::align256(ctas * 2 * kMaxRowsBlock * 2 * sizeof(float));
@@ -479,8 +506,11 @@ cudaError_t launch_prepare(const ChunkArgs& a, cudaStream_t s) {
   const int64_t warps = a.units * groups;
   const dim3 grid((unsigned)((warps + kPrepWarps - 1) / kPrepWarps)), block(32 * kPrepWarps);
   kvc::count_launch();
-  if (a.cap_lh) return kvc::chunk_launch(chunk_prepare_kernel<T, D, true>, grid, block, 0, s, a, groups);
-  return kvc::chunk_launch(chunk_prepare_kernel<T, D, false>, grid, block, 0, s, a, groups);
+  const cudaError_t e = a.cap_lh ? kvc::chunk_launch(chunk_prepare_kernel<T, D, true>, grid, block, 0, s, a, groups)
+                                 : kvc::chunk_launch(chunk_prepare_kernel<T, D, false>, grid, block, 0, s, a, groups);
+  if (e != cudaSuccess || !(a.window > 0.f)) return e;
+  kvc::count_launch();
+  return kvc::chunk_launch(chunk_window_kernel, dim3((unsigned)a.units), dim3(kWinThreads), 0, s, a);
 }
 
 template <typename T, int D>
@@ -607,7 +637,8 @@ static int chunk_workspace(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c
   const ChunkLayout w = chunk_layout(p, c);
   if (!workspace || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return KVC_EWORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  a.rec = reinterpret_cast<ChunkUnit*>(ws + w.rec);
+  a.rec = reinterpret_cast<int4*>(ws + w.rec);
+  a.first = reinterpret_cast<int32_t*>(ws + w.first);
   a.seg = reinterpret_cast<ChunkSeg*>(ws + w.seg);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float*>(ws + w.ml);

@@ -17,9 +17,10 @@
 
 namespace kvc {
 
-struct ChunkUnit {                     // 16 bytes
+struct ChunkUnit {                     // as stored: 16 bytes (len, n, off)
   int32_t len, n;                      // entries before the chunk, new tokens (0: skipped)
   int64_t off;                         // first row (contiguous cache)
+  int32_t first;                       // entries below this 128-multiple are outside every token's window
 };
 
 // Where a CTA's piece of the step line starts: the item, and whether inside it.
@@ -47,7 +48,8 @@ struct ChunkArgs {
   const int32_t* n_new;                // null: T
   const float* slopes;
   // workspace
-  ChunkUnit* rec;                      // [units]
+  int4* rec;                           // [units] records (store_unit / load_unit)
+  int32_t* first;                      // [units], written and read when there is a window
   ChunkSeg* seg;                       // [grid]
   float* part;                         // per CTA two slots (kvc_chunk.cu)
   float* part_ml;
@@ -90,17 +92,21 @@ __device__ __forceinline__ RowMap row_map(const kvc::ChunkArgs& a, int64_t u, in
   return m;
 }
 
-__device__ __forceinline__ kvc::ChunkUnit load_unit(const kvc::ChunkUnit* rec, int64_t u) {
-  const int4 v = __ldcg(reinterpret_cast<const int4*>(rec) + u);
+__device__ __forceinline__ void store_unit(const kvc::ChunkArgs& a, int64_t u, int len, int n, int64_t off) {
+  a.rec[u] = make_int4(len, n, (int)(uint32_t)off, (int)(off >> 32));
+}
+__device__ __forceinline__ kvc::ChunkUnit load_unit(const kvc::ChunkArgs& a, int64_t u) {
+  const int4 v = __ldcg(a.rec + u);
   kvc::ChunkUnit r;
   r.len = v.x;
   r.n = v.y;
   r.off = ((int64_t)(uint32_t)v.z) | ((int64_t)v.w << 32);
+  r.first = a.window > 0.f ? __ldcg(a.first + u) : 0;
   return r;
 }
 
-// Steps of attention item i: key tiles of kTile entries that the row block's
-// last token sees; 0 past the unit's tokens.
+// Steps of attention item i: key tiles of kTile entries from the unit's first
+// visible one to the row block's last token; 0 past the unit's tokens.
 template <int kTile>
 struct AttnCost {
   const kvc::ChunkArgs& a;
@@ -108,9 +114,9 @@ struct AttnCost {
   __device__ __forceinline__ int operator()(int64_t i, kvc::ChunkUnit& r) const {
     const int64_t u = i / a.rp;
     const int t0 = (int)(i - u * a.rp) * a.tpb;
-    r = load_unit(a.rec, u);
+    r = load_unit(a, u);
     if (t0 >= r.n) return 0;
-    return (r.len + min(r.n, t0 + a.tpb) + kTile - 1) / kTile;
+    return (r.len + min(r.n, t0 + a.tpb) + kTile - 1) / kTile - r.first / kTile;
   }
 };
 
@@ -173,18 +179,18 @@ struct Walk {
   Piece p;
   kvc::ChunkUnit r;
   int item, tb, te, tiles;
-  bool first;
-  __device__ __forceinline__ Walk(const Cost& c, const Piece& pc) : cost(c), p(pc), item(pc.item), first(true) {}
+  bool begun;
+  __device__ __forceinline__ Walk(const Cost& c, const Piece& pc) : cost(c), p(pc), item(pc.item), begun(false) {}
   __device__ __forceinline__ bool next() {
-    if (!first) {
+    if (begun) {
       p.start += tiles;
       ++item;
     }
     if (p.item < 0 || p.start >= p.hi) return false;
     while ((tiles = cost(item, r)) == 0) ++item;      // a step follows: p.start < p.hi <= all steps
-    tb = first ? (int)(p.lo - p.start) : 0;
+    tb = begun ? 0 : (int)(p.lo - p.start);
     te = (int)min((long long)tiles, p.hi - p.start);
-    first = false;
+    begun = true;
     return true;
   }
   __device__ __forceinline__ bool whole() const { return tb == 0 && te == tiles; }
@@ -197,15 +203,15 @@ struct MassCost {
   const kvc::ChunkArgs& a;
   __device__ __forceinline__ int64_t items() const { return a.units; }
   __device__ __forceinline__ int row_tiles(const kvc::ChunkUnit& r) const { return max(1, (r.n + a.tt - 1) / a.tt); }
-  __device__ __forceinline__ int key_tiles(const kvc::ChunkUnit& r) const { return (r.len + r.n + kTile - 1) / kTile; }
+  __device__ __forceinline__ int key_tiles(const kvc::ChunkUnit& r) const { return (r.len + r.n + kTile - 1) / kTile - r.first / kTile; }
   __device__ __forceinline__ int64_t operator()(int64_t u, kvc::ChunkUnit& r) const {
-    r = load_unit(a.rec, u);
+    r = load_unit(a, u);
     return (int64_t)key_tiles(r) * row_tiles(r);
   }
 };
 
 // for (MassWalk w(cost, piece); w.next(); ): row tiles [w.tb, w.te) of the w.rs of
-// key tile w.tile of unit w.u.
+// key tile w.tile (counted from the unit's first visible one) of unit w.u.
 template <int kTile>
 struct MassWalk {
   const MassCost<kTile>& cost;

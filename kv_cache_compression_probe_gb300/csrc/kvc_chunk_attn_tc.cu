@@ -39,7 +39,7 @@ using namespace kvctc;
 
 constexpr int kThreads = 640;
 constexpr int kBias = 4;               // bias tiles in flight
-constexpr float kFar = 60.f;           // a row's reference may be off its maximum by this much (base 2)
+constexpr float kFar = 0x1p60f;        // a tile's sum of numerators may be this large or (at first) its inverse
 constexpr int kCols = 512;             // TMEM columns
 
 template <int D>
@@ -49,6 +49,7 @@ struct AttnSmem {
   alignas(1024) unsigned char q[2][kTileBytes];
   alignas(1024) unsigned char ring[kStages][kTileBytes];
   alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - first new position
+  int lm_any[kBias];                                   // some ln m of the tile is not 0
   float xtop[2][2][128], xl[2][2][128];                // what the two halves of a row tell each other
   float m1[128], l1[128];                              // stream 1's statistics (entry streams)
   uint64_t full[kStages], empty[kStages], q_full[2], q_empty[2], bias_full[kBias], bias_empty[kBias];
@@ -73,13 +74,17 @@ struct RowScore {
   float slope, tok, edge;              // bias slope (rel - tok); sees rel > edge
 };
 
-// Scores (less `base`) of four entries c .. c + 3 of a tile.  kCut: the row sees
-// only the first `lim` entries of the tile.
-template <bool kCap, bool kPos, bool kCut>
+// Scores (less the reference) of four entries c .. c + 3 of a tile.  kLm: some ln m
+// of the tile is not 0.  kCut: the row sees only the first `lim` entries.
+template <bool kCap, bool kPos, bool kLm, bool kCut>
 __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, const float* lm, const float* rel, int c,
                                         uint64_t mbase, int lim, float (&f)[4]) {
-  const float4 b = *reinterpret_cast<const float4*>(lm + c);
-  uint64_t x0 = add2(pk(b.x, b.y), mbase), x1 = add2(pk(b.z, b.w), mbase);
+  uint64_t x0 = mbase, x1 = mbase;
+  if constexpr (kLm) {
+    const float4 b = *reinterpret_cast<const float4*>(lm + c);
+    x0 = add2(pk(b.x, b.y), mbase);
+    x1 = add2(pk(b.z, b.w), mbase);
+  }
   if constexpr (kCap) {
     const uint64_t co = pk(r.cap_out, r.cap_out);
     x0 = fma2(pk(tanh_f(__uint_as_float(s[0]) * r.cap_in), tanh_f(__uint_as_float(s[1]) * r.cap_in)), co, x0);
@@ -111,15 +116,13 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 }
 
 // Numerators 2^(s - base) of a row over 64 entries of a tile, packed as bf16 pairs;
-// their sum in fp32 and the largest s - base.  All products are fetched first: one
-// long stretch of independent work hides the latencies that blocks of 16 showed
-// (250 cycles a block for 80 instructions).
-template <bool kCap, bool kPos, bool kCut>
-__device__ __forceinline__ void numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel, float base,
-                                           int lim, uint32_t (&p)[32], float& top, float& sum) {
+// returns their sum in fp32.  The products come from TMEM in blocks of 16, the next
+// block on its way while one is worked on.
+template <bool kCap, bool kPos, bool kLm, bool kCut>
+__device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,
+                                            float base, int lim, uint32_t (&p)[32]) {
   const uint64_t mb = pk(-base, -base);
   uint64_t s0 = 0, s1 = 0;
-  float t0 = -INFINITY, t1 = -INFINITY;
   uint32_t s[2][16];
   tld16(ts, s[0]);
 #pragma unroll
@@ -129,9 +132,7 @@ __device__ __forceinline__ void numerators(const RowScore& r, uint32_t ts, const
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       float f[4];
-      scores4<kCap, kPos, kCut>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
-      t0 = kvcd::fmax3(t0, f[0], f[1]);
-      t1 = kvcd::fmax3(t1, f[2], f[3]);
+      scores4<kCap, kPos, kLm, kCut>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = kvcd::ex2(f[i]);
       s0 = add2(s0, pk(f[0], f[1]));
@@ -140,10 +141,29 @@ __device__ __forceinline__ void numerators(const RowScore& r, uint32_t ts, const
       p[q * 8 + e / 2 + 1] = bf16x2(f[2], f[3]);
     }
   }
-  top = fmaxf(t0, t1);
   float a0, a1;
   upk(add2(s0, s1), a0, a1);
-  sum = a0 + a1;
+  return a0 + a1;
+}
+
+// Largest score of a row over 64 entries (rare: kept small).
+template <bool kCap, bool kPos>
+__device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const float* lm, const float* rel, int lim) {
+  float t = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < 64; q += 16) {
+    uint32_t s[16];
+    tld16(ts + q, s);
+    wait_ld(s);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float f[4];
+      scores4<kCap, kPos, true, true>(r, s + e, lm, rel, q + e, 0ull, lim, f);
+      t = kvcd::fmax3(t, f[0], f[1]);
+      t = kvcd::fmax3(t, f[2], f[3]);
+    }
+  }
+  return t;
 }
 
 template <int D, bool kRowStreams, bool kCap, bool kPos>
@@ -191,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) a.seg[blockIdx.x] = ChunkSeg{piece.item, piece.item >= 0 && piece.lo > piece.start};
   if (a.len_out)
     for (int64_t u = (int64_t)blockIdx.x * kThreads + tid; u < a.units; u += (int64_t)gridDim.x * kThreads) {
-      const ChunkUnit r = kvcd::load_unit(a.rec, u);
+      const ChunkUnit r = kvcd::load_unit(a, u);
       const int64_t gu = kvcd::unit_global(a, u);
       a.len_out[gu] = r.n > 0 ? r.len + r.n : a.len_lh[gu];
     }
@@ -240,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&sm.empty[ring.slot], (uint32_t)(ring.phase ^ 1), ns, abort_flag);
           if (!ok) break;
           if (!a.withhold) {
-            copy_tile<D>(a, rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]), (w.te - 1 - t) * 128, total,
+            copy_tile<D>(a, rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]), w.r.first + (w.te - 1 - t) * 128, total,
                          &sm.full[ring.slot], lane);
             issued |= 1u << ring.slot;
             issued_phase = (issued_phase & ~(1u << ring.slot)) | ((uint32_t)ring.phase << ring.slot);
@@ -307,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // rows past the last entry: V zero (P is 0 there, but they may hold anything)
       auto clear_tail = [&](int slot, int tile) {
-        const int valid = total - (w.te - 1 - tile) * 128;
+        const int valid = total - w.r.first - (w.te - 1 - tile) * 128;
         if (valid >= 128) return;
         for (int z = lane; z < (128 - valid) * 8 * kBlocks; z += 32) {
           const int r = valid + z / (8 * kBlocks), h = (z >> 3) & (kBlocks - 1), c = z & 7;
@@ -372,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lm[4], rel[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int e = t * 128 + lane + 32 * j;
+          const int e = w.r.first + t * 128 + lane + 32 * j;
           lm[j] = rel[j] = 0.f;
           if (e < total) {
             const int64_t row = rows(e);
@@ -388,8 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm.lm[b][lane + 32 * j] = lm[j];
           if (kPos) sm.rel[b][lane + 32 * j] = rel[j];
         }
-        __syncwarp();
-        if (lane == 0) kvcd::mbar_arrive(&sm.bias_full[b]);
+        const bool any = __any_sync(KVC_FULL_MASK, lm[0] != 0.f || lm[1] != 0.f || lm[2] != 0.f || lm[3] != 0.f);
+        if (lane == 0) {
+          sm.lm_any[b] = any;
+          kvcd::mbar_arrive(&sm.bias_full[b]);
+        }
       }
     }
   } else {
@@ -424,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = w.te - w.tb;
       const bool mine = !kRowStreams || st == 0 || t0 < w.r.n;     // this stream has work
       float m = 0.f, l = 0.f;                          // the row's reference, and this half's sum
+      bool settled = false;                            // the reference fits the entries seen so far
       for (int i = 0; i < nt; ++i, ++cnt) {
         if (!kRowStreams && (i & 1) != st) continue;
         const int b = cnt % kBias, tile = w.te - 1 - i;
@@ -437,25 +461,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         if (busy) {
           // The numerators are taken relative to m at once; if the row's largest score turns
-          // out more than 2^kFar away (only ever for its first entries, or after a leap), both
-          // halves agree on a new m, rescale O and do the tile again.
-          const int lim = live ? see - tile * 128 - half * 64 : 64;
+          // out too far away (only ever for its first entries, or after a leap), both halves
+          // agree on a new m, rescale O and do the tile again.
+          const int lim = live ? see - w.r.first - tile * 128 - half * 64 : 64;
           const float *lm = sm.lm[b] + half * 64, *rel = sm.rel[b] + half * 64;
           const bool cut = __any_sync(KVC_FULL_MASK, lim < 64);
           uint32_t p[32];
-          float top, sum;
-          if (cut) numerators<kCap, kPos, true>(rs, ts, lm, rel, m, lim, p, top, sum);
-          else numerators<kCap, kPos, false>(rs, ts, lm, rel, m, lim, p, top, sum);
-          const bool seen = l > 0.f;
-          const bool far = live && (top > kFar || (!seen && top < -kFar && top > -INFINITY));
+          float sum;
+          if (cut) sum = numerators<kCap, kPos, true, true>(rs, ts, lm, rel, m, lim, p);
+          else if (kCap || kPos || sm.lm_any[b]) sum = numerators<kCap, kPos, true, false>(rs, ts, lm, rel, m, lim, p);
+          else sum = numerators<kCap, kPos, kCap || kPos, false>(rs, ts, lm, rel, m, lim, p);
+          // the sum tells whether the reference was near enough: above 2^60 (or not a number)
+          // it was too low; a row's first sum below 2^-60 may have lost entries
+          settled |= l > 0.f;
+          const bool far = live && lim > 0 && (!(sum < kFar) || (!settled && !(sum > 1.f / kFar)));
           if (named_or(pair, 64, far)) {
+            const float top = score_max<kCap, kPos>(rs, ts, lm, rel, lim);
             sm.xtop[st][half][row] = top;
             sm.xl[st][half][row] = l;
             named_or(pair, 64, false);
             const float t = fmaxf(top, sm.xtop[st][half ^ 1][row]);
-            const bool any_seen = seen || sm.xl[st][half ^ 1][row] > 0.f;
-            const bool move = live && (t > kFar || (!any_seen && t < -kFar && t > -INFINITY));
-            const float f = move ? kvcd::ex2(-t) : 1.f;
+            const bool any_seen = l > 0.f || sm.xl[st][half ^ 1][row] > 0.f;
+            const bool move = live && t > (any_seen ? m + 48.f : -INFINITY);
+            const float f = move ? kvcd::ex2(m - t) : 1.f;
             l = move ? (any_seen ? l * f : 0.f) : l;
             // S is ready, so the product before has ended and O is at rest
             if ((kRowStreams ? i > 0 : i > 1) && __any_sync(KVC_FULL_MASK, move && any_seen)) {
@@ -470,8 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tst16(to + c, o);
               }
             }
-            if (move) m += t;
-            if (__any_sync(KVC_FULL_MASK, move)) numerators<kCap, kPos, true>(rs, ts, lm, rel, m, lim, p, top, sum);
+            if (move) m = t;
+            settled = any_seen || t > -INFINITY;
+            sum = numerators<kCap, kPos, true, true>(rs, ts, lm, rel, m, lim, p);
             named_or(pair, 64, false);                 // xtop and xl may be written again
           }
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk >= kK) ok = warp_wait(&sm.k_empty[ks], (uint32_t)((nk / kK - 1) & 1), ns, abort_flag);
       if (!ok) break;
       if (!a.withhold) {
-        copy_tile<D>(a, rows, &kmap, kvcd::smem_u32(sm.k[ks]), w.tile * 128, w.r.len + w.r.n, &sm.k_full[ks], lane);
+        copy_tile<D>(a, rows, &kmap, kvcd::smem_u32(sm.k[ks]), w.r.first + w.tile * 128, w.r.len + w.r.n, &sm.k_full[ks], lane);
         k_loads = nk + 1;
       }
       for (int rt = w.tb; rt < w.te; ++rt, ++nq) {
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = w.te - w.tb;
       const int taker = (nq + steps - 1) % kGroups;    // the group of the last step writes the result
       const int mine = (grp - nq % kGroups + kGroups) % kGroups;   // this group's first step of the item
-      const int e = w.tile * 128 + key, total = w.r.len + w.r.n;
+      const int e0 = w.r.first + w.tile * 128, e = e0 + key, total = w.r.len + w.r.n;
       float lm = 0.f, rel = 0.f, old = 0.f, acc = 0.f;
       int64_t row = 0;
       if (mine < steps || taker == grp) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           warp_wait(&sm.s_full[grp], phase, ns, abort_flag);
           phase ^= 1;
           fence_after();
-          const bool edge = used < 128 || t0 + a.tt > w.r.n || w.tile * 128 + 127 > w.r.len + t0 || a.window > 0.f;
+          const bool edge = used < 128 || t0 + a.tt > w.r.n || e0 + 127 > w.r.len + t0 || a.window > 0.f;
           for (int c = 0; c < cols; c += 32) {         // the second half's columns may be stale: cols is a
             uint32_t s0[16], s1[16];                   // multiple of 16 and they are skipped below
             tld16(ts + c, s0);

@@ -147,8 +147,8 @@ __device__ __forceinline__ float tanh_f(float y) {
 
 // Waits for a phase; gives up when another role has, or after `ns` nanoseconds.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
-  if (*abort) return false;
   if (kvcd::mbar_try_wait(bar, parity)) return true;
+  if (*abort) return false;
   const uint64_t t0 = kvcd::global_timer_ns();
   while (!kvcd::mbar_try_wait(bar, parity)) {
     if (*abort) return false;
