@@ -474,8 +474,8 @@ int kvc_tree_cuts(const kvc_params* p, const int32_t* ctx_len, const void* K,
  * KVC_EDEVICE; one with len + n_b > cap_lh as KVC_ECAPACITY (nothing is
  * appended, its out, lse and length stay).  The workspace needs no
  * initialisation; calls that overlap must not share one.
- * Errors: KVC_EINVAL (also q, k_new, v_new, Kp, Vp or out off a 16-byte
- * boundary), KVC_EWORKSPACE, KVC_ECUDA. */
+ * Errors: KVC_EINVAL (also q, k_new, v_new, Kp or Vp off a 16-byte boundary, out
+ * off a 32-byte boundary), KVC_EWORKSPACE, KVC_ECUDA. */
 int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const void* q, const void* k_new,
                    const void* v_new, const float* pos_new, void* Kp, void* Vp, float* logm,
                    float* pos, const int32_t* len_lh, const int32_t* cap_lh,

@@ -26,30 +26,45 @@ constexpr int kKeys = 64;              // entries per tile of the fp32 kernels
 constexpr int kSimtThreads = 256;
 
 // ---------------------------------------------------------------- prepare
-// One warp per (unit, group of 16 new tokens): checks the unit, appends the
-// group's keys and values (kAppend) and writes the unit's record.  Bound by the
-// bytes of the chunk's keys and values, or by latency for one token.
-constexpr int kPrepTok = 16;
+// One warp per (unit, group of 8 new tokens): checks the unit, appends the group's
+// keys and values (kAppend) and writes the unit's record.  The rows to append are
+// fetched before anything is known about the unit, so that their latency and that
+// of the checks overlap.
+constexpr int kPrepTok = 8;
 constexpr int kPrepWarps = 4;
 
 template <typename T, int D, bool kAppend>
 __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArgs a, int groups) {
+  constexpr int kVec = D * (int)sizeof(T) / 16;        // 16-byte vectors of a row
+  constexpr int kPer = kPrepTok * kVec / 32;           // vectors of K (and of V) per lane
   kvcd::pdl_trigger();
-  kvcd::pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * kPrepWarps + (threadIdx.x >> 5);
   const int64_t u = w / groups;
   const int g = (int)(w - u * groups);
+  kvcd::pdl_wait();
   if (u >= a.units) return;
-  const int b = (int)(u / a.per_seq);
+  const int b = (int)(u / a.per_seq), t0 = g * kPrepTok;
+  uint4 kx[kPer], vx[kPer];
+  if (kAppend) {
+    const uint4* kn = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_new) + u * a.T * D);
+    const uint4* vn = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_new) + u * a.T * D);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = t0 * kVec + lane + 32 * i;
+      if (at < a.T * kVec) { kx[i] = __ldg(kn + at); vx[i] = __ldg(vn + at); }
+    }
+  }
   const int64_t gu = kvcd::unit_global(a, u);
   const int len = a.len_lh[gu];
   const int n = a.n_new ? a.n_new[b] : a.T;
   const int64_t off = a.page_table ? 0 : a.off_lh[gu];
+  const int cap = kAppend ? a.cap_lh[gu] : 0;
+  const float pos0 = kAppend ? a.pos_new[b] : 0.f;
   int bad = KVC_OK;
   if (len < 0 || n < 0 || n > a.T || off < 0 || (int64_t)len + n > a.packed_rows) bad = KVC_EDEVICE;
   else if (!a.page_table && off + len + n > a.packed_rows) bad = KVC_EDEVICE;
-  else if (kAppend && (int64_t)len + n > a.cap_lh[gu]) bad = KVC_ECAPACITY;
+  else if (kAppend && (int64_t)len + n > cap) bad = KVC_ECAPACITY;
   else if (a.page_table) {
     const int need = (int)(((int64_t)len + n + (1 << a.page_shift) - 1) >> a.page_shift);
     if (need > a.max_pages) {
@@ -58,7 +73,11 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
       const int32_t* tab = a.page_table + gu * a.max_pages;
       const int64_t pages = a.packed_rows >> a.page_shift;
       bool ok = true;
-      for (int i = lane; i < need; i += 32) ok &= tab[i] >= 0 && tab[i] < pages;
+#pragma unroll 4
+      for (int i = lane; i < need; i += 32) {
+        const int page = __ldg(tab + i);
+        ok &= page >= 0 && page < pages;
+      }
       if (!__all_sync(KVC_FULL_MASK, ok)) bad = KVC_EDEVICE;
     }
   }
@@ -67,21 +86,20 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
     kvcd::store_unit(a, u, bad == KVC_OK ? len : 0, bad == KVC_OK ? n : 0, off);
   }
   if (!kAppend || bad != KVC_OK) return;
-  constexpr int kVec = D * (int)sizeof(T) / 16;        // 16-byte vectors of a row
   const kvcd::RowMap rows = kvcd::row_map(a, u, off);
-  const int t0 = g * kPrepTok, t1 = min(n, t0 + kPrepTok);
-  const uint4* kn = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_new) + u * a.T * D);
-  const uint4* vn = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_new) + u * a.T * D);
-  for (int i = lane; i < (t1 - t0) * kVec; i += 32) {
-    const int t = t0 + i / kVec, v = i % kVec;
-    const int64_t row = rows(len + t);
-    reinterpret_cast<uint4*>(static_cast<T*>(a.Kp) + row * D)[v] = kn[t * kVec + v];
-    reinterpret_cast<uint4*>(static_cast<T*>(a.Vp) + row * D)[v] = vn[t * kVec + v];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = lane + 32 * i, t = t0 + at / kVec;
+    if (t < n) {
+      const int64_t row = rows(len + t) * kVec + at % kVec;
+      static_cast<uint4*>(a.Kp)[row] = kx[i];
+      static_cast<uint4*>(a.Vp)[row] = vx[i];
+    }
   }
-  for (int t = t0 + lane; t < t1; t += 32) {
-    const int64_t row = rows(len + t);
+  if (lane < kPrepTok && t0 + lane < n) {
+    const int64_t row = rows(len + t0 + lane);
     a.logm[row] = 0.f;
-    a.pos[row] = a.pos_new[b] + (float)t;
+    a.pos[row] = pos0 + (float)(t0 + lane);
   }
 }
 
@@ -90,7 +108,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
 // entry inside the first token's window (the widest).  Tiles before it are seen by
 // no token: attention leaves them out, and the mass of their entries only decays.
 // In a cache in position order these are all the tiles outside the window.
-constexpr int kWinThreads = 512;
+constexpr int kWinThreads = 1024;
 __global__ void __launch_bounds__(kWinThreads) chunk_window_kernel(ChunkArgs a) {
   __shared__ int s_first;
   kvcd::pdl_trigger();
@@ -103,8 +121,17 @@ __global__ void __launch_bounds__(kWinThreads) chunk_window_kernel(ChunkArgs a) 
   const kvcd::RowMap rows = kvcd::row_map(a, u, ((int64_t)(uint32_t)v.z) | ((int64_t)v.w << 32));
   const float edge = a.pos_new[u / a.per_seq] - a.window;
   int mine = len;                                       // the chunk's own entries are always live
-  for (int e = threadIdx.x; e < len && mine == len; e += kWinThreads)
-    if (a.pos[rows(e)] > edge) mine = e;
+  for (int e0 = threadIdx.x; e0 < len && mine == len; e0 += 8 * kWinThreads) {
+    float p[8];                                         // eight loads in flight
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + i * kWinThreads;
+      p[i] = e < len ? a.pos[rows(e)] : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+      if (p[i] > edge) mine = e0 + i * kWinThreads;
+  }
   mine = __reduce_min_sync(KVC_FULL_MASK, mine);
   if ((threadIdx.x & 31) == 0) atomicMin(&s_first, mine);
   __syncthreads();
@@ -663,7 +690,7 @@ extern "C" int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const voi
       (!off_lh && c->page_rows == 0))
     return KVC_EINVAL;
   if (misaligned16(q) || misaligned16(k_new) || misaligned16(v_new) || misaligned16(Kp) || misaligned16(Vp) ||
-      misaligned16(out))
+      (reinterpret_cast<uintptr_t>(out) & 31))
     return KVC_EINVAL;
   ChunkArgs a = {};
   kvc::chunk_fill(a, p, c);

@@ -110,20 +110,24 @@ __device__ __forceinline__ kvc::ChunkUnit load_unit(const kvc::ChunkArgs& a, int
 template <int kTile>
 struct AttnCost {
   const kvc::ChunkArgs& a;
-  __device__ __forceinline__ int64_t items() const { return a.units * a.rp; }
-  __device__ __forceinline__ int operator()(int64_t i, kvc::ChunkUnit& r) const {
-    const int64_t u = i / a.rp;
-    const int t0 = (int)(i - u * a.rp) * a.tpb;
-    r = load_unit(a, u);
+  __device__ __forceinline__ int items() const { return (int)a.units * a.rp; }   // below 2^31 (chunk_check)
+  __device__ __forceinline__ int operator()(int i, kvc::ChunkUnit& r) const {
+    r = load_unit(a, (int)((unsigned)i / (unsigned)a.rp));
+    return of(i, r);
+  }
+  __device__ __forceinline__ int of(int i, const kvc::ChunkUnit& r) const {   // r: the item's record
+    const int t0 = (int)((unsigned)i % (unsigned)a.rp) * a.tpb;
     if (t0 >= r.n) return 0;
     return (r.len + min(r.n, t0 + a.tpb) + kTile - 1) / kTile - r.first / kTile;
   }
 };
 
 // Block-wide: this CTA's piece [lo, hi) of the step line and the item that holds
-// step lo, with that item's first step.  item = -1 for an empty piece.
+// step lo, with that item's first step and its unit's record.  item = -1 for an
+// empty piece.
 struct Piece {
   long long lo, hi, start;
+  kvc::ChunkUnit r;
   int item;
 };
 struct LocateSmem {
@@ -133,12 +137,15 @@ struct LocateSmem {
 template <int kThreads, class Cost>
 __device__ Piece locate_piece(const Cost& cost, LocateSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t n = cost.items();
-  const int64_t per = (n + kThreads - 1) / kThreads;
-  const int64_t i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  const int n = cost.items();
+  const int per = (int)((unsigned)(n + kThreads - 1) / kThreads);
+  const int i0 = min((long long)n, (long long)tid * per), i1 = min((long long)n, (long long)i0 + per);
   kvc::ChunkUnit r;
+  r.len = r.n = r.first = 0;
+  r.off = 0;
   long long mine = 0;
-  for (int64_t i = i0; i < i1; ++i) mine += cost(i, r);
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) mine += cost(i, r);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -148,23 +155,29 @@ __device__ Piece locate_piece(const Cost& cost, LocateSmem& sm) {
   if (lane == 31) sm.warp[warp] = incl;
   __syncthreads();
   long long before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sm.warp[w];
     total += sm.warp[w];
   }
-  const long long q = (total + gridDim.x - 1) / gridDim.x;
+  const long long all = total + gridDim.x - 1;
+  const long long q = all >> 31 ? all / gridDim.x : (long long)((unsigned)all / gridDim.x);
   const long long lo = min(total, (long long)blockIdx.x * q), hi = min(total, lo + q);
   long long at = before + incl - mine;
   if (lo >= hi) {
-    if (tid == 0) sm.piece = Piece{lo, hi, 0, -1};
+    if (tid == 0) sm.piece = Piece{lo, hi, 0, r, -1};
   } else if (at <= lo && lo < at + mine) {
-    for (int64_t i = i0; i < i1; ++i) {
-      const int c = cost(i, r);
-      if (lo < at + c) {
-        sm.piece = Piece{lo, hi, at, (int)i};
-        break;
+    if (per == 1) {                                    // r is that item's record already
+      sm.piece = Piece{lo, hi, at, r, i0};
+    } else {
+      for (int i = i0; i < i1; ++i) {
+        const int64_t c = cost(i, r);
+        if (lo < at + c) {
+          sm.piece = Piece{lo, hi, at, r, i};
+          break;
+        }
+        at += c;
       }
-      at += c;
     }
   }
   __syncthreads();
@@ -180,14 +193,18 @@ struct Walk {
   kvc::ChunkUnit r;
   int item, tb, te, tiles;
   bool begun;
-  __device__ __forceinline__ Walk(const Cost& c, const Piece& pc) : cost(c), p(pc), item(pc.item), begun(false) {}
+  __device__ __forceinline__ Walk(const Cost& c, const Piece& pc) : cost(c), p(pc), r(pc.r), item(pc.item), begun(false) {}
   __device__ __forceinline__ bool next() {
     if (begun) {
       p.start += tiles;
       ++item;
     }
     if (p.item < 0 || p.start >= p.hi) return false;
-    while ((tiles = cost(item, r)) == 0) ++item;      // a step follows: p.start < p.hi <= all steps
+    if (begun) {
+      while ((tiles = cost(item, r)) == 0) ++item;    // a step follows: p.start < p.hi <= all steps
+    } else {
+      tiles = cost.of(item, r);
+    }
     tb = begun ? 0 : (int)(p.lo - p.start);
     te = (int)min((long long)tiles, p.hi - p.start);
     begun = true;
@@ -201,7 +218,7 @@ struct Walk {
 template <int kTile>
 struct MassCost {
   const kvc::ChunkArgs& a;
-  __device__ __forceinline__ int64_t items() const { return a.units; }
+  __device__ __forceinline__ int items() const { return (int)a.units; }
   __device__ __forceinline__ int row_tiles(const kvc::ChunkUnit& r) const { return max(1, (r.n + a.tt - 1) / a.tt); }
   __device__ __forceinline__ int key_tiles(const kvc::ChunkUnit& r) const { return (r.len + r.n + kTile - 1) / kTile - r.first / kTile; }
   __device__ __forceinline__ int64_t operator()(int64_t u, kvc::ChunkUnit& r) const {
@@ -221,12 +238,11 @@ struct MassWalk {
   int rs, tile, tiles, tb, te;
   long long at;
   __device__ __forceinline__ MassWalk(const MassCost<kTile>& c, const Piece& p)
-      : cost(c), left(p.item >= 0 ? p.hi - p.lo : 0), u(p.item), rs(0), at(p.lo - p.start) {}
+      : cost(c), left(p.item >= 0 ? p.hi - p.lo : 0), u(p.item), r(p.r), rs(0), at(p.lo - p.start) {}
   __device__ __forceinline__ bool next() {
     if (rs > 0) left -= te - tb;
     if (left <= 0) return false;
     if (rs == 0) {                                     // the piece's first item
-      cost(u, r);
       rs = cost.row_tiles(r);
       tiles = cost.key_tiles(r);
       tile = (int)(at / rs);
@@ -251,9 +267,7 @@ struct MassWalk {
 template <int kTile>
 __device__ __forceinline__ kvc::ChunkSeg mass_seg(const MassCost<kTile>& cost, const Piece& p) {
   if (p.item < 0) return kvc::ChunkSeg{-1, 0};
-  kvc::ChunkUnit r;
-  cost(p.item, r);
-  const int rs = cost.row_tiles(r);
+  const int rs = cost.row_tiles(p.r);
   const long long at = p.lo - p.start;
   return kvc::ChunkSeg{((int64_t)p.item << 32) | (at / rs), at % rs > 0};
 }

@@ -20,7 +20,7 @@
 //                rows: the bound is HBM, and the two streams halve the latency
 //                of a tile's chain).
 // Warps: 0 copies (TMA), 1 issues the products, 2 and 3 fetch ln m and positions
-// of alternate tiles, 4..11 and 12..19 are the softmax of the two streams.  The
+// of alternate tiles (and 3 clears the V rows past the last entry), 4..11 and 12..19 are the softmax of the two streams.  The
 // work is cut as kvc_chunk.cuh says; persistent, one CTA per SM (512 TMEM
 // columns: S, S, O, O; P lies in S's place).
 #include <cudaTypedefs.h>
@@ -48,12 +48,13 @@ struct AttnSmem {
   static constexpr uint32_t kTileBytes = 128 * D * 2;
   alignas(1024) unsigned char q[2][kTileBytes];
   alignas(1024) unsigned char ring[kStages][kTileBytes];
-  alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - first new position
+  alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - the row block's
+  float rel_min[kBias];                                // least position of the tile's entries
   int lm_any[kBias];                                   // some ln m of the tile is not 0
   float xtop[2][2][128], xl[2][2][128];                // what the two halves of a row tell each other
   float m1[128], l1[128];                              // stream 1's statistics (entry streams)
   uint64_t full[kStages], empty[kStages], q_full[2], q_empty[2], bias_full[kBias], bias_empty[kBias];
-  uint64_t s_full[2], p_full[2], o_done[2], j_full, j_free, drain;
+  uint64_t s_full[2], p_full[2], o_done[2], j_full, j_free, tail_here, cleared, drain;
   kvcd::LocateSmem loc;
   uint32_t tmem;
   int abort;
@@ -71,19 +72,28 @@ struct Ring {
 // What a thread needs to turn the products of its row into base-2 scores.
 struct RowScore {
   float scale, cap_in, cap_out;        // s log2 e = scale dot, or cap_out tanh(cap_in dot)
-  float slope, tok, edge;              // bias slope (rel - tok); sees rel > edge
+  float slope, shift;                  // distance bias slope rel - shift
+  float edge;                          // window: sees rel > edge
 };
 
-// Scores (less the reference) of four entries c .. c + 3 of a tile.  kLm: some ln m
-// of the tile is not 0.  kCut: the row sees only the first `lim` entries.
-template <bool kCap, bool kPos, bool kLm, bool kCut>
+// Scores (plus `base`, both halves of a pair) of four entries c .. c + 3 of a tile.
+// kLm: some ln m of the tile is not 0.  kMask: the row sees only the first `lim`
+// entries, and of these those beyond the window's edge.
+template <bool kCap, bool kPos, bool kLm, bool kMask>
 __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, const float* lm, const float* rel, int c,
-                                        uint64_t mbase, int lim, float (&f)[4]) {
-  uint64_t x0 = mbase, x1 = mbase;
+                                        uint64_t base, int lim, float (&f)[4]) {
+  uint64_t x0 = base, x1 = base;
   if constexpr (kLm) {
     const float4 b = *reinterpret_cast<const float4*>(lm + c);
-    x0 = add2(pk(b.x, b.y), mbase);
-    x1 = add2(pk(b.z, b.w), mbase);
+    x0 = add2(pk(b.x, b.y), base);
+    x1 = add2(pk(b.z, b.w), base);
+  }
+  float4 d;
+  if constexpr (kPos) {
+    d = *reinterpret_cast<const float4*>(rel + c);
+    const uint64_t sl = pk(r.slope, r.slope);
+    x0 = fma2(sl, pk(d.x, d.y), x0);
+    x1 = fma2(sl, pk(d.z, d.w), x1);
   }
   if constexpr (kCap) {
     const uint64_t co = pk(r.cap_out, r.cap_out);
@@ -94,22 +104,15 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
     x0 = fma2(pk(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, x0);
     x1 = fma2(pk(__uint_as_float(s[2]), __uint_as_float(s[3])), sc, x1);
   }
-  if constexpr (kPos) {
-    const float4 d = *reinterpret_cast<const float4*>(rel + c);
-    const uint64_t sl = pk(r.slope, r.slope), mt = pk(-r.tok, -r.tok);
-    x0 = fma2(sl, add2(pk(d.x, d.y), mt), x0);
-    x1 = fma2(sl, add2(pk(d.z, d.w), mt), x1);
-    upk(x0, f[0], f[1]);
-    upk(x1, f[2], f[3]);
-    f[0] = d.x > r.edge ? f[0] : -INFINITY;
-    f[1] = d.y > r.edge ? f[1] : -INFINITY;
-    f[2] = d.z > r.edge ? f[2] : -INFINITY;
-    f[3] = d.w > r.edge ? f[3] : -INFINITY;
-  } else {
-    upk(x0, f[0], f[1]);
-    upk(x1, f[2], f[3]);
-  }
-  if constexpr (kCut) {
+  upk(x0, f[0], f[1]);
+  upk(x1, f[2], f[3]);
+  if constexpr (kMask) {
+    if constexpr (kPos) {
+      f[0] = d.x > r.edge ? f[0] : -INFINITY;
+      f[1] = d.y > r.edge ? f[1] : -INFINITY;
+      f[2] = d.z > r.edge ? f[2] : -INFINITY;
+      f[3] = d.w > r.edge ? f[3] : -INFINITY;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = c + e < lim ? f[e] : -INFINITY;
   }
@@ -118,10 +121,11 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 // Numerators 2^(s - base) of a row over 64 entries of a tile, packed as bf16 pairs;
 // returns their sum in fp32.  The products come from TMEM in blocks of 16, the next
 // block on its way while one is worked on.
-template <bool kCap, bool kPos, bool kLm, bool kCut>
+template <bool kCap, bool kPos, bool kLm, bool kMask>
 __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,
                                             float base, int lim, uint32_t (&p)[32]) {
-  const uint64_t mb = pk(-base, -base);
+  const float sh = kPos ? -(base + r.shift) : -base;
+  const uint64_t mb = pk(sh, sh);
   uint64_t s0 = 0, s1 = 0;
   uint32_t s[2][16];
   tld16(ts, s[0]);
@@ -132,7 +136,7 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       float f[4];
-      scores4<kCap, kPos, kLm, kCut>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
+      scores4<kCap, kPos, kLm, kMask>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = kvcd::ex2(f[i]);
       s0 = add2(s0, pk(f[0], f[1]));
@@ -150,6 +154,7 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
 template <bool kCap, bool kPos>
 __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const float* lm, const float* rel, int lim) {
   float t = -INFINITY;
+  const uint64_t mb = kPos ? pk(-r.shift, -r.shift) : 0ull;
 #pragma unroll 1
   for (int q = 0; q < 64; q += 16) {
     uint32_t s[16];
@@ -158,7 +163,7 @@ __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       float f[4];
-      scores4<kCap, kPos, true, true>(r, s + e, lm, rel, q + e, 0ull, lim, f);
+      scores4<kCap, kPos, true, true>(r, s + e, lm, rel, q + e, mb, lim, f);
       t = kvcd::fmax3(t, f[0], f[1]);
       t = kvcd::fmax3(t, f[2], f[3]);
     }
@@ -192,6 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     kvcd::mbar_init(&sm.j_full, 4);
     kvcd::mbar_init(&sm.j_free, 8);
+    kvcd::mbar_init(&sm.tail_here, 1);
+    kvcd::mbar_init(&sm.cleared, 1);
     kvcd::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     kvcd::fence_mbar_init();
@@ -209,12 +216,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const kvcd::AttnCost<128> cost{a};
   const kvcd::Piece piece = kvcd::locate_piece<kThreads>(cost, sm.loc);
   if (tid == 0) a.seg[blockIdx.x] = ChunkSeg{piece.item, piece.item >= 0 && piece.lo > piece.start};
-  if (a.len_out)
-    for (int64_t u = (int64_t)blockIdx.x * kThreads + tid; u < a.units; u += (int64_t)gridDim.x * kThreads) {
-      const ChunkUnit r = kvcd::load_unit(a, u);
-      const int64_t gu = kvcd::unit_global(a, u);
-      a.len_out[gu] = r.n > 0 ? r.len + r.n : a.len_lh[gu];
-    }
   const uint32_t tmem = sm.tmem;
   volatile int* abort_flag = &sm.abort;
   const uint64_t ns = a.wait_ns;
@@ -270,126 +271,159 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ products (one lane issues)
-    Ring ring;
-    int li = 0;
-    uint32_t pphase = 0;                               // bit s: parity of stream s's next P
-    bool ok = true;
-    auto take = [&](int& slot) {                       // the next K or V tile
-      ok = ok && warp_wait(&sm.full[ring.slot], (uint32_t)ring.phase, ns, abort_flag);
-      slot = ring.slot;
-      ring.step<kStages>();
-      fence_after();
-      return ok;
-    };
-    const uint32_t q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK), k_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboK);
-    const uint32_t v_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboMN);
-    constexpr uint32_t kTile16 = Smem::kTileBytes >> 4;          // tile stride in descriptor units
-    auto qk = [&](int s, int slot, int qtile, bool last_q, uint64_t* q_done) {  // S_s = Q K^T
-      const uint32_t qb = q_lo + qtile * kTile16, kb = k_lo + slot * kTile16, d = tmem + s * 128;
-      if (elect_one()) {
+    // ------------------------------------------------------------ products
+    // One thread does it all: between two products nothing but the waits for P and for the
+    // next K and V tile, which are taken ahead of P.
+    if (elect_one()) {
+      Ring ring;
+      int li = 0;
+      uint32_t pphase = 0, cphase = 0;                 // bit s: parity of stream s's next P; of the cleared tails
+      bool ok = true;
+      auto take = [&](int& slot) {                     // the next K or V tile
+        ok = ok && wait_or_abort(&sm.full[ring.slot], (uint32_t)ring.phase, ns, abort_flag);
+        slot = ring.slot;
+        ring.step<kStages>();
+        return ok;
+      };
+      const uint32_t q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK), k_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboK);
+      const uint32_t v_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboMN);
+      constexpr uint32_t kTile16 = Smem::kTileBytes >> 4;        // tile stride in descriptor units
+      auto qk = [&](int s, int slot, int qtile) {      // S_s = Q K^T
+        const uint32_t qb = q_lo + qtile * kTile16, kb = k_lo + slot * kTile16, d = tmem + s * 128;
+        fence_after();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
           mma_ss(d, desc(qb + at), desc(kb + at), idesc(128, false), k > 0);
         }
         commit(&sm.s_full[s]);
-        if (last_q) commit(q_done);
-      }
-      __syncwarp();
-    };
-    auto wait_p = [&](int s) {
-      ok = ok && warp_wait(&sm.p_full[s], (pphase >> s) & 1, ns, abort_flag);
-      pphase ^= 1u << s;
-      fence_after();
-      return ok;
-    };
-    auto pv = [&](int s, int slot, bool first, bool last) {  // O_s += P_s V
-      const uint32_t vb = v_lo + slot * kTile16, d = tmem + 256 + s * D, p = tmem + s * 128;
-      if (elect_one()) {
+      };
+      auto wait_p = [&](int s) {
+        ok = ok && wait_or_abort(&sm.p_full[s], (pphase >> s) & 1, ns, abort_flag);
+        pphase ^= 1u << s;
+        return ok;
+      };
+      auto pv = [&](int s, int slot, bool first, bool last) {    // O_s += P_s V
+        const uint32_t vb = v_lo + slot * kTile16, d = tmem + 256 + s * D, p = tmem + s * 128;
+        fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ts(d, p + (k >> 2) * 64 + (k & 3) * 8, desc(vb + k * 128), idesc(D, true), !(first && k == 0));
+        for (int k = 0; k < 8; ++k)
+          mma_ts(d, p + (k >> 2) * 64 + (k & 3) * 8, desc(vb + k * 128), idesc(D, true), !(first && k == 0));
         if (last) commit(&sm.o_done[s]);
+      };
+      for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next(); ++li) {
+        const int t0 = (int)((unsigned)w.item % (unsigned)a.rp) * a.tpb;
+        const int nt = w.te - w.tb;
+        const int ns2 = kRowStreams && t0 + a.tt < w.r.n ? 2 : 1;
+        const int qb = kRowStreams ? 0 : li & 1, use = kRowStreams ? li : li >> 1;
+        // the piece's first V tile holds rows past the last entry: warp 3 clears them
+        const bool tail = w.r.len + w.r.n - w.r.first < w.te * 128;
+        ok = wait_or_abort(&sm.q_full[qb], (uint32_t)(use & 1), ns, abort_flag);
+        int slot = 0;
+        if (!take(slot)) break;
+        if constexpr (kRowStreams) {
+          for (int s = 0; s < ns2; ++s) qk(s, slot, s);
+          commit(&sm.empty[slot]);
+          if (nt == 1) commit(&sm.q_empty[qb]);
+          for (int i = 0; ok && i < nt; ++i) {
+            int vs = 0, ks = 0;
+            if (!take(vs)) break;
+            if (i == 0 && tail) kvcd::mbar_arrive(&sm.tail_here);
+            if (i + 1 < nt && !take(ks)) break;
+            if (i == 0 && tail) {
+              ok = wait_or_abort(&sm.cleared, cphase, ns, abort_flag);
+              cphase ^= 1;
+            }
+            for (int s = 0; s < ns2; ++s) {
+              if (!wait_p(s)) break;
+              pv(s, vs, i == 0, i + 1 == nt);
+              if (s + 1 == ns2) commit(&sm.empty[vs]);
+              if (i + 1 < nt) {
+                qk(s, ks, s);
+                if (s + 1 == ns2) commit(&sm.empty[ks]);
+              }
+            }
+            if (i + 2 == nt) commit(&sm.q_empty[qb]);
+          }
+        } else {
+          qk(0, slot, qb);
+          commit(&sm.empty[slot]);
+          if (nt > 1) {
+            if (!take(slot)) break;
+            qk(1, slot, qb);
+            commit(&sm.empty[slot]);
+          }
+          if (nt <= 2) commit(&sm.q_empty[qb]);
+          for (int j = 0; ok && j < nt; ++j) {
+            const int s = j & 1;
+            int ks = 0;
+            if (!take(slot)) break;
+            if (j == 0 && tail) kvcd::mbar_arrive(&sm.tail_here);
+            if (j + 2 < nt && !take(ks)) break;
+            if (j == 0 && tail) {
+              ok = wait_or_abort(&sm.cleared, cphase, ns, abort_flag);
+              cphase ^= 1;
+            }
+            if (!wait_p(s)) break;
+            pv(s, slot, j < 2, j + 2 >= nt);
+            commit(&sm.empty[slot]);
+            if (j + 2 < nt) {
+              qk(s, ks, qb);
+              commit(&sm.empty[ks]);
+              if (j + 3 == nt) commit(&sm.q_empty[qb]);
+            }
+          }
+        }
       }
-      __syncwarp();
-    };
-    auto release = [&](int slot) {
-      if (elect_one()) commit(&sm.empty[slot]);
-      __syncwarp();
-    };
-    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next(); ++li) {
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ ln m and positions
+    if (warp == 3 && a.len_out)
+      for (int64_t u = (int64_t)blockIdx.x * 32 + lane; u < a.units; u += (int64_t)gridDim.x * 32) {
+        const ChunkUnit r = kvcd::load_unit(a, u);
+        const int64_t gu = kvcd::unit_global(a, u);
+        a.len_out[gu] = r.n > 0 ? r.len + r.n : a.len_lh[gu];
+      }
+    // Row streams share a ring of kBias tiles, which the two warps fill in turn; entry streams
+    // have a ring of kBias / 2 each, filled by a warp each (a stream that waited for a slot the
+    // other one uses could take an old phase for the one it needs).
+    int cnt = 0;                                       // tiles so far (entry streams: of this warp's stream)
+    int loads = 0;                                     // K and V tiles before this piece
+    uint32_t tails = 0;                                // cleared so far
+    bool ok = true;
+    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next();) {
       const int64_t u = w.item / a.rp;
-      const int t0 = (int)(w.item - u * a.rp) * a.tpb;
-      const int total = w.r.len + w.r.n, nt = w.te - w.tb;
-      const int ns2 = kRowStreams && t0 + a.tt < w.r.n ? 2 : 1;
-      const int qb = kRowStreams ? 0 : li & 1, use = kRowStreams ? li : li >> 1;
-      ok = warp_wait(&sm.q_full[qb], (uint32_t)(use & 1), ns, abort_flag);
-      if (!ok) break;
-      // rows past the last entry: V zero (P is 0 there, but they may hold anything)
-      auto clear_tail = [&](int slot, int tile) {
-        const int valid = total - w.r.first - (w.te - 1 - tile) * 128;
-        if (valid >= 128) return;
+      const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
+      const int total = w.r.len + w.r.n;
+      // the row block's first token
+      const float pos0 = kPos ? a.pos_new[u / a.per_seq] + (float)((int)(w.item - u * a.rp) * a.tpb) : 0.f;
+      // Warp 3, once its part of the first tile is out of the way: rows past the last entry of
+      // the piece's first V tile become zero (P is 0 there, but they may hold anything).
+      const int nt = w.te - w.tb, valid = total - w.r.first - (w.te - 1) * 128;
+      const int v0 = loads + (kRowStreams || nt == 1 ? 1 : 2);   // the load that brings that tile
+      bool tail = warp == 3 && valid < 128;
+      loads += 2 * nt;
+      auto clear_tail = [&]() {
+        tail = false;
+        const int slot = v0 % kStages;
+        ok = warp_wait(&sm.tail_here, tails & 1, ns, abort_flag);
+        if (!ok) return;
+        ++tails;
         for (int z = lane; z < (128 - valid) * 8 * kBlocks; z += 32) {
           const int r = valid + z / (8 * kBlocks), h = (z >> 3) & (kBlocks - 1), c = z & 7;
           *reinterpret_cast<uint4*>(sm.ring[slot] + h * kHalf + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
         }
         kvcd::fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.cleared);
       };
-      int slot;
-      if constexpr (kRowStreams) {
-        if (!take(slot)) break;
-        for (int s = 0; s < ns2; ++s) qk(s, slot, s, nt == 1 && s + 1 == ns2, &sm.q_empty[qb]);
-        release(slot);
-        for (int i = 0; ok && i < nt; ++i) {
-          int vs = 0, ks = 0;
-          if (!take(vs)) break;                        // usually there already: waited for before P
-          clear_tail(vs, i);
-          if (i + 1 < nt && !take(ks)) break;
-          for (int s = 0; s < ns2; ++s) {
-            if (!wait_p(s)) break;
-            pv(s, vs, i == 0, i + 1 == nt);
-            if (s + 1 == ns2) release(vs);
-            if (i + 1 < nt) {
-              qk(s, ks, s, i + 2 == nt && s + 1 == ns2, &sm.q_empty[qb]);
-              if (s + 1 == ns2) release(ks);
-            }
-          }
-        }
-      } else {
-        for (int j = 0; ok && j < min(2, nt); ++j) {
-          if (!take(slot)) break;
-          qk(j, slot, qb, j + 1 == nt, &sm.q_empty[qb]);
-          release(slot);
-        }
-        for (int j = 0; ok && j < nt; ++j) {
-          const int s = j & 1;
-          int ks = 0;
-          if (!take(slot)) break;
-          clear_tail(slot, j);
-          if (j + 2 < nt && !take(ks)) break;
-          if (!wait_p(s)) break;
-          pv(s, slot, j < 2, j + 2 >= nt);
-          release(slot);
-          if (j + 2 < nt) {
-            qk(s, ks, qb, j + 3 == nt, &sm.q_empty[qb]);
-            release(ks);
-          }
-        }
-      }
-    }
-  } else if (warp < 4) {
-    // ------------------------------------------------------------ ln m and positions
-    int cnt = 0;                                       // tiles so far; this warp takes every other one
-    bool ok = true;
-    for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next();) {
-      const int64_t u = w.item / a.rp;
-      const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
-      const int total = w.r.len + w.r.n;
-      const float pos0 = kPos ? a.pos_new[u / a.per_seq] : 0.f;
-      for (int t = w.te - 1; ok && t >= w.tb; --t, ++cnt) {
-        if ((cnt & 1) != (warp & 1)) continue;
-        float lm[4], rel[4];
+      for (int t = w.te - 1; ok && t >= w.tb; --t) {
+        if (tail && t < w.te - 1) clear_tail();
+        if (!ok) break;
+        const int at = kRowStreams ? cnt++ : w.te - 1 - t;
+        if ((at & 1) != (warp & 1)) continue;
+        float lm[4], rel[4], low = INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = w.r.first + t * 128 + lane + 32 * j;
@@ -397,10 +431,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (e < total) {
             const int64_t row = rows(e);
             lm[j] = __ldcg(a.logm + row) * kvcd::kLog2eC;
-            if (kPos) rel[j] = __ldcg(a.pos + row) - pos0;
+            if (kPos) {
+              rel[j] = __ldcg(a.pos + row) - pos0;
+              low = fminf(low, rel[j]);
+            }
           }
         }
-        const int b = cnt % kBias, use = cnt / kBias;
+        if (kPos) low = -kvcd::warp_max(-low);
+        const int b = kRowStreams ? at % kBias : (warp & 1) * (kBias / 2) + cnt % (kBias / 2);
+        const int use = kRowStreams ? at / kBias : cnt / (kBias / 2);
+        if (!kRowStreams) ++cnt;
         if (use > 0) ok = warp_wait(&sm.bias_empty[b], (uint32_t)((use - 1) & 1), ns, abort_flag);
         if (!ok) break;
 #pragma unroll
@@ -411,9 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool any = __any_sync(KVC_FULL_MASK, lm[0] != 0.f || lm[1] != 0.f || lm[2] != 0.f || lm[3] != 0.f);
         if (lane == 0) {
           sm.lm_any[b] = any;
+          if (kPos) sm.rel_min[b] = low;
           kvcd::mbar_arrive(&sm.bias_full[b]);
         }
       }
+      if (ok && tail) clear_tail();
     }
   } else {
     // ------------------------------------------------------------ softmax and output
@@ -425,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t ts = tl + st * 128 + half * 64, to = tl + 256 + st * D + half * (D / 2);
     uint32_t sphase = 0, ophase[2] = {0, 0};
-    int cnt = 0;                                       // bias tiles so far
+    int cnt = 0;                                       // bias tiles so far (of this stream's ring)
     // entry streams: stream 1 hands m and l over (j_full) and touches its output again only
     // when stream 0 has read it (j_free); both complete once per joined piece
     uint32_t joins = 0;
@@ -442,21 +484,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       rs.cap_in = kCap ? a.scale / a.softcap : 0.f;
       rs.cap_out = kCap ? a.softcap * kvcd::kLog2eC : 0.f;
       rs.slope = kPos && a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
-      rs.tok = (float)tok;
-      rs.edge = kPos && a.window > 0.f ? rs.tok - a.window : -INFINITY;
+      // positions count from the row block's first token, so that near entries, the ones whose
+      // bias is small, lose nothing in slope rel - slope tok
+      const float tokf = (float)(tok - (int)(w.item - u * a.rp) * a.tpb);
+      rs.shift = rs.slope * tokf;
+      rs.edge = kPos && a.window > 0.f ? tokf - a.window : -INFINITY;
       const int nt = w.te - w.tb;
       const bool mine = !kRowStreams || st == 0 || t0 < w.r.n;     // this stream has work
       float m = 0.f, l = 0.f;                          // the row's reference, and this half's sum
       bool settled = false;                            // the reference fits the entries seen so far
-      for (int i = 0; i < nt; ++i, ++cnt) {
+      for (int i = 0; i < nt; ++i) {
         if (!kRowStreams && (i & 1) != st) continue;
-        const int b = cnt % kBias, tile = w.te - 1 - i;
-        warp_wait(&sm.bias_full[b], (uint32_t)((cnt / kBias) & 1), ns, abort_flag);
+        const int b = kRowStreams ? cnt % kBias : st * (kBias / 2) + cnt % (kBias / 2), tile = w.te - 1 - i;
+        const int bias_use = cnt / (kRowStreams ? kBias : kBias / 2);
+        ++cnt;
+        warp_join(&sm.bias_full[b], (uint32_t)(bias_use & 1), ns, abort_flag);
         if (!mine) {
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           continue;
         }
-        warp_wait(&sm.s_full[st], sphase, ns, abort_flag);
+        warp_join(&sm.s_full[st], sphase, ns, abort_flag);
         sphase ^= 1;
         fence_after();
         if (busy) {
@@ -465,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // agree on a new m, rescale O and do the tile again.
           const int lim = live ? see - w.r.first - tile * 128 - half * 64 : 64;
           const float *lm = sm.lm[b] + half * 64, *rel = sm.rel[b] + half * 64;
-          const bool cut = __any_sync(KVC_FULL_MASK, lim < 64);
+          const bool cut = __any_sync(KVC_FULL_MASK, lim < 64 || (kPos && live && !(sm.rel_min[b] > rs.edge)));
           uint32_t p[32];
           float sum;
           if (cut) sum = numerators<kCap, kPos, true, true>(rs, ts, lm, rel, m, lim, p);
@@ -506,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           l += sum;
           if (!kRowStreams && st == 1 && joined) {     // stream 0 has read the results before
-            warp_wait(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
+            warp_join(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
             joined = false;
           }
           tst16(ts, reinterpret_cast<const uint32_t(&)[16]>(p[0]));
@@ -515,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           if (!kRowStreams && st == 1 && joined) {
-            warp_wait(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
+            warp_join(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
             joined = false;
           }
         }
@@ -550,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             joined = true;
             continue;
           }
-          warp_wait(&sm.o_done[0], ophase[0], ns, abort_flag);
-          warp_wait(&sm.o_done[1], ophase[1], ns, abort_flag);
+          warp_join(&sm.o_done[0], ophase[0], ns, abort_flag);
+          warp_join(&sm.o_done[1], ophase[1], ns, abort_flag);
           ophase[0] ^= 1;
           ophase[1] ^= 1;
-          warp_wait(&sm.j_full, joins & 1, ns, abort_flag);
+          warp_join(&sm.j_full, joins & 1, ns, abort_flag);
           const float mb = sm.m1[row], lb = sm.l1[row];
           const float mn = fmaxf(m, mb);
           f0 = m == -INFINITY ? 0.f : kvcd::ex2(m - mn);
@@ -562,11 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = fmaf(l, f0, lb * f1);
           m = mn;
         } else {
-          warp_wait(&sm.o_done[0], ophase[0], ns, abort_flag);
+          warp_join(&sm.o_done[0], ophase[0], ns, abort_flag);
           ophase[0] ^= 1;
         }
       } else {
-        warp_wait(&sm.o_done[st], ophase[0], ns, abort_flag);
+        warp_join(&sm.o_done[st], ophase[0], ns, abort_flag);
         ophase[0] ^= 1;
       }
       fence_after();
@@ -589,14 +636,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
           }
           const int at = half * (D / 2) + c;
+          uint32_t x[8];
           if (live && whole) {
-            uint4* op = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + at);
-            op[0] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
-            op[1] = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
-          } else if (live) {
-            float4* pp = reinterpret_cast<float4*>(a.part + slot * D + at);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pp[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) x[e] = bf16x2(v[2 * e], v[2 * e + 1]);
+            store32(static_cast<__nv_bfloat16*>(a.out) + orow * D + at, x);
+          } else if (live) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(v[8 * h + e]);
+              store32(a.part + slot * D + at + 8 * h, x);
+            }
           }
         }
         if (half == 0 && live && whole && a.lse) a.lse[orow] = l > 0.f ? m + log2f(l) : -INFINITY;
@@ -620,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i)
         if ((q_issued >> i) & 1) kvcd::mbar_wait(&sm.q_full[i], (q_phase >> i) & 1);
     }
-    if (warp == 1 && lane == 0) {                      // and every issued product ends
+    if (warp == 1 && elect_one()) {                    // and every issued product ends
       commit(&sm.drain);
       kvcd::mbar_wait(&sm.drain, 0);
     }

@@ -63,11 +63,11 @@ __device__ __forceinline__ void add16(const ChunkArgs& a, const uint32_t (&s)[16
       x1 = fma2(pk(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, x1);
     }
     float4 t;
-    if constexpr (kPos || kEdge) t = *reinterpret_cast<const float4*>(tok + c);
+    if constexpr (kEdge) t = *reinterpret_cast<const float4*>(tok + c);
     if constexpr (kPos) {
       const float4 sl = *reinterpret_cast<const float4*>(slope + c);
-      x0 = fma2(pk(sl.x, sl.y), add2(rel2, pk(-t.x, -t.y)), x0);
-      x1 = fma2(pk(sl.z, sl.w), add2(rel2, pk(-t.z, -t.w)), x1);
+      x0 = fma2(pk(sl.x, sl.y), rel2, x0);
+      x1 = fma2(pk(sl.z, sl.w), rel2, x1);
     }
     float f[4];
     upk(x0, f[0], f[1]);
@@ -204,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = lane + 32 * j, g = r / a.tt, t = rt * a.tt + r % a.tt;
           nl[j] = -INFINITY;
           sl[j] = 0.f;
-          tk[j] = (float)t;
+          tk[j] = (float)(r % a.tt);                   // tokens and positions count from the row tile's first
           if (r < used && t < w.r.n) {
             const float lse = __ldcg(a.lse + (w.u * a.G + g) * a.T + t);
-            if (lse != -INFINITY) nl[j] = -lse;
             if (kPos && a.slopes) sl[j] = a.slopes[(w.u % a.H) * a.G + g] * kvcd::kLog2eC;
+            if (lse != -INFINITY) nl[j] = -lse - sl[j] * tk[j];
           }
         }
         const int b = nq % kGroups;
@@ -248,14 +248,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (taker == grp && e < w.r.len) old = a.mass[row];
         }
         uint64_t sum0 = 0, sum1 = 0;
-        const float first_tok = (float)(e - w.r.len);  // tokens from this one on see the entry
         for (int i = mine; i < steps; i += kGroups) {
           const int t0 = (w.tb + i) * a.tt;
           warp_wait(&sm.r_full[grp], phase, ns, abort_flag);
           warp_wait(&sm.s_full[grp], phase, ns, abort_flag);
           phase ^= 1;
           fence_after();
-          const bool edge = used < 128 || t0 + a.tt > w.r.n || e0 + 127 > w.r.len + t0 || a.window > 0.f;
+          const float first_tok = (float)(e - w.r.len - t0);  // tokens from this one on see the entry
+          const float rel_t = rel - (float)t0;
+          const bool edge = used < 128 || t0 + a.tt > w.r.n || e0 + 127 > w.r.len + t0 ||
+                            (kPos && a.window > 0.f && __any_sync(KVC_FULL_MASK, e < total && !(rel_t > (float)a.tt - a.window)));
           for (int c = 0; c < cols; c += 32) {         // the second half's columns may be stale: cols is a
             uint32_t s0[16], s1[16];                   // multiple of 16 and they are skipped below
             tld16(ts + c, s0);
@@ -264,11 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_ld(s1);
             const float *nl = sm.nl[grp] + c, *sl = sm.slope[grp] + c, *tk = sm.tok[grp] + c;
             if (edge) {
-              add16<kCap, kPos, true>(a, s0, nl, sl, tk, lm, rel, first_tok, sum0, sum1);
-              if (c + 16 < cols) add16<kCap, kPos, true>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel, first_tok, sum0, sum1);
+              add16<kCap, kPos, true>(a, s0, nl, sl, tk, lm, rel_t, first_tok, sum0, sum1);
+              if (c + 16 < cols) add16<kCap, kPos, true>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel_t, first_tok, sum0, sum1);
             } else {
-              add16<kCap, kPos, false>(a, s0, nl, sl, tk, lm, rel, first_tok, sum0, sum1);
-              add16<kCap, kPos, false>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel, first_tok, sum0, sum1);
+              add16<kCap, kPos, false>(a, s0, nl, sl, tk, lm, rel_t, first_tok, sum0, sum1);
+              add16<kCap, kPos, false>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel_t, first_tok, sum0, sum1);
             }
           }
           fence_before();
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, k_loads - kK); i < k_loads; ++i) kvcd::mbar_wait(&sm.k_full[i % kK], (uint32_t)((i / kK) & 1));
       for (int i = max(0, q_loads - kQ); i < q_loads; ++i) kvcd::mbar_wait(&sm.q_full[i % kQ], (uint32_t)((i / kQ) & 1));
     }
-    if (warp == 1 && lane == 0) {                      // and every issued product ends
+    if (warp == 1 && elect_one()) {                    // and every issued product ends
       commit(&sm.drain);
       kvcd::mbar_wait(&sm.drain, 0);
     }

@@ -104,6 +104,11 @@ __device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, int x,
       : "memory");
 }
 
+// 32 bytes, one whole sector, in one store (32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), KVC_I4(v, 0), KVC_I4(v, 4) : "memory");
+}
+
 // Packed pairs of fp32.
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
@@ -160,7 +165,12 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
   return true;
 }
 
-// The same for a whole warp: every lane gets the same answer.
+// The same for a whole warp, which leaves converged.
+__device__ __forceinline__ void warp_join(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
+  wait_or_abort(bar, parity, ns, abort);
+  __syncwarp();
+}
+// And every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
   return __all_sync(KVC_FULL_MASK, wait_or_abort(bar, parity, ns, abort));
 }

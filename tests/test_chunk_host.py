@@ -179,6 +179,12 @@ def test_row_arrays_off_a_16_byte_boundary_are_rejected(lib, name, idx):
     assert CALLS[name](lib, _params(), _chunk(), ptrs) == kvc.KVC_EINVAL
 
 
+def test_output_is_written_in_whole_sectors(lib):
+    ptrs = _fake(14)
+    ptrs[11] = VP(4096 * 12 + 16)
+    assert _attn(lib, _params(), _chunk(), ptrs) == kvc.KVC_EINVAL
+
+
 def test_scalars_are_checked(lib):
     p, c = _params(), _chunk()
     for decay in (-0.1, 1.1, float("nan")):

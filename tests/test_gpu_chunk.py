@@ -42,6 +42,10 @@ CASES = {
     "many units": dict(lens=np.arange(7 * 3 * 16) * 3 % 211, n_new=[1, 2, 3, 4, 5, 6, 7], B=7, L=3, H=16, G=2),
     "row tiles of every count": dict(lens=np.arange(24) * 97 % 1500 + 300, n_new=[1, 65, 129, 194], B=4, L=3, H=2,
                                      G=2, d=64, page=64, softcap=30.0),
+    "runs of short units": dict(lens=np.where(np.arange(3000) % 7 == 3, 300, np.arange(3000) % 90), n_new=[1], L=250,
+                                H=12, G=1, d=64),
+    "runs of short units, paged": dict(lens=np.where(np.arange(1500) % 19 == 3, 500, np.arange(1500) % 60),
+                                       n_new=[3, 1, 0], B=3, L=50, H=10, G=2, page=16),
     "layer range": dict(lens=[5, 70, 200, 130, 64, 9, 1, 300], n_new=[9, 20], B=2, L=4, layers=(1, 3)),
     "no n_new": dict(lens=[5, 70], n_new=[9, 9], B=2, pass_n_new=False),
     # scores
