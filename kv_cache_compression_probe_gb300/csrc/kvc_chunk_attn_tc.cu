@@ -48,9 +48,11 @@ struct AttnSmem {
   static constexpr uint32_t kTileBytes = 128 * D * 2;
   alignas(1024) unsigned char q[2][kTileBytes];
   alignas(1024) unsigned char ring[kStages][kTileBytes];
-  alignas(16) float lm[kBias][128], rel[kBias][128];   // base-2 ln m; position - the row block's
+  alignas(16) unsigned char ext_k[kBias][4096];        // the extra step's entry columns, or (capped) base-2 ln m
+  alignas(16) unsigned char ext_q[2][4096];            // and row factors
+  alignas(16) float rel[kBias][128];                   // position - the row block's first
   float rel_min[kBias];                                // least position of the tile's entries
-  int lm_any[kBias];                                   // some ln m of the tile is not 0
+  int extra[kBias];                                    // the tile needs the extra step
   float xtop[2][2][128], xl[2][2][128];                // what the two halves of a row tell each other
   float m1[128], l1[128];                              // stream 1's statistics (entry streams)
   uint64_t full[kStages], empty[kStages], q_full[2], q_empty[2], bias_full[kBias], bias_empty[kBias];
@@ -69,34 +71,37 @@ struct Ring {
   }
 };
 
+// What a kernel does with the products, by what the call asks for.
+//   kSums   ln m and the distance bias are part of the product: an extra 16-wide step
+//           of Q K^T adds them (ext_key, ext_row)
+//   kWindow the same, and entries beyond the window are left out
+//   kCapped the tanh comes between the product and them, so they are added per score
+//           from shared memory
+enum Mode { kSums, kWindow, kCapped };
+
 // What a thread needs to turn the products of its row into base-2 scores.
 struct RowScore {
-  float scale, cap_in, cap_out;        // s log2 e = scale dot, or cap_out tanh(cap_in dot)
+  float scale, cap_in, cap_out;        // s log2 e = scale product, or cap_out tanh(cap_in product)
   float slope, shift;                  // distance bias slope rel - shift
   float edge;                          // window: sees rel > edge
 };
 
 // Scores (plus `base`, both halves of a pair) of four entries c .. c + 3 of a tile.
-// kLm: some ln m of the tile is not 0.  kMask: the row sees only the first `lim`
-// entries, and of these those beyond the window's edge.
-template <bool kCap, bool kPos, bool kLm, bool kMask>
+// kMask: the row sees only the first `lim` entries, and of these those beyond the
+// window's edge.  (A broadcast from shared memory costs its full width, 512 bytes a
+// warp for four floats: per-entry values read here bounded the kernel, which is why
+// the product carries them.)
+template <int kMode, bool kMask>
 __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, const float* lm, const float* rel, int c,
                                         uint64_t base, int lim, float (&f)[4]) {
   uint64_t x0 = base, x1 = base;
-  if constexpr (kLm) {
-    const float4 b = *reinterpret_cast<const float4*>(lm + c);
-    x0 = add2(pk(b.x, b.y), base);
-    x1 = add2(pk(b.z, b.w), base);
-  }
   float4 d;
-  if constexpr (kPos) {
-    d = *reinterpret_cast<const float4*>(rel + c);
-    const uint64_t sl = pk(r.slope, r.slope);
-    x0 = fma2(sl, pk(d.x, d.y), x0);
-    x1 = fma2(sl, pk(d.z, d.w), x1);
-  }
-  if constexpr (kCap) {
-    const uint64_t co = pk(r.cap_out, r.cap_out);
+  if constexpr (kMode == kCapped || (kMode == kWindow && kMask)) d = *reinterpret_cast<const float4*>(rel + c);
+  if constexpr (kMode == kCapped) {
+    const float4 b = *reinterpret_cast<const float4*>(lm + c);
+    const uint64_t sl = pk(r.slope, r.slope), co = pk(r.cap_out, r.cap_out);
+    x0 = fma2(sl, pk(d.x, d.y), add2(pk(b.x, b.y), base));
+    x1 = fma2(sl, pk(d.z, d.w), add2(pk(b.z, b.w), base));
     x0 = fma2(pk(tanh_f(__uint_as_float(s[0]) * r.cap_in), tanh_f(__uint_as_float(s[1]) * r.cap_in)), co, x0);
     x1 = fma2(pk(tanh_f(__uint_as_float(s[2]) * r.cap_in), tanh_f(__uint_as_float(s[3]) * r.cap_in)), co, x1);
   } else {
@@ -107,7 +112,7 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
   upk(x0, f[0], f[1]);
   upk(x1, f[2], f[3]);
   if constexpr (kMask) {
-    if constexpr (kPos) {
+    if constexpr (kMode != kSums) {
       f[0] = d.x > r.edge ? f[0] : -INFINITY;
       f[1] = d.y > r.edge ? f[1] : -INFINITY;
       f[2] = d.z > r.edge ? f[2] : -INFINITY;
@@ -121,10 +126,10 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 // Numerators 2^(s - base) of a row over 64 entries of a tile, packed as bf16 pairs;
 // returns their sum in fp32.  The products come from TMEM in blocks of 16, the next
 // block on its way while one is worked on.
-template <bool kCap, bool kPos, bool kLm, bool kMask>
+template <int kMode, bool kMask>
 __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,
                                             float base, int lim, uint32_t (&p)[32]) {
-  const float sh = kPos ? -(base + r.shift) : -base;
+  const float sh = -(base + r.shift);
   const uint64_t mb = pk(sh, sh);
   uint64_t s0 = 0, s1 = 0;
   uint32_t s[2][16];
@@ -136,7 +141,7 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       float f[4];
-      scores4<kCap, kPos, kLm, kMask>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
+      scores4<kMode, kMask>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = kvcd::ex2(f[i]);
       s0 = add2(s0, pk(f[0], f[1]));
@@ -151,10 +156,10 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
 }
 
 // Largest score of a row over 64 entries (rare: kept small).
-template <bool kCap, bool kPos>
+template <int kMode>
 __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const float* lm, const float* rel, int lim) {
   float t = -INFINITY;
-  const uint64_t mb = kPos ? pk(-r.shift, -r.shift) : 0ull;
+  const uint64_t mb = pk(-r.shift, -r.shift);
 #pragma unroll 1
   for (int q = 0; q < 64; q += 16) {
     uint32_t s[16];
@@ -163,7 +168,7 @@ __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       float f[4];
-      scores4<kCap, kPos, true, true>(r, s + e, lm, rel, q + e, mb, lim, f);
+      scores4<kMode, true>(r, s + e, lm, rel, q + e, mb, lim, f);
       t = kvcd::fmax3(t, f[0], f[1]);
       t = kvcd::fmax3(t, f[2], f[3]);
     }
@@ -171,7 +176,41 @@ __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const
   return t;
 }
 
-template <int D, bool kRowStreams, bool kCap, bool kPos>
+// The extra step.  Its 16 columns hold, per entry, ln m and the position split into
+// bf16 parts (8 bits each, so three parts are the fp32 value) over sqrt(d)'s inverse,
+// and per row the factors: 1 for the parts of ln m, the parts of the head's slope for
+// those of the position.  Rows of 8 x 16 bytes (no swizzle), 256 bytes per 8 rows.
+__device__ __forceinline__ void split3(float x, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    p[i] = __bfloat16_as_ushort(h);
+    x = isinf(x) ? 0.f : x - __bfloat162float(h);
+  }
+}
+__device__ __forceinline__ void ext_store(unsigned char* tile, int row, const uint4& c0, const uint4& c1) {
+  unsigned char* p = tile + (row >> 3) * 256 + (row & 7) * 16;
+  *reinterpret_cast<uint4*>(p) = c0;
+  *reinterpret_cast<uint4*>(p + 128) = c1;
+}
+// Columns: l0 l1 l2 | r0 r1 r2 r0 r1 | r0 r2 r1
+__device__ __forceinline__ void ext_key(unsigned char* tile, int row, float lm, float rel) {
+  uint32_t l[3], r[3];
+  split3(lm, l);
+  split3(rel, r);
+  ext_store(tile, row, make_uint4(l[0] | l[1] << 16, l[2] | r[0] << 16, r[1] | r[2] << 16, r[0] | r[1] << 16),
+            make_uint4(r[0] | r[2] << 16, r[1], 0, 0));
+}
+// Factors: 1 1 1 | s0 s0 s0 s1 s1 | s2 s1 s2
+__device__ __forceinline__ void ext_row(unsigned char* tile, int row, float slope) {
+  uint32_t p[3];
+  split3(slope, p);
+  constexpr uint32_t one = 0x3f80;
+  ext_store(tile, row, make_uint4(one | one << 16, one | p[0] << 16, p[0] | p[0] << 16, p[1] | p[1] << 16),
+            make_uint4(p[2] | p[1] << 16, p[2], 0, 0));
+}
+
+template <int D, bool kRowStreams, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ChunkArgs a) {
@@ -186,10 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) { kvcd::mbar_init(&sm.full[i], 1); kvcd::mbar_init(&sm.empty[i], 1); }
     for (int i = 0; i < kBias; ++i) {
       kvcd::mbar_init(&sm.bias_full[i], 1);
-      kvcd::mbar_init(&sm.bias_empty[i], kRowStreams ? 16 : 8);
+      // released by the softmax warps that read it, else by the products
+      kvcd::mbar_init(&sm.bias_empty[i], kMode == kSums ? 1 : kRowStreams ? 16 : 8);
     }
     for (int i = 0; i < 2; ++i) {
-      kvcd::mbar_init(&sm.q_full[i], 1);
+      kvcd::mbar_init(&sm.q_full[i], kMode != kCapped && a.slopes ? 2 : 1);
       kvcd::mbar_init(&sm.q_empty[i], 1);
       kvcd::mbar_init(&sm.s_full[i], 1);
       kvcd::mbar_init(&sm.p_full[i], 8);
@@ -208,6 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "r"((uint32_t)kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (kMode != kCapped && !a.slopes) {                 // the same factors for every row
+    for (int r = tid; r < 256; r += kThreads) ext_row(sm.ext_q[r >> 7], r & 127, 0.f);
+    kvcd::fence_proxy_async_smem();
   }
   fence_before();
   __syncthreads();
@@ -288,7 +332,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK), k_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboK);
       const uint32_t v_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboMN);
       constexpr uint32_t kTile16 = Smem::kTileBytes >> 4;        // tile stride in descriptor units
-      auto qk = [&](int s, int slot, int qtile) {      // S_s = Q K^T
+      const uint32_t eq_lo = ext_lo(kvcd::smem_u32(sm.ext_q[0])), ek_lo = ext_lo(kvcd::smem_u32(sm.ext_k[0]));
+      int bcnt[2] = {0, 0};                            // bias tiles so far (row streams: [0])
+      int bslot = 0;
+      auto take_bias = [&](int s) {                    // the tile's extra columns
+        if (kMode == kCapped) return ok;
+        const int c = bcnt[kRowStreams ? 0 : s]++;
+        bslot = kRowStreams ? c % kBias : s * (kBias / 2) + c % (kBias / 2);
+        const int use = kRowStreams ? c / kBias : c / (kBias / 2);
+        ok = ok && wait_or_abort(&sm.bias_full[bslot], (uint32_t)(use & 1), ns, abort_flag);
+        return ok;
+      };
+      auto qk = [&](int s, int slot, int qtile, int eq, bool last) {   // S_s = Q K^T (+ the extra step)
         const uint32_t qb = q_lo + qtile * kTile16, kb = k_lo + slot * kTile16, d = tmem + s * 128;
         fence_after();
 #pragma unroll
@@ -296,7 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
           mma_ss(d, desc(qb + at), desc(kb + at), idesc(128, false), k > 0);
         }
+        if (kMode != kCapped && sm.extra[bslot])
+          mma_ss(d, ext_desc(eq_lo + eq * 256), ext_desc(ek_lo + bslot * 256), idesc(128, false), 1);
         commit(&sm.s_full[s]);
+        if (kMode == kSums && last) commit(&sm.bias_empty[bslot]);
       };
       auto wait_p = [&](int s) {
         ok = ok && wait_or_abort(&sm.p_full[s], (pphase >> s) & 1, ns, abort_flag);
@@ -320,16 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool tail = w.r.len + w.r.n - w.r.first < w.te * 128;
         ok = wait_or_abort(&sm.q_full[qb], (uint32_t)(use & 1), ns, abort_flag);
         int slot = 0;
-        if (!take(slot)) break;
+        if (!take(slot) || !take_bias(0)) break;
         if constexpr (kRowStreams) {
-          for (int s = 0; s < ns2; ++s) qk(s, slot, s);
+          for (int s = 0; s < ns2; ++s) qk(s, slot, s, 0, s + 1 == ns2);
           commit(&sm.empty[slot]);
           if (nt == 1) commit(&sm.q_empty[qb]);
           for (int i = 0; ok && i < nt; ++i) {
             int vs = 0, ks = 0;
             if (!take(vs)) break;
             if (i == 0 && tail) kvcd::mbar_arrive(&sm.tail_here);
-            if (i + 1 < nt && !take(ks)) break;
+            if (i + 1 < nt && (!take(ks) || !take_bias(0))) break;
             if (i == 0 && tail) {
               ok = wait_or_abort(&sm.cleared, cphase, ns, abort_flag);
               cphase ^= 1;
@@ -339,18 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               pv(s, vs, i == 0, i + 1 == nt);
               if (s + 1 == ns2) commit(&sm.empty[vs]);
               if (i + 1 < nt) {
-                qk(s, ks, s);
+                qk(s, ks, s, 0, s + 1 == ns2);
                 if (s + 1 == ns2) commit(&sm.empty[ks]);
               }
             }
             if (i + 2 == nt) commit(&sm.q_empty[qb]);
           }
         } else {
-          qk(0, slot, qb);
+          qk(0, slot, qb, qb, true);
           commit(&sm.empty[slot]);
           if (nt > 1) {
-            if (!take(slot)) break;
-            qk(1, slot, qb);
+            if (!take(slot) || !take_bias(1)) break;
+            qk(1, slot, qb, qb, true);
             commit(&sm.empty[slot]);
           }
           if (nt <= 2) commit(&sm.q_empty[qb]);
@@ -359,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ks = 0;
             if (!take(slot)) break;
             if (j == 0 && tail) kvcd::mbar_arrive(&sm.tail_here);
-            if (j + 2 < nt && !take(ks)) break;
+            if (j + 2 < nt && (!take(ks) || !take_bias(s))) break;
             if (j == 0 && tail) {
               ok = wait_or_abort(&sm.cleared, cphase, ns, abort_flag);
               cphase ^= 1;
@@ -368,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pv(s, slot, j < 2, j + 2 >= nt);
             commit(&sm.empty[slot]);
             if (j + 2 < nt) {
-              qk(s, ks, qb);
+              qk(s, ks, qb, qb, true);
               commit(&sm.empty[ks]);
               if (j + 3 == nt) commit(&sm.q_empty[qb]);
             }
@@ -391,13 +449,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cnt = 0;                                       // tiles so far (entry streams: of this warp's stream)
     int loads = 0;                                     // K and V tiles before this piece
     uint32_t tails = 0;                                // cleared so far
+    int li = 0;
     bool ok = true;
     for (kvcd::Walk<kvcd::AttnCost<128>> w(cost, piece); ok && w.next();) {
       const int64_t u = w.item / a.rp;
       const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
       const int total = w.r.len + w.r.n;
-      // the row block's first token
-      const float pos0 = kPos ? a.pos_new[u / a.per_seq] + (float)((int)(w.item - u * a.rp) * a.tpb) : 0.f;
+      const bool with_pos = kMode != kSums || a.slopes;
+      const int t0 = (int)((unsigned)w.item % (unsigned)a.rp) * a.tpb;
+      const float pos0 = with_pos ? a.pos_new[u / a.per_seq] + (float)t0 : 0.f;   // the row block's first token
+      if (kMode != kCapped && a.slopes && warp == 2) { // the row factors of this piece's head
+        const int qb = kRowStreams ? 0 : li & 1, use = kRowStreams ? li : li >> 1;
+        if (use > 0) ok = warp_wait(&sm.q_empty[qb], (uint32_t)((use - 1) & 1), ns, abort_flag);
+        if (!ok) break;
+        for (int r = lane; r < 128; r += 32) {
+          const int g = r / a.tt;
+          ext_row(sm.ext_q[qb], r, g < a.G ? a.slopes[(u % a.H) * a.G + g] / a.scale : 0.f);
+        }
+        kvcd::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.q_full[qb]);
+      }
+      ++li;
       // Warp 3, once its part of the first tile is out of the way: rows past the last entry of
       // the piece's first V tile become zero (P is 0 there, but they may hold anything).
       const int nt = w.te - w.tb, valid = total - w.r.first - (w.te - 1) * 128;
@@ -419,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) kvcd::mbar_arrive(&sm.cleared);
       };
       for (int t = w.te - 1; ok && t >= w.tb; --t) {
-        if (tail && t < w.te - 1) clear_tail();
+        // (the products take a piece's first tile, or two, before they look for V)
+        if (tail && t < w.te - (kRowStreams ? 1 : 2)) clear_tail();
         if (!ok) break;
         const int at = kRowStreams ? cnt++ : w.te - 1 - t;
         if ((at & 1) != (warp & 1)) continue;
@@ -430,14 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           lm[j] = rel[j] = 0.f;
           if (e < total) {
             const int64_t row = rows(e);
-            lm[j] = __ldcg(a.logm + row) * kvcd::kLog2eC;
-            if (kPos) {
+            lm[j] = __ldcg(a.logm + row);
+            if (with_pos) {
               rel[j] = __ldcg(a.pos + row) - pos0;
               low = fminf(low, rel[j]);
             }
           }
         }
-        if (kPos) low = -kvcd::warp_max(-low);
+        if (kMode == kWindow) low = -kvcd::warp_max(-low);
         const int b = kRowStreams ? at % kBias : (warp & 1) * (kBias / 2) + cnt % (kBias / 2);
         const int use = kRowStreams ? at / kBias : cnt / (kBias / 2);
         if (!kRowStreams) ++cnt;
@@ -445,13 +519,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sm.lm[b][lane + 32 * j] = lm[j];
-          if (kPos) sm.rel[b][lane + 32 * j] = rel[j];
+          const int r = lane + 32 * j;
+          if (kMode == kCapped) reinterpret_cast<float*>(sm.ext_k[b])[r] = lm[j] * kvcd::kLog2eC;
+          else ext_key(sm.ext_k[b], r, lm[j] / a.scale, a.slopes ? rel[j] : 0.f);
+          if (kMode != kSums) sm.rel[b][r] = rel[j];
         }
-        const bool any = __any_sync(KVC_FULL_MASK, lm[0] != 0.f || lm[1] != 0.f || lm[2] != 0.f || lm[3] != 0.f);
+        const bool extra = a.slopes || __any_sync(KVC_FULL_MASK, lm[0] != 0.f || lm[1] != 0.f || lm[2] != 0.f || lm[3] != 0.f);
+        if (kMode != kCapped) kvcd::fence_proxy_async_smem();
+        __syncwarp();
         if (lane == 0) {
-          sm.lm_any[b] = any;
-          if (kPos) sm.rel_min[b] = low;
+          sm.extra[b] = extra;
+          if (kMode == kWindow) sm.rel_min[b] = low;
           kvcd::mbar_arrive(&sm.bias_full[b]);
         }
       }
@@ -481,14 +559,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int see = live ? w.r.len + tok + 1 : 0;    // entries this row sees
       RowScore rs;
       rs.scale = a.scale_log2;
-      rs.cap_in = kCap ? a.scale / a.softcap : 0.f;
-      rs.cap_out = kCap ? a.softcap * kvcd::kLog2eC : 0.f;
-      rs.slope = kPos && a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
+      rs.cap_in = kMode == kCapped ? a.scale / a.softcap : 0.f;
+      rs.cap_out = kMode == kCapped ? a.softcap * kvcd::kLog2eC : 0.f;
+      rs.slope = a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
       // positions count from the row block's first token, so that near entries, the ones whose
       // bias is small, lose nothing in slope rel - slope tok
       const float tokf = (float)(tok - (int)(w.item - u * a.rp) * a.tpb);
       rs.shift = rs.slope * tokf;
-      rs.edge = kPos && a.window > 0.f ? tokf - a.window : -INFINITY;
+      rs.edge = a.window > 0.f ? tokf - a.window : -INFINITY;
       const int nt = w.te - w.tb;
       const bool mine = !kRowStreams || st == 0 || t0 < w.r.n;     // this stream has work
       float m = 0.f, l = 0.f;                          // the row's reference, and this half's sum
@@ -498,9 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = kRowStreams ? cnt % kBias : st * (kBias / 2) + cnt % (kBias / 2), tile = w.te - 1 - i;
         const int bias_use = cnt / (kRowStreams ? kBias : kBias / 2);
         ++cnt;
-        warp_join(&sm.bias_full[b], (uint32_t)(bias_use & 1), ns, abort_flag);
+        if (kMode != kSums) warp_join(&sm.bias_full[b], (uint32_t)(bias_use & 1), ns, abort_flag);
         if (!mine) {
-          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          if (kMode != kSums && lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           continue;
         }
         warp_join(&sm.s_full[st], sphase, ns, abort_flag);
@@ -511,19 +589,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           // out too far away (only ever for its first entries, or after a leap), both halves
           // agree on a new m, rescale O and do the tile again.
           const int lim = live ? see - w.r.first - tile * 128 - half * 64 : 64;
-          const float *lm = sm.lm[b] + half * 64, *rel = sm.rel[b] + half * 64;
-          const bool cut = __any_sync(KVC_FULL_MASK, lim < 64 || (kPos && live && !(sm.rel_min[b] > rs.edge)));
+          const float *lm = reinterpret_cast<const float*>(sm.ext_k[b]) + half * 64, *rel = sm.rel[b] + half * 64;
+          const bool cut = __any_sync(KVC_FULL_MASK, lim < 64 || (kMode == kWindow && live && !(sm.rel_min[b] > rs.edge)) ||
+                                                              (kMode == kCapped && a.window > 0.f));
           uint32_t p[32];
           float sum;
-          if (cut) sum = numerators<kCap, kPos, true, true>(rs, ts, lm, rel, m, lim, p);
-          else if (kCap || kPos || sm.lm_any[b]) sum = numerators<kCap, kPos, true, false>(rs, ts, lm, rel, m, lim, p);
-          else sum = numerators<kCap, kPos, kCap || kPos, false>(rs, ts, lm, rel, m, lim, p);
+          if (cut) sum = numerators<kMode, true>(rs, ts, lm, rel, m, lim, p);
+          else sum = numerators<kMode, false>(rs, ts, lm, rel, m, lim, p);
           // the sum tells whether the reference was near enough: above 2^60 (or not a number)
           // it was too low; a row's first sum below 2^-60 may have lost entries
           settled |= l > 0.f;
           const bool far = live && lim > 0 && (!(sum < kFar) || (!settled && !(sum > 1.f / kFar)));
           if (named_or(pair, 64, far)) {
-            const float top = score_max<kCap, kPos>(rs, ts, lm, rel, lim);
+            const float top = score_max<kMode>(rs, ts, lm, rel, lim);
             sm.xtop[st][half][row] = top;
             sm.xl[st][half][row] = l;
             named_or(pair, 64, false);
@@ -547,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (move) m = t;
             settled = any_seen || t > -INFINITY;
-            sum = numerators<kCap, kPos, true, true>(rs, ts, lm, rel, m, lim, p);
+            sum = numerators<kMode, true>(rs, ts, lm, rel, m, lim, p);
             named_or(pair, 64, false);                 // xtop and xl may be written again
           }
-          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          if (kMode != kSums && lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           l += sum;
           if (!kRowStreams && st == 1 && joined) {     // stream 0 has read the results before
             warp_join(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
@@ -560,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tst16(ts + 16, reinterpret_cast<const uint32_t(&)[16]>(p[16]));
           wait_st();
         } else {
-          if (lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
+          if (kMode != kSums && lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);
           if (!kRowStreams && st == 1 && joined) {
             warp_join(&sm.j_free, (joins - 1) & 1, ns, abort_flag);
             joined = false;
@@ -697,26 +775,24 @@ PFN_cuTensorMapEncodeTiled_v12000 enc_fn() {
   return g_enc;
 }
 
-template <int D, bool kRowStreams, bool kCap, bool kPos>
+template <int D, bool kRowStreams, int kMode>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a, int sms,
                    cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(chunk_attn_tc_kernel<D, kRowStreams, kCap, kPos>,
+  cudaError_t e = cudaFuncSetAttribute(chunk_attn_tc_kernel<D, kRowStreams, kMode>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return kvc::chunk_launch(chunk_attn_tc_kernel<D, kRowStreams, kCap, kPos>, dim3(sms), dim3(kThreads), smem, s, km, vm,
+  return kvc::chunk_launch(chunk_attn_tc_kernel<D, kRowStreams, kMode>, dim3(sms), dim3(kThreads), smem, s, km, vm,
                            qm, a);
 }
 
 template <int D, bool kRowStreams>
 cudaError_t launch_mods(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a,
                         int sms, cudaStream_t s) {
-  const bool cap = a.softcap > 0.f, pos = a.slopes || a.window > 0.f;
-  if (cap) return pos ? launch<D, kRowStreams, true, true>(km, vm, qm, a, sms, s)
-                      : launch<D, kRowStreams, true, false>(km, vm, qm, a, sms, s);
-  return pos ? launch<D, kRowStreams, false, true>(km, vm, qm, a, sms, s)
-             : launch<D, kRowStreams, false, false>(km, vm, qm, a, sms, s);
+  if (a.softcap > 0.f) return launch<D, kRowStreams, kCapped>(km, vm, qm, a, sms, s);
+  if (a.window > 0.f) return launch<D, kRowStreams, kWindow>(km, vm, qm, a, sms, s);
+  return launch<D, kRowStreams, kSums>(km, vm, qm, a, sms, s);
 }
 
 }  // namespace

@@ -18,6 +18,11 @@ constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo << 16); }
 constexpr uint32_t kLboK = 1, kLboMN = kHalf >> 4;
 __device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+// K-major without swizzle: 8-row x 16-byte blocks, 128 bytes to the next along K, 256
+// to the next 8 rows (a 16-wide operand of 32 bytes a row).
+constexpr uint32_t kExtHi = (256 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t ext_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((128u >> 4) << 16); }
+__device__ __forceinline__ uint64_t ext_desc(uint32_t lo) { return ((uint64_t)kExtHi << 32) | lo; }
 // bf16 x bf16 -> fp32, M = 128; b_mn: the B operand is MN-major.
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24) | (b_mn ? 1u << 16 : 0u);
