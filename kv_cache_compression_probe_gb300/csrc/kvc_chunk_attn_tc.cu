@@ -75,9 +75,10 @@ struct Ring {
 //   kSums   ln m and the distance bias are part of the product: an extra 16-wide step
 //           of Q K^T adds them (ext_key, ext_row)
 //   kWindow the same, and entries beyond the window are left out
-//   kCapped the tanh comes between the product and them, so they are added per score
-//           from shared memory
-enum Mode { kSums, kWindow, kCapped };
+//   kCapped the tanh comes between the product and ln m, which is added per score from
+//           shared memory
+//   kCapPos the same with a distance bias or a window
+enum Mode { kSums, kWindow, kCapped, kCapPos };
 
 // What a thread needs to turn the products of its row into base-2 scores.
 struct RowScore {
@@ -96,12 +97,17 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
                                         uint64_t base, int lim, float (&f)[4]) {
   uint64_t x0 = base, x1 = base;
   float4 d;
-  if constexpr (kMode == kCapped || (kMode == kWindow && kMask)) d = *reinterpret_cast<const float4*>(rel + c);
-  if constexpr (kMode == kCapped) {
+  if constexpr (kMode == kCapPos || (kMode == kWindow && kMask)) d = *reinterpret_cast<const float4*>(rel + c);
+  if constexpr (kMode >= kCapped) {
     const float4 b = *reinterpret_cast<const float4*>(lm + c);
-    const uint64_t sl = pk(r.slope, r.slope), co = pk(r.cap_out, r.cap_out);
-    x0 = fma2(sl, pk(d.x, d.y), add2(pk(b.x, b.y), base));
-    x1 = fma2(sl, pk(d.z, d.w), add2(pk(b.z, b.w), base));
+    const uint64_t co = pk(r.cap_out, r.cap_out);
+    x0 = add2(pk(b.x, b.y), base);
+    x1 = add2(pk(b.z, b.w), base);
+    if constexpr (kMode == kCapPos) {
+      const uint64_t sl = pk(r.slope, r.slope);
+      x0 = fma2(sl, pk(d.x, d.y), x0);
+      x1 = fma2(sl, pk(d.z, d.w), x1);
+    }
     x0 = fma2(pk(tanh_f(__uint_as_float(s[0]) * r.cap_in), tanh_f(__uint_as_float(s[1]) * r.cap_in)), co, x0);
     x1 = fma2(pk(tanh_f(__uint_as_float(s[2]) * r.cap_in), tanh_f(__uint_as_float(s[3]) * r.cap_in)), co, x1);
   } else {
@@ -112,7 +118,7 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
   upk(x0, f[0], f[1]);
   upk(x1, f[2], f[3]);
   if constexpr (kMask) {
-    if constexpr (kMode != kSums) {
+    if constexpr (kMode == kWindow || kMode == kCapPos) {
       f[0] = d.x > r.edge ? f[0] : -INFINITY;
       f[1] = d.y > r.edge ? f[1] : -INFINITY;
       f[2] = d.z > r.edge ? f[2] : -INFINITY;
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       kvcd::mbar_init(&sm.bias_empty[i], kMode == kSums ? 1 : kRowStreams ? 16 : 8);
     }
     for (int i = 0; i < 2; ++i) {
-      kvcd::mbar_init(&sm.q_full[i], kMode != kCapped && a.slopes ? 2 : 1);
+      kvcd::mbar_init(&sm.q_full[i], kMode < kCapped && a.slopes ? 2 : 1);
       kvcd::mbar_init(&sm.q_empty[i], 1);
       kvcd::mbar_init(&sm.s_full[i], 1);
       kvcd::mbar_init(&sm.p_full[i], 8);
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (kMode != kCapped && !a.slopes) {                 // the same factors for every row
+  if (kMode < kCapped && !a.slopes) {                 // the same factors for every row
     for (int r = tid; r < 256; r += kThreads) ext_row(sm.ext_q[r >> 7], r & 127, 0.f);
     kvcd::fence_proxy_async_smem();
   }
@@ -295,9 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_phase = (q_phase & ~(1u << qb)) | ((uint32_t)(use & 1) << qb);
       }
       // K and V tiles in the order the products take them: K runs one tile (row
-      // streams) or two (entry streams) ahead of V
+      // streams) or two (entry streams) ahead of V.  Rows are looked up a tile ahead.
       constexpr int kAhead = kRowStreams ? 1 : 2;
+      auto first_entry = [&](int t) { return w.r.first + (w.te - 1 - t) * 128; };
+      int next = tile_row(rows, first_entry(0), total, lane), row[3] = {0, 0, 0};
       for (int i = 0; ok && i < nt + kAhead; ++i) {
+        row[2] = row[1];
+        row[1] = row[0];
+        row[0] = next;
+        if (i + 1 < nt) next = tile_row(rows, first_entry(i + 1), total, lane);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {                  // v = 0: V of tile i - kAhead; 1: K of tile i
           const int t = v ? i : i - kAhead;
@@ -305,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&sm.empty[ring.slot], (uint32_t)(ring.phase ^ 1), ns, abort_flag);
           if (!ok) break;
           if (!a.withhold) {
-            copy_tile<D>(a, rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]), w.r.first + (w.te - 1 - t) * 128, total,
-                         &sm.full[ring.slot], lane);
+            copy_tile<D>(rows, v ? &kmap : &vmap, kvcd::smem_u32(sm.ring[ring.slot]),
+                         tile_boxes(rows, first_entry(t), total), row[v ? 0 : kAhead], &sm.full[ring.slot], lane);
             issued |= 1u << ring.slot;
             issued_phase = (issued_phase & ~(1u << ring.slot)) | ((uint32_t)ring.phase << ring.slot);
           }
@@ -335,12 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t eq_lo = ext_lo(kvcd::smem_u32(sm.ext_q[0])), ek_lo = ext_lo(kvcd::smem_u32(sm.ext_k[0]));
       int bcnt[2] = {0, 0};                            // bias tiles so far (row streams: [0])
       int bslot = 0;
+      bool extra = false;
       auto take_bias = [&](int s) {                    // the tile's extra columns
-        if (kMode == kCapped) return ok;
+        if (kMode >= kCapped) return ok;
         const int c = bcnt[kRowStreams ? 0 : s]++;
         bslot = kRowStreams ? c % kBias : s * (kBias / 2) + c % (kBias / 2);
         const int use = kRowStreams ? c / kBias : c / (kBias / 2);
         ok = ok && wait_or_abort(&sm.bias_full[bslot], (uint32_t)(use & 1), ns, abort_flag);
+        extra = sm.extra[bslot] != 0;
         return ok;
       };
       auto qk = [&](int s, int slot, int qtile, int eq, bool last) {   // S_s = Q K^T (+ the extra step)
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
           mma_ss(d, desc(qb + at), desc(kb + at), idesc(128, false), k > 0);
         }
-        if (kMode != kCapped && sm.extra[bslot])
+        if (kMode < kCapped && extra)
           mma_ss(d, ext_desc(eq_lo + eq * 256), ext_desc(ek_lo + bslot * 256), idesc(128, false), 1);
         commit(&sm.s_full[s]);
         if (kMode == kSums && last) commit(&sm.bias_empty[bslot]);
@@ -455,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t u = w.item / a.rp;
       const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
       const int total = w.r.len + w.r.n;
-      const bool with_pos = kMode != kSums || a.slopes;
+      const bool with_pos = kMode == kWindow || kMode == kCapPos || a.slopes;
       const int t0 = (int)((unsigned)w.item % (unsigned)a.rp) * a.tpb;
       const float pos0 = with_pos ? a.pos_new[u / a.per_seq] + (float)t0 : 0.f;   // the row block's first token
-      if (kMode != kCapped && a.slopes && warp == 2) { // the row factors of this piece's head
+      if (kMode < kCapped && a.slopes && warp == 2) { // the row factors of this piece's head
         const int qb = kRowStreams ? 0 : li & 1, use = kRowStreams ? li : li >> 1;
         if (use > 0) ok = warp_wait(&sm.q_empty[qb], (uint32_t)((use - 1) & 1), ns, abort_flag);
         if (!ok) break;
@@ -520,12 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int r = lane + 32 * j;
-          if (kMode == kCapped) reinterpret_cast<float*>(sm.ext_k[b])[r] = lm[j] * kvcd::kLog2eC;
+          if (kMode >= kCapped) reinterpret_cast<float*>(sm.ext_k[b])[r] = lm[j] * kvcd::kLog2eC;
           else ext_key(sm.ext_k[b], r, lm[j] / a.scale, a.slopes ? rel[j] : 0.f);
-          if (kMode != kSums) sm.rel[b][r] = rel[j];
+          if (kMode == kWindow || kMode == kCapPos) sm.rel[b][r] = rel[j];
         }
         const bool extra = a.slopes || __any_sync(KVC_FULL_MASK, lm[0] != 0.f || lm[1] != 0.f || lm[2] != 0.f || lm[3] != 0.f);
-        if (kMode != kCapped) kvcd::fence_proxy_async_smem();
+        if (kMode < kCapped) kvcd::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           sm.extra[b] = extra;
@@ -559,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int see = live ? w.r.len + tok + 1 : 0;    // entries this row sees
       RowScore rs;
       rs.scale = a.scale_log2;
-      rs.cap_in = kMode == kCapped ? a.scale / a.softcap : 0.f;
-      rs.cap_out = kMode == kCapped ? a.softcap * kvcd::kLog2eC : 0.f;
+      rs.cap_in = kMode >= kCapped ? a.scale / a.softcap : 0.f;
+      rs.cap_out = kMode >= kCapped ? a.softcap * kvcd::kLog2eC : 0.f;
       rs.slope = a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
       // positions count from the row block's first token, so that near entries, the ones whose
       // bias is small, lose nothing in slope rel - slope tok
@@ -591,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int lim = live ? see - w.r.first - tile * 128 - half * 64 : 64;
           const float *lm = reinterpret_cast<const float*>(sm.ext_k[b]) + half * 64, *rel = sm.rel[b] + half * 64;
           const bool cut = __any_sync(KVC_FULL_MASK, lim < 64 || (kMode == kWindow && live && !(sm.rel_min[b] > rs.edge)) ||
-                                                              (kMode == kCapped && a.window > 0.f));
+                                                              (kMode == kCapPos && a.window > 0.f));
           uint32_t p[32];
           float sum;
           if (cut) sum = numerators<kMode, true>(rs, ts, lm, rel, m, lim, p);
@@ -790,7 +804,9 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorM
 template <int D, bool kRowStreams>
 cudaError_t launch_mods(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a,
                         int sms, cudaStream_t s) {
-  if (a.softcap > 0.f) return launch<D, kRowStreams, kCapped>(km, vm, qm, a, sms, s);
+  if (a.softcap > 0.f)
+    return a.slopes || a.window > 0.f ? launch<D, kRowStreams, kCapPos>(km, vm, qm, a, sms, s)
+                                      : launch<D, kRowStreams, kCapped>(km, vm, qm, a, sms, s);
   if (a.window > 0.f) return launch<D, kRowStreams, kWindow>(km, vm, qm, a, sms, s);
   return launch<D, kRowStreams, kSums>(km, vm, qm, a, sms, s);
 }

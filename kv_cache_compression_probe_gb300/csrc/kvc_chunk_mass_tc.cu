@@ -140,11 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
       const kvcd::RowMap rows = kvcd::row_map(a, w.u, w.r.off);
+      const int e0 = w.r.first + w.tile * 128, boxes = tile_boxes(rows, e0, w.r.len + w.r.n);
+      const int row = tile_row(rows, e0, w.r.len + w.r.n, lane);
       const int ks = nk % kK;
       if (nk >= kK) ok = warp_wait(&sm.k_empty[ks], (uint32_t)((nk / kK - 1) & 1), ns, abort_flag);
       if (!ok) break;
       if (!a.withhold) {
-        copy_tile<D>(a, rows, &kmap, kvcd::smem_u32(sm.k[ks]), w.r.first + w.tile * 128, w.r.len + w.r.n, &sm.k_full[ks], lane);
+        copy_tile<D>(rows, &kmap, kvcd::smem_u32(sm.k[ks]), boxes, row, &sm.k_full[ks], lane);
         k_loads = nk + 1;
       }
       for (int rt = w.tb; rt < w.te; ++rt, ++nq) {

@@ -192,32 +192,28 @@ __device__ __forceinline__ bool named_or(int id, int n, bool v) {
   return r != 0;
 }
 
-// Copies of one 128-entry tile of K or V, issued by a whole warp: entries from
-// e0 on, of `total` in all, into `dst` (64-feature blocks kHalf apart),
-// completing on `bar`.  Contiguous: one box per block, rows past the last
-// entry included.  Paged: one box per page (or part of one); boxes with no entry
-// are not copied.  The caller's lane 0 has not yet announced the bytes.
+// Copies of one 128-entry tile of K or V, entries from e0 on, of `total` in all, by
+// a whole warp.  Contiguous: one box per 64-feature block, rows past the last entry
+// included.  Paged: one box per page (or part of one) and block; boxes with no entry
+// are not copied.  tile_row is what a lane has to look up first (the row of its box),
+// so that a caller can do it ahead.
+__device__ __forceinline__ int tile_boxes(const kvcd::RowMap& rows, int e0, int total) {
+  const int shift = min(rows.shift, 7);
+  return rows.table ? (min(128, total - e0) + (1 << shift) - 1) >> shift : 1;
+}
+__device__ __forceinline__ int tile_row(const kvcd::RowMap& rows, int e0, int total, int lane) {
+  return lane < tile_boxes(rows, e0, total) ? (int)rows(e0 + (lane << min(rows.shift, 7))) : 0;
+}
 template <int D>
-__device__ __forceinline__ void copy_tile(const kvc::ChunkArgs& a, const kvcd::RowMap& rows, const CUtensorMap* map,
-                                          uint32_t dst, int e0, int total, uint64_t* bar, int lane) {
+__device__ __forceinline__ void copy_tile(const kvcd::RowMap& rows, const CUtensorMap* map, uint32_t dst, int boxes,
+                                          int row, uint64_t* bar, int lane) {
   constexpr int kBlocks = D / 64;
-  if (!rows.table) {
-    if (lane == 0) {
-      kvcd::mbar_arrive_expect_tx(bar, kBlocks * kHalf);
-#pragma unroll
-      for (int h = 0; h < kBlocks; ++h) tma2d(dst + h * kHalf, map, h * 64, (int)(rows.off + e0), bar);
-    }
-    return;
-  }
-  const int box = min(1 << rows.shift, 128);
-  const int n = (min(128, total - e0) + box - 1) / box;          // boxes with entries
-  int y = 0;
-  if (lane < n) y = (int)rows(e0 + lane * box);
-  if (lane == 0) kvcd::mbar_arrive_expect_tx(bar, n * box * 128 * kBlocks);
+  const uint32_t bytes = rows.table ? 128u << min(rows.shift, 7) : kHalf;   // of one box
+  if (lane == 0) kvcd::mbar_arrive_expect_tx(bar, boxes * bytes * kBlocks);
   __syncwarp();
-  if (lane < n)
+  if (lane < boxes)
 #pragma unroll
-    for (int h = 0; h < kBlocks; ++h) tma2d(dst + h * kHalf + lane * box * 128, map, h * 64, y, bar);
+    for (int h = 0; h < kBlocks; ++h) tma2d(dst + h * kHalf + lane * bytes, map, h * 64, row, bar);
 }
 
 }  // namespace kvctc
