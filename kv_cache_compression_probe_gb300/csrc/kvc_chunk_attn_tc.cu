@@ -335,11 +335,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       int li = 0;
       uint32_t pphase = 0, cphase = 0;                 // bit s: parity of stream s's next P; of the cleared tails
       bool ok = true;
-      auto take = [&](int& slot) {                     // the next K or V tile
-        ok = ok && wait_or_abort(&sm.full[ring.slot], (uint32_t)ring.phase, ns, abort_flag);
+      // The next K or V tile.  `ahead`: it has been seen to be there (look_ahead, called while
+      // the tensor cores are busy, saves the wait's latency when they are not).
+      bool ahead[2] = {false, false};
+      auto take = [&](int& slot, bool& seen) {
+        ok = ok && (seen || wait_or_abort(&sm.full[ring.slot], (uint32_t)ring.phase, ns, abort_flag));
+        seen = false;
         slot = ring.slot;
         ring.step<kStages>();
         return ok;
+      };
+      auto look_ahead = [&](bool two) {
+        ahead[0] = mbar_test(&sm.full[ring.slot], (uint32_t)ring.phase);
+        if (two) {
+          Ring r2 = ring;
+          r2.step<kStages>();
+          ahead[1] = mbar_test(&sm.full[r2.slot], (uint32_t)r2.phase);
+        }
       };
       const uint32_t q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK), k_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboK);
       const uint32_t v_lo = desc_lo(kvcd::smem_u32(sm.ring[0]), kLboMN);
@@ -347,15 +359,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t eq_lo = ext_lo(kvcd::smem_u32(sm.ext_q[0])), ek_lo = ext_lo(kvcd::smem_u32(sm.ext_k[0]));
       int bcnt[2] = {0, 0};                            // bias tiles so far (row streams: [0])
       int bslot = 0;
-      bool extra = false;
+      bool extra = false, bias_seen = false;
+      auto bias_at = [&](int s, int& b, uint32_t& parity) {
+        const int c = bcnt[kRowStreams ? 0 : s];
+        b = kRowStreams ? c % kBias : s * (kBias / 2) + c % (kBias / 2);
+        parity = (uint32_t)((kRowStreams ? c / kBias : c / (kBias / 2)) & 1);
+      };
       auto take_bias = [&](int s) {                    // the tile's extra columns
         if (kMode >= kCapped) return ok;
-        const int c = bcnt[kRowStreams ? 0 : s]++;
-        bslot = kRowStreams ? c % kBias : s * (kBias / 2) + c % (kBias / 2);
-        const int use = kRowStreams ? c / kBias : c / (kBias / 2);
-        ok = ok && wait_or_abort(&sm.bias_full[bslot], (uint32_t)(use & 1), ns, abort_flag);
+        uint32_t parity;
+        bias_at(s, bslot, parity);
+        ++bcnt[kRowStreams ? 0 : s];
+        ok = ok && (bias_seen || wait_or_abort(&sm.bias_full[bslot], parity, ns, abort_flag));
+        bias_seen = false;
         extra = sm.extra[bslot] != 0;
         return ok;
+      };
+      auto look_bias = [&](int s) {
+        if (kMode >= kCapped) return;
+        int b;
+        uint32_t parity;
+        bias_at(s, b, parity);
+        bias_seen = mbar_test(&sm.bias_full[b], parity);
       };
       auto qk = [&](int s, int slot, int qtile, int eq, bool last) {   // S_s = Q K^T (+ the extra step)
         const uint32_t qb = q_lo + qtile * kTile16, kb = k_lo + slot * kTile16, d = tmem + s * 128;
@@ -392,16 +417,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool tail = w.r.len + w.r.n - w.r.first < w.te * 128;
         ok = wait_or_abort(&sm.q_full[qb], (uint32_t)(use & 1), ns, abort_flag);
         int slot = 0;
-        if (!take(slot) || !take_bias(0)) break;
+        bool none = false;
+        if (!take(slot, none) || !take_bias(0)) break;
         if constexpr (kRowStreams) {
           for (int s = 0; s < ns2; ++s) qk(s, slot, s, 0, s + 1 == ns2);
           commit(&sm.empty[slot]);
           if (nt == 1) commit(&sm.q_empty[qb]);
           for (int i = 0; ok && i < nt; ++i) {
             int vs = 0, ks = 0;
-            if (!take(vs)) break;
+            if (!take(vs, ahead[0])) break;
             if (i == 0 && tail) kvcd::mbar_arrive(&sm.tail_here);
-            if (i + 1 < nt && (!take(ks) || !take_bias(0))) break;
+            if (i + 1 < nt && (!take(ks, ahead[1]) || !take_bias(0))) break;
             if (i == 0 && tail) {
               ok = wait_or_abort(&sm.cleared, cphase, ns, abort_flag);
               cphase ^= 1;
@@ -410,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!wait_p(s)) break;
               pv(s, vs, i == 0, i + 1 == nt);
               if (s + 1 == ns2) commit(&sm.empty[vs]);
+              if (i + 1 < nt && s == 0) look_ahead(i + 2 < nt);
+              if (i + 2 < nt && s == 1) look_bias(0);
               if (i + 1 < nt) {
                 qk(s, ks, s, 0, s + 1 == ns2);
                 if (s + 1 == ns2) commit(&sm.empty[ks]);
@@ -421,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           qk(0, slot, qb, qb, true);
           commit(&sm.empty[slot]);
           if (nt > 1) {
-            if (!take(slot) || !take_bias(1)) break;
+            if (!take(slot, none) || !take_bias(1)) break;
             qk(1, slot, qb, qb, true);
             commit(&sm.empty[slot]);
           }
@@ -429,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; ok && j < nt; ++j) {
             const int s = j & 1;
             int ks = 0;
-            if (!take(slot)) break;
+            if (!take(slot, none)) break;
             if (j == 0 && tail) kvcd::mbar_arrive(&sm.tail_here);
-            if (j + 2 < nt && (!take(ks) || !take_bias(s))) break;
+            if (j + 2 < nt && (!take(ks, none) || !take_bias(s))) break;
             if (j == 0 && tail) {
               ok = wait_or_abort(&sm.cleared, cphase, ns, abort_flag);
               cphase ^= 1;

@@ -155,6 +155,17 @@ __device__ __forceinline__ float tanh_f(float y) {
   return z < 0.5f ? p : fmaf(-2.f, r, 1.f);
 }
 
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(kvcd::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for a phase; gives up when another role has, or after `ns` nanoseconds.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
   if (kvcd::mbar_try_wait(bar, parity)) return true;
