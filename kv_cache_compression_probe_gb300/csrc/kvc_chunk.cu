@@ -559,7 +559,7 @@ cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
   a.tpb = a.tt;
   a.rp = (a.T + a.tpb - 1) / a.tpb;
   const size_t smem = sizeof(SimtSmem<D, MR>);
-  cudaError_t e = cudaFuncSetAttribute(chunk_attn_simt_kernel<T, D, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = kvc::chunk_allow_smem<chunk_attn_simt_kernel<T, D, MR>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms;
   e = kvc::chunk_launch(chunk_attn_simt_kernel<T, D, MR>, dim3(grid), dim3(kSimtThreads), smem, s, a);
@@ -605,7 +605,7 @@ cudaError_t launch_mass(ChunkArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   a.tt = std::min(64 / a.G, a.T);
   const size_t smem = sizeof(SimtSmem<D, 64>);
-  e = cudaFuncSetAttribute(chunk_mass_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = kvc::chunk_allow_smem<chunk_mass_simt_kernel<T, D>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms;
   e = kvc::chunk_launch(chunk_mass_simt_kernel<T, D>, dim3(grid), dim3(kSimtThreads), smem, s, a);

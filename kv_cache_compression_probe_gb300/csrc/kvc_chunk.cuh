@@ -11,6 +11,7 @@
 // and an item that crosses a cut leaves one partial result per CTA, which a
 // combine kernel joins in CTA order (so results do not depend on timing).
 #pragma once
+#include <atomic>
 #include <utility>
 
 #include "kvc_common.cuh"
@@ -298,6 +299,20 @@ cudaError_t chunk_launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Allows a kernel its dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t chunk_allow_smem(size_t bytes) {
+  static std::atomic<uint32_t> done[8];                // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 256) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  const uint32_t bit = 1u << (dev & 31);
+  if (done[dev >> 5].load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev >> 5].fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Argument checks shared by the calls (p, c and the page table), and the fields

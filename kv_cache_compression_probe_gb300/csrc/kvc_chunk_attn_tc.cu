@@ -821,8 +821,7 @@ template <int D, bool kRowStreams, int kMode>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a, int sms,
                    cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(chunk_attn_tc_kernel<D, kRowStreams, kMode>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = kvc::chunk_allow_smem<chunk_attn_tc_kernel<D, kRowStreams, kMode>>(smem);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
   return kvc::chunk_launch(chunk_attn_tc_kernel<D, kRowStreams, kMode>, dim3(sms), dim3(kThreads), smem, s, km, vm,

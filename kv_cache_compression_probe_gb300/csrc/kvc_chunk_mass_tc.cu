@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool kCap, bool kPos>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& qm, const ChunkArgs& a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(MassSmem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(chunk_mass_tc_kernel<D, kCap, kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = kvc::chunk_allow_smem<chunk_mass_tc_kernel<D, kCap, kPos>>(smem);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
   return kvc::chunk_launch(chunk_mass_tc_kernel<D, kCap, kPos>, dim3(sms), dim3(kThreads), smem, s, km, qm, a);

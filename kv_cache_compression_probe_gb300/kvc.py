@@ -136,6 +136,32 @@ def _ptr(t):
     return c_void_p(t.data_ptr())
 
 
+def _ptrs(*tensors):
+    """Addresses of the tensors of one call: contiguous and on the current CUDA
+    device (the one whose kernels the call launches); None stays None."""
+    dev = torch._C._cuda_getDevice()
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        try:
+            good = t.get_device() == dev and t.is_contiguous()
+        except AttributeError:
+            raise TypeError("expected a torch.Tensor") from None
+        if not good:
+            raise ValueError("tensors passed to libkvc must be contiguous and on the current CUDA device")
+        out.append(t.data_ptr())
+    return out
+
+
+def _raw_stream(stream):
+    """The stream's handle; torch's current stream of the current device by default."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _stream(stream):
     if stream is None:
         return c_void_p(torch.cuda.current_stream().cuda_stream)
@@ -337,23 +363,18 @@ def kvc_chunk_attn(p, c, q, k_new, v_new, pos_new, Kp, Vp, logm, pos, len_lh, ca
                    lse, len_out, workspace, stream=None):
     """Attention of a chunk of new tokens over the packed cache (contiguous rows
     or pages); lse, len_out and, with pages, off_lh may be None."""
-    w, wb = _ws(workspace)
-    _check(lib().kvc_chunk_attn(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(k_new),
-                                _ptr(v_new), _ptr(pos_new), _ptr(Kp), _ptr(Vp), _ptr(logm),
-                                _ptr(pos), _ptr(len_lh), _ptr(cap_lh), _ptr(off_lh), _ptr(out),
-                                _ptr(lse), _ptr(len_out), w, wb, _stream(stream)),
-           "kvc_chunk_attn")
+    _check(lib().kvc_chunk_attn(p, c, *_ptrs(q, k_new, v_new, pos_new, Kp, Vp, logm, pos, len_lh,
+                                             cap_lh, off_lh, out, lse, len_out, workspace),
+                                workspace.nbytes, _raw_stream(stream)), "kvc_chunk_attn")
 
 
 def kvc_chunk_mass(p, c, q, Kp, logm, pos, pos_new, len_lh, off_lh, lse, decay, mass, workspace,
                    stream=None):
     """mass = decay * mass + the attention weight every entry received from the
     chunk (len_lh: the lengths before it)."""
-    w, wb = _ws(workspace)
-    _check(lib().kvc_chunk_mass(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(Kp), _ptr(logm),
-                                _ptr(pos), _ptr(pos_new), _ptr(len_lh), _ptr(off_lh), _ptr(lse),
-                                float(decay), _ptr(mass), w, wb, _stream(stream)),
-           "kvc_chunk_mass")
+    a = _ptrs(q, Kp, logm, pos, pos_new, len_lh, off_lh, lse, mass, workspace)
+    _check(lib().kvc_chunk_mass(p, c, *a[:8], decay, a[8], a[9], workspace.nbytes,
+                                _raw_stream(stream)), "kvc_chunk_mass")
 
 
 def kvc_mass_evict_workspace_bytes(p, c, max_len: int) -> int:
@@ -363,11 +384,9 @@ def kvc_mass_evict_workspace_bytes(p, c, max_len: int) -> int:
 def kvc_mass_evict(p, c, mass, keep_lh, recent, pos_next, Kp, Vp, logm, pos, len_lh, off_lh,
                    len_out, max_len, workspace, stream=None):
     """Per-(b, l, h) eviction down to keep_lh entries by mass, in place."""
-    w, wb = _ws(workspace)
-    _check(lib().kvc_mass_evict(ctypes.byref(p), ctypes.byref(c), _ptr(mass), _ptr(keep_lh),
-                                int(recent), _ptr(pos_next), _ptr(Kp), _ptr(Vp), _ptr(logm),
-                                _ptr(pos), _ptr(len_lh), _ptr(off_lh), _ptr(len_out),
-                                int(max_len), w, wb, _stream(stream)), "kvc_mass_evict")
+    a = _ptrs(mass, keep_lh, pos_next, Kp, Vp, logm, pos, len_lh, off_lh, len_out, workspace)
+    _check(lib().kvc_mass_evict(p, c, a[0], a[1], recent, *a[2:10], max_len, a[10], workspace.nbytes,
+                                _raw_stream(stream)), "kvc_mass_evict")
 
 
 def workspace(which: int, p: kvc_params, device="cuda", zero=False) -> torch.Tensor:
