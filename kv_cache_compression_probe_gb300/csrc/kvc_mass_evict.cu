@@ -1,12 +1,18 @@
 // kvc_mass_evict: per-(b,l,h) eviction by accumulated attention mass.
 //
-// One CTA per (b,l,h) finds the smallest key that stays (a radix select over
-// the 32-bit order code of the mass; protected entries have the largest code)
-// and lists the moves: evicted entries below the new length ("holes") take the
-// staying entries at or above it, both in index order.  A second kernel moves
-// the rows.  Moving only those rows, instead of compacting the cache, keeps the
-// traffic at twice the moved rows; the row order stops following the positions,
-// so protection goes by position and not by index.
+// Plan: a CTA per (b,l,h), or a cluster of 8 when there are few and long ones,
+// reads the masses and positions once, keeps a 32-bit order code per entry in shared
+// memory (protected entries have the largest code) and finds the smallest code that
+// stays by a radix select of 11 bits at a time; the CTAs of a cluster add their
+// histograms through distributed shared memory.  Then it lists the moves: evicted
+// entries below the new length ("holes") take the staying entries at or above it,
+// both in index order.  Bound by latency: one read of 8 bytes an entry, then a dozen
+// block-wide steps on shared memory.
+// Move: a second kernel copies the rows.  Moving only those, instead of compacting
+// the cache, keeps the traffic at twice the moved rows; the row order stops
+// following the positions, so protection goes by position and not by index.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kvc_chunk.cuh"
@@ -16,7 +22,12 @@ namespace {
 
 using kvc::ChunkArgs;
 
+namespace cg = cooperative_groups;
+
 constexpr int kPlanThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kCluster = 8;            // CTAs of a cluster
+constexpr int kMaxKeys = 50000;        // order codes of one CTA in shared memory (200 KB)
 constexpr int kMoveRows = 32;          // row moves per CTA and turn
 
 struct EvictArgs {
@@ -64,34 +75,51 @@ __device__ __forceinline__ int block_prefix(int v, int* s_warp, int& excl) {
   return s_warp[31];
 }
 
-__global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(EvictArgs ea) {
+struct PlanSmem {
+  uint32_t hist[2][kBins];             // passes alternate, so one barrier a pass is enough
+  int warp[32];
+  int ties, holes, movers, safe;       // this CTA's counts, read by the cluster
+  int ok;
+  uint32_t prefix;
+  int rem;
+};
+
+// kKeys: the codes are in shared memory; else every pass forms them from global memory.
+template <bool kKeys>
+__global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_constant__ EvictArgs ea) {
   const ChunkArgs& a = ea.a;
-  __shared__ uint32_t hist[256];
-  __shared__ int s_warp[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_rem, s_ok;
+  extern __shared__ __align__(16) unsigned char plan_raw[];
+  PlanSmem& sm = *reinterpret_cast<PlanSmem*>(plan_raw);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(plan_raw + sizeof(PlanSmem));
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), nr = (int)cluster.num_blocks();
+  auto sync = [&]() {
+    if (nr > 1) cluster.sync();
+    else __syncthreads();
+  };
   kvcd::pdl_trigger();
   kvcd::pdl_wait();
-  const int64_t u = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t u = blockIdx.x / nr;
   const int64_t gu = kvcd::unit_global(a, u);
-  const int tid = threadIdx.x;
-  const int len = a.len_lh[gu];
+  const int len = a.len_lh[gu], keep = ea.keep_lh[gu];
   const int64_t off = a.page_table ? 0 : a.off_lh[gu];
-  if (tid == 0) s_ok = len >= 0 && len <= ea.max_len && len <= a.packed_rows && off >= 0 &&
-                       (a.page_table || off + len <= a.packed_rows);
-  __syncthreads();
-  bool ok = s_ok != 0;
+  const float safe_from = ea.pos_next[u / a.per_seq] - ea.recent;
+  bool ok = len >= 0 && len <= ea.max_len && len <= a.packed_rows && off >= 0 &&
+            (a.page_table || off + len <= a.packed_rows);
   if (ok && a.page_table) {
     const int need = (int)(((int64_t)len + (1 << a.page_shift) - 1) >> a.page_shift);
     ok = need <= a.max_pages;
     if (ok) {
       const int32_t* tab = a.page_table + gu * a.max_pages;
       const int64_t pages = a.packed_rows >> a.page_shift;
-      for (int i = tid; i < need; i += kPlanThreads) ok &= tab[i] >= 0 && tab[i] < pages;
+      for (int i = tid; i < need; i += kPlanThreads) ok &= __ldg(tab + i) >= 0 && __ldg(tab + i) < pages;
     }
   }
-  if (!__syncthreads_and(ok)) {
-    if (tid == 0) {
+  if (tid == 0) sm.safe = sm.ties = sm.holes = sm.movers = 0;
+  for (int i = tid; i < kBins; i += kPlanThreads) sm.hist[0][i] = 0;
+  if (!__syncthreads_and(ok)) {                        // every CTA of the cluster sees the same
+    if (tid == 0 && rank == 0) {
       kvcd::record_error(a.err, KVC_EDEVICE);
       ea.n_moves[u] = 0;
       a.len_out[gu] = len;
@@ -99,87 +127,114 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(EvictArgs ea) {
     return;
   }
   const kvcd::RowMap rows = kvcd::row_map(a, u, off);
-  const float safe = ea.pos_next[u / a.per_seq] - ea.recent;
-  auto code = [&](int e) {
-    const int64_t row = rows(e);
-    return mass_code(a.mass[row], a.pos[row] >= safe);
+  const int share = (len + nr - 1) / nr;
+  const int lo = min(len, rank * share), n = min(len, lo + share) - lo;   // this CTA's entries
+  auto form = [&](int i) {
+    const int64_t row = rows(lo + i);
+    return mass_code(a.mass[row], a.pos[row] >= safe_from);
   };
-  // every thread owns a contiguous range of entries, so index order is thread order
-  const int per = (len + kPlanThreads - 1) / kPlanThreads;
-  const int i0 = min(len, tid * per), i1 = min(len, i0 + per);
-  int mine = 0, excl;
-  for (int e = i0; e < i1; ++e) mine += code(e) == 0xffffffffu;
-  const int n_protected = block_prefix(mine, s_warp, excl);
-  const int B = min(len, max(max(0, ea.keep_lh[gu]), n_protected));
-  if (tid == 0) { s_prefix = 0; s_rem = B; }
-  // the B-th largest code, 8 bits at a time (not needed when all or none stay)
-  for (int shift = 24; shift >= 0 && B > 0 && B < len; shift -= 8) {
-    for (int i = tid; i < 256; i += kPlanThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t pre = s_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int e = tid; e < len; e += kPlanThreads) {
-      const uint32_t k = code(e);
-      if ((k & mask) == pre) atomicAdd(&hist[(k >> shift) & 255], 1u);
-    }
-    __syncthreads();
-    if (tid < 32) {                                    // lane: digits 255-8l .. 248-8l, descending
-      int cnt[8], sum = 0;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) { cnt[x] = (int)hist[255 - 8 * tid - x]; sum += cnt[x]; }
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(KVC_FULL_MASK, incl, o);
-        if (tid >= o) incl += v;
-      }
-      const int rem0 = s_rem;
-      const unsigned hit = __ballot_sync(KVC_FULL_MASK, incl >= rem0);
-      if (tid == __ffs(hit) - 1) {
-        int rem = rem0 - (incl - sum), x = 0;
-        while (x < 7 && cnt[x] < rem) rem -= cnt[x++];
-        s_prefix = pre | ((uint32_t)(255 - 8 * tid - x) << shift);
-        s_rem = rem;
-      }
-    }
-    __syncthreads();
+  auto code = [&](int i) { return kKeys ? keys[i] : form(i); };
+  int mine = 0;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const uint32_t k = form(i);
+    if (kKeys) keys[i] = k;
+    mine += k == 0xffffffffu;
   }
-  __syncthreads();
-  const uint32_t cut = s_prefix;
-  const int rem = s_rem;                               // how many of the entries at the cut stay
+  mine = __reduce_add_sync(KVC_FULL_MASK, mine);
+  if (lane == 0 && mine) atomicAdd(&sm.safe, mine);
+  sync();
+  auto total = [&](int PlanSmem::*m) {                 // a count over the cluster
+    int t = 0;
+    for (int r = 0; r < nr; ++r) t += cluster.map_shared_rank(&sm, r)->*m;
+    return t;
+  };
+  auto before = [&](int PlanSmem::*m) {                // and over the CTAs before this one
+    int t = 0;
+    for (int r = 0; r < rank; ++r) t += cluster.map_shared_rank(&sm, r)->*m;
+    return t;
+  };
+  const int B = min(len, max(max(0, keep), total(&PlanSmem::safe)));
   const bool all = B >= len, none = B == 0;
-  int ties = 0;
-  if (!all && !none)
-    for (int e = i0; e < i1; ++e) ties += code(e) == cut;
-  int tie0;
-  block_prefix(ties, s_warp, tie0);
-  // holes (evicted, below B) and movers (staying, at or above B) before this thread's range
-  int nh = 0, nm = 0, tie = tie0;
-  auto stays = [&](int e) {
+  uint32_t cut = 0;
+  int rem = B;                                         // how many of the entries at the cut stay
+  // the B-th largest code, 11 or 10 bits at a time (not needed when all or none stay)
+  for (int pass = 0; pass < 3 && !all && !none; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 1 ? 11 : 10));
+    uint32_t* hist = sm.hist[pass & 1];
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const uint32_t k = code(i);
+      if ((k & mask) == cut) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+    }
+    sync();
+    for (int i = tid; i < kBins; i += kPlanThreads) sm.hist[(pass + 1) & 1][i] = 0;
+    // thread t holds bins 2t from the top and the next one down
+    const int b0 = bins - 1 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    if (b0 > 0)
+      for (int r = 0; r < nr; ++r) {
+        const uint32_t* h = cluster.map_shared_rank(hist, r);
+        c0 += (int)h[b0];
+        c1 += (int)h[b0 - 1];
+      }
+    int excl;
+    block_prefix(c0 + c1, sm.warp, excl);
+    if (excl < rem && rem <= excl + c0 + c1) {         // one thread: the counts reach rem here
+      const bool second = rem > excl + c0;
+      sm.prefix = cut | ((uint32_t)(second ? b0 - 1 : b0) << shift);
+      sm.rem = rem - excl - (second ? c0 : 0);
+    }
+    __syncthreads();
+    cut = sm.prefix;
+    rem = sm.rem;
+  }
+  // contiguous ranges per thread (an odd count keeps them off each other's banks), so that
+  // thread order is index order
+  const int per = ((n + kPlanThreads - 1) / kPlanThreads) | 1;
+  const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  int tie0 = 0;
+  if (!all && !none) {
+    int ties = 0;
+    for (int i = i0; i < i1; ++i) ties += code(i) == cut;
+    const int t = block_prefix(ties, sm.warp, tie0);
+    if (tid == 0) sm.ties = t;
+    sync();
+    tie0 += before(&PlanSmem::ties);
+  }
+  int tie = tie0;
+  auto stays = [&](int i) {
     if (all || none) return all;
-    const uint32_t k = code(e);
+    const uint32_t k = code(i);
     return k > cut || (k == cut && tie++ < rem);
   };
-  for (int e = i0; e < i1; ++e) {
-    const bool s = stays(e);
-    if (e < B) nh += !s; else nm += s;
+  int nh = 0, nm = 0, h0, m0;
+  for (int i = i0; i < i1; ++i) {
+    const bool s = stays(i);
+    if (lo + i < B) nh += !s;
+    else nm += s;
   }
-  int h0, m0;
-  const int holes = block_prefix(nh, s_warp, h0);
-  block_prefix(nm, s_warp, m0);
+  const int th = block_prefix(nh, sm.warp, h0), tm = block_prefix(nm, sm.warp, m0);
+  if (tid == 0) { sm.holes = th; sm.movers = tm; }
+  sync();
+  h0 += before(&PlanSmem::holes);
+  m0 += before(&PlanSmem::movers);
   int2* mv = ea.moves + u * ea.cols;
   tie = tie0;
-  for (int e = i0; e < i1; ++e) {
-    const bool s = stays(e);
-    if (e < B && !s) mv[h0++].x = e;
-    else if (e >= B && s) mv[m0++].y = e;
-  }
-  if (tid == 0) {
-    ea.n_moves[u] = holes;
+  if (nh + nm > 0)
+    for (int i = i0; i < i1; ++i) {
+      const bool s = stays(i);
+      if (lo + i < B && !s) mv[h0++].x = lo + i;
+      else if (lo + i >= B && s) mv[m0++].y = lo + i;
+    }
+  if (rank == 0 && tid == 0) {
+    ea.n_moves[u] = total(&PlanSmem::holes);
     a.len_out[gu] = B;
   }
+  if (nr > 1) cluster.sync();                          // nobody leaves while its counts are read
 }
 
-__global__ void __launch_bounds__(256) mass_move_kernel(EvictArgs ea) {
+__global__ void __launch_bounds__(256) mass_move_kernel(const __grid_constant__ EvictArgs ea) {
   const ChunkArgs& a = ea.a;
   kvcd::pdl_trigger();
   kvcd::pdl_wait();
@@ -257,7 +312,30 @@ extern "C" int kvc_mass_evict(const kvc_params* p, const kvc_chunk* c, float* ma
   ea.cols = max_len / 2 + 1;
   ea.vec = p->d * (p->dtype == KVC_BF16 ? 2 : 4) / 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = kvc::chunk_launch(mass_plan_kernel, dim3((unsigned)ea.a.units), dim3(kPlanThreads), 0, s, ea);
+  // A cluster of 8 per (b,l,h) when that still leaves an SM to each CTA and there are entries
+  // enough to share.
+  const int nr = ea.a.units * kCluster <= sms && max_len > 4096 ? kCluster : 1;
+  const int64_t share = ((int64_t)max_len + nr - 1) / nr;
+  const bool in_smem = share <= kMaxKeys;
+  const size_t smem = sizeof(PlanSmem) + (in_smem ? share * sizeof(uint32_t) : 0);
+  cudaError_t e = in_smem ? kvc::chunk_allow_smem<mass_plan_kernel<true>>(sizeof(PlanSmem) + kMaxKeys * sizeof(uint32_t))
+                          : cudaSuccess;
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ea.a.units * nr));
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = nr;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = in_smem ? cudaLaunchKernelEx(&cfg, mass_plan_kernel<true>, ea) : cudaLaunchKernelEx(&cfg, mass_plan_kernel<false>, ea);
+  }
   if (e != cudaSuccess) return kvc::cuda_status(e);
   kvc::count_launch(2);
   // at most max_len / 2 moves per unit, usually few: about 8 CTAs per SM stride over them

@@ -64,6 +64,9 @@ CASES = {
     "all protected": (dict(lens=[700, 30], n_new=[0], H=2), 0.1, 100000),
     "layer range": (dict(lens=[5, 70, 200, 130, 64, 9, 1, 300], n_new=[0, 0], B=2, L=4, layers=(1, 3)), 0.5, 8),
     "long": (dict(lens=[70001, 40], n_new=[0], H=2), 0.4, 1000),
+    "long, spread over a cluster": (dict(lens=[70001, 5000, 4097, 8191, 3, 0, 20000, 12345], n_new=[0], H=8, d=64), 0.4, 1000),
+    "longer than shared memory": (dict(lens=[410003, 1000], n_new=[0], H=2, d=64), 0.7, 100),
+    "one unit per CTA, long": (dict(lens=[60001] + [10] * 23, n_new=[0], H=24, d=64), 0.3, 100),
     "many units": (dict(lens=np.arange(600) * 7 % 301, n_new=[0, 0], B=2, L=20, H=15), 0.7, 20),
 }
 
