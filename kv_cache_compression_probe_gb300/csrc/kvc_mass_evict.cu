@@ -1,6 +1,6 @@
 // kvc_mass_evict: per-(b,l,h) eviction by accumulated attention mass.
 //
-// Plan: a CTA per (b,l,h), or a cluster of 8 when there are few and long ones,
+// Plan: a CTA per (b,l,h), or a cluster of up to 8 when there are few and long ones,
 // reads the masses and positions once, keeps a 32-bit order code per entry in shared
 // memory (protected entries have the largest code) and finds the smallest code that
 // stays by a radix select of 11 bits at a time; the CTAs of a cluster add their
@@ -24,9 +24,9 @@ using kvc::ChunkArgs;
 
 namespace cg = cooperative_groups;
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;     // 256 (b,l,h) of 4200 entries: 256, 512, 1024 threads took 28, 20, 27 us
 constexpr int kBins = 2048;
-constexpr int kCluster = 8;            // CTAs of a cluster
+constexpr int kCluster = 8;            // CTAs of a cluster at most
 constexpr int kMaxKeys = 50000;        // order codes of one CTA in shared memory (200 KB)
 constexpr int kMoveRows = 32;          // row moves per CTA and turn
 
@@ -62,7 +62,7 @@ __device__ __forceinline__ int block_prefix(int v, int* s_warp, int& excl) {
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    int w = s_warp[lane];
+    int w = lane < kPlanThreads / 32 ? s_warp[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(KVC_FULL_MASK, w, o);
@@ -169,21 +169,31 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_co
     }
     sync();
     for (int i = tid; i < kBins; i += kPlanThreads) sm.hist[(pass + 1) & 1][i] = 0;
-    // thread t holds bins 2t from the top and the next one down
-    const int b0 = bins - 1 - 2 * tid;
-    int c0 = 0, c1 = 0;
+    // a thread holds kOwn bins, from the top down
+    constexpr int kOwn = kBins / kPlanThreads;
+    const int b0 = bins - 1 - kOwn * tid;
+    int c[kOwn], sum = 0;
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) c[x] = 0;
     if (b0 > 0)
       for (int r = 0; r < nr; ++r) {
-        const uint32_t* h = cluster.map_shared_rank(hist, r);
-        c0 += (int)h[b0];
-        c1 += (int)h[b0 - 1];
+        const uint32_t* h = nr > 1 ? cluster.map_shared_rank(hist, r) : hist;
+#pragma unroll
+        for (int x = 0; x < kOwn; ++x) c[x] += (int)h[b0 - x];
       }
-    int excl;
-    block_prefix(c0 + c1, sm.warp, excl);
-    if (excl < rem && rem <= excl + c0 + c1) {         // one thread: the counts reach rem here
-      const bool second = rem > excl + c0;
-      sm.prefix = cut | ((uint32_t)(second ? b0 - 1 : b0) << shift);
-      sm.rem = rem - excl - (second ? c0 : 0);
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) sum += c[x];
+    int at;
+    block_prefix(sum, sm.warp, at);
+    if (at < rem && rem <= at + sum) {                 // one thread: the counts reach rem here
+#pragma unroll
+      for (int x = 0; x < kOwn; ++x) {
+        if (at < rem && rem <= at + c[x]) {
+          sm.prefix = cut | ((uint32_t)(b0 - x) << shift);
+          sm.rem = rem - at;
+        }
+        at += c[x];
+      }
     }
     __syncthreads();
     cut = sm.prefix;
@@ -312,9 +322,10 @@ extern "C" int kvc_mass_evict(const kvc_params* p, const kvc_chunk* c, float* ma
   ea.cols = max_len / 2 + 1;
   ea.vec = p->d * (p->dtype == KVC_BF16 ? 2 : 4) / 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // A cluster of 8 per (b,l,h) when that still leaves an SM to each CTA and there are entries
-  // enough to share.
-  const int nr = ea.a.units * kCluster <= sms && max_len > 4096 ? kCluster : 1;
+  // A cluster of up to 8 per (b,l,h) while that leaves an SM to each CTA and more than 1024
+  // entries a share.
+  int nr = 1;
+  while (nr < kCluster && ea.a.units * nr * 2 <= sms && max_len / (nr * 2) > 1024) nr *= 2;
   const int64_t share = ((int64_t)max_len + nr - 1) / nr;
   const bool in_smem = share <= kMaxKeys;
   const size_t smem = sizeof(PlanSmem) + (in_smem ? share * sizeof(uint32_t) : 0);
