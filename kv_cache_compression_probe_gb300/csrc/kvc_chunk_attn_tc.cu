@@ -185,20 +185,7 @@ __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const
 // The extra step.  Its 16 columns hold, per entry, ln m and the position split into
 // bf16 parts (8 bits each, so three parts are the fp32 value) over sqrt(d)'s inverse,
 // and per row the factors: 1 for the parts of ln m, the parts of the head's slope for
-// those of the position.  Rows of 8 x 16 bytes (no swizzle), 256 bytes per 8 rows.
-__device__ __forceinline__ void split3(float x, uint32_t (&p)[3]) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(x);
-    p[i] = __bfloat16_as_ushort(h);
-    x = isinf(x) ? 0.f : x - __bfloat162float(h);
-  }
-}
-__device__ __forceinline__ void ext_store(unsigned char* tile, int row, const uint4& c0, const uint4& c1) {
-  unsigned char* p = tile + (row >> 3) * 256 + (row & 7) * 16;
-  *reinterpret_cast<uint4*>(p) = c0;
-  *reinterpret_cast<uint4*>(p + 128) = c1;
-}
+// those of the position.
 // Columns: l0 l1 l2 | r0 r1 r2 r0 r1 | r0 r2 r1
 __device__ __forceinline__ void ext_key(unsigned char* tile, int row, float lm, float rel) {
   uint32_t l[3], r[3];

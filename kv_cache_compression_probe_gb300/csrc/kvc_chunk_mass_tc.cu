@@ -8,9 +8,12 @@
 // in turn, each with its own TMEM buffer, which hides the latency of a step's
 // chain; a key tile with several steps is joined through shared memory in group
 // order.  Few rows: HBM is the bound (K is read once); many rows: the exponential
-// unit (one exponential a score), just above the tensor cores' own time.
-// Warps: 0 copies (TMA), 1 issues the products, 2 and 3 fetch the row statistics
-// of alternate steps, 4..19 are the four groups.
+// unit (one exponential a score), just above the tensor cores' own time.  Then the
+// product also carries -lse and ln m (an extra 16-wide step), so that a score costs a
+// multiplication, an exponential and an addition: values read per score from shared
+// memory would cost its full width.
+// Warps: 0 copies (TMA; and the entries' ln m), 1 issues the products, 2 and 3 fetch
+// the row statistics of alternate steps, 4..19 are the four groups.
 #include <algorithm>
 
 #include "kvc_chunk_tc.cuh"
@@ -25,16 +28,24 @@ constexpr int kGroups = 4;
 constexpr int kThreads = 128 + kGroups * 128;
 constexpr int kCols = 512;             // a 128-column buffer per group
 
+// What a kernel adds to the products: kPlain and the rest from shared memory, kExtra
+// (several row tiles, no cap, bias or window) in the product itself.
+enum Mode { kPlain, kExtra, kCapped, kPos, kCapPos };
+
+// Key and query tiles in flight: keys stream past one row tile, or stay while row
+// tiles stream past them.
+constexpr int kTiles = 6;
+__device__ __forceinline__ int key_slots(bool several) { return several ? 2 : 4; }
+
 template <int D>
 struct MassSmem {
-  static constexpr int kK = 4, kQ = 2; // key and query tiles in flight
   static constexpr uint32_t kTileBytes = 128 * D * 2;
-  alignas(1024) unsigned char k[kK][kTileBytes];
-  alignas(1024) unsigned char q[kQ][kTileBytes];
+  alignas(1024) unsigned char tile[kTiles][kTileBytes];          // key slots, then query slots
+  alignas(16) unsigned char ext_k[2][4096], ext_q[kGroups][4096];
   alignas(16) float nl[kGroups][128];                  // -lse of a row, -inf for rows that add nothing
   alignas(16) float slope[kGroups][128], tok[kGroups][128];
   float hand[kGroups][128];
-  uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ];
+  uint64_t k_full[4], k_empty[4], q_full[4], q_empty[4];
   uint64_t r_full[kGroups], r_empty[kGroups], s_full[kGroups], s_empty[kGroups];
   uint64_t hand_full, hand_empty, drain;
   kvcd::LocateSmem loc;
@@ -89,19 +100,48 @@ __device__ __forceinline__ void add16(const ChunkArgs& a, const uint32_t (&s)[16
   }
 }
 
-template <int D, bool kCap, bool kPos>
+// Sum over 16 columns whose products are the whole score.  kEdge as in add16.
+template <bool kEdge>
+__device__ __forceinline__ void sum16(const ChunkArgs& a, const uint32_t (&s)[16], const float* tok, float first_tok,
+                                      uint64_t& sum0, uint64_t& sum1) {
+  const uint64_t sc = pk(a.scale_log2, a.scale_log2);
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    float f[4];
+    upk(mul2(pk(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc), f[0], f[1]);
+    upk(mul2(pk(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc), f[2], f[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = kvcd::ex2(f[e]);
+    if constexpr (kEdge) {
+      const float4 t = *reinterpret_cast<const float4*>(tok + c);
+      f[0] = t.x >= first_tok ? f[0] : 0.f;
+      f[1] = t.y >= first_tok ? f[1] : 0.f;
+      f[2] = t.z >= first_tok ? f[2] : 0.f;
+      f[3] = t.w >= first_tok ? f[3] : 0.f;
+    }
+    sum0 = add2(sum0, pk(f[0], f[1]));
+    sum1 = add2(sum1, pk(f[2], f[3]));
+  }
+}
+
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_mass_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ ChunkArgs a) {
   using Smem = MassSmem<D>;
-  constexpr int kBlocks = D / 64, kK = Smem::kK, kQ = Smem::kQ;
+  constexpr int kBlocks = D / 64;
+  constexpr bool kCap = kMode == kCapped || kMode == kCapPos, kBias = kMode == kPos || kMode == kCapPos;
   extern __shared__ __align__(1024) unsigned char mass_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(mass_raw) + 1023) & ~uintptr_t(1023));
   kvcd::pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < kK; ++i) { kvcd::mbar_init(&sm.k_full[i], 1); kvcd::mbar_init(&sm.k_empty[i], 1); }
-    for (int i = 0; i < kQ; ++i) { kvcd::mbar_init(&sm.q_full[i], 1); kvcd::mbar_init(&sm.q_empty[i], 1); }
+    for (int i = 0; i < 4; ++i) {
+      kvcd::mbar_init(&sm.k_full[i], kMode == kExtra ? 2 : 1);    // copy and extra columns
+      kvcd::mbar_init(&sm.k_empty[i], 1);
+      kvcd::mbar_init(&sm.q_full[i], 1);
+      kvcd::mbar_init(&sm.q_empty[i], 1);
+    }
     for (int i = 0; i < kGroups; ++i) {
       kvcd::mbar_init(&sm.r_full[i], 1);
       kvcd::mbar_init(&sm.r_empty[i], 4);
@@ -131,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &sm.abort;
   const uint64_t ns = a.wait_ns;
   const int used = a.G * a.tt, cols = (used + 15) & ~15;         // rows of a row tile; columns of S^T
+  const int kK = key_slots(a.T > a.tt), kQ = min(4, kTiles - kK);
   int k_loads = 0, q_loads = 0;                        // copies issued (for the drain after a give-up)
 
   if (warp == 0) {
@@ -138,6 +179,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_all();
     int nk = 0, nq = 0;
     bool ok = true;
+    float lm[4] = {0.f, 0.f, 0.f, 0.f};
+    auto fetch_lm = [&](const kvcd::MassWalk<128>& w) {
+      const kvcd::RowMap rows = kvcd::row_map(a, w.u, w.r.off);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = w.r.first + w.tile * 128 + lane + 32 * j;
+        lm[j] = e < w.r.len + w.r.n ? __ldcg(a.logm + rows(e)) : 0.f;
+      }
+    };
     for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
       const kvcd::RowMap rows = kvcd::row_map(a, w.u, w.r.off);
       const int e0 = w.r.first + w.tile * 128, boxes = tile_boxes(rows, e0, w.r.len + w.r.n);
@@ -146,83 +196,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk >= kK) ok = warp_wait(&sm.k_empty[ks], (uint32_t)((nk / kK - 1) & 1), ns, abort_flag);
       if (!ok) break;
       if (!a.withhold) {
-        copy_tile<D>(rows, &kmap, kvcd::smem_u32(sm.k[ks]), boxes, row, &sm.k_full[ks], lane);
+        copy_tile<D>(rows, &kmap, kvcd::smem_u32(sm.tile[ks]), boxes, row, &sm.k_full[ks], lane);
         k_loads = nk + 1;
+      }
+      if (kMode == kExtra) {                           // the entries' columns: 1 1 1 l0 l1 l2
+        if (nk == 0) fetch_lm(w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t l[3];
+          split3(lm[j] / a.scale, l);
+          ext_store(sm.ext_k[ks], lane + 32 * j, make_uint4(0x3f803f80, 0x3f80 | l[0] << 16, l[1] | l[2] << 16, 0),
+                    make_uint4(0, 0, 0, 0));
+        }
+        kvcd::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) kvcd::mbar_arrive(&sm.k_full[ks]);
+        kvcd::MassWalk<128> ahead = w;                 // the next item's, on their way meanwhile
+        if (ahead.next()) fetch_lm(ahead);
       }
       for (int rt = w.tb; rt < w.te; ++rt, ++nq) {
         const int qs = nq % kQ;
-        if (nq >= kQ) ok = warp_wait(&sm.q_empty[qs], (uint32_t)((nq / kQ - 1) & 1), ns, abort_flag);
+        // (kExtra: kQ = kGroups, so a step's query slot is free when its products are there)
+        if (nq >= kQ)
+          ok = warp_wait(kMode == kExtra ? &sm.s_full[qs] : &sm.q_empty[qs], (uint32_t)((nq / kQ - 1) & 1), ns, abort_flag);
         if (!ok) break;
         if (lane == 0 && !a.withhold) {
           kvcd::mbar_arrive_expect_tx(&sm.q_full[qs], (uint32_t)(used * 128 * kBlocks));
 #pragma unroll
           for (int h = 0; h < kBlocks; ++h)
-            tma3d(kvcd::smem_u32(sm.q[qs]) + h * kHalf, &qmap, h * 64, rt * a.tt, (int)(w.u * a.G), &sm.q_full[qs]);
+            tma3d(kvcd::smem_u32(sm.tile[kK + qs]) + h * kHalf, &qmap, h * 64, rt * a.tt, (int)(w.u * a.G), &sm.q_full[qs]);
         }
         if (!a.withhold) q_loads = nq + 1;
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ products (one lane issues)
-    int nk = 0, nq = 0;
-    bool ok = true;
-    const uint32_t k_lo = desc_lo(kvcd::smem_u32(sm.k[0]), kLboK), q_lo = desc_lo(kvcd::smem_u32(sm.q[0]), kLboK);
-    const uint32_t id = idesc(cols, false);
-    for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
-      const int ks = nk % kK;
-      ok = warp_wait(&sm.k_full[ks], (uint32_t)((nk / kK) & 1), ns, abort_flag);
-      for (int rt = w.tb; ok && rt < w.te; ++rt, ++nq) {
-        const int qs = nq % kQ, sb = nq % kGroups;
-        ok = warp_wait(&sm.q_full[qs], (uint32_t)((nq / kQ) & 1), ns, abort_flag);
-        if (ok && nq >= kGroups)
-          ok = warp_wait(&sm.s_empty[sb], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
-        if (!ok) break;
-        fence_after();
-        const uint32_t kb = k_lo + ks * (Smem::kTileBytes >> 4), qb = q_lo + qs * (Smem::kTileBytes >> 4);
-        const uint32_t d = tmem + sb * 128;
-        if (elect_one()) {
+    // ------------------------------------------------------------ products
+    // One thread.  kExtra: it waits for one barrier a step, r_full: the warp that writes the
+    // row's extra columns has waited for the query tile, and for the group that read the
+    // buffer last.  (Three waits and three commits a step took 1300 cycles against the
+    // products' 580.)
+    if (elect_one()) {
+      int nk = 0, nq = 0;
+      bool ok = true;
+      const uint32_t lo = desc_lo(kvcd::smem_u32(sm.tile[0]), kLboK), id = idesc(cols, false);
+      const uint32_t ek_lo = ext_lo(kvcd::smem_u32(sm.ext_k[0])), eq_lo = ext_lo(kvcd::smem_u32(sm.ext_q[0]));
+      for (kvcd::MassWalk<128> w(cost, piece); ok && w.next(); ++nk) {
+        const int ks = nk % kK;
+        ok = wait_or_abort(&sm.k_full[ks], (uint32_t)((nk / kK) & 1), ns, abort_flag);
+        for (int rt = w.tb; ok && rt < w.te; ++rt, ++nq) {
+          const int qs = nq % kQ, sb = nq % kGroups;
+          if (kMode == kExtra) {
+            ok = wait_or_abort(&sm.r_full[sb], (uint32_t)((nq / kGroups) & 1), ns, abort_flag);
+          } else {
+            ok = wait_or_abort(&sm.q_full[qs], (uint32_t)((nq / kQ) & 1), ns, abort_flag);
+            if (ok && nq >= kGroups)
+              ok = wait_or_abort(&sm.s_empty[sb], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
+          }
+          if (!ok) break;
+          fence_after();
+          const uint32_t kb = lo + ks * (Smem::kTileBytes >> 4), qb = lo + (kK + qs) * (Smem::kTileBytes >> 4);
+          const uint32_t d = tmem + sb * 128;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
             mma_ss(d, desc(kb + at), desc(qb + at), id, k > 0);
           }
+          if (kMode == kExtra) mma_ss(d, ext_desc(ek_lo + ks * 256), ext_desc(eq_lo + sb * 256), id, 1);
           commit(&sm.s_full[sb]);
-          commit(&sm.q_empty[qs]);
+          if (kMode != kExtra) commit(&sm.q_empty[qs]);
           if (rt + 1 == w.te) commit(&sm.k_empty[ks]);
         }
-        __syncwarp();
       }
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------ row statistics
     int nq = 0;
     bool ok = true;
+    int g[4], dt[4];                           // this lane's rows: head and token in the tile
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      g[j] = (lane + 32 * j) / a.tt;
+      dt[j] = (lane + 32 * j) % a.tt;
+    }
     for (kvcd::MassWalk<128> w(cost, piece); ok && w.next();) {
+      // this warp's steps: every other one; their LSEs are fetched a step ahead
+      auto lse_at = [&](int j, int rt) {
+        const int t = rt * a.tt + dt[j];
+        return g[j] < a.G && t < w.r.n ? __ldcg(a.lse + (w.u * a.G + g[j]) * a.T + t) : -INFINITY;
+      };
+      float next[4], slope[4];
+      const int rt0 = w.tb + ((nq & 1) != (warp & 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        next[j] = rt0 < w.te ? lse_at(j, rt0) : 0.f;
+        slope[j] = kBias && a.slopes && g[j] < a.G ? a.slopes[(w.u % a.H) * a.G + g[j]] * kvcd::kLog2eC : 0.f;
+      }
       for (int rt = w.tb; ok && rt < w.te; ++rt, ++nq) {
         if ((nq & 1) != (warp & 1)) continue;
         float nl[4], sl[4], tk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int r = lane + 32 * j, g = r / a.tt, t = rt * a.tt + r % a.tt;
-          nl[j] = -INFINITY;
-          sl[j] = 0.f;
-          tk[j] = (float)(r % a.tt);                   // tokens and positions count from the row tile's first
-          if (r < used && t < w.r.n) {
-            const float lse = __ldcg(a.lse + (w.u * a.G + g) * a.T + t);
-            if (kPos && a.slopes) sl[j] = a.slopes[(w.u % a.H) * a.G + g] * kvcd::kLog2eC;
-            if (lse != -INFINITY) nl[j] = -lse - sl[j] * tk[j];
-          }
+          const float lse = next[j];
+          tk[j] = (float)dt[j];                        // tokens and positions count from the row tile's first
+          sl[j] = slope[j];
+          nl[j] = lse != -INFINITY ? -lse - sl[j] * tk[j] : -INFINITY;
+          if (rt + 2 < w.te) next[j] = lse_at(j, rt + 2);
         }
         const int b = nq % kGroups;
+        uint4 ext[4];                                  // n0 n1 n2 1 1 1 (-lse over the scale)
+        if (kMode == kExtra) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t n[3];
+            split3(nl[j] / a.scale_log2, n);
+            ext[j] = make_uint4(n[0] | n[1] << 16, n[2] | 0x3f800000, 0x3f803f80, 0);
+            if (rt * a.tt + dt[j] >= w.r.n) tk[j] = -INFINITY;   // a row past the tokens sees nothing
+          }
+          ok = warp_wait(&sm.q_full[nq % kQ], (uint32_t)((nq / kQ) & 1), ns, abort_flag);
+          if (!ok) break;
+        }
         if (nq >= kGroups) ok = warp_wait(&sm.r_empty[b], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int r = lane + 32 * j;
-          sm.nl[b][r] = nl[j];
           sm.tok[b][r] = tk[j];
-          if (kPos) sm.slope[b][r] = sl[j];
+          if (kMode == kExtra) {
+            ext_store(sm.ext_q[b], r, ext[j], make_uint4(0, 0, 0, 0));
+          } else {
+            sm.nl[b][r] = nl[j];
+            if (kBias) sm.slope[b][r] = sl[j];
+          }
         }
+        if (kMode == kExtra) kvcd::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) kvcd::mbar_arrive(&sm.r_full[b]);
       }
@@ -245,40 +352,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine < steps || taker == grp) {
         if (e < total) {
           row = kvcd::row_map(a, w.u, w.r.off)(e);
-          lm = __ldcg(a.logm + row) * kvcd::kLog2eC;
-          if (kPos) rel = __ldcg(a.pos + row) - a.pos_new[w.u / a.per_seq];
+          if (kMode != kExtra) lm = __ldcg(a.logm + row) * kvcd::kLog2eC;
+          if (kBias) rel = __ldcg(a.pos + row) - a.pos_new[w.u / a.per_seq];
           if (taker == grp && e < w.r.len) old = a.mass[row];
         }
         uint64_t sum0 = 0, sum1 = 0;
         for (int i = mine; i < steps; i += kGroups) {
           const int t0 = (w.tb + i) * a.tt;
-          warp_wait(&sm.r_full[grp], phase, ns, abort_flag);
-          warp_wait(&sm.s_full[grp], phase, ns, abort_flag);
+          if (kMode != kExtra) warp_join(&sm.r_full[grp], phase, ns, abort_flag);
+          warp_join(&sm.s_full[grp], phase, ns, abort_flag);
           phase ^= 1;
           fence_after();
           const float first_tok = (float)(e - w.r.len - t0);  // tokens from this one on see the entry
           const float rel_t = rel - (float)t0;
           const bool edge = used < 128 || t0 + a.tt > w.r.n || e0 + 127 > w.r.len + t0 ||
-                            (kPos && a.window > 0.f && __any_sync(KVC_FULL_MASK, e < total && !(rel_t > (float)a.tt - a.window)));
-          for (int c = 0; c < cols; c += 32) {         // the second half's columns may be stale: cols is a
-            uint32_t s0[16], s1[16];                   // multiple of 16 and they are skipped below
-            tld16(ts + c, s0);
-            if (c + 16 < cols) tld16(ts + c + 16, s1);
-            wait_ld(s0);
-            wait_ld(s1);
-            const float *nl = sm.nl[grp] + c, *sl = sm.slope[grp] + c, *tk = sm.tok[grp] + c;
-            if (edge) {
-              add16<kCap, kPos, true>(a, s0, nl, sl, tk, lm, rel_t, first_tok, sum0, sum1);
-              if (c + 16 < cols) add16<kCap, kPos, true>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel_t, first_tok, sum0, sum1);
-            } else {
-              add16<kCap, kPos, false>(a, s0, nl, sl, tk, lm, rel_t, first_tok, sum0, sum1);
-              add16<kCap, kPos, false>(a, s1, nl + 16, sl + 16, tk + 16, lm, rel_t, first_tok, sum0, sum1);
+                            (kBias && a.window > 0.f && __any_sync(KVC_FULL_MASK, e < total && !(rel_t > (float)a.tt - a.window)));
+          if constexpr (kMode == kExtra) {             // 128 columns
+            uint32_t s[2][16];
+            tld16(ts, s[0]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              wait_ld(s[q & 1]);
+              if (q < 7) tld16(ts + (q + 1) * 16, s[(q + 1) & 1]);
+              if (edge) sum16<true>(a, s[q & 1], sm.tok[grp] + q * 16, first_tok, sum0, sum1);
+              else sum16<false>(a, s[q & 1], nullptr, 0.f, sum0, sum1);
+            }
+          } else {
+            for (int c = 0; c < cols; c += 16) {
+              uint32_t s[16];
+              tld16(ts + c, s);
+              wait_ld(s);
+              const float *nl = sm.nl[grp] + c, *sl = sm.slope[grp] + c, *tk = sm.tok[grp] + c;
+              if (edge) add16<kCap, kBias, true>(a, s, nl, sl, tk, lm, rel_t, first_tok, sum0, sum1);
+              else add16<kCap, kBias, false>(a, s, nl, sl, tk, lm, rel_t, first_tok, sum0, sum1);
             }
           }
           fence_before();
           __syncwarp();
           if (lane == 0) {
-            kvcd::mbar_arrive(&sm.s_empty[grp]);
+            if (kMode != kExtra) kvcd::mbar_arrive(&sm.s_empty[grp]);
             kvcd::mbar_arrive(&sm.r_empty[grp]);
           }
         }
@@ -330,20 +442,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_flag && tid == 0) kvcd::record_error(a.err, KVC_ETIMEOUT);
 }
 
-template <int D, bool kCap, bool kPos>
+template <int D, int kMode>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& qm, const ChunkArgs& a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(MassSmem<D>) + 1024;
-  cudaError_t e = kvc::chunk_allow_smem<chunk_mass_tc_kernel<D, kCap, kPos>>(smem);
+  cudaError_t e = kvc::chunk_allow_smem<chunk_mass_tc_kernel<D, kMode>>(smem);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return kvc::chunk_launch(chunk_mass_tc_kernel<D, kCap, kPos>, dim3(sms), dim3(kThreads), smem, s, km, qm, a);
+  return kvc::chunk_launch(chunk_mass_tc_kernel<D, kMode>, dim3(sms), dim3(kThreads), smem, s, km, qm, a);
 }
 
 template <int D>
 cudaError_t launch_mods(const CUtensorMap& km, const CUtensorMap& qm, const ChunkArgs& a, int sms, cudaStream_t s) {
   const bool cap = a.softcap > 0.f, pos = a.slopes || a.window > 0.f;
-  if (cap) return pos ? launch<D, true, true>(km, qm, a, sms, s) : launch<D, true, false>(km, qm, a, sms, s);
-  return pos ? launch<D, false, true>(km, qm, a, sms, s) : launch<D, false, false>(km, qm, a, sms, s);
+  if (cap) return pos ? launch<D, kCapPos>(km, qm, a, sms, s) : launch<D, kCapped>(km, qm, a, sms, s);
+  if (pos) return launch<D, kPos>(km, qm, a, sms, s);
+  return a.T > a.tt ? launch<D, kExtra>(km, qm, a, sms, s) : launch<D, kPlain>(km, qm, a, sms, s);
 }
 
 }  // namespace

@@ -133,6 +133,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // (bf16(lo), bf16(hi)) in one register, each rounded to nearest.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
@@ -166,6 +171,22 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// An extra 16-wide step of a product carries per-row and per-entry terms of the scores:
+// the fp32 value x as the sum of three bf16 parts (8 bits each), times 1.  ext_store
+// writes a row's 16 columns (8-row blocks of 16-byte pieces, as ext_desc says).
+__device__ __forceinline__ void split3(float x, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    p[i] = __bfloat16_as_ushort(h);
+    x = isinf(x) ? 0.f : x - __bfloat162float(h);
+  }
+}
+__device__ __forceinline__ void ext_store(unsigned char* tile, int row, const uint4& c0, const uint4& c1) {
+  unsigned char* p = tile + (row >> 3) * 256 + (row & 7) * 16;
+  *reinterpret_cast<uint4*>(p) = c0;
+  *reinterpret_cast<uint4*>(p + 128) = c1;
+}
 // Waits for a phase; gives up when another role has, or after `ns` nanoseconds.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
   if (kvcd::mbar_try_wait(bar, parity)) return true;
