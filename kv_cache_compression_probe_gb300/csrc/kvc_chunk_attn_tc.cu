@@ -82,12 +82,12 @@ enum Mode { kSums, kWindow, kCapped, kCapPos };
 
 // What a thread needs to turn the products of its row into base-2 scores.
 struct RowScore {
-  float scale, cap_in, cap_out;        // s log2 e = scale product, or cap_out tanh(cap_in product)
+  float scale, cap_in, cap_out;        // s log2 e = scale product, or cap_out tanh(y), 2^(cap_in product) = e^2y
   float slope, shift;                  // distance bias slope rel - shift
   float edge;                          // window: sees rel > edge
 };
 
-// Scores (plus `base`, both halves of a pair) of four entries c .. c + 3 of a tile.
+// Scores (plus `base`, both halves of a pair; capped: base includes cap_out) of four entries c .. c + 3 of a tile.
 // kMask: the row sees only the first `lim` entries, and of these those beyond the
 // window's edge.  (A broadcast from shared memory costs its full width, 512 bytes a
 // warp for four floats: per-entry values read here bounded the kernel, which is why
@@ -100,7 +100,9 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
   if constexpr (kMode == kCapPos || (kMode == kWindow && kMask)) d = *reinterpret_cast<const float4*>(rel + c);
   if constexpr (kMode >= kCapped) {
     const float4 b = *reinterpret_cast<const float4*>(lm + c);
-    const uint64_t co = pk(r.cap_out, r.cap_out);
+    // cap tanh(y) = cap - 2 cap / (1 + e^2y), off by up to 2^-23 of the cap (the log-sum-exp
+    // and the rounded numerators lose nothing by that)
+    const uint64_t ci = pk(r.cap_in, r.cap_in), m2 = pk(-2.f * r.cap_out, -2.f * r.cap_out), one = pk(1.f, 1.f);
     x0 = add2(pk(b.x, b.y), base);
     x1 = add2(pk(b.z, b.w), base);
     if constexpr (kMode == kCapPos) {
@@ -108,8 +110,13 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
       x0 = fma2(sl, pk(d.x, d.y), x0);
       x1 = fma2(sl, pk(d.z, d.w), x1);
     }
-    x0 = fma2(pk(tanh_f(__uint_as_float(s[0]) * r.cap_in), tanh_f(__uint_as_float(s[1]) * r.cap_in)), co, x0);
-    x1 = fma2(pk(tanh_f(__uint_as_float(s[2]) * r.cap_in), tanh_f(__uint_as_float(s[3]) * r.cap_in)), co, x1);
+    float e0, e1, e2, e3;
+    upk(mul2(pk(__uint_as_float(s[0]), __uint_as_float(s[1])), ci), e0, e1);
+    upk(mul2(pk(__uint_as_float(s[2]), __uint_as_float(s[3])), ci), e2, e3);
+    upk(add2(pk(kvcd::ex2(e0), kvcd::ex2(e1)), one), e0, e1);
+    upk(add2(pk(kvcd::ex2(e2), kvcd::ex2(e3)), one), e2, e3);
+    x0 = fma2(pk(rcp(e0), rcp(e1)), m2, x0);
+    x1 = fma2(pk(rcp(e2), rcp(e3)), m2, x1);
   } else {
     const uint64_t sc = pk(r.scale, r.scale);
     x0 = fma2(pk(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, x0);
@@ -135,7 +142,7 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 template <int kMode, bool kMask>
 __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,
                                             float base, int lim, uint32_t (&p)[32]) {
-  const float sh = -(base + r.shift);
+  const float sh = r.cap_out - (base + r.shift);
   const uint64_t mb = pk(sh, sh);
   uint64_t s0 = 0, s1 = 0;
   uint32_t s[2][16];
@@ -165,7 +172,7 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
 template <int kMode>
 __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const float* lm, const float* rel, int lim) {
   float t = -INFINITY;
-  const uint64_t mb = pk(-r.shift, -r.shift);
+  const uint64_t mb = pk(r.cap_out - r.shift, r.cap_out - r.shift);
 #pragma unroll 1
   for (int q = 0; q < 64; q += 16) {
     uint32_t s[16];
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int see = live ? w.r.len + tok + 1 : 0;    // entries this row sees
       RowScore rs;
       rs.scale = a.scale_log2;
-      rs.cap_in = kMode >= kCapped ? a.scale / a.softcap : 0.f;
+      rs.cap_in = kMode >= kCapped ? 2.f * a.scale_log2 / a.softcap : 0.f;
       rs.cap_out = kMode >= kCapped ? a.softcap * kvcd::kLog2eC : 0.f;
       rs.slope = a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
       // positions count from the row block's first token, so that near entries, the ones whose

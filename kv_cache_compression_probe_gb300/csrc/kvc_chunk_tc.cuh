@@ -145,6 +145,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // tanh(y) in fp32: y times a degree-5 polynomial in y^2 below y^2 = 1/2 (least
 // squares of the relative error over that range; off by at most 9e-8 of the
 // value), 1 - 2 / (1 + e^2y) above, where nothing cancels.
@@ -155,9 +161,7 @@ __device__ __forceinline__ float tanh_f(float y) {
   p = fmaf(z, p, 0.13328056037425995f);
   p = fmaf(z, p, -0.3333311080932617f);
   p = fmaf(y * z, p, y);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + kvcd::ex2(y * 2.885390081777927f)));
-  return z < 0.5f ? p : fmaf(-2.f, r, 1.f);
+  return z < 0.5f ? p : fmaf(-2.f, rcp(1.f + kvcd::ex2(y * 2.885390081777927f)), 1.f);
 }
 
 // Whether a phase has completed, without waiting.
