@@ -368,56 +368,67 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkA
 // Block x joins the partial results of the item that the cut before CTA x
 // splits, if that is the item's first cut: the head piece lies in slot 2(x-1)+1,
 // the following pieces in slots 2x, 2(x+1), ...  blockIdx.y takes a group of
-// rows, a warp a row.
+// rows, a warp a row.  Bound by latency, so several pieces are fetched at a time before
+// anything is known about them: four where rows are few and pieces many, two in the
+// large row blocks, whose items are seldom cut twice (their bytes count: 128 KB a piece).
 template <typename T, int D, int kRowsBlock>
-__global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkArgs a, int grid) {
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a, int grid) {
   kvcd::pdl_trigger();
   kvcd::pdl_wait();
-  const int x = blockIdx.x + 1;
-  const ChunkSeg s = a.seg[x], before = a.seg[x - 1];
+  const int x = blockIdx.x + 1, lane = threadIdx.x & 31;
+  constexpr int C = D / 32, kFetch = kRowsBlock > 128 ? 2 : 4;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const ChunkSeg before = a.seg[x - 1], s = a.seg[x];
   if (!s.mid || (before.mid && before.item == s.item)) return;
-  int y1 = x + 1;                                      // pieces x .. y1 - 1 follow the head
-  while (y1 < grid && a.seg[y1].mid && a.seg[y1].item == s.item) ++y1;
-  const int64_t u = s.item / a.rp;
-  const int t0 = (int)(s.item - u * a.rp) * a.tpb;
-  const ChunkUnit rec = kvcd::load_unit(a, u);
-  const int lane = threadIdx.x & 31;
-  constexpr int C = D / 32;
-  const int rows_tile = a.G * a.tt;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < kRowsBlock; r += gridDim.y * 8) {
-    const int tile = kRowsBlock > 128 ? r >> 7 : 0, rt = kRowsBlock > 128 ? r & 127 : r;
-    const int t = t0 + tile * a.tt + rt % a.tt;
-    if (rt >= rows_tile || t >= rec.n || tile * a.tt >= a.tpb) continue;
-    float M = -INFINITY, l = 0.f, o[C];
+  const int u = (int)((unsigned)s.item / (unsigned)a.rp);
+  const int t0 = ((int)s.item - u * a.rp) * a.tpb;
+  const int tile = kRowsBlock > 128 ? r >> 7 : 0, rt = kRowsBlock > 128 ? r & 127 : r;
+  const int g = rt / a.tt, t = t0 + tile * a.tt + rt % a.tt;
+  if (g >= a.G || t >= a.T || tile * a.tt >= a.tpb) return;
+  const int n = __ldcg(a.rec + u).y;                    // new tokens (on its way with the pieces)
+  float M = -INFINITY, l = 0.f, o[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = 0.f;
-    for (int y = x - 1; y < y1; ++y) {
-      const int64_t prow = ((int64_t)y * 2 + (y == x - 1 ? 1 : 0)) * kRowsBlock + r;
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + prow * 2);
-      float pv[C];
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+  bool more = true;                                     // pieces x .. follow the head, as long as they start inside the item
+  for (int y0 = x - 1; more; y0 += kFetch) {
+    float2 ml[kFetch];
+    float pv[kFetch][C];
+    bool in[kFetch];
+#pragma unroll
+    for (int i = 0; i < kFetch; ++i) {
+      const int y = y0 + i;
+      const ChunkSeg p = y < grid ? a.seg[y] : ChunkSeg{-1, 0};
+      in[i] = y == x - 1 || (p.mid && p.item == s.item);
+      const int64_t prow = ((int64_t)min(y, grid - 1) * 2 + (y == x - 1 ? 1 : 0)) * kRowsBlock + r;
+      ml[i] = *reinterpret_cast<const float2*>(a.part_ml + prow * 2);
       const float* po = a.part + prow * D + lane * C;
       if constexpr (C == 4) {
         const float4 v = *reinterpret_cast<const float4*>(po);
-        pv[0] = v.x; pv[1] = v.y; pv[2] = v.z; pv[3] = v.w;
+        pv[i][0] = v.x; pv[i][1] = v.y; pv[i][2] = v.z; pv[i][3] = v.w;
       } else {
         const float2 v = *reinterpret_cast<const float2*>(po);
-        pv[0] = v.x; pv[1] = v.y;
+        pv[i][0] = v.x; pv[i][1] = v.y;
       }
-      const float Mn = fmaxf(M, ml.x);
-      if (Mn == -INFINITY) continue;                   // nothing seen so far
-      const float f0 = exp2f(M - Mn), f1 = exp2f(ml.x - Mn);
-      l = fmaf(l, f0, ml.y * f1);
+    }
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = f1 == 0.f ? o[c] * f0 : fmaf(o[c], f0, pv[c] * f1);
+    for (int i = 0; i < kFetch; ++i) {
+      more = more && in[i];
+      if (!more || ml[i].x == -INFINITY) continue;       // not the item's, or it saw nothing
+      const float Mn = fmaxf(M, ml[i].x);
+      const float f0 = exp2f(M - Mn), f1 = exp2f(ml[i].x - Mn);
+      l = fmaf(l, f0, ml[i].y * f1);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = fmaf(o[c], f0, pv[i][c] * f1);
       M = Mn;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t orow = (u * a.G + rt / a.tt) * a.T + t;
-    T* op = static_cast<T*>(a.out) + orow * D + lane * C;
-#pragma unroll
-    for (int c = 0; c < C; ++c) op[c] = kvcd::from_f<T>(o[c] * inv);
-    if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? M + log2f(l) : -INFINITY;
   }
+  if (t >= n) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int64_t orow = ((int64_t)u * a.G + g) * a.T + t;
+  T* op = static_cast<T*>(a.out) + orow * D + lane * C;
+#pragma unroll
+  for (int c = 0; c < C; ++c) op[c] = kvcd::from_f<T>(o[c] * inv);
+  if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? M + log2f(l) : -INFINITY;
 }
 
 // ---------------------------------------------------------------- fp32 mass
@@ -544,7 +555,7 @@ template <typename T, int D>
 cudaError_t launch_combine(const ChunkArgs& a, int rows_block, int grid, cudaStream_t s) {
   if (grid < 2) return cudaSuccess;
   kvc::count_launch();
-  const dim3 g(grid - 1, rows_block / 16);
+  const dim3 g(grid - 1, rows_block / 8);
   switch (rows_block) {
     case 16: return kvc::chunk_launch(chunk_combine_kernel<T, D, 16>, g, dim3(256), 0, s, a, grid);
     case 64: return kvc::chunk_launch(chunk_combine_kernel<T, D, 64>, g, dim3(256), 0, s, a, grid);
