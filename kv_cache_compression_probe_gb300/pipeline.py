@@ -128,6 +128,7 @@ class Compressor:
         p.tree_cuts = self.cuts.data_ptr() if self.cuts is not None else None
         p.salient_extract = 1 if salient else 0
         self._graphs = {}
+        self._ws_chunk = None
 
     # ---------------------------------------------------------------- calls
     # With graph=True a call is captured into a CUDA graph once per set of
@@ -292,6 +293,29 @@ class Compressor:
                             self.pos, self.len_lh, self.cap_lh, self.off_lh, out, self.ws_decode,
                             stream)
 
+    def extend(self, q, k_new, v_new, out, pos_new, n_new=None, lse=None, layers=None, softcap=0.0,
+               window=0.0, slopes=None, stream=None):
+        """A chunk of new tokens over the packed cache (kvc_chunk_attn): the
+        follow-up turn of a conversation, or drafted tokens.  q, out
+        [B, Lr, H*G, T, d], k_new, v_new [B, Lr, H, T, d] over the layers
+        (begin, end), all of them by default; pos_new [B] f32 the position of
+        each sequence's first new token; n_new [B] int32 when not every
+        sequence has T.  The tokens are appended (len_lh advances) and take
+        rows of the decode reserve."""
+        p = self.p
+        if p.packed_rows == 0:                       # built without the tensor-core decode
+            p = kvc.kvc_params.from_buffer_copy(p)
+            p.packed_rows = self.Kp.shape[0]
+        l0, l1 = layers or (0, p.L)
+        c = kvc.make_chunk(q.shape[3], l0, l1, n_new=n_new, softcap=softcap, window=window,
+                           slopes=slopes)
+        need = kvc.kvc_chunk_workspace_bytes(p, c)
+        if self._ws_chunk is None or self._ws_chunk.numel() < need:
+            self._ws_chunk = torch.empty(need, dtype=torch.uint8, device=self.device)
+        kvc.kvc_chunk_attn(p, c, q, k_new, v_new, pos_new, self.Kp, self.Vp, self.logm, self.pos,
+                           self.len_lh, self.cap_lh, self.off_lh, out, lse, self.len_lh,
+                           self._ws_chunk, stream)
+
     def decode_many(self, q_all, kn_all, vn_all, out_all, pos_all=None, graph=True):
         """T = q_all.shape[0] decode steps back to back (step t reads q_all[t],
         kn_all[t], vn_all[t] and writes out_all[t]).  With graph=True the T calls
@@ -455,6 +479,90 @@ class EvictingCache:
         o = blh * self.cap
         return (self.K[o:o + n].float().cpu().numpy(), self.V[o:o + n].float().cpu().numpy(),
                 self.pos[o:o + n].cpu().numpy())
+
+
+class ChunkedCache:
+    """A cache of bounded size that a prompt of any length streams through, chunk
+    by chunk, and that decoding goes on with.
+
+    Every (b, l, h) owns pages for `budget` entries and one chunk of T tokens.
+    A step attends (kvc_chunk_attn), adds the chunk's attention weight to the
+    entries' masses (kvc_chunk_mass) and, with evict=True, drops what has least
+    of it until `budget` entries are left (kvc_mass_evict), the last `recent`
+    positions always staying.  Nothing waits for the device, so steps can be
+    captured into a CUDA graph.  The class only allocates and marshals.
+    """
+
+    def __init__(self, p: kvc.kvc_params, budget: int, T: int, page_rows: int = 64,
+                 recent: int = 128, decay: float = 1.0, softcap: float = 0.0, window: float = 0.0,
+                 slopes=None, device="cuda"):
+        if not 0 <= recent <= budget:
+            raise ValueError("the protected positions must fit the budget")
+        B, L, H = p.B, p.L, p.H
+        self.budget, self.recent, self.decay = int(budget), int(recent), float(decay)
+        per = -(-(self.budget + int(T)) // page_rows)
+        self.cap = per * page_rows
+        rows = B * L * H * self.cap
+        self.p = kvc.kvc_params.from_buffer_copy(p)
+        self.p.packed_rows = rows
+        z = dict(device=device)
+        dt = TORCH_DT[p.dtype]
+        self.K = torch.zeros((rows, p.d), dtype=dt, **z)
+        self.V = torch.zeros((rows, p.d), dtype=dt, **z)
+        self.logm = torch.zeros((rows,), dtype=torch.float32, **z)
+        self.pos = torch.zeros((rows,), dtype=torch.float32, **z)
+        self.mass = torch.zeros((rows,), dtype=torch.float32, **z)
+        self.table = torch.arange(B * L * H * per, dtype=torch.int32, **z).view(B, L, H, per)
+        self.len_lh = torch.zeros((B, L, H), dtype=torch.int32, **z)
+        self.len_new = torch.zeros((B, L, H), dtype=torch.int32, **z)
+        self.cap_lh = torch.full((B, L, H), self.cap, dtype=torch.int32, **z)
+        self.keep_lh = torch.full((B, L, H), self.budget, dtype=torch.int32, **z)
+        self.pos_next = torch.zeros((B,), dtype=torch.float32, **z)
+        self.n_new = torch.zeros((B,), dtype=torch.int32, **z)
+        self.lse = torch.empty((B, L, p.H * p.G, int(T)), dtype=torch.float32, **z)
+        self._mods = dict(page_rows=page_rows, page_table=self.table, n_new=self.n_new,
+                          softcap=softcap, window=window, slopes=slopes)
+        self.T = int(T)
+        c = self._chunk(self.T)
+        self.ws = torch.empty(max(kvc.kvc_chunk_workspace_bytes(self.p, c),
+                                  kvc.kvc_mass_evict_workspace_bytes(self.p, c, self.cap)),
+                              dtype=torch.uint8, device=device)
+
+    def _chunk(self, T):
+        return kvc.make_chunk(T, 0, self.p.L, **self._mods)
+
+    def step(self, q, k_new, v_new, out, n_new=None, evict=True, stream=None):
+        """One chunk of q.shape[3] <= T tokens per sequence (n_new [B] int32 on the
+        device when not every sequence has that many): q, out [B, L, H*G, T', d],
+        k_new, v_new [B, L, H, T', d].  With a `stream`, it must be torch's current
+        one."""
+        T = q.shape[3]
+        if T > self.T:
+            raise ValueError(f"a chunk of {T} tokens, the cache was built for {self.T}")
+        if n_new is None:
+            self.n_new.fill_(T)
+        else:
+            self.n_new.copy_(n_new)
+        c = self._chunk(T)
+        lse = self.lse if T == self.T else self.lse.view(-1)[:self.lse.numel() // self.T * T]
+        kvc.kvc_chunk_attn(self.p, c, q, k_new, v_new, self.pos_next, self.K, self.V, self.logm,
+                           self.pos, self.len_lh, self.cap_lh, None, out, lse, self.len_new,
+                           self.ws, stream)
+        kvc.kvc_chunk_mass(self.p, c, q, self.K, self.logm, self.pos, self.pos_next, self.len_lh,
+                           None, lse, self.decay, self.mass, self.ws, stream)
+        self.pos_next.add_(self.n_new)
+        if evict:
+            kvc.kvc_mass_evict(self.p, c, self.mass, self.keep_lh, self.recent, self.pos_next,
+                               self.K, self.V, self.logm, self.pos, self.len_new, None,
+                               self.len_lh, self.cap, self.ws, stream)
+        else:
+            self.len_lh.copy_(self.len_new)
+
+    def entries(self, b: int, l: int, h: int):
+        """(K, V, pos, mass) of the entries (b, l, h) holds, in row order (host copies)."""
+        n = int(self.len_lh[b, l, h])
+        o = ((b * self.p.L + l) * self.p.H + h) * self.cap
+        return tuple(t[o:o + n].float().cpu().numpy() for t in (self.K, self.V, self.pos, self.mass))
 
 
 def pad_bounds(bounds_list, S_max: int) -> np.ndarray:
