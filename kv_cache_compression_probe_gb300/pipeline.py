@@ -113,10 +113,12 @@ class Compressor:
         cap = packed_capacity(p, self.ctx_host)
         # the tensor-core decode needs the extent of the packed cache
         p.packed_rows = cap if tensor_cores else 0
-        self.Kp = torch.empty((cap, p.d), dtype=dt, **z)
-        self.Vp = torch.empty((cap, p.d), dtype=dt, **z)
-        self.logm = torch.empty((cap,), dtype=f32, **z)
-        self.pos = torch.empty((cap,), dtype=f32, **z)
+        # zeros: the rows of the decode reserve, which no call writes before they are
+        # appended to, hold the same thing in every run
+        self.Kp = torch.zeros((cap, p.d), dtype=dt, **z)
+        self.Vp = torch.zeros((cap, p.d), dtype=dt, **z)
+        self.logm = torch.zeros((cap,), dtype=f32, **z)
+        self.pos = torch.zeros((cap,), dtype=f32, **z)
         self.ws_score = kvc.workspace(kvc.KVC_WS_SCORE, p, device)
         self.ws_select = kvc.workspace(kvc.KVC_WS_SELECT, p, device)
         self.ws_pack = kvc.workspace(kvc.KVC_WS_PACK, p, device)

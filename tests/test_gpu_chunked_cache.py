@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
 def kvc():
     from kv_cache_compression_probe_gb300 import build, kvc as K
     build.build()
-    return K
+    yield K
+    torch.cuda.empty_cache()                           # buffers full of NaN stay with this module
 
 
 def _cache(kvc, dtype, d=128, **kw):
