@@ -181,7 +181,8 @@ int64_t kvc_launch_count(void);
 /* Bounded device waits (no counterpart on the pages: error handling of this
  * library).  Kernels that pipeline copies and tensor-core products through
  * mbarriers (the tensor-core passes of kvc_score, both decode kernels of the
- * kvc_decode_attn family) give up a wait after first_wait_ns nanoseconds of
+ * kvc_decode_attn family, the bf16 kernels of kvc_chunk_attn and kvc_chunk_mass)
+ * give up a wait after first_wait_ns nanoseconds of
  * global time: the CTA then stops issuing work, waits (with its own fixed
  * limits: 2 s for copies and products already issued, 0.1 s in the probe
  * passes) for what it has in flight, frees its tensor memory, records
@@ -496,8 +497,9 @@ size_t kvc_chunk_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk
  * start from 0 (what mass held there is not read).  A row with lse = -inf adds
  * nothing.  mass: f32 laid out like logm ([packed_rows]).  0 <= decay <= 1.
  * Sums run in a fixed order: the same call gives the same bits.  Checks and
- * skipped (l,h) as in kvc_chunk_attn (no capacity is involved).  Errors:
- * KVC_EINVAL, KVC_EWORKSPACE, KVC_ECUDA. */
+ * skipped (l,h) as in kvc_chunk_attn (no capacity is involved; here no two (b,l,h)
+ * of a call may share pages, since each updates its rows' mass).  Errors:
+ * KVC_EINVAL (also q or Kp off a 16-byte boundary), KVC_EWORKSPACE, KVC_ECUDA. */
 int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const void* q, const void* Kp,
                    const float* logm, const float* pos, const float* pos_new,
                    const int32_t* len_lh, const int64_t* off_lh, const float* lse, float decay,
@@ -517,7 +519,8 @@ int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const void* q, const
  * skipped (len_out = len_lh) and reported as KVC_EDEVICE.  c gives the layer
  * range and the pages (its other members are not read, but must be valid).
  * Two (b,l,h) of one call must not share the pages that it changes.
- * Errors: KVC_EINVAL, KVC_EWORKSPACE, KVC_ECUDA. */
+ * Errors: KVC_EINVAL (also Kp or Vp off a 16-byte boundary, and more than 65535
+ * (b,l,h) in the range), KVC_EWORKSPACE, KVC_ECUDA. */
 int kvc_mass_evict(const kvc_params* p, const kvc_chunk* c, float* mass, const int32_t* keep_lh,
                    int32_t recent, const float* pos_next, void* Kp, void* Vp, float* logm,
                    float* pos, const int32_t* len_lh, const int64_t* off_lh, int32_t* len_out,

@@ -274,3 +274,64 @@ def test_waits_give_up_and_the_next_call_is_right(kvc):
         assert kvc.kvc_device_error() == 0
         ch.check_attn(s)
         ch.check_mass(s, s["lse"].cpu().numpy(), 0.5)
+
+
+def test_the_binding_refuses_tensors_it_cannot_pass(kvc):
+    ch = Chunk(kvc, [100, 64], [3], H=2)
+    for name, bad in (("q", lambda t: t.cpu()), ("K", lambda t: t.t()), ("out", lambda t: t.transpose(2, 3)),
+                      ("len", lambda t: t.cpu())):
+        s = ch.upload()
+        s[name] = bad(s[name])
+        with pytest.raises(ValueError):
+            ch.attn(s)
+    s = ch.upload()
+    s["pos"] = 5
+    with pytest.raises(TypeError):
+        ch.run_mass(s, 0.5)
+
+
+def test_repeated_calls_share_a_workspace(kvc):
+    """One workspace serves calls of every shape one after the other, back to back on a stream."""
+    kws = [dict(lens=[700, 90, 1300, 64], n_new=[40, 21], B=2, H=2), dict(lens=[9000, 5], n_new=[1], H=2, seed=1),
+           dict(lens=[0, 3, 128, 200], n_new=[2], H=4, G=2, d=64, seed=2),
+           dict(lens=[300, 50], n_new=[40], H=2, window=33.5, seed=3),
+           dict(lens=[90, 700], n_new=[5], H=2, dtype="f32", seed=4)]
+    chs = [Chunk(kvc, **kw) for kw in kws]
+    ss = [c.upload() for c in chs]
+    ws = torch.empty(max(s["ws"].numel() for s in ss), dtype=torch.uint8, device="cuda")
+    for s in ss:
+        s["ws"] = ws
+    for _ in range(3):
+        for c, s in zip(chs, ss):
+            s["mass"].copy_(torch.from_numpy(c.mass))
+            c.attn(s)
+            c.run_mass(s, 0.5)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    for c, s in zip(chs, ss):
+        c.check_attn(s)
+        c.check_mass(s, s["lse"].cpu().numpy(), 0.5)
+
+
+def test_pages_shared_between_sequences(kvc):
+    """Two sequences over the same pages of a common prompt (attention only reads them), each
+    with a page of its own for the new tokens."""
+    ch = Chunk(kvc, [128, 128], [9, 9], B=2, H=1, page=64, reserve=64)
+    ch.table[1, :2] = ch.table[0, :2]
+    s = ch.upload()
+    ch.attn(s)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(s)
+
+
+def test_a_length_past_the_pages_is_reported(kvc):
+    """More entries than the page table has columns for, and a cache row number that does not fit
+    the extent's last, partial page."""
+    ch = Chunk(kvc, [60, 70], [4], H=2, page=16)
+    ch.table = ch.table[:, :4].copy()                   # 64 rows: the second unit needs 74
+    s = ch.upload()
+    ch.attn(s)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == kvc.KVC_EDEVICE
+    assert s["len_out"].view(-1).tolist() == [64, 70]
