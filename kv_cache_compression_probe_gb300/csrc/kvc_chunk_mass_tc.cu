@@ -35,6 +35,11 @@ enum Mode { kPlain, kExtra, kCapped, kPos, kCapPos };
 // Key and query tiles in flight: keys stream past one row tile, or stay while row
 // tiles stream past them.
 constexpr int kTiles = 6;
+// With one row tile of up to 64 rows the query rows come with the keys: four places of
+// 64 rows in the query slots, one barrier and one release for both (a tile's keys take
+// 1400 cycles of HBM, and the single thread that issues the products needed as long for
+// its waits and commits).
+constexpr uint32_t kFoldHalf = 64 * 128;   // of a 64-feature block
 __device__ __forceinline__ int key_slots(bool several) { return several ? 2 : 4; }
 
 template <int D>
@@ -130,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ ChunkArgs a) {
   using Smem = MassSmem<D>;
   constexpr int kBlocks = D / 64;
+  constexpr uint32_t kFoldPlace = kBlocks * kFoldHalf;
   constexpr bool kCap = kMode == kCapped || kMode == kCapPos, kBias = kMode == kPos || kMode == kCapPos;
   extern __shared__ __align__(1024) unsigned char mass_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(mass_raw) + 1023) & ~uintptr_t(1023));
@@ -172,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t ns = a.wait_ns;
   const int used = a.G * a.tt, cols = (used + 15) & ~15;         // rows of a row tile; columns of S^T
   const int kK = key_slots(a.T > a.tt), kQ = min(4, kTiles - kK);
+  const bool fold = kMode != kExtra && a.T <= a.tt && used <= 64;
   int k_loads = 0, q_loads = 0;                        // copies issued (for the drain after a give-up)
 
   if (warp == 0) {
@@ -195,6 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ks = nk % kK;
       if (nk >= kK) ok = warp_wait(&sm.k_empty[ks], (uint32_t)((nk / kK - 1) & 1), ns, abort_flag);
       if (!ok) break;
+      if (fold && !a.withhold && lane == 0) {
+        mbar_expect(&sm.k_full[ks], (uint32_t)(used * 128 * kBlocks));
+#pragma unroll
+        for (int h = 0; h < kBlocks; ++h)
+          tma3d(kvcd::smem_u32(sm.tile[4]) + ks * kFoldPlace + h * kFoldHalf, &qmap, h * 64, w.tb * a.tt, (int)(w.u * a.G),
+                &sm.k_full[ks]);
+      }
       if (!a.withhold) {
         copy_tile<D>(rows, &kmap, kvcd::smem_u32(sm.tile[ks]), boxes, row, &sm.k_full[ks], lane);
         k_loads = nk + 1;
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         kvcd::MassWalk<128> ahead = w;                 // the next item's, on their way meanwhile
         if (ahead.next()) fetch_lm(ahead);
       }
-      for (int rt = w.tb; rt < w.te; ++rt, ++nq) {
+      for (int rt = w.tb; rt < w.te && !fold; ++rt, ++nq) {
         const int qs = nq % kQ;
         // (kExtra: kQ = kGroups, so a step's query slot is free when its products are there)
         if (nq >= kQ)
@@ -248,22 +262,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kMode == kExtra) {
             ok = wait_or_abort(&sm.r_full[sb], (uint32_t)((nq / kGroups) & 1), ns, abort_flag);
           } else {
-            ok = wait_or_abort(&sm.q_full[qs], (uint32_t)((nq / kQ) & 1), ns, abort_flag);
+            ok = fold || wait_or_abort(&sm.q_full[qs], (uint32_t)((nq / kQ) & 1), ns, abort_flag);
             if (ok && nq >= kGroups)
               ok = wait_or_abort(&sm.s_empty[sb], (uint32_t)((nq / kGroups - 1) & 1), ns, abort_flag);
           }
           if (!ok) break;
           fence_after();
-          const uint32_t kb = lo + ks * (Smem::kTileBytes >> 4), qb = lo + (kK + qs) * (Smem::kTileBytes >> 4);
+          const uint32_t kb = lo + ks * (Smem::kTileBytes >> 4);
+          const uint32_t qb = lo + (fold ? 4 * (Smem::kTileBytes >> 4) + ks * (kFoldPlace >> 4)
+                                         : (kK + qs) * (Smem::kTileBytes >> 4));
+          const uint32_t q_half = (fold ? kFoldHalf : kHalf) >> 4;
           const uint32_t d = tmem + sb * 128;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
-            mma_ss(d, desc(kb + at), desc(qb + at), id, k > 0);
+            mma_ss(d, desc(kb + (k >> 2) * (kHalf >> 4) + (k & 3) * 2), desc(qb + (k >> 2) * q_half + (k & 3) * 2), id, k > 0);
           }
           if (kMode == kExtra) mma_ss(d, ext_desc(ek_lo + ks * 256), ext_desc(eq_lo + sb * 256), id, 1);
           commit(&sm.s_full[sb]);
-          if (kMode != kExtra) commit(&sm.q_empty[qs]);
+          if (kMode != kExtra && !fold) commit(&sm.q_empty[qs]);
           if (rt + 1 == w.te) commit(&sm.k_empty[ks]);
         }
       }

@@ -164,6 +164,11 @@ __device__ __forceinline__ float tanh_f(float y) {
   return z < 0.5f ? p : fmaf(-2.f, rcp(1.f + kvcd::ex2(y * 2.885390081777927f)), 1.f);
 }
 
+// Announces bytes of copies without arriving.
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(kvcd::smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Whether a phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
