@@ -8,7 +8,9 @@
 // entries below the new length ("holes") take the staying entries at or above it,
 // both in index order.  Bound by latency: one read of 8 bytes an entry, then a dozen
 // block-wide steps on shared memory.
-// Measured: 256 (b,l,h) of 3300..5100 entries 20 us, 64 of 5000..8192 15 us.
+// Measured, both kernels: 256 (b,l,h) of 3300..5100 entries 20 us, 64 of 5000..8192 with 34 MB
+// to move 35 us.  Loads in batches of eight, one barrier per prefix, protected entries kept out
+// of the histograms and a search that ends once a whole bin stays took 2 to 5 us off.
 // Move: a second kernel copies the rows (5 TB/s for 34 MB moved).  Moving only those, instead of compacting
 // the cache, keeps the traffic at twice the moved rows; the row order stops
 // following the positions, so protection goes by position and not by index.
@@ -50,39 +52,45 @@ __device__ __forceinline__ uint32_t mass_code(float m, bool is_protected) {
   return kvcd::float_key(m == 0.f ? 0.f : m);          // -0 is 0; codes 0x007fffff (-inf) .. 0xff800000 (inf)
 }
 
-// Exclusive prefix of `v` over the block; returns the total.
-__device__ __forceinline__ int block_prefix(int v, int* s_warp, int& excl) {
+// Exclusive prefixes of N counts over the block, and their totals.  One barrier: every warp
+// adds up the warps' sums itself, and calls alternate between two buffers.
+template <int N>
+__device__ __forceinline__ void block_prefix(const int (&v)[N], int (*s_warp)[32], int (&excl)[N], int (&total)[N]) {
+  constexpr int kWarps = kPlanThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
+  int incl[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(KVC_FULL_MASK, incl, o);
-    if (lane >= o) incl += x;
-  }
-  __syncthreads();
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    int w = lane < kPlanThreads / 32 ? s_warp[lane] : 0;
+  for (int c = 0; c < N; ++c) {
+    incl[c] = v[c];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(KVC_FULL_MASK, incl[c], o);
+      if (lane >= o) incl[c] += x;
+    }
+    if (lane == 31) s_warp[c][warp] = incl[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    int w = lane < kWarps ? s_warp[c][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
       const int x = __shfl_up_sync(KVC_FULL_MASK, w, o);
       if (lane >= o) w += x;
     }
-    s_warp[lane] = w;
+    const int before = __shfl_sync(KVC_FULL_MASK, w, max(warp - 1, 0));
+    excl[c] = incl[c] - v[c] + (warp > 0 ? before : 0);
+    total[c] = __shfl_sync(KVC_FULL_MASK, w, kWarps - 1);
   }
-  __syncthreads();
-  excl = incl - v + (warp > 0 ? s_warp[warp - 1] : 0);
-  return s_warp[31];
 }
 
 struct PlanSmem {
   uint32_t hist[2][kBins];             // passes alternate, so one barrier a pass is enough
-  int warp[32];
+  int warp[2][2][32];                  // sums of block_prefix: two buffers of two counts
   int ties, holes, movers, safe;       // this CTA's counts, read by the cluster
   int ok;
   uint32_t prefix;
-  int rem;
+  int rem, found;                      // entries of the bin that stay; whether that is all of it
 };
 
 // kKeys: the codes are in shared memory; else every pass forms them from global memory.
@@ -136,11 +144,23 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_co
   };
   auto code = [&](int i) { return kKeys ? keys[i] : form(i); };
   int mine = 0;
-#pragma unroll 4
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const uint32_t k = form(i);
-    if (kKeys) keys[i] = k;
-    mine += k == 0xffffffffu;
+  constexpr int kBatch = 8;                            // loads in flight per thread, times two
+  for (int i0 = tid; i0 < n; i0 += kBatch * kPlanThreads) {
+    float m[kBatch], p[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int64_t row = rows(lo + min(i0 + x * kPlanThreads, n - 1));
+      m[x] = a.mass[row];
+      p[x] = a.pos[row];
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int i = i0 + x * kPlanThreads;
+      if (i >= n) break;
+      const uint32_t k = mass_code(m[x], p[x] >= safe_from);
+      if (kKeys) keys[i] = k;
+      mine += k == 0xffffffffu;
+    }
   }
   mine = __reduce_add_sync(KVC_FULL_MASK, mine);
   if (lane == 0 && mine) atomicAdd(&sm.safe, mine);
@@ -155,18 +175,22 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_co
     for (int r = 0; r < rank; ++r) t += cluster.map_shared_rank(&sm, r)->*m;
     return t;
   };
-  const int B = min(len, max(max(0, keep), total(&PlanSmem::safe)));
+  const int safe = total(&PlanSmem::safe), B = min(len, max(max(0, keep), safe));
   const bool all = B >= len, none = B == 0;
-  uint32_t cut = 0;
-  int rem = B;                                         // how many of the entries at the cut stay
-  // the B-th largest code, 11 or 10 bits at a time (not needed when all or none stay)
-  for (int pass = 0; pass < 3 && !all && !none; ++pass) {
+  // The B-th largest code, 11 or 10 bits at a time.  The histograms leave the protected entries
+  // out (they would all hit one bin), and the search ends as soon as a whole bin stays: then its
+  // lower end cuts as well.  Nothing to look for when all, none or the protected ones stay.
+  uint32_t cut = safe == B ? 0xffffffffu : 0u;
+  int rem = safe == B ? B : B - safe;                  // how many of the entries at the cut stay
+  bool found = all || none || safe == B;               // every entry at or above the cut stays
+  int turn = 0;
+  for (int pass = 0; pass < 3 && !found; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
     const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 1 ? 11 : 10));
     uint32_t* hist = sm.hist[pass & 1];
     for (int i = tid; i < n; i += kPlanThreads) {
       const uint32_t k = code(i);
-      if ((k & mask) == cut) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+      if ((k & mask) == cut && k != 0xffffffffu) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
     }
     sync();
     for (int i = tid; i < kBins; i += kPlanThreads) sm.hist[(pass + 1) & 1][i] = 0;
@@ -185,13 +209,19 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_co
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) sum += c[x];
     int at;
-    block_prefix(sum, sm.warp, at);
+    {
+      int excl[1], all_bins[1];
+      block_prefix<1>({sum}, sm.warp[turn], excl, all_bins);
+      turn ^= 1;
+      at = excl[0];
+    }
     if (at < rem && rem <= at + sum) {                 // one thread: the counts reach rem here
 #pragma unroll
       for (int x = 0; x < kOwn; ++x) {
         if (at < rem && rem <= at + c[x]) {
           sm.prefix = cut | ((uint32_t)(b0 - x) << shift);
           sm.rem = rem - at;
+          sm.found = rem - at == c[x];
         }
         at += c[x];
       }
@@ -199,40 +229,41 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_co
     __syncthreads();
     cut = sm.prefix;
     rem = sm.rem;
+    found = sm.found;
   }
   // contiguous ranges per thread (an odd count keeps them off each other's banks), so that
   // thread order is index order
   const int per = ((n + kPlanThreads - 1) / kPlanThreads) | 1;
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
   int tie0 = 0;
-  if (!all && !none) {
-    int ties = 0;
-    for (int i = i0; i < i1; ++i) ties += code(i) == cut;
-    const int t = block_prefix(ties, sm.warp, tie0);
-    if (tid == 0) sm.ties = t;
+  if (!found) {                                        // the first `rem` of the equal codes at the cut stay
+    int ties[1] = {0}, excl[1], t[1];
+    for (int i = i0; i < i1; ++i) ties[0] += code(i) == cut;
+    block_prefix<1>(ties, sm.warp[turn], excl, t);
+    turn ^= 1;
+    if (tid == 0) sm.ties = t[0];
     sync();
-    tie0 += before(&PlanSmem::ties);
+    tie0 = excl[0] + before(&PlanSmem::ties);
   }
   int tie = tie0;
   auto stays = [&](int i) {
     if (all || none) return all;
     const uint32_t k = code(i);
-    return k > cut || (k == cut && tie++ < rem);
+    return k > cut || (k == cut && (found || tie++ < rem));
   };
-  int nh = 0, nm = 0, h0, m0;
+  int count[2] = {0, 0}, at[2], sums[2];               // holes and movers
   for (int i = i0; i < i1; ++i) {
     const bool s = stays(i);
-    if (lo + i < B) nh += !s;
-    else nm += s;
+    if (lo + i < B) count[0] += !s;
+    else count[1] += s;
   }
-  const int th = block_prefix(nh, sm.warp, h0), tm = block_prefix(nm, sm.warp, m0);
-  if (tid == 0) { sm.holes = th; sm.movers = tm; }
+  block_prefix<2>(count, sm.warp[turn], at, sums);
+  if (tid == 0) { sm.holes = sums[0]; sm.movers = sums[1]; }
   sync();
-  h0 += before(&PlanSmem::holes);
-  m0 += before(&PlanSmem::movers);
+  int h0 = at[0] + before(&PlanSmem::holes), m0 = at[1] + before(&PlanSmem::movers);
   int2* mv = ea.moves + u * ea.cols;
   tie = tie0;
-  if (nh + nm > 0)
+  if (count[0] + count[1] > 0)
     for (int i = i0; i < i1; ++i) {
       const bool s = stays(i);
       if (lo + i < B && !s) mv[h0++].x = lo + i;

@@ -90,6 +90,24 @@ def test_eviction(kvc, name, masses):
     _check(ch, s, keep, recent)
 
 
+@pytest.mark.parametrize("recent", [0, 50])
+@pytest.mark.parametrize("step", [1 << 21, 1 << 10, 1])
+def test_the_cut_falls_at_every_level_of_the_search(kvc, step, recent):
+    # masses in pairs whose bit patterns are `step` apart: their codes part in the first, second
+    # or last digit of the search; an even target keeps whole pairs, an odd one parts a pair
+    ch = Chunk(kvc, [400, 401, 6001, 2], [0], H=4, T=1, seed=step % 97)
+    rng = np.random.default_rng(5)
+    for u in range(4):
+        r = ch.rows(u, int(ch.lens[u]))
+        bits = np.uint32(0x04000000) + np.uint32(step) * (np.arange(len(r), dtype=np.uint32) // 2 % 900)
+        ch.mass[r] = rng.permutation(bits).view(np.float32)
+    for keep in (100, 101, 399, 5000, 5001):
+        s = _run(kvc, ch, [keep] * 4, recent)
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_error() == 0
+        _check(ch, s, [keep] * 4, recent)
+
+
 def test_in_place_lengths_and_a_second_eviction(kvc):
     ch = Chunk(kvc, [700, 30, 1025, 64], [0, 0], B=2, H=2, T=1)
     keep = np.asarray([500, 30, 800, 10])
