@@ -23,7 +23,7 @@
 // of alternate tiles (and 3 clears the V rows past the last entry), 4..11 and 12..19 are the softmax of the two streams.  The
 // work is cut as kvc_chunk.cuh says; persistent, one CTA per SM (512 TMEM
 // columns: S, S, O, O; P lies in S's place).
-// Measured (d 128, G 4): 2048 tokens over 16K entries, 8 KV heads: 377 us, 1370
+// Measured (d 128, G 4): 2048 tokens over 16K entries, 8 KV heads: 375 us, 1375
 // TFLOP/s; one token over 256 caches of 3200..5000 entries: 98 us, 5.5 TB/s.
 #include <cudaTypedefs.h>
 

@@ -196,12 +196,23 @@ __device__ __forceinline__ void ext_store(unsigned char* tile, int row, const ui
   *reinterpret_cast<uint4*>(p) = c0;
   *reinterpret_cast<uint4*>(p + 128) = c1;
 }
+// A suspended wait of the hardware's own length (with a hint of 1 ms, as elsewhere here, the
+// 2048-token chunk took 378 us instead of 375 and the 1024-token masses 93.4 instead of 92.2).
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(kvcd::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Waits for a phase; gives up when another role has, or after `ns` nanoseconds.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* abort) {
-  if (kvcd::mbar_try_wait(bar, parity)) return true;
+  if (mbar_try(bar, parity)) return true;
   if (*abort) return false;
   const uint64_t t0 = kvcd::global_timer_ns();
-  while (!kvcd::mbar_try_wait(bar, parity)) {
+  while (!mbar_try(bar, parity)) {
     if (*abort) return false;
     if (kvcd::global_timer_ns() - t0 > ns) {
       *abort = 1;
