@@ -131,6 +131,7 @@ class Compressor:
         p.salient_extract = 1 if salient else 0
         self._graphs = {}
         self._ws_chunk = None
+        self._ws_outgrown = []                       # calls in flight or captured may still use them
 
     # ---------------------------------------------------------------- calls
     # With graph=True a call is captured into a CUDA graph once per set of
@@ -313,6 +314,8 @@ class Compressor:
                            slopes=slopes)
         need = kvc.kvc_chunk_workspace_bytes(p, c)
         if self._ws_chunk is None or self._ws_chunk.numel() < need:
+            if self._ws_chunk is not None:
+                self._ws_outgrown.append(self._ws_chunk)
             self._ws_chunk = torch.empty(need, dtype=torch.uint8, device=self.device)
         kvc.kvc_chunk_attn(p, c, q, k_new, v_new, pos_new, self.Kp, self.Vp, self.logm, self.pos,
                            self.len_lh, self.cap_lh, self.off_lh, out, lse, self.len_lh,

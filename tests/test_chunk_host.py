@@ -206,3 +206,23 @@ def test_make_chunk_checks_types():
     c = kvc.make_chunk(3, 1, 2, softcap=5.0, window=7.0)
     assert (c.T, c.layer_begin, c.layer_end, c.page_rows, c.max_pages) == (3, 1, 2, 0, 0)
     assert c.page_table is None and c.n_new is None and c.slopes is None
+
+
+def test_extend_keeps_an_outgrown_workspace(monkeypatch):
+    # a call captured with the smaller workspace replays with it after a larger turn
+    from kv_cache_compression_probe_gb300 import kvc, pipeline
+    used = []
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_attn", lambda *a: used.append(a[-2].data_ptr()))
+    comp = object.__new__(pipeline.Compressor)
+    comp.p = kvc.make_params(B=1, L=2, H=2, G=4, d=128, P=1, W=1, n_max=64, S_max=1)
+    comp.device, comp._ws_chunk, comp._ws_outgrown = "cpu", None, []
+    comp.Kp = torch.zeros(64, 128)
+    for name in ("Vp", "logm", "pos", "len_lh", "cap_lh", "off_lh"):
+        setattr(comp, name, None)
+    sizes = {1: 256, 40: 1024, 2: 256, 300: 4096}
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_workspace_bytes", lambda p, c: sizes[c.T])
+    for T in (1, 40, 2, 300):
+        q = torch.zeros(1, 2, 8, T, 128)
+        comp.extend(q, None, None, None, None)
+    assert used[1] == used[2] and len(set(used)) == 3
+    assert [w.data_ptr() for w in comp._ws_outgrown] + [comp._ws_chunk.data_ptr()] == [used[0], used[1], used[3]]
