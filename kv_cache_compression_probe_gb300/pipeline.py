@@ -310,6 +310,10 @@ class Compressor:
             p = kvc.kvc_params.from_buffer_copy(p)
             p.packed_rows = self.Kp.shape[0]
         l0, l1 = layers or (0, p.L)
+        _check_chunk(p, l1 - l0, q, k_new, v_new, out,
+                     pos_new=(pos_new, (p.B,), torch.float32), n_new=(n_new, (p.B,), torch.int32),
+                     lse=(lse, (p.B, l1 - l0, p.H * p.G, *q.shape[3:4]), torch.float32),
+                     slopes=(slopes, (p.H * p.G,), torch.float32))
         c = kvc.make_chunk(q.shape[3], l0, l1, n_new=n_new, softcap=softcap, window=window,
                            slopes=slopes)
         need = kvc.kvc_chunk_workspace_bytes(p, c)
@@ -486,6 +490,19 @@ class EvictingCache:
                 self.pos[o:o + n].cpu().numpy())
 
 
+def _check_chunk(p: kvc.kvc_params, layers: int, q, k_new, v_new, out, **others):
+    """A chunk's tensors have the cache's type and the shapes the library reads;
+    the others are (tensor or None, shape, type)."""
+    if q.dim() != 5 or q.shape[3] < 1:
+        raise ValueError("q must be [B, layers, H*G, T, d]")
+    dt = TORCH_DT[p.dtype]
+    want = {"q": (q, p.H * p.G), "k_new": (k_new, p.H), "v_new": (v_new, p.H), "out": (out, p.H * p.G)}
+    want = {k: (t, (p.B, layers, heads, q.shape[3], p.d), dt) for k, (t, heads) in want.items()}
+    for name, (t, shape, dtype) in {**want, **others}.items():
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+            raise ValueError(f"{name} must be {list(shape)} {dtype}")
+
+
 class ChunkedCache:
     """A cache of bounded size that a prompt of any length streams through, chunk
     by chunk, and that decoding goes on with.
@@ -503,6 +520,8 @@ class ChunkedCache:
                  slopes=None, device="cuda"):
         if not 0 <= recent <= budget:
             raise ValueError("the protected positions must fit the budget")
+        if slopes is not None and (tuple(slopes.shape) != (p.H * p.G,) or slopes.dtype != torch.float32):
+            raise ValueError(f"slopes must be [{p.H * p.G}] float32")
         B, L, H = p.B, p.L, p.H
         self.budget, self.recent, self.decay = int(budget), int(recent), float(decay)
         per = -(-(self.budget + int(T)) // page_rows)
@@ -541,6 +560,7 @@ class ChunkedCache:
         device when not every sequence has that many): q, out [B, L, H*G, T', d],
         k_new, v_new [B, L, H, T', d].  With a `stream`, it must be torch's current
         one."""
+        _check_chunk(self.p, self.p.L, q, k_new, v_new, out)
         T = q.shape[3]
         if T > self.T:
             raise ValueError(f"a chunk of {T} tokens, the cache was built for {self.T}")

@@ -214,7 +214,7 @@ def test_extend_keeps_an_outgrown_workspace(monkeypatch):
     used = []
     monkeypatch.setattr(pipeline.kvc, "kvc_chunk_attn", lambda *a: used.append(a[-2].data_ptr()))
     comp = object.__new__(pipeline.Compressor)
-    comp.p = kvc.make_params(B=1, L=2, H=2, G=4, d=128, P=1, W=1, n_max=64, S_max=1)
+    comp.p = kvc.make_params(B=1, L=2, H=2, G=4, d=128, P=1, W=1, n_max=64, S_max=1, dtype=kvc.KVC_BF16)
     comp.device, comp._ws_chunk, comp._ws_outgrown = "cpu", None, []
     comp.Kp = torch.zeros(64, 128)
     for name in ("Vp", "logm", "pos", "len_lh", "cap_lh", "off_lh"):
@@ -222,7 +222,43 @@ def test_extend_keeps_an_outgrown_workspace(monkeypatch):
     sizes = {1: 256, 40: 1024, 2: 256, 300: 4096}
     monkeypatch.setattr(pipeline.kvc, "kvc_chunk_workspace_bytes", lambda p, c: sizes[c.T])
     for T in (1, 40, 2, 300):
-        q = torch.zeros(1, 2, 8, T, 128)
-        comp.extend(q, None, None, None, None)
+        q, k = (torch.zeros(1, 2, n, T, 128, dtype=torch.bfloat16) for n in (8, 2))
+        comp.extend(q, k, k, q, torch.zeros(1))
     assert used[1] == used[2] and len(set(used)) == 3
     assert [w.data_ptr() for w in comp._ws_outgrown] + [comp._ws_chunk.data_ptr()] == [used[0], used[1], used[3]]
+
+
+BAD_CHUNKS = {
+    "q of another type": dict(q=torch.zeros(1, 2, 8, 4, 128)),
+    "q of four dimensions": dict(q=torch.zeros(1, 2, 8, 128, dtype=torch.bfloat16)),
+    "q of three dimensions": dict(q=torch.zeros(8, 4, 128, dtype=torch.bfloat16)),
+    "no token": {n: torch.zeros(1, 2, h, 0, 128, dtype=torch.bfloat16)
+                 for n, h in (("q", 8), ("k_new", 2), ("v_new", 2), ("out", 8))},
+    "fewer keys than queries": dict(k_new=torch.zeros(1, 2, 2, 3, 128, dtype=torch.bfloat16)),
+    "values for every query head": dict(v_new=torch.zeros(1, 2, 8, 4, 128, dtype=torch.bfloat16)),
+    "a short out": dict(out=torch.zeros(1, 2, 8, 3, 128, dtype=torch.bfloat16)),
+    "a layer less": dict(out=torch.zeros(1, 1, 8, 4, 128, dtype=torch.bfloat16)),
+    "counts of 64 bits": dict(n_new=torch.zeros(1, dtype=torch.int64)),
+    "counts of another batch": dict(n_new=torch.zeros(2, dtype=torch.int32)),
+}
+
+
+@pytest.mark.parametrize("name", list(BAD_CHUNKS))
+def test_extend_and_step_refuse_tensors_of_other_shapes(monkeypatch, name):
+    from kv_cache_compression_probe_gb300 import pipeline
+    calls = []
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_attn", lambda *a: calls.append(a))
+    p = kvc.make_params(B=1, L=2, H=2, G=4, d=128, P=1, W=1, n_max=64, S_max=1, dtype=kvc.KVC_BF16)
+    x = {n: torch.zeros(1, 2, h, 4, 128, dtype=torch.bfloat16)
+         for n, h in (("q", 8), ("k_new", 2), ("v_new", 2), ("out", 8))}
+    x.update(BAD_CHUNKS[name])
+    comp = object.__new__(pipeline.Compressor)
+    comp.p, comp.device, comp._ws_chunk, comp.Kp = p, "cpu", None, torch.zeros(64, 128)
+    with pytest.raises(ValueError):
+        comp.extend(pos_new=torch.zeros(1), **x)
+    if "n_new" not in x:                                # (the cache copies the counts into its own)
+        cache = object.__new__(pipeline.ChunkedCache)
+        cache.p, cache.T = p, 40
+        with pytest.raises(ValueError):
+            cache.step(**x)
+    assert not calls
