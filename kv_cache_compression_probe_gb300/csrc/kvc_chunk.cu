@@ -668,7 +668,9 @@ void chunk_fill(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c) {
   while (c->page_rows >> (a.page_shift + 1)) ++a.page_shift;
   a.scale = 1.f / sqrtf((float)p->d);
   a.scale_log2 = a.scale * kvcd::kLog2eC;
-  a.softcap = c->softcap;
+  // Beyond these a cap has no effect on scores of any size that fp32 sums tell apart (above), or
+  // leaves nothing of them (below); the reciprocal and the base-2 cap stay finite and normal.
+  a.softcap = c->softcap > 0.f ? std::min(std::max(c->softcap, 0x1p-64f), 0x1p64f) : 0.f;
   a.window = c->window;
   a.wait_ns = wait_limit_ns();
   a.withhold = withhold_copies();

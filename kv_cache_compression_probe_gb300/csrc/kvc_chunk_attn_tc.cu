@@ -80,16 +80,32 @@ struct Ring {
 //   kCapped the tanh comes between the product and ln m, which is added per score from
 //           shared memory
 //   kCapPos the same with a distance bias or a window
-enum Mode { kSums, kWindow, kCapped, kCapPos };
+//   kCapLarge a cap above kShortCap, with or without bias and window
+enum Mode { kSums, kWindow, kCapped, kCapPos, kCapLarge };
+
+// Largest cap of the short form cap - 2 cap / (1 + e^2y) of cap tanh(y).  It costs one
+// exponential and one reciprocal, but cancels: the score is off by up to 4.5 * 2^-23 of the
+// cap (2^-22 of e^2y from ex2, 2^-24 from the sum, 2^-23 from rcp, and two roundings of values
+// the cap's size), 3.4e-5 at 64, whatever the score is.  Above, tanh_f costs a polynomial as well
+// and is off by 9e-8 of the score.  Short form and tanh_f: drafts over pages 62 and 92 us, one
+// token over 256 caches of 3200..5000 entries 126 and 206, 2048 tokens over 16K 666 and 1160.
+constexpr float kShortCap = 64.f;
 
 // What a thread needs to turn the products of its row into base-2 scores.
 struct RowScore {
-  float scale, cap_in, cap_out;        // s log2 e = scale product, or cap_out tanh(y), 2^(cap_in product) = e^2y
+  float scale, cap_in, cap_out;        // s log2 e = scale product, or cap_out tanh(y), y = cap_in product
+                                       // (short form: 2^(cap_in product) = e^2y)
   float slope, shift;                  // distance bias slope rel - shift
   float edge;                          // window: sees rel > edge
 };
 
-// Scores (plus `base`, both halves of a pair; capped: base includes cap_out) of four entries c .. c + 3 of a tile.
+// What the base of a row's scores includes of the cap.
+template <int kMode>
+__device__ __forceinline__ float cap_base(const RowScore& r) {
+  return kMode == kCapped || kMode == kCapPos ? r.cap_out : 0.f;
+}
+
+// Scores (plus `base`, both halves of a pair; base includes cap_base) of four entries c .. c + 3 of a tile.
 // kMask: the row sees only the first `lim` entries, and of these those beyond the
 // window's edge.  (A broadcast from shared memory costs its full width, 512 bytes a
 // warp for four floats: per-entry values read here bounded the kernel, which is why
@@ -99,15 +115,13 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
                                         uint64_t base, int lim, float (&f)[4]) {
   uint64_t x0 = base, x1 = base;
   float4 d;
-  if constexpr (kMode == kCapPos || (kMode == kWindow && kMask)) d = *reinterpret_cast<const float4*>(rel + c);
+  if constexpr (kMode >= kCapPos || (kMode == kWindow && kMask)) d = *reinterpret_cast<const float4*>(rel + c);
   if constexpr (kMode >= kCapped) {
     const float4 b = *reinterpret_cast<const float4*>(lm + c);
-    // cap tanh(y) = cap - 2 cap / (1 + e^2y), off by up to 2^-23 of the cap (the log-sum-exp
-    // and the rounded numerators lose nothing by that)
-    const uint64_t ci = pk(r.cap_in, r.cap_in), m2 = pk(-2.f * r.cap_out, -2.f * r.cap_out), one = pk(1.f, 1.f);
+    const uint64_t ci = pk(r.cap_in, r.cap_in);
     x0 = add2(pk(b.x, b.y), base);
     x1 = add2(pk(b.z, b.w), base);
-    if constexpr (kMode == kCapPos) {
+    if constexpr (kMode >= kCapPos) {
       const uint64_t sl = pk(r.slope, r.slope);
       x0 = fma2(sl, pk(d.x, d.y), x0);
       x1 = fma2(sl, pk(d.z, d.w), x1);
@@ -115,10 +129,17 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
     float e0, e1, e2, e3;
     upk(mul2(pk(__uint_as_float(s[0]), __uint_as_float(s[1])), ci), e0, e1);
     upk(mul2(pk(__uint_as_float(s[2]), __uint_as_float(s[3])), ci), e2, e3);
-    upk(add2(pk(kvcd::ex2(e0), kvcd::ex2(e1)), one), e0, e1);
-    upk(add2(pk(kvcd::ex2(e2), kvcd::ex2(e3)), one), e2, e3);
-    x0 = fma2(pk(rcp(e0), rcp(e1)), m2, x0);
-    x1 = fma2(pk(rcp(e2), rcp(e3)), m2, x1);
+    if constexpr (kMode == kCapLarge) {
+      const uint64_t co = pk(r.cap_out, r.cap_out);
+      x0 = fma2(pk(tanh_f(e0), tanh_f(e1)), co, x0);
+      x1 = fma2(pk(tanh_f(e2), tanh_f(e3)), co, x1);
+    } else {                                           // cap tanh(y) = cap - 2 cap / (1 + e^2y)
+      const uint64_t m2 = pk(-2.f * r.cap_out, -2.f * r.cap_out), one = pk(1.f, 1.f);
+      upk(add2(pk(kvcd::ex2(e0), kvcd::ex2(e1)), one), e0, e1);
+      upk(add2(pk(kvcd::ex2(e2), kvcd::ex2(e3)), one), e2, e3);
+      x0 = fma2(pk(rcp(e0), rcp(e1)), m2, x0);
+      x1 = fma2(pk(rcp(e2), rcp(e3)), m2, x1);
+    }
   } else {
     const uint64_t sc = pk(r.scale, r.scale);
     x0 = fma2(pk(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, x0);
@@ -127,7 +148,7 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
   upk(x0, f[0], f[1]);
   upk(x1, f[2], f[3]);
   if constexpr (kMask) {
-    if constexpr (kMode == kWindow || kMode == kCapPos) {
+    if constexpr (kMode == kWindow || kMode >= kCapPos) {
       f[0] = d.x > r.edge ? f[0] : -INFINITY;
       f[1] = d.y > r.edge ? f[1] : -INFINITY;
       f[2] = d.z > r.edge ? f[2] : -INFINITY;
@@ -144,7 +165,7 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 template <int kMode, bool kMask>
 __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,
                                             float base, int lim, uint32_t (&p)[32]) {
-  const float sh = r.cap_out - (base + r.shift);
+  const float sh = cap_base<kMode>(r) - (base + r.shift);
   const uint64_t mb = pk(sh, sh);
   uint64_t s0 = 0, s1 = 0;
   uint32_t s[2][16];
@@ -174,7 +195,7 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
 template <int kMode>
 __device__ __forceinline__ float score_max(const RowScore& r, uint32_t ts, const float* lm, const float* rel, int lim) {
   float t = -INFINITY;
-  const uint64_t mb = pk(r.cap_out - r.shift, r.cap_out - r.shift);
+  const uint64_t mb = pk(cap_base<kMode>(r) - r.shift, cap_base<kMode>(r) - r.shift);
 #pragma unroll 1
   for (int q = 0; q < 64; q += 16) {
     uint32_t s[16];
@@ -493,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t u = w.item / a.rp;
       const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
       const int total = w.r.len + w.r.n;
-      const bool with_pos = kMode == kWindow || kMode == kCapPos || a.slopes;
+      const bool with_pos = a.window > 0.f || a.slopes;
       const int t0 = (int)((unsigned)w.item % (unsigned)a.rp) * a.tpb;
       const float pos0 = with_pos ? a.pos_new[u / a.per_seq] + (float)t0 : 0.f;   // the row block's first token
       if (kMode < kCapped && a.slopes && warp == 2) { // the row factors of this piece's head
@@ -560,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = lane + 32 * j;
           if (kMode >= kCapped) reinterpret_cast<float*>(sm.ext_k[b])[r] = lm[j] * kvcd::kLog2eC;
           else ext_key(sm.ext_k[b], r, lm[j] / a.scale, a.slopes ? rel[j] : 0.f);
-          if (kMode == kWindow || kMode == kCapPos) sm.rel[b][r] = rel[j];
+          if (kMode == kWindow || kMode >= kCapPos) sm.rel[b][r] = rel[j];
         }
         const bool extra = a.slopes || __any_sync(KVC_FULL_MASK, lm[0] != 0.f || lm[1] != 0.f || lm[2] != 0.f || lm[3] != 0.f);
         if (kMode < kCapped) kvcd::fence_proxy_async_smem();
@@ -597,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int see = live ? w.r.len + tok + 1 : 0;    // entries this row sees
       RowScore rs;
       rs.scale = a.scale_log2;
-      rs.cap_in = kMode >= kCapped ? 2.f * a.scale_log2 / a.softcap : 0.f;
+      rs.cap_in = kMode == kCapLarge ? a.scale / a.softcap : kMode >= kCapped ? 2.f * a.scale_log2 / a.softcap : 0.f;
       rs.cap_out = kMode >= kCapped ? a.softcap * kvcd::kLog2eC : 0.f;
       rs.slope = a.slopes && live ? a.slopes[(u % a.H) * a.G + g] * kvcd::kLog2eC : 0.f;
       // positions count from the row block's first token, so that near entries, the ones whose
@@ -629,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int lim = live ? see - w.r.first - tile * 128 - half * 64 : 64;
           const float *lm = reinterpret_cast<const float*>(sm.ext_k[b]) + half * 64, *rel = sm.rel[b] + half * 64;
           const bool cut = __any_sync(KVC_FULL_MASK, lim < 64 || (kMode == kWindow && live && !(sm.rel_min[b] > rs.edge)) ||
-                                                              (kMode == kCapPos && a.window > 0.f));
+                                                              (kMode >= kCapPos && a.window > 0.f));
           uint32_t p[32];
           float sum;
           if (cut) sum = numerators<kMode, true>(rs, ts, lm, rel, m, lim, p);
@@ -827,6 +848,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorM
 template <int D, bool kRowStreams>
 cudaError_t launch_mods(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const ChunkArgs& a,
                         int sms, cudaStream_t s) {
+  if (a.softcap > kShortCap) return launch<D, kRowStreams, kCapLarge>(km, vm, qm, a, sms, s);
   if (a.softcap > 0.f)
     return a.slopes || a.window > 0.f ? launch<D, kRowStreams, kCapPos>(km, vm, qm, a, sms, s)
                                       : launch<D, kRowStreams, kCapped>(km, vm, qm, a, sms, s);

@@ -1,0 +1,77 @@
+"""The chunk calls at the ends of what they accept: caps of every size.  Small cases
+against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from tests.chunk_cases import Chunk
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvc():
+    from kv_cache_compression_probe_gb300 import build, kvc as K
+    build.build()
+    yield K
+    torch.cuda.empty_cache()                           # buffers full of NaN stay with this module
+
+
+# ------------------------------------------------------------------ caps
+FAST_CAP = 64.0                                        # up to here bf16 attention may use the short form
+
+
+class Capped(Chunk):
+    def score_error(self, u):
+        """Bound on the error of each natural-log score that does not grow with the cap: the d
+        products in fp32 (as in Chunk), cap * tanh(s / cap) off by at most 2^-21 of its
+        value (tanh by 9e-8, a product and a sum, each half a step of 2^-24), ln m and bias a
+        handful of half steps.  The short form cap - 2 cap / (1 + e^2y) adds the errors of e^2y
+        (2^-22 of it), of the sum (2^-24), the reciprocal (2^-23) and of two roundings at the
+        cap's size: 4.5 * 2^-23 of the cap, up to FAST_CAP and on the bf16 path only."""
+        K, V, lm, pos, q, (b, lr, hs, n, n0) = self.entries(u)
+        dots = np.abs(q) @ np.abs(K).T / np.sqrt(self.d)
+        size = dots + np.abs(np.where(np.isinf(lm), 0.0, lm))
+        if self.slopes is not None:
+            gap = np.abs((float(self.pos_new[b]) + np.arange(n))[:, None] - pos[None])
+            size = size + self.slopes_of(u)[:, None, None] * gap
+        short = 4.5 * 2.0 ** -23 * self.softcap if self.dtype == "bf16" and self.softcap <= FAST_CAP else 0.0
+        return self.d * 2.0 ** -23 * dots + 2.0 ** -21 * size + short
+
+
+CAPS = (1e-30, 30.0, 64.0, 65.0, 1e3, 1e5, 1e7, 1e20, 3e38)
+CAP_CASES = {
+    "one token": (dict(lens=[300, 1025], n_new=[1], H=2), "bf16"),
+    "one token, slopes, window, paged": (dict(lens=[300, 1025], n_new=[1], H=2, slopes=True, window=700.0, page=64), "bf16"),
+    "chunk": (dict(lens=[300, 50], n_new=[140], H=2), "bf16"),
+    "chunk, slopes, d 64": (dict(lens=[300, 50], n_new=[150], H=2, slopes=True, d=64), "bf16"),
+    "f32 chunk": (dict(lens=[300, 50], n_new=[40], H=2, slopes=True), "f32"),
+}
+
+
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("name", list(CAP_CASES))
+def test_caps_of_every_size(kvc, name, cap):
+    """Attention, then the mass from its lse: both match the oracle, and the weights of all
+    rows add up to their number."""
+    kw, dtype = CAP_CASES[name]
+    ch = Capped(kvc, dtype=dtype, softcap=cap, qscale=2.0, seed=11, **kw)
+    s = ch.upload()
+    ch.attn(s)
+    ch.run_mass(s, 0.0)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(s, name)
+    lse = s["lse"].cpu().numpy()
+    ch.check_mass(s, lse, 0.0, name)
+    mass = s["mass"].double().cpu().numpy()
+    for u in ch.units:
+        where = ch.entries(u)[5]
+        n, n0 = where[3], where[4]
+        r = ch.rows(u, n0 + n)
+        # a row's weights: the error of every score twice (lse and mass form it anew), of the lse
+        # (half a step of its value) and of 2^x and the sums
+        rows = ch.G * n
+        tol = rows * (2 * ch.score_error(u).max() + 2.0 ** -23 * (np.abs(lse[lse != 7.0]).max() + 1)
+                      + 2.0 ** -20 + (n0 + n) * 2.0 ** -24)
+        assert abs(mass[r].sum() - rows) <= tol, (name, u, mass[r].sum() - rows, tol)
