@@ -497,13 +497,27 @@ size_t kvc_chunk_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk
  * start from 0 (what mass held there is not read).  A row with lse = -inf adds
  * nothing.  mass: f32 laid out like logm ([packed_rows]).  0 <= decay <= 1.
  * Sums run in a fixed order: the same call gives the same bits.  Checks and
- * skipped (l,h) as in kvc_chunk_attn (no capacity is involved; here no two (b,l,h)
- * of a call may share pages, since each updates its rows' mass).  Errors:
- * KVC_EINVAL (also q or Kp off a 16-byte boundary), KVC_EWORKSPACE, KVC_ECUDA. */
+ * skipped (l,h) as in kvc_chunk_attn (a skipped one's mass stays, without decay),
+ * but here no two (b,l,h) of a call may share pages, since each updates its rows'
+ * mass.  Capacities are not known to this call: an (l,h) without room for its
+ * tokens, which kvc_chunk_attn skips, is skipped here (KVC_ECAPACITY) only when
+ * its contiguous rows would reach into those of the next (b,l,h) in [B, L, H]
+ * order.  A caller whose cache can be full passes cap_lh to kvc_chunk_mass_cap.
+ * Errors: KVC_EINVAL (also q or Kp off a 16-byte boundary), KVC_EWORKSPACE,
+ * KVC_ECUDA. */
 int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const void* q, const void* Kp,
                    const float* logm, const float* pos, const float* pos_new,
                    const int32_t* len_lh, const int64_t* off_lh, const float* lse, float decay,
                    float* mass, void* workspace, size_t ws_bytes, void* stream);
+
+/* kvc_chunk_mass with the capacities that kvc_chunk_attn was given: cap_lh
+ * [B, L, H] int32 (NULL: as kvc_chunk_mass).  An (l,h) with len_lh + n_b > cap_lh
+ * is skipped and reported as KVC_ECAPACITY, as kvc_chunk_attn skipped it. */
+int kvc_chunk_mass_cap(const kvc_params* p, const kvc_chunk* c, const void* q, const void* Kp,
+                       const float* logm, const float* pos, const float* pos_new,
+                       const int32_t* len_lh, const int32_t* cap_lh, const int64_t* off_lh,
+                       const float* lse, float decay, float* mass, void* workspace,
+                       size_t ws_bytes, void* stream);
 
 /* Eviction by accumulated mass, each (l,h) by itself: an entry is protected
  * when pos_e >= pos_next[b] - recent; B = min(len_lh, max(keep_lh, protected

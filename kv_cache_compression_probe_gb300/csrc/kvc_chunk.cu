@@ -29,7 +29,7 @@ constexpr int kKeys = 64;              // entries per tile of the fp32 kernels
 constexpr int kSimtThreads = 256;
 
 // ---------------------------------------------------------------- prepare
-// One warp per (unit, group of 8 new tokens): checks the unit, appends the group's
+// One warp per (unit, group of 8 new tokens; mass: one per unit): checks the unit, appends the group's
 // keys and values (kAppend) and writes the unit's record.  The rows to append are
 // fetched before anything is known about the unit, so that their latency and that
 // of the checks overlap.
@@ -62,12 +62,21 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
   const int len = a.len_lh[gu];
   const int n = a.n_new ? a.n_new[b] : a.T;
   const int64_t off = a.page_table ? 0 : a.off_lh[gu];
-  const int cap = kAppend ? a.cap_lh[gu] : 0;
+  const int cap = a.cap_lh ? a.cap_lh[gu] : INT_MAX;
+  // Mass: the next (b,l,h)'s first row and entries.  A unit that attention skipped for want of
+  // capacity would reach into them.
+  int64_t next_off = -1;
+  int next_has = 0;
+  if (!kAppend && !a.page_table && gu + 1 < a.units / a.per_seq * (a.lh_span + a.lh_gap)) {
+    next_off = a.off_lh[gu + 1];
+    next_has = max(a.len_lh[gu + 1], a.n_new ? a.n_new[(gu + 1) / (a.lh_span + a.lh_gap)] : a.T);
+  }
   const float pos0 = kAppend ? a.pos_new[b] : 0.f;
   int bad = KVC_OK;
   if (len < 0 || n < 0 || n > a.T || off < 0 || (int64_t)len + n > a.packed_rows) bad = KVC_EDEVICE;
   else if (!a.page_table && off + len + n > a.packed_rows) bad = KVC_EDEVICE;
-  else if (kAppend && (int64_t)len + n > cap) bad = KVC_ECAPACITY;
+  else if ((int64_t)len + n > cap) bad = KVC_ECAPACITY;
+  else if (next_off > off && off + len + n > next_off && next_has > 0) bad = KVC_ECAPACITY;
   else if (a.page_table) {
     const int need = (int)(((int64_t)len + n + (1 << a.page_shift) - 1) >> a.page_shift);
     if (need > a.max_pages) {
@@ -543,12 +552,12 @@ bool misaligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) 
 
 template <typename T, int D>
 cudaError_t launch_prepare(const ChunkArgs& a, cudaStream_t s) {
-  const int groups = a.cap_lh ? (a.T + kPrepTok - 1) / kPrepTok : 1;
+  const int groups = a.k_new ? (a.T + kPrepTok - 1) / kPrepTok : 1;
   const int64_t warps = a.units * groups;
   const dim3 grid((unsigned)((warps + kPrepWarps - 1) / kPrepWarps)), block(32 * kPrepWarps);
   kvc::count_launch();
-  const cudaError_t e = a.cap_lh ? kvc::chunk_launch(chunk_prepare_kernel<T, D, true>, grid, block, 0, s, a, groups)
-                                 : kvc::chunk_launch(chunk_prepare_kernel<T, D, false>, grid, block, 0, s, a, groups);
+  const cudaError_t e = a.k_new ? kvc::chunk_launch(chunk_prepare_kernel<T, D, true>, grid, block, 0, s, a, groups)
+                                : kvc::chunk_launch(chunk_prepare_kernel<T, D, false>, grid, block, 0, s, a, groups);
   if (e != cudaSuccess || !(a.window > 0.f)) return e;
   kvc::count_launch();
   return kvc::chunk_launch(chunk_window_kernel, dim3((unsigned)a.units), dim3(kWinThreads), 0, s, a);
@@ -732,6 +741,15 @@ extern "C" int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const voi
                               const float* logm, const float* pos, const float* pos_new,
                               const int32_t* len_lh, const int64_t* off_lh, const float* lse, float decay,
                               float* mass, void* workspace, size_t ws_bytes, void* stream) {
+  return kvc_chunk_mass_cap(p, c, q, Kp, logm, pos, pos_new, len_lh, nullptr, off_lh, lse, decay, mass, workspace,
+                            ws_bytes, stream);
+}
+
+extern "C" int kvc_chunk_mass_cap(const kvc_params* p, const kvc_chunk* c, const void* q, const void* Kp,
+                                  const float* logm, const float* pos, const float* pos_new,
+                                  const int32_t* len_lh, const int32_t* cap_lh, const int64_t* off_lh,
+                                  const float* lse, float decay, float* mass, void* workspace,
+                                  size_t ws_bytes, void* stream) {
   int st = kvc::chunk_check(p, c);
   if (st != KVC_OK) return st;
   if (!q || !Kp || !logm || !pos || !pos_new || !len_lh || !lse || !mass || (!off_lh && c->page_rows == 0) ||
@@ -746,7 +764,7 @@ extern "C" int kvc_chunk_mass(const kvc_params* p, const kvc_chunk* c, const voi
   const int sms = kvc::sm_count();
   if (!a.err || sms <= 0 || !kvc::chunk_tc_available()) return KVC_ECUDA;
   a.q = q; a.Kp = const_cast<void*>(Kp); a.logm = const_cast<float*>(logm); a.pos = const_cast<float*>(pos);
-  a.pos_new = pos_new; a.len_lh = len_lh; a.off_lh = off_lh; a.lse = const_cast<float*>(lse);
+  a.pos_new = pos_new; a.len_lh = len_lh; a.cap_lh = cap_lh; a.off_lh = off_lh; a.lse = const_cast<float*>(lse);
   a.decay = decay; a.mass = mass;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;

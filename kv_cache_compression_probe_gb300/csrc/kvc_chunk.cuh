@@ -31,7 +31,7 @@ struct ChunkSeg {
 
 struct ChunkArgs {
   const void* q;
-  const void* k_new;
+  const void* k_new;                   // null: nothing to append (mass)
   const void* v_new;
   const float* pos_new;
   void* Kp;
@@ -39,7 +39,7 @@ struct ChunkArgs {
   float* logm;
   float* pos;
   const int32_t* len_lh;
-  const int32_t* cap_lh;               // null: no append (mass)
+  const int32_t* cap_lh;               // null: no capacity is checked (mass only)
   const int64_t* off_lh;
   void* out;
   float* lse;                          // attention: written when not null; mass: read

@@ -27,8 +27,8 @@ EXPORTED = ("kvc_status_string", "kvc_last_cuda_error", "kvc_device_error", "kvc
             "kvc_partition", "kvc_decode_attn_noalloc", "kvc_decode_attn_lse", "kvc_token_alpha",
             "kvc_evict_workspace_bytes", "kvc_evict_topb", "kvc_set_phase_timing",
             "kvc_score_phase_ms", "kvc_decode_attn_layers", "kvc_tree_cuts", "kvc_set_wait_limit",
-            "kvc_chunk_attn", "kvc_chunk_workspace_bytes", "kvc_chunk_mass", "kvc_mass_evict",
-            "kvc_mass_evict_workspace_bytes")
+            "kvc_chunk_attn", "kvc_chunk_workspace_bytes", "kvc_chunk_mass", "kvc_chunk_mass_cap",
+            "kvc_mass_evict", "kvc_mass_evict_workspace_bytes")
 
 
 class kvc_params(ctypes.Structure):
@@ -118,6 +118,8 @@ def lib():
         L.kvc_chunk_workspace_bytes.restype = c_size_t
         L.kvc_chunk_mass.argtypes = [_P, _C] + [vp] * 8 + [c_float, vp, vp, c_size_t, vp]
         L.kvc_chunk_mass.restype = c_int
+        L.kvc_chunk_mass_cap.argtypes = [_P, _C] + [vp] * 9 + [c_float, vp, vp, c_size_t, vp]
+        L.kvc_chunk_mass_cap.restype = c_int
         L.kvc_mass_evict.argtypes = [_P, _C, vp, vp, c_int32] + [vp] * 8 + [c_int32, vp, c_size_t, vp]
         L.kvc_mass_evict.restype = c_int
         L.kvc_mass_evict_workspace_bytes.argtypes = [_P, _C, c_int32]
@@ -369,12 +371,13 @@ def kvc_chunk_attn(p, c, q, k_new, v_new, pos_new, Kp, Vp, logm, pos, len_lh, ca
 
 
 def kvc_chunk_mass(p, c, q, Kp, logm, pos, pos_new, len_lh, off_lh, lse, decay, mass, workspace,
-                   stream=None):
+                   stream=None, cap_lh=None):
     """mass = decay * mass + the attention weight every entry received from the
-    chunk (len_lh: the lengths before it)."""
-    a = _ptrs(q, Kp, logm, pos, pos_new, len_lh, off_lh, lse, mass, workspace)
-    _check(lib().kvc_chunk_mass(p, c, *a[:8], decay, a[8], a[9], workspace.nbytes,
-                                _raw_stream(stream)), "kvc_chunk_mass")
+    chunk (len_lh: the lengths before it).  cap_lh, the capacities kvc_chunk_attn was
+    given, is needed where a (b, l, h) may have been full: it is skipped here too."""
+    a = _ptrs(q, Kp, logm, pos, pos_new, len_lh, cap_lh, off_lh, lse, mass, workspace)
+    _check(lib().kvc_chunk_mass_cap(p, c, *a[:9], decay, a[9], a[10], workspace.nbytes,
+                                    _raw_stream(stream)), "kvc_chunk_mass")
 
 
 def kvc_mass_evict_workspace_bytes(p, c, max_len: int) -> int:

@@ -574,7 +574,7 @@ class ChunkedCache:
                            self.pos, self.len_lh, self.cap_lh, None, out, lse, self.len_new,
                            self.ws, stream)
         kvc.kvc_chunk_mass(self.p, c, q, self.K, self.logm, self.pos, self.pos_next, self.len_lh,
-                           None, lse, self.decay, self.mass, self.ws, stream)
+                           None, lse, self.decay, self.mass, self.ws, stream, self.cap_lh)
         self.pos_next.add_(self.n_new)
         if evict:
             kvc.kvc_mass_evict(self.p, c, self.mass, self.keep_lh, self.recent, self.pos_next,

@@ -1,0 +1,67 @@
+"""Host-side checks of the chunk calls' further forms (no GPU: the fake pointers are
+never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+from kv_cache_compression_probe_gb300 import kvc
+from tests.test_chunk_host import BAD_CHUNK, BAD_PARAMS, PAGED, VP, _chunk, _fake, _params
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kv_cache_compression_probe_gb300 import build
+    build.build()
+    return kvc.lib()
+
+
+# ------------------------------------------------------------------ mass with capacities
+def _mass_cap(lib, p, c, ptrs=None, ws=VP(1 << 20), nb=1 << 40, decay=1.0):
+    a = ptrs or _fake(10)
+    return lib.kvc_chunk_mass_cap(ctypes.byref(p), ctypes.byref(c) if c else None, *a[:9], ctypes.c_float(decay),
+                                  a[9], ws, ctypes.c_size_t(nb), None)
+
+
+def test_mass_with_capacities_checks_its_arguments(lib):
+    p, c = _params(), _chunk()
+    for bad in BAD_CHUNK:
+        assert _mass_cap(lib, p, _chunk(**bad)) == kvc.KVC_EINVAL, bad
+    for bad in BAD_PARAMS:
+        assert _mass_cap(lib, _params(**bad), c) == kvc.KVC_EINVAL, bad
+    assert _mass_cap(lib, p, None) == kvc.KVC_EINVAL
+    for i in range(10):                                 # the capacities may be missing, and off_lh with pages
+        ptrs = _fake(10)
+        ptrs[i] = None
+        want = kvc.KVC_EWORKSPACE if i == 6 else kvc.KVC_EINVAL
+        assert _mass_cap(lib, p, c, ptrs, None) == want, i
+        if i == 7:
+            assert _mass_cap(lib, p, _chunk(**PAGED), ptrs, None) == kvc.KVC_EWORKSPACE
+    for decay in (-0.1, 1.1, float("nan")):
+        assert _mass_cap(lib, p, c, decay=decay) == kvc.KVC_EINVAL
+
+
+def test_a_step_hands_its_capacities_to_both_calls(monkeypatch):
+    """ChunkedCache: what attention skips for want of room, the mass call skips as well."""
+    from kv_cache_compression_probe_gb300 import pipeline
+    cache = _cpu_cache(monkeypatch, pipeline)
+    seen = {}
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_attn", lambda *a: seen.update(attn=a))
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_mass", lambda *a: seen.update(mass=a))
+    monkeypatch.setattr(pipeline.kvc, "kvc_mass_evict", lambda *a: None)
+    cache.step(**_tokens(4))
+    assert any(x is cache.cap_lh for x in seen["attn"]) and seen["mass"][14] is cache.cap_lh
+
+
+def _cpu_cache(monkeypatch, pipeline, **kw):
+    """A ChunkedCache in host memory; the library's calls are to be replaced."""
+    monkeypatch.setattr(pipeline.kvc, "make_chunk", lambda T, l0, l1, **mods: (T, l0, l1))
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_workspace_bytes", lambda p, c: 256)
+    monkeypatch.setattr(pipeline.kvc, "kvc_mass_evict_workspace_bytes", lambda p, c, n: 256)
+    p = kvc.make_params(B=2, L=2, H=2, G=4, d=128, P=1, W=1, n_max=64, S_max=1, dtype=kvc.KVC_BF16)
+    return pipeline.ChunkedCache(p, **dict(dict(budget=32, T=8, page_rows=16, recent=4, device="cpu"), **kw))
+
+
+def _tokens(T):
+    return {n: torch.zeros(2, 2, h, T, 128, dtype=torch.bfloat16)
+            for n, h in (("q", 8), ("k_new", 2), ("v_new", 2), ("out", 8))}

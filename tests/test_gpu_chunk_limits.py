@@ -1,5 +1,5 @@
-"""The chunk calls at the ends of what they accept: caps of every size.  Small cases
-against the float64 oracle."""
+"""The chunk calls at the ends of what they accept: caps of every size, caches without
+room.  Small cases against the float64 oracle."""
 import numpy as np
 import pytest
 import torch
@@ -75,3 +75,55 @@ def test_caps_of_every_size(kvc, name, cap):
         tol = rows * (2 * ch.score_error(u).max() + 2.0 ** -23 * (np.abs(lse[lse != 7.0]).max() + 1)
                       + 2.0 ** -20 + (n0 + n) * 2.0 ** -24)
         assert abs(mass[r].sum() - rows) <= tol, (name, u, mass[r].sum() - rows, tol)
+
+
+# ------------------------------------------------------------------ no room
+def _full(kvc, page, dtype, **kw):
+    """Four sequences, the second without room for its tokens; its rows end where the third's begin
+    (with a reserve: that many rows before)."""
+    ch = Chunk(kvc, [100, 90, 300, 64], [5, 2, 3, 4], B=4, H=1, T=5, page=page, dtype=dtype, seed=9, **kw)
+    ch.n[1] = 5                                        # the capacity is for two
+    ch.n_u = np.repeat(ch.n, ch.L * ch.H)
+    for t in (ch.q, ch.k_new, ch.v_new):
+        t[1] = torch.randn(t[1].shape).to(t.dtype)
+    ch.caps = ch.caps - kw.get("reserve", 0)
+    return ch
+
+
+def _mass(kvc, ch, s, decay, cap):
+    kvc.kvc_chunk_mass(s["p"], s["c"], s["q"], s["K"], s["logm"], s["pos"], s["pos_new"], s["len"],
+                       None if ch.page else s["off"], s["lse"], decay, s["mass"], s["ws"], None, cap)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("how", ["packed", "packed, capacities not passed", "spread", "paged", "window"])
+def test_a_full_unit_is_left_out_of_the_mass_too(kvc, how, dtype):
+    """Attention skips a unit without room; the mass call after it leaves that unit's mass and
+    its neighbours' alone."""
+    page = 16 if how == "paged" else 0
+    kw = dict(reserve=8) if how == "spread" else dict(window=50.0) if how == "window" else {}
+    ch = _full(kvc, page, dtype, **kw)
+    s = ch.upload()
+    ch.attn(s)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == kvc.KVC_ECAPACITY
+    _mass(kvc, ch, s, 0.5, None if "not passed" in how else s["cap"])
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == kvc.KVC_ECAPACITY
+    ch.units = [0, 2, 3]                               # check_mass: every other row as it was
+    ch.check_mass(s, s["lse"].cpu().numpy(), 0.5, how)
+
+
+def test_mass_with_room_everywhere_is_the_same_with_capacities(kvc):
+    ch = Chunk(kvc, [100, 90, 300, 64], [5, 3], B=2, H=2, reserve=1)
+    s = ch.upload()
+    ch.attn(s)
+    m0 = s["mass"].clone()
+    _mass(kvc, ch, s, 0.5, None)
+    m1 = s["mass"].clone()
+    s["mass"].copy_(m0)
+    _mass(kvc, ch, s, 0.5, s["cap"])
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    assert torch.equal(s["mass"].view(torch.int32), m1.view(torch.int32))
+    ch.check_mass(s, s["lse"].cpu().numpy(), 0.5)
