@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kWinThreads) chunk_window_kernel(ChunkArgs a) 
   const int4 v = __ldcg(a.rec + u);                     // the prepare kernel's record
   const int len = v.x;
   const kvcd::RowMap rows = kvcd::row_map(a, u, ((int64_t)(uint32_t)v.z) | ((int64_t)v.w << 32));
-  const float edge = a.pos_new[u / a.per_seq] - a.window;
+  const float pos0 = a.pos_new[u / a.per_seq];
   int mine = len;                                       // the chunk's own entries are always live
   for (int e0 = threadIdx.x; e0 < len && mine == len; e0 += 8 * kWinThreads) {
     float p[8];                                         // eight loads in flight
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kWinThreads) chunk_window_kernel(ChunkArgs a) 
     }
 #pragma unroll
     for (int i = 7; i >= 0; --i)
-      if (p[i] > edge) mine = e0 + i * kWinThreads;
+      if (p[i] - pos0 > -a.window) mine = e0 + i * kWinThreads;
   }
   mine = __reduce_min_sync(KVC_FULL_MASK, mine);
   if ((threadIdx.x & 31) == 0) atomicMin(&s_first, mine);
@@ -680,7 +680,10 @@ void chunk_fill(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c) {
   // Beyond these a cap has no effect on scores of any size that fp32 sums tell apart (above), or
   // leaves nothing of them (below); the reciprocal and the base-2 cap stay finite and normal.
   a.softcap = c->softcap > 0.f ? std::min(std::max(c->softcap, 0x1p-64f), 0x1p64f) : 0.f;
-  a.window = c->window;
+  // Distances are multiples of 1/2, so the next multiple of 1/2 is the same window, and the
+  // kernels' differences of positions and windows are exact (token - 33.0000038 is not: it can round to
+  // the position of an entry inside).  A float of 2^22 or more is a multiple of 1/2 itself.
+  a.window = c->window < 0x1p22f ? 0.5f * ceilf(2.f * c->window) : c->window;
   a.wait_ns = wait_limit_ns();
   a.withhold = withhold_copies();
 }

@@ -1,5 +1,5 @@
 """The chunk calls at the ends of what they accept: caps of every size, caches without
-room.  Small cases against the float64 oracle."""
+room, windows that are no multiple of 1/2.  Small cases against the float64 oracle."""
 import numpy as np
 import pytest
 import torch
@@ -127,3 +127,41 @@ def test_mass_with_room_everywhere_is_the_same_with_capacities(kvc):
     assert kvc.kvc_device_error() == 0
     assert torch.equal(s["mass"].view(torch.int32), m1.view(torch.int32))
     ch.check_mass(s, s["lse"].cpu().numpy(), 0.5)
+
+
+# ------------------------------------------------------------------ windows
+def _next(x):
+    return float(np.nextafter(np.float32(x), np.float32(np.inf)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [33.7, _next(33.0), _next(0.0), 0.25])
+def test_windows_between_the_half_integers(kvc, window, dtype):
+    """Positions are multiples of 1/2, a window need not be: an entry just inside it is seen,
+    whatever pos_token - window rounds to."""
+    ch = Chunk(kvc, [300, 50], [140], H=2, dtype=dtype, window=window, seed=3)
+    s = ch.upload()
+    ch.attn(s)
+    ch.run_mass(s, 0.5)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(s, window)
+    ch.check_mass(s, s["lse"].cpu().numpy(), 0.5, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_edge_at_a_far_position(kvc, dtype):
+    """The only visible old entry lies alone in its tile, half a position inside the window, at a
+    position where fp32 keeps halves only."""
+    ch = Chunk(kvc, [700], [3], dtype=dtype, window=33.7, seed=4)
+    ch.pos_new[:] = 5000001.0
+    r = ch.rows(0, 700)
+    ch.pos[r] = 4000000.0 + np.arange(700)
+    ch.pos[r[200]] = 4999967.5                         # 33.5 before the first new token
+    s = ch.upload()
+    ch.attn(s)
+    ch.run_mass(s, 0.5)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(s, "edge")
+    ch.check_mass(s, s["lse"].cpu().numpy(), 0.5, "edge")
