@@ -467,8 +467,9 @@ int kvc_tree_cuts(const kvc_params* p, const int32_t* ctx_len, const void* K,
  * caller that verifies drafts keeps the old lengths until it knows how many
  * tokens stand), or NULL.  Positions must be multiples of 1/2 below 2^23.
  * Every value the rows in use hold must be finite, except that log m may be
- * -inf (the entry is never seen).  Pages may be shared between (b,l,h) as
- * long as the rows appended by a call belong to one only.
+ * -inf (the entry is never seen); values v up to 2^64 (the sums before the
+ * division by the softmax's denominator have to fit fp32).  Pages may be shared
+ * between (b,l,h) as long as the rows appended by a call belong to one only.
  * p->packed_rows must be the extent of Kp, Vp, logm and pos (1 .. 2^31 - 1).
  * An (l,h) with a length or n_b out of range, a page number or row range
  * outside the extent, or too few page_table columns is skipped and reported as

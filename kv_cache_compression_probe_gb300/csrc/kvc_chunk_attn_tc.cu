@@ -7,7 +7,8 @@
 //   O[128 rows x d] += P V               (P as the TMEM operand, V MN-major)
 // with the reference m and the sum l of each row in registers.  m need not be
 // the maximum, only near enough that nothing over- or underflows: fp32 and bf16
-// have the same exponent range, so a reference off by up to 2^60 costs nothing.
+// have the same exponent range, so a reference off by up to 2^30 costs nothing (and
+// leaves O room for values up to 2^64: 2^31 a tile, 2^24 tiles, 2^119 in all).
 // It starts at 0, a tile takes one pass, and only a row whose maximum lies further
 // away has its tile done again and O rescaled.  Tiles go from the newest entries to
 // the oldest, so with a distance bias the first tile holds the largest scores.
@@ -41,7 +42,8 @@ using namespace kvctc;
 
 constexpr int kThreads = 640;
 constexpr int kBias = 4;               // bias tiles in flight
-constexpr float kFar = 0x1p60f;        // a tile's sum of numerators may be this large or (at first) its inverse
+constexpr float kFar = 0x1p30f;        // half a tile's sum of numerators may be this large or (at first) its inverse
+constexpr float kLeap = 16.f;          // and then its largest of 64 is above the reference by 24 at least
 constexpr int kCols = 512;             // TMEM columns
 
 template <int D>
@@ -655,8 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float sum;
           if (cut) sum = numerators<kMode, true>(rs, ts, lm, rel, m, lim, p);
           else sum = numerators<kMode, false>(rs, ts, lm, rel, m, lim, p);
-          // the sum tells whether the reference was near enough: above 2^60 (or not a number)
-          // it was too low; a row's first sum below 2^-60 may have lost entries
+          // the sum tells whether the reference was near enough: above 2^30 (or not a number)
+          // it was too low; a row's first sum below 2^-30 may have lost entries
           settled |= l > 0.f;
           const bool far = live && lim > 0 && (!(sum < kFar) || (!settled && !(sum > 1.f / kFar)));
           if (named_or(pair, 64, far)) {
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_or(pair, 64, false);
             const float t = fmaxf(top, sm.xtop[st][half ^ 1][row]);
             const bool any_seen = l > 0.f || sm.xl[st][half ^ 1][row] > 0.f;
-            const bool move = live && t > (any_seen ? m + 48.f : -INFINITY);
+            const bool move = live && t > (any_seen ? m + kLeap : -INFINITY);
             const float f = move ? kvcd::ex2(m - t) : 1.f;
             l = move ? (any_seen ? l * f : 0.f) : l;
             // S is ready, so the product before has ended and O is at rest

@@ -1,5 +1,6 @@
 """The chunk calls at the ends of what they accept: caps of every size, caches without
-room, windows that are no multiple of 1/2.  Small cases against the float64 oracle."""
+room, windows that are no multiple of 1/2, values of 2^64.  Small cases against the
+float64 oracle."""
 import numpy as np
 import pytest
 import torch
@@ -165,3 +166,23 @@ def test_window_edge_at_a_far_position(kvc, dtype):
     assert kvc.kvc_device_error() == 0
     ch.check_attn(s, "edge")
     ch.check_mass(s, s["lse"].cpu().numpy(), 0.5, "edge")
+
+
+# ------------------------------------------------------------------ large values
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("natural", [37.1, -37.1, 90.0, 19.0])
+def test_values_up_to_2_64(kvc, natural, n, dtype):
+    """All scores far from 0 and |v| up to 2^64: nothing overflows on the way to the average."""
+    ch = Chunk(kvc, [5000], [n], dtype=dtype, seed=5)
+    r = ch.rows(0, 5000)
+    k = natural * np.sqrt(ch.d) / ch.d
+    ch.q[:], ch.K[r], ch.k_new[:] = 1.0, k, k
+    ch.logm[r] = 0.0
+    ch.V[r] = (ch.V[r].float().abs().clamp(0.25, 1.0) * 2.0 ** 64).to(ch.V.dtype)
+    ch.v_new[:] = (ch.v_new.float().abs().clamp(0.25, 1.0) * 2.0 ** 64).to(ch.V.dtype)
+    s = ch.upload()
+    ch.attn(s)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(s, natural)
