@@ -560,7 +560,8 @@ class ChunkedCache:
         device when not every sequence has that many): q, out [B, L, H*G, T', d],
         k_new, v_new [B, L, H, T', d].  With a `stream`, it must be torch's current
         one."""
-        _check_chunk(self.p, self.p.L, q, k_new, v_new, out)
+        _check_chunk(self.p, self.p.L, q, k_new, v_new, out,
+                     n_new=(n_new, (self.p.B,), torch.int32))
         T = q.shape[3]
         if T > self.T:
             raise ValueError(f"a chunk of {T} tokens, the cache was built for {self.T}")

@@ -65,3 +65,31 @@ def _cpu_cache(monkeypatch, pipeline, **kw):
 def _tokens(T):
     return {n: torch.zeros(2, 2, h, T, 128, dtype=torch.bfloat16)
             for n, h in (("q", 8), ("k_new", 2), ("v_new", 2), ("out", 8))}
+
+
+# ------------------------------------------------------------------ ChunkedCache.step
+def _quiet(monkeypatch, pipeline, calls):
+    for n in ("kvc_chunk_attn", "kvc_chunk_mass", "kvc_mass_evict"):
+        monkeypatch.setattr(pipeline.kvc, n, lambda *a, n=n: calls.append(n))
+
+
+BAD_COUNTS = {
+    "64 bits": torch.tensor([3, 1]),
+    "floats": torch.tensor([3.0, 1.5]),
+    "one for all": torch.tensor([3], dtype=torch.int32),
+    "a number": torch.tensor(3, dtype=torch.int32),
+    "a sequence more": torch.tensor([3, 1, 2], dtype=torch.int32),
+    "two dimensions": torch.tensor([[3, 1]], dtype=torch.int32),
+}
+
+
+@pytest.mark.parametrize("name", list(BAD_COUNTS))
+def test_step_refuses_counts_of_another_type_or_shape(monkeypatch, name):
+    from kv_cache_compression_probe_gb300 import pipeline
+    cache, calls = _cpu_cache(monkeypatch, pipeline), []
+    _quiet(monkeypatch, pipeline, calls)
+    with pytest.raises(ValueError):
+        cache.step(n_new=BAD_COUNTS[name], **_tokens(4))
+    assert not calls and not cache.n_new.any() and not cache.pos_next.any()
+    cache.step(n_new=torch.tensor([3, 1], dtype=torch.int32), **_tokens(4))
+    assert len(calls) == 3 and cache.n_new.tolist() == [3, 1]
