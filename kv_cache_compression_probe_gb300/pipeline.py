@@ -559,7 +559,9 @@ class ChunkedCache:
         """One chunk of q.shape[3] <= T tokens per sequence (n_new [B] int32 on the
         device when not every sequence has that many): q, out [B, L, H*G, T', d],
         k_new, v_new [B, L, H, T', d].  With a `stream`, it must be torch's current
-        one."""
+        one.  A sequence without room for its tokens (evict=False before), or with a
+        count above T', is skipped: it takes no token, its masses do not decay, its
+        next position stays, and kvc_device_error reports it."""
         _check_chunk(self.p, self.p.L, q, k_new, v_new, out,
                      n_new=(n_new, (self.p.B,), torch.int32))
         T = q.shape[3]
@@ -576,7 +578,8 @@ class ChunkedCache:
                            self.ws, stream)
         kvc.kvc_chunk_mass(self.p, c, q, self.K, self.logm, self.pos, self.pos_next, self.len_lh,
                            None, lse, self.decay, self.mass, self.ws, stream, self.cap_lh)
-        self.pos_next.add_(self.n_new)
+        # what was taken, not what was asked for: units that the device skipped keep their length
+        self.pos_next.add_((self.len_new - self.len_lh).flatten(1).amax(1))
         if evict:
             kvc.kvc_mass_evict(self.p, c, self.mass, self.keep_lh, self.recent, self.pos_next,
                                self.K, self.V, self.logm, self.pos, self.len_new, None,

@@ -93,3 +93,28 @@ def test_step_refuses_counts_of_another_type_or_shape(monkeypatch, name):
     assert not calls and not cache.n_new.any() and not cache.pos_next.any()
     cache.step(n_new=torch.tensor([3, 1], dtype=torch.int32), **_tokens(4))
     assert len(calls) == 3 and cache.n_new.tolist() == [3, 1]
+
+
+@pytest.mark.parametrize("evict", [True, False])
+def test_positions_advance_only_with_the_tokens_taken(monkeypatch, evict):
+    """A sequence whose units the device skipped (a count above T, or no room) keeps its next
+    position, so that its later tokens get theirs."""
+    from kv_cache_compression_probe_gb300 import pipeline
+    cache = _cpu_cache(monkeypatch, pipeline)
+    _quiet(monkeypatch, pipeline, [])
+
+    def attn(p, c, q, k, v, pos_new, K, V, logm, pos, len_lh, cap_lh, off, out, lse, len_out, ws, stream):
+        n = cache.n_new[:, None, None]
+        took = (n <= q.shape[3]) & (len_lh + n <= cap_lh)
+        len_out.copy_(torch.where(took, len_lh + n, len_lh))
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_attn", attn)
+    monkeypatch.setattr(pipeline.kvc, "kvc_mass_evict", lambda *a: a[12].copy_(a[10]))
+    at = [0, 0]
+    for ns, took in (([4, 4], [4, 4]), ([9, 2], [0, 2]), ([1, 0], [1, 0]), ([8, 8], [8, 8]), ([8, 8], [8, 8]),
+                     ([8, 8], [8, 8]), ([8, 8], [8, 8]), ([8, 8], [8, 8]), ([8, 2], [0, 2])):
+        if ns == [8, 2]:                                # 45 and 46 of the 48 rows are taken
+            assert cache.len_lh[:, 0, 0].tolist() == [45, 46]
+        cache.step(n_new=torch.tensor(ns, dtype=torch.int32), evict=evict, **_tokens(max(1, min(8, max(ns)))))
+        at = [a + t for a, t in zip(at, took)]
+        assert cache.pos_next.tolist() == at
+        assert cache.len_lh[:, 1, 1].tolist() == at

@@ -186,3 +186,38 @@ def test_values_up_to_2_64(kvc, natural, n, dtype):
     torch.cuda.synchronize()
     assert kvc.kvc_device_error() == 0
     ch.check_attn(s, natural)
+
+
+# ------------------------------------------------------------------ a step that is skipped
+def test_a_skipped_step_leaves_no_gap(kvc):
+    """A cache that is asked for more than it has room for goes on as if it had not been asked."""
+    from kv_cache_compression_probe_gb300.pipeline import ChunkedCache
+
+    def make():
+        p = kvc.make_params(B=2, L=2, H=2, G=4, d=64, P=1, W=1, n_max=64, S_max=1, dtype=kvc.KVC_BF16)
+        sl = 2.0 ** -torch.arange(1, 9, dtype=torch.float32, device="cuda")
+        return ChunkedCache(p, budget=32, T=8, page_rows=16, recent=4, slopes=sl, window=40.0)
+    g = torch.Generator().manual_seed(2)
+    caches, outs = (make(), make()), ([], [])
+    for ns, evict, refused in (([8, 8], True, False), ([8, 5], False, False), ([8, 8], False, False),
+                               ([8, 8], False, False), ([8, 8], False, False), ([8, 8], False, False),
+                               ([8, 1], False, True), ([9, 0], False, True), ([0, 2], True, False), ([8, 8], True, False)):
+        x = [torch.randn((2, 2, h, 8, 64), generator=g).to(torch.bfloat16).cuda() for h in (8, 2, 2)]
+        for k, cache in enumerate(caches):
+            n = torch.tensor([0, ns[1]] if refused and k else ns, dtype=torch.int32, device="cuda")
+            if refused and k and ns[1] == 0:           # the other cache is not asked at all
+                continue
+            out = torch.zeros_like(x[0])
+            cache.step(*x, out, n, evict=evict)
+            torch.cuda.synchronize()
+            code = kvc.kvc_device_error()
+            if refused and k == 0:
+                assert code == (kvc.KVC_ECAPACITY if ns[0] == 8 else kvc.KVC_EDEVICE)
+            else:
+                assert code == 0
+                if not refused:
+                    outs[k].append(out)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.equal(caches[0].pos_next, caches[1].pos_next) and caches[0].pos_next.tolist() == [56.0, 56.0]
+    assert torch.equal(caches[0].len_lh, caches[1].len_lh)
