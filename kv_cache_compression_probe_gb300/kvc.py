@@ -138,10 +138,13 @@ def _ptr(t):
     return c_void_p(t.data_ptr())
 
 
-def _ptrs(*tensors):
-    """Addresses of the tensors of one call: contiguous and on the current CUDA
-    device (the one whose kernels the call launches); None stays None."""
-    dev = torch._C._cuda_getDevice()
+def _ptrs(c, *tensors):
+    """Addresses of the tensors of one call with chunk block c: contiguous and, like the
+    block's own, on the current CUDA device (the one whose kernels the call launches);
+    None stays None."""
+    dev = torch.cuda.current_device()
+    if getattr(c, "_devices", ()) not in ((), (dev,)):
+        raise ValueError("the chunk block's tensors must be on the current CUDA device")
     out = []
     for t in tensors:
         if t is None:
@@ -160,8 +163,13 @@ def _ptrs(*tensors):
 def _raw_stream(stream):
     """The stream's handle; torch's current stream of the current device by default."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        # torch.cuda.current_stream().cuda_stream, without its 2.8 us (a call takes 12)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if stream.device_index != torch.cuda.current_device():
+        raise ValueError("the stream must belong to the current CUDA device")
+    return stream.cuda_stream
 
 
 def _stream(stream):
@@ -209,6 +217,7 @@ def make_chunk(T, layer_begin=0, layer_end=1, page_rows=0, page_table=None, n_ne
             raise TypeError(f"{name} must be {dt}")
         setattr(c, name, _ptr(t))
     c._keep = (page_table, n_new, slopes)
+    c._devices = tuple({t.get_device() for t in c._keep if t is not None})
     return c
 
 
@@ -365,8 +374,8 @@ def kvc_chunk_attn(p, c, q, k_new, v_new, pos_new, Kp, Vp, logm, pos, len_lh, ca
                    lse, len_out, workspace, stream=None):
     """Attention of a chunk of new tokens over the packed cache (contiguous rows
     or pages); lse, len_out and, with pages, off_lh may be None."""
-    _check(lib().kvc_chunk_attn(p, c, *_ptrs(q, k_new, v_new, pos_new, Kp, Vp, logm, pos, len_lh,
-                                             cap_lh, off_lh, out, lse, len_out, workspace),
+    _check(lib().kvc_chunk_attn(p, c, *_ptrs(c, q, k_new, v_new, pos_new, Kp, Vp, logm, pos,
+                                             len_lh, cap_lh, off_lh, out, lse, len_out, workspace),
                                 workspace.nbytes, _raw_stream(stream)), "kvc_chunk_attn")
 
 
@@ -375,7 +384,7 @@ def kvc_chunk_mass(p, c, q, Kp, logm, pos, pos_new, len_lh, off_lh, lse, decay, 
     """mass = decay * mass + the attention weight every entry received from the
     chunk (len_lh: the lengths before it).  cap_lh, the capacities kvc_chunk_attn was
     given, is needed where a (b, l, h) may have been full: it is skipped here too."""
-    a = _ptrs(q, Kp, logm, pos, pos_new, len_lh, cap_lh, off_lh, lse, mass, workspace)
+    a = _ptrs(c, q, Kp, logm, pos, pos_new, len_lh, cap_lh, off_lh, lse, mass, workspace)
     _check(lib().kvc_chunk_mass_cap(p, c, *a[:9], decay, a[9], a[10], workspace.nbytes,
                                     _raw_stream(stream)), "kvc_chunk_mass")
 
@@ -387,7 +396,7 @@ def kvc_mass_evict_workspace_bytes(p, c, max_len: int) -> int:
 def kvc_mass_evict(p, c, mass, keep_lh, recent, pos_next, Kp, Vp, logm, pos, len_lh, off_lh,
                    len_out, max_len, workspace, stream=None):
     """Per-(b, l, h) eviction down to keep_lh entries by mass, in place."""
-    a = _ptrs(mass, keep_lh, pos_next, Kp, Vp, logm, pos, len_lh, off_lh, len_out, workspace)
+    a = _ptrs(c, mass, keep_lh, pos_next, Kp, Vp, logm, pos, len_lh, off_lh, len_out, workspace)
     _check(lib().kvc_mass_evict(p, c, a[0], a[1], recent, *a[2:10], max_len, a[10], workspace.nbytes,
                                 _raw_stream(stream)), "kvc_mass_evict")
 

@@ -564,6 +564,8 @@ class ChunkedCache:
         next position stays, and kvc_device_error reports it."""
         _check_chunk(self.p, self.p.L, q, k_new, v_new, out,
                      n_new=(n_new, (self.p.B,), torch.int32))
+        if stream is not None and kvc._raw_stream(stream) != kvc._raw_stream(None):
+            raise ValueError("the stream must be torch's current one")
         T = q.shape[3]
         if T > self.T:
             raise ValueError(f"a chunk of {T} tokens, the cache was built for {self.T}")

@@ -118,3 +118,81 @@ def test_positions_advance_only_with_the_tokens_taken(monkeypatch, evict):
         at = [a + t for a, t in zip(at, took)]
         assert cache.pos_next.tolist() == at
         assert cache.len_lh[:, 1, 1].tolist() == at
+
+
+# ------------------------------------------------------------------ streams and devices
+class _Stream:
+    """A stream of device `dev`, as far as the binding looks at it."""
+
+    def __init__(self, dev, handle):
+        self.device_index, self.cuda_stream = dev, handle
+
+
+class _Tensor:
+    def __init__(self, dev):
+        self.dev, self.nbytes = dev, 1 << 20
+
+    def get_device(self):
+        return self.dev
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096 * (self.dev + 1)
+
+
+class _Lib:
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.streams.append(a[-1]) or kvc.KVC_OK
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """The binding as it would be with device 1 current and stream 77 on it; returns the library."""
+    fake = _Lib()
+    monkeypatch.setattr(kvc.torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(kvc.torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(kvc.torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + 7 * d, raising=False)
+    monkeypatch.setattr(kvc.torch.cuda, "Stream", _Stream)
+    monkeypatch.setattr(kvc, "lib", lambda: fake)
+    return fake
+
+
+def _calls(c, dev, stream):
+    t = _Tensor(dev)
+    yield lambda: kvc.kvc_chunk_attn(None, c, *[t] * 15, stream)
+    yield lambda: kvc.kvc_chunk_mass(None, c, *[t] * 8, 1.0, t, t, stream)
+    yield lambda: kvc.kvc_mass_evict(None, c, t, t, 4, *[t] * 8, 100, t, stream)
+
+
+def test_streams_and_tensors_of_another_device_are_refused(two_devices):
+    for stream in (None, _Stream(1, 5), 9):
+        for call in _calls(_chunk(), 1, stream):
+            call()
+    assert two_devices.streams == [77] * 3 + [5] * 3 + [9] * 3
+    other = _chunk()
+    other._devices = (0,)                               # a page table, say
+    both = _chunk()
+    both._devices = (0, 1)
+    for c, dev, stream in ((_chunk(), 1, _Stream(0, 5)), (_chunk(), 0, None), (other, 1, None), (both, 1, None)):
+        for call in _calls(c, dev, stream):
+            with pytest.raises(ValueError):
+                call()
+    assert len(two_devices.streams) == 9
+
+
+def test_step_refuses_a_stream_that_is_not_the_current_one(monkeypatch, two_devices):
+    from kv_cache_compression_probe_gb300 import pipeline
+    cache, calls = _cpu_cache(monkeypatch, pipeline), []
+    _quiet(monkeypatch, pipeline, calls)
+    for stream in (_Stream(1, 5), 5, _Stream(0, 77)):
+        with pytest.raises(ValueError):
+            cache.step(stream=stream, **_tokens(4))
+    assert not calls and not cache.pos_next.any()
+    for stream in (_Stream(1, 77), 77, None):
+        cache.step(stream=stream, **_tokens(4))
+    assert len(calls) == 9
