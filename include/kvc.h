@@ -486,7 +486,8 @@ int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const void* q, const
 
 /* Workspace bytes of kvc_chunk_attn and kvc_chunk_mass (one buffer may serve
  * both, call after call; 256-byte aligned device memory, no initialisation
- * needed); 0 for invalid arguments.  Depends on p, T and the layer range. */
+ * needed); 0 for invalid arguments.  Depends on d, the type and the number of
+ * (b,l,h) in the layer range, not on T. */
 size_t kvc_chunk_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk* c /* host */);
 
 /* The attention weight every entry received from the chunk, accumulated:

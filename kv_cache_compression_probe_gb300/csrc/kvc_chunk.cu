@@ -532,19 +532,22 @@ struct ChunkLayout {
   size_t rec, first, seg, part, ml, total;
 };
 
-constexpr int kMaxRowsBlock = 256;     // rows of one partial result at most
-constexpr int kCtaPerSm = 2;           // pieces per SM at most
+// Partial results: two per CTA.  The bf16 kernels run one CTA per SM, with up to 256 rows (mass:
+// 128 entries); the fp32 kernels two, with up to 64 rows (64 entries).
+constexpr int kMaxRowsTc = 256, kCtasTc = 1, kMaxRowsSimt = 64, kCtasSimt = 2;
 
 ChunkLayout chunk_layout(const kvc_params* p, const kvc_chunk* c) {
   const size_t units = (size_t)p->B * p->H * (c->layer_end - c->layer_begin);
-  const size_t ctas = (size_t)kCtaPerSm * std::max(kvc::sm_count(), 1);
+  const bool tc = p->dtype == KVC_BF16;
+  const size_t ctas = (size_t)(tc ? kCtasTc : kCtasSimt) * std::max(kvc::sm_count(), 1);
+  const size_t rows = ctas * 2 * (tc ? kMaxRowsTc : kMaxRowsSimt);
   ChunkLayout w;
   w.rec = 0;
   w.first = kvc::align256(units * sizeof(int4));
   w.seg = w.first + kvc::align256(units * sizeof(int32_t));
   w.part = w.seg + kvc::align256(ctas * sizeof(ChunkSeg));
-  w.ml = w.part + kvc::align256(ctas * 2 * kMaxRowsBlock * p->d * sizeof(float));
-  w.total = w.ml + kvc::align256(ctas * 2 * kMaxRowsBlock * 2 * sizeof(float));
+  w.ml = w.part + kvc::align256(rows * p->d * sizeof(float));
+  w.total = w.ml + kvc::align256(rows * 2 * sizeof(float));
   return w;
 }
 
@@ -584,7 +587,7 @@ cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(SimtSmem<D, MR>);
   cudaError_t e = kvc::chunk_allow_smem<chunk_attn_simt_kernel<T, D, MR>>(smem);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sms;
+  const int grid = kCtasSimt * sms;
   e = kvc::chunk_launch(chunk_attn_simt_kernel<T, D, MR>, dim3(grid), dim3(kSimtThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
@@ -630,7 +633,7 @@ cudaError_t launch_mass(ChunkArgs& a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(SimtSmem<D, 64>);
   e = kvc::chunk_allow_smem<chunk_mass_simt_kernel<T, D>>(smem);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sms;
+  const int grid = kCtasSimt * sms;
   e = kvc::chunk_launch(chunk_mass_simt_kernel<T, D>, dim3(grid), dim3(kSimtThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();

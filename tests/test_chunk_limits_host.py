@@ -196,3 +196,40 @@ def test_step_refuses_a_stream_that_is_not_the_current_one(monkeypatch, two_devi
     for stream in (_Stream(1, 77), 77, None):
         cache.step(stream=stream, **_tokens(4))
     assert len(calls) == 9
+
+
+# ------------------------------------------------------------------ workspaces
+def test_workspace_depends_on_the_units_only(lib):
+    """As much as the kernels use (without a GPU the library counts one SM): a record and a tile
+    number per (b,l,h), and two partial results per CTA, of 256 rows (bf16) or 64 (fp32, two CTAs)."""
+    for dtype, rows in ((kvc.KVC_BF16, 512), (kvc.KVC_F32, 256)):
+        for d in (64, 128):
+            for B, L, H in ((1, 1, 1), (2, 4, 2), (16, 32, 8)):
+                p = _params(B=B, L=L, H=H, d=d, dtype=dtype, packed_rows=1 << 20)
+                sizes = {kvc.kvc_chunk_workspace_bytes(p, _chunk(T=T, layer_end=L, **more))
+                         for T in (1, 40, 2048, 65536) for more in ({}, PAGED, dict(window=5.0, softcap=3.0))}
+                units = B * L * H
+                need = 16 * units + 4 * units + 16 + rows * (d + 2) * 4
+                assert len(sizes) == 1
+                if not torch.cuda.is_available():
+                    assert need <= sizes.pop() <= need + 5 * 256
+
+
+def test_extend_grows_its_workspace_with_the_layers(monkeypatch, lib):
+    """With the library's own sizes: a larger layer range outgrows the workspace, which stays alive for
+    calls captured with it; more tokens do not."""
+    from kv_cache_compression_probe_gb300 import pipeline
+    used = []
+    monkeypatch.setattr(pipeline.kvc, "kvc_chunk_attn", lambda *a: used.append(a[-2]))
+    comp = object.__new__(pipeline.Compressor)
+    comp.p = kvc.make_params(B=4, L=32, H=8, G=1, d=64, P=1, W=1, n_max=64, S_max=1, dtype=kvc.KVC_BF16)
+    comp.device, comp._ws_chunk, comp._ws_outgrown = "cpu", None, []
+    comp.Kp = torch.zeros(64, 64)
+    for name in ("Vp", "logm", "pos", "len_lh", "cap_lh", "off_lh"):
+        setattr(comp, name, None)
+    for T, layers in ((1, (0, 1)), (9, (3, 4)), (1, (0, 32)), (9, None), (2, (5, 6))):
+        n = 32 if layers is None else layers[1] - layers[0]
+        q = torch.zeros(4, n, 8, T, 64, dtype=torch.bfloat16)
+        comp.extend(q, q, q, q, torch.zeros(4), layers=layers)
+    assert used[0] is used[1] and used[2] is used[3] and used[3] is used[4] and used[0] is not used[2]
+    assert len(comp._ws_outgrown) == 1 and comp._ws_outgrown[0] is used[0]
