@@ -163,35 +163,14 @@ struct SimtSmem {
   kvcd::LocateSmem loc;
 };
 
-// Rows [first, first + count) of a [.., D] array given by `row`, as fp32 in
-// shared memory; rows past `count` are zeroed.
-template <typename T, int D, int kRows, int kStride, class RowFn>
-__device__ __forceinline__ void stage_rows(float* dst, const T* src, int count, RowFn row) {
-  constexpr int kE = 16 / (int)sizeof(T);
-  constexpr int kVec = D / kE;
+// `count` rows of a [.., D] array in shared memory, row r from row(r); the rest of the kRows zeroed.
+template <int D, int kRows, int kStride, class RowFn>
+__device__ __forceinline__ void stage_rows(float* dst, const float* src, int count, RowFn row) {
+  constexpr int kVec = D / 4;
   for (int i = threadIdx.x; i < kRows * kVec; i += kSimtThreads) {
     const int r = i / kVec, v = i % kVec;
-    float x[kE];
-    if (r < count) {
-      const uint4 w = *reinterpret_cast<const uint4*>(src + row(r) * D + v * kE);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = __uint_as_float(ws[e] << 16);
-          x[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(ws[e]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kE; ++e) x[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < kE; e += 4)
-      *reinterpret_cast<float4*>(dst + r * kStride + v * kE + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    *reinterpret_cast<float4*>(dst + r * kStride + v * 4) =
+        r < count ? *reinterpret_cast<const float4*>(src + row(r) * D + v * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
@@ -239,7 +218,7 @@ __device__ __forceinline__ void stage_bias(const ChunkArgs& a, float* lm, float*
 }
 
 // ---------------------------------------------------------------- fp32 attention
-template <typename T, int D, int MR>
+template <int D, int MR>
 __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkArgs a) {
   constexpr int R = MR / 16, C = D / 64;               // rows and 4-feature groups per thread
   extern __shared__ __align__(16) unsigned char simt_raw[];
@@ -265,7 +244,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkA
     const kvcd::RowMap rows = kvcd::row_map(a, u, w.r.off);
     const int used = a.G * a.tt;                       // rows of the block in use
     __syncthreads();
-    stage_rows<T, D, MR, D + 4>(&sm.q[0][0], static_cast<const T*>(a.q), used, [&](int r) {
+    stage_rows<D, MR, D + 4>(&sm.q[0][0], static_cast<const float*>(a.q), used, [&](int r) {
       return (u * a.G + r / a.tt) * a.T + min(a.T - 1, t0 + r % a.tt);
     });
     int tok[R], lim[R];
@@ -289,8 +268,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkA
       const int e0 = w.r.first + tile * kKeys, cnt = min(kKeys, total - e0);
       __syncthreads();
       auto row = [&](int r) { return rows(e0 + r); };
-      stage_rows<T, D, kKeys, D + 4>(&sm.k[0][0], static_cast<const T*>(a.Kp), cnt, row);
-      stage_rows<T, D, kKeys, D>(&sm.v[0][0], static_cast<const T*>(a.Vp), cnt, row);
+      stage_rows<D, kKeys, D + 4>(&sm.k[0][0], static_cast<const float*>(a.Kp), cnt, row);
+      stage_rows<D, kKeys, D>(&sm.v[0][0], static_cast<const float*>(a.Vp), cnt, row);
       stage_bias(a, sm.lm, sm.rel, e0, cnt, rows, pos0);
       __syncthreads();
       float s[R][4];
@@ -362,7 +341,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_attn_simt_kernel(ChunkA
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            static_cast<T*>(a.out)[orow * D + c * 64 + tx * 4 + e] = kvcd::from_f<T>(o[i][c][e] * inv);
+            static_cast<float*>(a.out)[orow * D + c * 64 + tx * 4 + e] = o[i][c][e] * inv;
         if (a.lse && tx == 0) a.lse[orow] = l[i] > 0.f ? m[i] + log2f(l[i]) : -INFINITY;
       } else {
         const int64_t prow = slot * MR + r;
@@ -445,7 +424,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- fp32 mass
 // The tile's keys stay in shared memory while the query rows pass.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkArgs a) {
   constexpr int MR = 64, R = 4;
   extern __shared__ __align__(16) unsigned char simt_raw[];
@@ -466,13 +445,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2) chunk_mass_simt_kernel(ChunkA
     const int cnt = min(kKeys, w.r.len + w.r.n - e0);
     const int used = a.G * a.tt;
     __syncthreads();
-    stage_rows<T, D, kKeys, D + 4>(&sm.k[0][0], static_cast<const T*>(a.Kp), cnt, [&](int r) { return rows(e0 + r); });
+    stage_rows<D, kKeys, D + 4>(&sm.k[0][0], static_cast<const float*>(a.Kp), cnt, [&](int r) { return rows(e0 + r); });
     stage_bias(a, sm.lm, sm.rel, e0, cnt, rows, pos0);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int rt = w.tb; rt < w.te; ++rt) {
       const int t0 = rt * a.tt;
       __syncthreads();
-      stage_rows<T, D, MR, D + 4>(&sm.q[0][0], static_cast<const T*>(a.q), used, [&](int r) {
+      stage_rows<D, MR, D + 4>(&sm.q[0][0], static_cast<const float*>(a.q), used, [&](int r) {
         return (u * a.G + r / a.tt) * a.T + min(a.T - 1, t0 + r % a.tt);
       });
       __syncthreads();
@@ -566,32 +545,27 @@ cudaError_t launch_prepare(const ChunkArgs& a, cudaStream_t s) {
   return kvc::chunk_launch(chunk_window_kernel, dim3((unsigned)a.units), dim3(kWinThreads), 0, s, a);
 }
 
-template <typename T, int D>
-cudaError_t launch_combine(const ChunkArgs& a, int rows_block, int grid, cudaStream_t s) {
+template <typename T, int D, int kRowsBlock>
+cudaError_t launch_combine(const ChunkArgs& a, int grid, cudaStream_t s) {
   if (grid < 2) return cudaSuccess;
   kvc::count_launch();
-  const dim3 g(grid - 1, rows_block / 8);
-  switch (rows_block) {
-    case 16: return kvc::chunk_launch(chunk_combine_kernel<T, D, 16>, g, dim3(256), 0, s, a, grid);
-    case 64: return kvc::chunk_launch(chunk_combine_kernel<T, D, 64>, g, dim3(256), 0, s, a, grid);
-    case 128: return kvc::chunk_launch(chunk_combine_kernel<T, D, 128>, g, dim3(256), 0, s, a, grid);
-    default: return kvc::chunk_launch(chunk_combine_kernel<T, D, 256>, g, dim3(256), 0, s, a, grid);
-  }
+  return kvc::chunk_launch(chunk_combine_kernel<T, D, kRowsBlock>, dim3(grid - 1, kRowsBlock / 8), dim3(256), 0, s, a,
+                           grid);
 }
 
-template <typename T, int D, int MR>
+template <int D, int MR>
 cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
   a.tt = std::min(MR / a.G, a.T);
   a.tpb = a.tt;
   a.rp = (a.T + a.tpb - 1) / a.tpb;
   const size_t smem = sizeof(SimtSmem<D, MR>);
-  cudaError_t e = kvc::chunk_allow_smem<chunk_attn_simt_kernel<T, D, MR>>(smem);
+  cudaError_t e = kvc::chunk_allow_smem<chunk_attn_simt_kernel<D, MR>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = kCtasSimt * sms;
-  e = kvc::chunk_launch(chunk_attn_simt_kernel<T, D, MR>, dim3(grid), dim3(kSimtThreads), smem, s, a);
+  e = kvc::chunk_launch(chunk_attn_simt_kernel<D, MR>, dim3(grid), dim3(kSimtThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return launch_combine<T, D>(a, MR, grid, s);
+  return launch_combine<float, D, MR>(a, grid, s);
 }
 
 template <int D>
@@ -599,15 +573,15 @@ cudaError_t launch_attn_bf16(ChunkArgs& a, int sms, int page_rows, cudaStream_t 
   cudaError_t e = launch_prepare<__nv_bfloat16, D>(a, s);
   if (e == cudaSuccess) e = kvc::chunk_attn_tc_launch(a, D, sms, page_rows, s);
   if (e != cudaSuccess) return e;
-  return launch_combine<__nv_bfloat16, D>(a, a.T > a.tt ? 256 : 128, sms, s);
+  return a.T > a.tt ? launch_combine<__nv_bfloat16, D, 256>(a, sms, s) : launch_combine<__nv_bfloat16, D, 128>(a, sms, s);
 }
 
-template <typename T, int D>
-cudaError_t launch_attn(ChunkArgs& a, int sms, cudaStream_t s) {
-  cudaError_t e = launch_prepare<T, D>(a, s);
+template <int D>
+cudaError_t launch_attn_f32(ChunkArgs& a, int sms, cudaStream_t s) {
+  cudaError_t e = launch_prepare<float, D>(a, s);
   if (e != cudaSuccess) return e;
-  if (a.G * a.T <= 16) return launch_attn_simt<T, D, 16>(a, sms, s);
-  return launch_attn_simt<T, D, 64>(a, sms, s);
+  if (a.G * a.T <= 16) return launch_attn_simt<D, 16>(a, sms, s);
+  return launch_attn_simt<D, 64>(a, sms, s);
 }
 
 template <int kTile>
@@ -625,16 +599,16 @@ cudaError_t launch_mass_bf16(ChunkArgs& a, int sms, int page_rows, cudaStream_t 
   return launch_mass_combine<128>(a, sms, s);
 }
 
-template <typename T, int D>
-cudaError_t launch_mass(ChunkArgs& a, int sms, cudaStream_t s) {
-  cudaError_t e = launch_prepare<T, D>(a, s);
+template <int D>
+cudaError_t launch_mass_f32(ChunkArgs& a, int sms, cudaStream_t s) {
+  cudaError_t e = launch_prepare<float, D>(a, s);
   if (e != cudaSuccess) return e;
   a.tt = std::min(64 / a.G, a.T);
   const size_t smem = sizeof(SimtSmem<D, 64>);
-  e = kvc::chunk_allow_smem<chunk_mass_simt_kernel<T, D>>(smem);
+  e = kvc::chunk_allow_smem<chunk_mass_simt_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = kCtasSimt * sms;
-  e = kvc::chunk_launch(chunk_mass_simt_kernel<T, D>, dim3(grid), dim3(kSimtThreads), smem, s, a);
+  e = kvc::chunk_launch(chunk_mass_simt_kernel<D>, dim3(grid), dim3(kSimtThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
   return launch_mass_combine<kKeys>(a, grid, s);
@@ -739,7 +713,7 @@ extern "C" int kvc_chunk_attn(const kvc_params* p, const kvc_chunk* c, const voi
   if (p->dtype == KVC_BF16)
     e = p->d == 128 ? launch_attn_bf16<128>(a, sms, c->page_rows, s) : launch_attn_bf16<64>(a, sms, c->page_rows, s);
   else
-    e = p->d == 128 ? launch_attn<float, 128>(a, sms, s) : launch_attn<float, 64>(a, sms, s);
+    e = p->d == 128 ? launch_attn_f32<128>(a, sms, s) : launch_attn_f32<64>(a, sms, s);
   return kvc::cuda_status(e);
 }
 
@@ -777,6 +751,6 @@ extern "C" int kvc_chunk_mass_cap(const kvc_params* p, const kvc_chunk* c, const
   if (p->dtype == KVC_BF16)
     e = p->d == 128 ? launch_mass_bf16<128>(a, sms, c->page_rows, s) : launch_mass_bf16<64>(a, sms, c->page_rows, s);
   else
-    e = p->d == 128 ? launch_mass<float, 128>(a, sms, s) : launch_mass<float, 64>(a, sms, s);
+    e = p->d == 128 ? launch_mass_f32<128>(a, sms, s) : launch_mass_f32<64>(a, sms, s);
   return kvc::cuda_status(e);
 }

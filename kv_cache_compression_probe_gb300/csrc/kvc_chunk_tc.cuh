@@ -69,21 +69,11 @@ __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.pr
 __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : KVC_P16(r, 0));
 }
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : KVC_P16(r, 0), KVC_P16(r, 16));
-}
-// 16 or 32 consecutive TMEM columns of this thread's lane (no wait).
+// 16 consecutive TMEM columns of this thread's lane (no wait).
 __device__ __forceinline__ void tld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : KVC_R16(r, 0)
-      : "r"(addr));
-}
-__device__ __forceinline__ void tld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : KVC_R16(r, 0), KVC_R16(r, 16)
       : "r"(addr));
 }
 __device__ __forceinline__ void tst16(uint32_t addr, const uint32_t (&r)[16]) {

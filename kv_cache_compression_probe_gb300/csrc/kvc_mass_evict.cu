@@ -88,7 +88,6 @@ struct PlanSmem {
   uint32_t hist[2][kBins];             // passes alternate, so one barrier a pass is enough
   int warp[2][2][32];                  // sums of block_prefix: two buffers of two counts
   int ties, holes, movers, safe;       // this CTA's counts, read by the cluster
-  int ok;
   uint32_t prefix;
   int rem, found;                      // entries of the bin that stay; whether that is all of it
 };
