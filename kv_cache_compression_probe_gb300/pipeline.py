@@ -511,7 +511,8 @@ class ChunkedCache:
     A step attends (kvc_chunk_attn), adds the chunk's attention weight to the
     entries' masses (kvc_chunk_mass) and, with evict=True, drops what has least
     of it until `budget` entries are left (kvc_mass_evict), the last `recent`
-    positions always staying.  Nothing waits for the device, so steps can be
+    positions always staying.  The masses decay once a step, for a chunk of T tokens as
+    for a single one (and for a sequence without new tokens).  Nothing waits for the device, so steps can be
     captured into a CUDA graph.  The class only allocates and marshals.
     """
 
@@ -520,6 +521,8 @@ class ChunkedCache:
                  slopes=None, device="cuda"):
         if not 0 <= recent <= budget:
             raise ValueError("the protected positions must fit the budget")
+        if not 0.0 <= decay <= 1.0:
+            raise ValueError("decay must be in 0..1")
         if slopes is not None and (tuple(slopes.shape) != (p.H * p.G,) or slopes.dtype != torch.float32):
             raise ValueError(f"slopes must be [{p.H * p.G}] float32")
         B, L, H = p.B, p.L, p.H
@@ -566,6 +569,8 @@ class ChunkedCache:
                      n_new=(n_new, (self.p.B,), torch.int32))
         if stream is not None and kvc._raw_stream(stream) != kvc._raw_stream(None):
             raise ValueError("the stream must be torch's current one")
+        if evict and self.p.B * self.p.L * self.p.H > 65535:
+            raise ValueError("the eviction takes up to 65535 (b, l, h)")
         T = q.shape[3]
         if T > self.T:
             raise ValueError(f"a chunk of {T} tokens, the cache was built for {self.T}")

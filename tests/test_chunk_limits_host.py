@@ -233,3 +233,22 @@ def test_extend_grows_its_workspace_with_the_layers(monkeypatch, lib):
         comp.extend(q, q, q, q, torch.zeros(4), layers=layers)
     assert used[0] is used[1] and used[2] is used[3] and used[3] is used[4] and used[0] is not used[2]
     assert len(comp._ws_outgrown) == 1 and comp._ws_outgrown[0] is used[0]
+
+
+# ------------------------------------------------------------------ no step ends half way
+def test_what_a_later_call_of_a_step_would_refuse_is_refused_first(monkeypatch):
+    """The eviction takes up to 65535 (b,l,h) and the mass call a decay in 0..1: a step that cannot end
+    does not begin."""
+    from kv_cache_compression_probe_gb300 import pipeline
+    for decay in (-0.1, 1.5, float("nan")):
+        with pytest.raises(ValueError):
+            _cpu_cache(monkeypatch, pipeline, decay=decay)
+    cache, calls = _cpu_cache(monkeypatch, pipeline), []
+    _quiet(monkeypatch, pipeline, calls)
+    cache.p.B = 16384                                   # 65536 (b,l,h)
+    x = {n: t[:1].expand(16384, *t.shape[1:]) for n, t in _tokens(1).items()}
+    with pytest.raises(ValueError):
+        cache.step(**x)
+    assert not calls and not cache.pos_next.any()
+    cache.step(evict=False, **x)
+    assert calls == ["kvc_chunk_attn", "kvc_chunk_mass"]
