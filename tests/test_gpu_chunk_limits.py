@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from tests.chunk_cases import Chunk
 
 pytestmark = pytest.mark.gpu
@@ -221,3 +222,50 @@ def test_a_skipped_step_leaves_no_gap(kvc):
         assert torch.equal(a, b)
     assert torch.equal(caches[0].pos_next, caches[1].pos_next) and caches[0].pos_next.tolist() == [56.0, 56.0]
     assert torch.equal(caches[0].len_lh, caches[1].len_lh)
+
+
+# ------------------------------------------------------------------ far rows
+FAR = 17_000_000                                       # rows: 2^31 elements of d 128 lie before them
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [0, 64])
+def test_rows_past_32_bit_offsets(kvc, page, dtype):
+    """Attention, mass and eviction of a cache whose rows begin beyond 2^31 elements."""
+    n = [5, 40]
+    ch = Chunk(kvc, [100, 300, 64, 700], n, B=2, H=2, dtype=dtype, page=page, window=200.0, slopes=True, seed=6)
+    s = ch.upload()
+    base = -(-FAR // 1024) * 1024
+    small = {k: s[k] for k in ("K", "V", "logm", "pos", "mass")}
+    for k, t in small.items():
+        s[k] = torch.empty((base + t.shape[0], *t.shape[1:]), dtype=t.dtype, device="cuda")
+        s[k][base:] = t
+    s["p"].packed_rows = base + ch.rows_total
+    s["off"] += base
+    if page:
+        s["c"]._keep[0].add_(base // page)
+    ch.attn(s)
+    ch.run_mass(s, 0.5)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(dict(s, **{k: s[k][base:] for k in small}), "far")
+    ch.check_mass(dict(s, mass=s["mass"][base:]), s["lse"].cpu().numpy(), 0.5, "far")
+    got = {k: s[k][base:].cpu() for k in small}        # and the eviction, from here
+    keep = s["len_out"] // 2
+    ws = torch.empty(kvc.kvc_mass_evict_workspace_bytes(s["p"], s["c"], 800), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(s["len_out"])
+    kvc.kvc_mass_evict(s["p"], s["c"], s["mass"], keep, 8, s["pos_new"], s["K"], s["V"], s["logm"], s["pos"],
+                       s["len_out"], None if page else s["off"], out, 800, ws)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    for u in ch.units:
+        b = u // 2
+        r = ch.rows(u, int(ch.lens[u]) + n[b])
+        B, holes, movers = O.mass_evict(got["mass"].numpy()[r], got["pos"].numpy()[r], len(r) // 2,
+                                        ch.pos_new[b] - np.float32(8))
+        assert int(out.view(-1)[u]) == B
+        for k, t in got.items():
+            t[r[holes]] = t[r[movers]]
+    for k, t in got.items():
+        bits = torch.int16 if t.element_size() == 2 else torch.int32
+        assert torch.equal(s[k][base:].cpu().view(bits), t.view(bits)), k
