@@ -269,3 +269,28 @@ def test_rows_past_32_bit_offsets(kvc, page, dtype):
     for k, t in got.items():
         bits = torch.int16 if t.element_size() == 2 else torch.int32
         assert torch.equal(s[k][base:].cpu().view(bits), t.view(bits)), k
+
+
+# ------------------------------------------------------------------ long chunks
+LONG = {
+    "slopes": dict(lens=[500, 130], n_new=[700], H=2, slopes=True, page=64),
+    "window": dict(lens=[500, 130], n_new=[700], H=2, window=300.0),
+    "cap": dict(lens=[500, 130], n_new=[700], H=2, softcap=20.0, qscale=3.0),
+    "all of it, ragged": dict(lens=[500, 130, 0, 900], n_new=[700, 333], B=2, H=2, softcap=50.0, slopes=True,
+                              window=411.5, page=128, qscale=3.0),
+    "4000 tokens": dict(lens=[300], n_new=[4000], G=1, d=64, slopes=True),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(LONG))
+def test_modified_scores_over_long_chunks(kvc, name, dtype):
+    """Many row tiles with a bias, a window or a cap: attention, and the mass from its lse."""
+    ch = Chunk(kvc, dtype=dtype, seed=30 + list(LONG).index(name), **LONG[name])
+    s = ch.upload()
+    ch.attn(s)
+    ch.run_mass(s, 0.9)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    ch.check_attn(s, name)
+    ch.check_mass(s, s["lse"].cpu().numpy(), 0.9, name)
