@@ -24,8 +24,8 @@
 // of alternate tiles (and 3 clears the V rows past the last entry), 4..11 and 12..19 are the softmax of the two streams.  The
 // work is cut as kvc_chunk.cuh says; persistent, one CTA per SM (512 TMEM
 // columns: S, S, O, O; P lies in S's place).
-// Measured (d 128, G 4): 2048 tokens over 16K entries, 8 KV heads: 375 us, 1375
-// TFLOP/s; one token over 256 caches of 3200..5000 entries: 98 us, 5.5 TB/s.
+// Measured (d 128, G 4): 2048 tokens over 16K entries, 8 KV heads: 371 us, 1390
+// TFLOP/s; one token over 256 caches of 3200..5000 entries: 95 us, 5.7 TB/s.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -162,7 +162,11 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 }
 
 // Numerators 2^(s - base) of a row over 64 entries of a tile, packed as bf16 pairs;
-// returns their sum in fp32.  The products come from TMEM in blocks of 16, the next
+// returns their sum in fp32, of the unrounded ones (the log-sum-exp goes on to the masses).  The
+// product with V takes both operands of one type, and V is bf16; independent roundings of the
+// numerators add as much error as that of the result (0.0023 instead of 0.0017 against 64 bits, for any
+// number of entries).  A second bf16 part of P would cost the exponentials twice, because 64 numerators
+// and their products do not fit this thread's 96 registers, and half as many products again.  The products come from TMEM in blocks of 16, the next
 // block on its way while one is worked on.
 template <int kMode, bool kMask>
 __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,

@@ -113,8 +113,8 @@ class Compressor:
         cap = packed_capacity(p, self.ctx_host)
         # the tensor-core decode needs the extent of the packed cache
         p.packed_rows = cap if tensor_cores else 0
-        # zeros: the rows of the decode reserve, which no call writes before they are
-        # appended to, hold the same thing in every run
+        # zeros: packed-cache files hold the rows of the decode reserve too, which no call
+        # writes before they are appended to; nothing of what the memory held before gets in
         self.Kp = torch.zeros((cap, p.d), dtype=dt, **z)
         self.Vp = torch.zeros((cap, p.d), dtype=dt, **z)
         self.logm = torch.zeros((cap,), dtype=f32, **z)
