@@ -163,6 +163,24 @@ typedef struct kvc_chunk {
                            pos_e) to its scores; NULL = off                       */
 } kvc_chunk;
 
+/* ---- 8-bit cache ------------------------------------------------------------- */
+/* kvc_q8_append, kvc_q8_pack, kvc_q8_select and kvc_q8_attn (no counterpart on the
+ * pages: a cache of half the bytes, next to the compressed one or of it).  The
+ * cache lives in pages of kvc_chunk.page_rows entries (16, 32, 64 or 128), each of one
+ * (b,l,h): row page * page_rows + i holds the page's entry i.  Keys and values are
+ * e4m3 codes times their page's scale, a power of two between 2^-40 and 2^40.
+ * The arrays are caller-owned device memory, the block is host memory. */
+typedef struct kvc_q8 {
+  uint8_t* K;           /* [packed_rows, d] e4m3 codes                            */
+  uint8_t* V;
+  float* k_scale;       /* [packed_rows / page_rows]                              */
+  float* v_scale;
+  int8_t* bounds;       /* [packed_rows / page_rows, 2, d]: least and largest
+                           rint(code / 4) of the page's keys per feature; NULL = not
+                           kept (kvc_q8_select needs them)                        */
+  float* logm;          /* [packed_rows]; NULL = 0 for every entry                */
+} kvc_q8;
+
 /* Human-readable name of a status code (static string). */
 const char* kvc_status_string(int status);
 
@@ -546,6 +564,85 @@ int kvc_mass_evict(const kvc_params* p, const kvc_chunk* c, float* mass, const i
  * initialisation needed); 0 for invalid arguments. */
 size_t kvc_mass_evict_workspace_bytes(const kvc_params* p /* host */,
                                       const kvc_chunk* c /* host */, int32_t max_len);
+
+/* ---- calls on the 8-bit cache -------------------------------------------------- */
+/* Shared rules.  c gives the layer range and the pages (page_rows 16, 32, 64 or 128;
+ * page_table is needed) and T; softcap, window and slopes must be off.  p->dtype is
+ * the type of q, k_new, v_new and out; p->packed_rows the extent of the cache's rows.
+ * Layouts as in kvc_chunk_attn.  Each call is one or a few kernels without allocation, so it can
+ * be captured.  Every value must be finite, but log m may be -inf.  Errors:
+ * KVC_EINVAL (also K, V, bounds, q, k_new or v_new off a 16-byte boundary, out off a
+ * 32-byte one), KVC_EWORKSPACE, KVC_ECUDA. */
+
+/* New tokens into the cache.  With rope_cos and rope_sin (kvc_rope_table's, n_half rows)
+ * token t of sequence b stands at position pos_new[b] + t, a multiple of 1/2, and its key and
+ * query rows are rotated (pairs j, j + d/2):
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * in fp32, each product and sum rounded by itself; without them (both NULL) rows stay as
+ * they are.  The n_b = n_new[b] keys and values become entries len_lh .. len_lh + n_b - 1
+ * of every (b,l,h) (log m = 0).  A page's scale is the larger of what it had (with entries
+ * of before) and 2^x, x the least integer with |value| <= 448 2^x for the new ones
+ * (held to -40 .. 40: larger values saturate); codes are rounded to nearest, and if the scale grows the
+ * page's old codes move to it, rounded again only where they become subnormal.  Bounds are kept up.
+ *   q, q_out  [B, Lr, H*G, T, d], both NULL when there are none; q_out may be q
+ *   len_out   [B, L, H], not len_lh itself: receives len_lh + n_b
+ * Rows t >= n_b of q_out are left as they were.  An (l,h) with a length or n_b out of range, a
+ * page number outside the extent, or a position outside the tables is skipped and reported as
+ * KVC_EDEVICE, one with len + n_b > cap_lh as KVC_ECAPACITY: len_out = len_lh, and its
+ * cache stays (queries are rotated all the same where their position is in the tables).
+ * Pages that a call appends to belong to one (b,l,h) only. */
+int kvc_q8_append(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const float* rope_cos,
+                  const float* rope_sin, int64_t n_half, const void* q, const void* k_new,
+                  const void* v_new, const float* pos_new, void* q_out, const int32_t* len_lh,
+                  const int32_t* cap_lh, int32_t* len_out, void* stream);
+
+/* A packed cache (kvc_merge_pack's, with `rows` rows) into the 8-bit one: the len_lh entries
+ * from row off_lh on fill the (b,l,h)'s pages from the first; scales, bounds and log m as
+ * above (logm and x->logm are both given or both NULL).  len_out (not len_lh itself) receives
+ * len_lh, or 0 for an (l,h) that is skipped: rows or pages out of range (KVC_EDEVICE), or
+ * len > cap_lh (KVC_ECAPACITY).  c->T and n_new are not used, but must be valid. */
+int kvc_q8_pack(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const void* Kp,
+                const void* Vp, const float* logm, int64_t rows, const int32_t* len_lh,
+                const int64_t* off_lh, const int32_t* cap_lh, int32_t* len_out, void* stream);
+
+/* The pages that every new token of a KV head attends over, by a cheap score.  Token t of an
+ * (l,h) sees the pages j <= own, own = (len_lh + t) / page_rows its own one.  If these are more
+ * than n_sel, it picks the pages j < first, j > own - recent, and of the others those of
+ * largest score (ties to the lower page) up to n_sel in all:
+ *   score_j = max_g fl(fl(D_gj k_scale_j) a_g),  D_gj = sum_f max(i_gf lo_jf, i_gf hi_jf),
+ *   a_g = max_f |q_gf|,  i_gf = rint(fl(q_gf fl(127 fl(1 / a_g))))   (0 for a_g = 0)
+ * an upper bound of the products with the page's keys, up to the rounding to 8 bits.  log m does
+ * not enter.  Call after kvc_q8_append of the same tokens (q is its q_out); len_lh are the
+ * lengths before it, len_new after it (its len_out), both [B, L, H]; n = len_new - len_lh.
+ * sel [B, Lr, H, T, n_sel] receives page numbers of the (b,l,h) (columns of its table) in
+ * ascending order, -1 after the last; rows t >= n stay as they were.  1 <= recent,
+ * 0 <= first, first + recent <= n_sel <= 32768, max_pages <= 32768, x->bounds given.  An (l,h)
+ * with lengths out of range is skipped, one with a page outside the extent gets
+ * unspecified pages of its own; both report KVC_EDEVICE. */
+int kvc_q8_select(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const void* q,
+                  const int32_t* len_lh, const int32_t* len_new, int32_t n_sel, int32_t first,
+                  int32_t recent, int32_t* sel, void* stream);
+
+/* Attention of the new tokens over the 8-bit cache, which holds them already: token t of
+ * the n = len_new - len_lh of an (l,h) attends over the entries e <= len_lh + t, with sel
+ * only over those in its pages:
+ *   s_e = q_t . k_e / sqrt(d) + logm_e,  out = sum_e softmax_e(s) v_e,  lse = log2 sum_e 2^(s_e log2 e)
+ * with fp32 statistics (bf16: the softmax's numerators are rounded to 11 bits).  A row whose
+ * scores are all -inf gets out = 0 and lse = -inf.  sel, n_sel as kvc_q8_select leaves them (each page once;
+ * numbers that are no page the token sees are passed over), NULL and 0 = all entries.
+ * lse [B, Lr, H*G, T] may be NULL.  Rows t >= n of out and lse stay as they were.  Query values
+ * up to 2^64.  An (l,h) with lengths out of range is skipped; with a page
+ * outside the extent its rows are unspecified; both report KVC_EDEVICE.  Workspace:
+ * kvc_q8_workspace_bytes, 256-byte aligned, no initialisation; calls that overlap must
+ * not share one. */
+int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const void* q,
+                const int32_t* len_lh, const int32_t* len_new, const int32_t* sel, int32_t n_sel,
+                void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of kvc_q8_attn for this n_sel (0: all entries); 0 for invalid
+ * arguments. */
+size_t kvc_q8_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk* c /* host */,
+                              int32_t n_sel);
 
 #ifdef __cplusplus
 }

@@ -28,7 +28,8 @@ EXPORTED = ("kvc_status_string", "kvc_last_cuda_error", "kvc_device_error", "kvc
             "kvc_evict_workspace_bytes", "kvc_evict_topb", "kvc_set_phase_timing",
             "kvc_score_phase_ms", "kvc_decode_attn_layers", "kvc_tree_cuts", "kvc_set_wait_limit",
             "kvc_chunk_attn", "kvc_chunk_workspace_bytes", "kvc_chunk_mass", "kvc_chunk_mass_cap",
-            "kvc_mass_evict", "kvc_mass_evict_workspace_bytes")
+            "kvc_mass_evict", "kvc_mass_evict_workspace_bytes", "kvc_q8_append", "kvc_q8_pack",
+            "kvc_q8_select", "kvc_q8_attn", "kvc_q8_workspace_bytes")
 
 
 class kvc_params(ctypes.Structure):
@@ -56,6 +57,13 @@ class kvc_chunk(ctypes.Structure):
     ]
 
 
+class kvc_q8(ctypes.Structure):
+    _fields_ = [
+        ("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("bounds", ctypes.c_void_p), ("logm", ctypes.c_void_p),
+    ]
+
+
 class KvcError(RuntimeError):
     def __init__(self, status: int, what: str):
         msg = f"{what}: {kvc_status_string(status)} ({status})"
@@ -68,6 +76,7 @@ class KvcError(RuntimeError):
 _lib = None
 _P = ctypes.POINTER(kvc_params)
 _C = ctypes.POINTER(kvc_chunk)
+_Q = ctypes.POINTER(kvc_q8)
 
 
 def lib():
@@ -124,6 +133,16 @@ def lib():
         L.kvc_mass_evict.restype = c_int
         L.kvc_mass_evict_workspace_bytes.argtypes = [_P, _C, c_int32]
         L.kvc_mass_evict_workspace_bytes.restype = c_size_t
+        L.kvc_q8_append.argtypes = [_P, _C, _Q, vp, vp, c_int64] + [vp] * 9
+        L.kvc_q8_append.restype = c_int
+        L.kvc_q8_pack.argtypes = [_P, _C, _Q] + [vp] * 3 + [c_int64] + [vp] * 5
+        L.kvc_q8_pack.restype = c_int
+        L.kvc_q8_select.argtypes = [_P, _C, _Q] + [vp] * 3 + [c_int32] * 3 + [vp] * 2
+        L.kvc_q8_select.restype = c_int
+        L.kvc_q8_attn.argtypes = [_P, _C, _Q] + [vp] * 4 + [c_int32] + [vp] * 3 + [c_size_t, vp]
+        L.kvc_q8_attn.restype = c_int
+        L.kvc_q8_workspace_bytes.argtypes = [_P, _C, c_int32]
+        L.kvc_q8_workspace_bytes.restype = c_size_t
         _lib = L
     return _lib
 
@@ -399,6 +418,65 @@ def kvc_mass_evict(p, c, mass, keep_lh, recent, pos_next, Kp, Vp, logm, pos, len
     a = _ptrs(c, mass, keep_lh, pos_next, Kp, Vp, logm, pos, len_lh, off_lh, len_out, workspace)
     _check(lib().kvc_mass_evict(p, c, a[0], a[1], recent, *a[2:10], max_len, a[10], workspace.nbytes,
                                 _raw_stream(stream)), "kvc_mass_evict")
+
+
+# ------------------------------------------------------------------ 8-bit cache
+def make_q8(K, V, k_scale, v_scale, bounds=None, logm=None) -> kvc_q8:
+    """A kvc_q8 block of CUDA tensors, which it keeps alive: K, V [rows, d] uint8 (e4m3
+    codes), k_scale, v_scale [pages] f32, bounds [pages, 2, d] int8 or None, logm [rows]
+    f32 or None."""
+    x = kvc_q8()
+    for name, t, dt in (("K", K, torch.uint8), ("V", V, torch.uint8), ("k_scale", k_scale, torch.float32),
+                        ("v_scale", v_scale, torch.float32), ("bounds", bounds, torch.int8),
+                        ("logm", logm, torch.float32)):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}")
+        setattr(x, name, _ptr(t))
+    x._keep = (K, V, k_scale, v_scale, bounds, logm)
+    if len({t.get_device() for t in x._keep if t is not None}) > 1:
+        raise ValueError("the tensors of an 8-bit cache must be on one device")
+    x._device = K.get_device()
+    return x
+
+
+def _q8_ptrs(c, x, *tensors):
+    if x._device != torch.cuda.current_device():
+        raise ValueError("the cache's tensors must be on the current CUDA device")
+    return _ptrs(c, *tensors)
+
+
+def kvc_q8_append(p, c, x, rope_cos, rope_sin, q, k_new, v_new, pos_new, q_out, len_lh, cap_lh,
+                  len_out, stream=None):
+    """Rotates the new tokens' queries and keys (by the tables; None: not) and appends keys
+    and values to the 8-bit cache x; q, q_out and pos_new may be None."""
+    a = _q8_ptrs(c, x, rope_cos, rope_sin, q, k_new, v_new, pos_new, q_out, len_lh, cap_lh, len_out)
+    _check(lib().kvc_q8_append(p, c, x, a[0], a[1], 0 if rope_cos is None else rope_cos.shape[0],
+                               *a[2:], _raw_stream(stream)), "kvc_q8_append")
+
+
+def kvc_q8_pack(p, c, x, Kp, Vp, logm, len_lh, off_lh, cap_lh, len_out, stream=None):
+    """A packed cache (Kp, Vp [rows, d], logm or None) into the pages of the 8-bit cache x."""
+    a = _q8_ptrs(c, x, Kp, Vp, logm, len_lh, off_lh, cap_lh, len_out)
+    _check(lib().kvc_q8_pack(p, c, x, *a[:3], Kp.shape[0], *a[3:], _raw_stream(stream)), "kvc_q8_pack")
+
+
+def kvc_q8_select(p, c, x, q, len_lh, len_new, first, recent, sel, stream=None):
+    """The pages every new token attends over, into sel [B, Lr, H, T, n_sel] int32."""
+    a = _q8_ptrs(c, x, q, len_lh, len_new, sel)
+    _check(lib().kvc_q8_select(p, c, x, *a[:3], sel.shape[-1], first, recent, a[3],
+                               _raw_stream(stream)), "kvc_q8_select")
+
+
+def kvc_q8_attn(p, c, x, q, len_lh, len_new, sel, out, lse, workspace, stream=None):
+    """Attention of the new tokens over the 8-bit cache x: over all entries (sel None) or
+    the pages of sel; lse may be None."""
+    a = _q8_ptrs(c, x, q, len_lh, len_new, sel, out, lse, workspace)
+    _check(lib().kvc_q8_attn(p, c, x, *a[:4], 0 if sel is None else sel.shape[-1], *a[4:],
+                             workspace.nbytes, _raw_stream(stream)), "kvc_q8_attn")
+
+
+def kvc_q8_workspace_bytes(p, c, n_sel: int = 0) -> int:
+    return int(lib().kvc_q8_workspace_bytes(ctypes.byref(p), ctypes.byref(c), int(n_sel)))
 
 
 def workspace(which: int, p: kvc_params, device="cuda", zero=False) -> torch.Tensor:
