@@ -1,16 +1,20 @@
 // kvc_q8_attn: attention over the 8-bit cache, over all entries or over picked pages.
 //
-// A warp works by itself: it streams 16-entry groups of codes from global memory into
-// registers, turns them into fp16 there (exact), and multiplies with mma.sync in the
-// transposed form, entries or features on the 16-wide side, query rows on the 8-wide one:
+// A warp works by itself on every fourth 16-entry group of its CTA's part of an item: groups of codes come through a
+// ring in shared memory that the warp fills itself (cp.async, three groups ahead), are turned into fp16 in registers (exact), and
+// multiplied with mma.sync in the transposed form, entries or features on the 16-wide side,
+// query rows on the 8-wide one:
 //   S^T[16 entries x 8 rows] += K[16 x 16 features] Q^T       (d / 16 products)
 //   O^T[16 features x 8 rows] += V^T[16 x 16 entries] P^T     (d / 16 products)
 // A product's 16 inner positions may stand for any 16 features (or entries), as long as both
-// operands agree, so each lane loads whole 16-byte pieces of a row and uses them as they are:
-// nothing passes through shared memory.  P goes from the layout of S^T's results to that of
-// P^T's operand by one 8x8 transposition (movmatrix) per product.
+// operands agree, so each lane takes whole 16-byte pieces of a row and uses them as they are.
+// P goes from the layout of S^T's results to that of P^T's operand by one 8x8 transposition
+// (movmatrix) per product.
 // Few rows (G heads of one token) fill the 8-wide side, where a tcgen05 product would use
 // 4 of its 128 rows and the codes would have to be written to shared memory as bf16 first.
+//
+// Rows are 16-byte pieces at place piece ^ (row mod 8) of the ring, and row i of a product's 16
+// is the group's row i ^ 4 (i & 1): then neither operand's loads have bank conflicts (d 128).
 //
 // fp16 operands: codes are exact; a query row is scaled by a power of two to a largest
 // magnitude in [2^14, 2^15), which leaves bf16 rows exact down to 2^-29 of it (fp32 rows are
@@ -20,10 +24,12 @@
 // 2^-24 is under 2^-31 of the largest.  Statistics and O are fp32; O is kept in units of the
 // scale of the values that came last, and moved by a power of two when that changes.
 //
-// The steps of all items (rows blocks of units, or picked pages of tokens) lie on one line that is cut into equal
-// pieces, one per warp; what a cut splits is joined in order by a combine kernel.
+// The groups of all items (row blocks of units, or picked pages of tokens) lie on one line that is
+// cut into equal pieces, one per CTA; a CTA's warps join their results in shared memory, and what a cut
+// splits is joined in order by a combine kernel.
 #include <algorithm>
 
+#include "kvc_chunk_tc.cuh"
 #include "kvc_q8.cuh"
 
 namespace {
@@ -39,9 +45,9 @@ struct Q8Attn {
   void* out;
   float* lse;
   const int32_t* sel;                  // null: all entries
-  float* part;                         // [pieces][2][rows][D]
+  float* part;                         // [CTAs][2][rows][D]
   float2* part_ml;
-  int2* tail;                          // [pieces]: the item a piece leaves unfinished, and its last piece
+  int2* tail;                          // [CTAs]: the item a piece leaves unfinished, and its last piece
   float scale_log2;
   int n_sel, tt, rp;                   // tokens per row block, row blocks per unit
 };
@@ -95,16 +101,17 @@ struct LocateSmem {
   long long total, start;
   int item;
 };
-// Block-wide: the total of steps, and the item that holds step lo (or -1), with its first step.
-template <int kGroups, bool kSel>
-__device__ __forceinline__ void locate(const Q8Attn& a, long long pieces, LocateSmem& sm, long long& q) {
+// Block-wide: this CTA's piece [lo, hi) of the line (q groups a piece), and the item that holds
+// lo, with its first group.
+template <bool kSel>
+__device__ __forceinline__ void locate(const Q8Attn& a, LocateSmem& sm, long long& q, long long& lo, long long& hi) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (int)a.x.units * a.rp;
   const int per = (n + kThreads - 1) / kThreads, i0 = min((long long)n, (long long)tid * per), i1 = min((long long)n, (long long)i0 + per);
   auto cost = [&](int i) {
     const int u = i / a.rp;
     const Unit r = load_unit(a.x, u);
-    return (item_groups<kSel>(a, r, (i - u * a.rp) * a.tt) + kGroups - 1) / kGroups;
+    return item_groups<kSel>(a, r, (i - u * a.rp) * a.tt);
   };
   long long mine = 0;
 #pragma unroll 4
@@ -116,7 +123,6 @@ __device__ __forceinline__ void locate(const Q8Attn& a, long long pieces, Locate
     if (lane >= o) incl += v;
   }
   if (lane == 31) sm.warp[warp] = incl;
-  if (tid == 0) sm.item = -1;
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
@@ -124,10 +130,11 @@ __device__ __forceinline__ void locate(const Q8Attn& a, long long pieces, Locate
     if (w < warp) before += sm.warp[w];
     total += sm.warp[w];
   }
-  q = (total + pieces - 1) / pieces;
-  const long long lo = (long long)blockIdx.x * kWarps * q;
+  q = max((total + gridDim.x - 1) / gridDim.x, (long long)kWarps);
+  lo = min(total, (long long)blockIdx.x * q);
+  hi = min(total, lo + q);
   long long at = before + incl - mine;
-  if (at <= lo && lo < at + mine) {
+  if (lo < hi && at <= lo && lo < at + mine) {
     for (int i = i0; i < i1; ++i) {
       const int c = cost(i);
       if (lo < at + c) {
@@ -138,55 +145,162 @@ __device__ __forceinline__ void locate(const Q8Attn& a, long long pieces, Locate
       at += c;
     }
   }
-  if (tid == 0) sm.total = total;
   __syncthreads();
 }
 
-// A lane's share of a group's codes: of K, 16-byte pieces h of rows g and g + 8; of V, the
-// features 16 g' (8 g' for d 64) of rows 2c, 2c+1, 2c+8, 2c+9 (lane = 4 g + c, g' = g).
-template <int D>
-struct KFrag { uint4 w[2][D / 64]; };
-template <int D> struct VFrag;
-template <> struct VFrag<128> { uint4 w[4]; };
-template <> struct VFrag<64> { uint2 w[4]; };
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
 
-template <typename T, int D, int NT, int kGroups, bool kSel>
-__global__ void __launch_bounds__(kThreads, NT == 1 && sizeof(T) == 2 ? 3 : 2)
-    q8_attn_kernel(const __grid_constant__ Q8Attn a) {
+// Shape of a kernel: CTAs per SM, and groups in a warp's ring.
+template <typename T, int NT>
+struct Shape {
+  static constexpr int kCtas = NT <= 2 && sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kStages = kCtas == 3 ? 4 : 6;
+};
+template <int D, int kStages>
+struct WarpRing {
+  static constexpr int kKeys = 16 * D, kStage = 2 * kKeys;       // bytes of a group's keys, of a group
+  alignas(128) unsigned char codes[kStages][kStage];             // later this warp's O
+  float lm[kStages][16];
+};
+template <int D, int NT, int kStages>
+struct AttnSmem {
+  WarpRing<D, kStages> ring[kWarps];
+  float2 ml[kWarps][NT * 8];
+  LocateSmem loc;
+};
+
+template <typename T, int D, int NT, bool kSel>
+__global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(const __grid_constant__ Q8Attn a) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kQ = kF32 ? 3 : 1, kP = kF32 ? 2 : 1;  // fp16 parts of a query row, of the numerators
   constexpr int kH = D / 64, kS = D / 16;              // 16-byte pieces of a row per lane, products
   constexpr int kRows = NT * 8;
   constexpr int kF = D / 8;                            // features of a lane's output
-  __shared__ LocateSmem sm;
+  constexpr int kStages = Shape<T, NT>::kStages;
+  using Smem = AttnSmem<D, NT, kStages>;
+  static_assert(kRows * D * 4 <= kStages * WarpRing<D, kStages>::kStage, "O takes the ring's place");
+  extern __shared__ __align__(128) unsigned char attn_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(attn_raw);
   const Q8Args& x = a.x;
-  kvcd::pdl_trigger();
   kvcd::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const long long pieces = (long long)gridDim.x * kWarps;
-  const int piece = blockIdx.x * kWarps + warp;
-  long long q;
-  locate<kGroups, kSel>(a, pieces, sm, q);
-  const long long lo = min(sm.total, (long long)piece * q), hi = min(sm.total, lo + q);
-  long long start = sm.start;
-  int item = sm.item, left = -1, left_to = 0;
+  long long q, lo, hi;
+  locate<kSel>(a, sm.loc, q, lo, hi);
+  long long start = sm.loc.start;
+  int item = sm.loc.item, left = -1, left_to = 0;
   bool bad = false;
+  WarpRing<D, kStages>& ring = sm.ring[warp];
+  const uint32_t codes0 = kvcd::smem_u32(ring.codes), lm0 = kvcd::smem_u32(ring.lm);
+  // where this lane's pieces lie in a group's keys and values, and where it copies to
+  const int pg = g ^ ((g & 1) << 2);                   // the group's row that stands at row g
+  auto place = [](int row, int chunk) {
+    return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+  };
+  uint32_t k_at[kH], v_at[2];
+#pragma unroll
+  for (int h = 0; h < kH; ++h) k_at[h] = place(pg, c + 4 * h);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = (2 * c + j) ^ (j << 2);
+    v_at[j] = D == 128 ? place(row, g) : place(row, g >> 1) + (g & 1) * 8;
+  }
+  constexpr int kPer = 32 / (D / 16), kCopies = 16 / kPer;       // rows of one copy instruction, copies
+  const int crow = lane / (D / 16), cchunk = lane % (D / 16);
+  uint32_t c_at[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) c_at[i] = place(crow + i * kPer, cchunk);
+
   for (long long at = lo; at < hi;) {
-    // the item that holds step `at`
+    // the item that holds group `at`
     Unit r;
-    int u, t0, groups, tiles;
+    int u, t0, groups;
     while (true) {
       u = item / a.rp;
       t0 = (item - u * a.rp) * a.tt;
       r = load_unit(x, u);
       groups = item_groups<kSel>(a, r, t0);
-      tiles = (groups + kGroups - 1) / kGroups;
-      if (at < start + tiles) break;
-      start += tiles;
+      if (at < start + groups) break;
+      start += groups;
       ++item;
     }
-    const int tb = (int)(at - start), te = (int)min((long long)tiles, hi - start);
+    const int tb = (int)(at - start), te = (int)min((long long)groups, hi - start);
     at = start + te;
+    const int count = max(0, (te - tb - warp + kWarps - 1) / kWarps);   // this warp's groups
+    const int total = r.len + r.n, all_see = r.len + t0 + 1;   // entries; those that every row sees
+    const int32_t* tab = x.table + r.gu * x.max_pages;
+    const int32_t* list = kSel ? a.sel + ((int64_t)u * x.T + t0) * a.n_sel : nullptr;
+    const int own = (r.len + t0) >> x.shift, inpage = (1 << x.shift) - 1;
+    // A window: lane i knows of the warp's group k0 + i its first entry and row (-1: none) and
+    // the exponents of its scales.
+    struct Window { int e0, row, exps; };
+    auto window = [&](int k0) {
+      Window w{0, -1, 0};
+      const int gi = tb + warp + kWarps * (k0 + lane);
+      if (gi < te) {
+        w.e0 = gi << 4;
+        bool ok = true;
+        if (kSel) {
+          const int per = x.shift - 4, no = __ldg(list + (gi >> per));
+          ok = (unsigned)no <= (unsigned)own;
+          w.e0 = (no << x.shift) + ((gi & ((1 << per) - 1)) << 4);
+        }
+        if (ok) {
+          const int page = __ldg(tab + (w.e0 >> x.shift));
+          if ((unsigned)page < (unsigned)x.pages) {
+            w.row = (page << x.shift) + (w.e0 & inpage);
+            w.exps = (kvcd::scale_exp(__ldg(x.k_scale + page)) + 64) | (kvcd::scale_exp(__ldg(x.v_scale + page)) + 64) << 8;
+          } else {
+            bad = true;
+          }
+        }
+      }
+      return w;
+    };
+    Window cur = window(0), nxt = window(32);
+    auto entry = [&](const Window& w, int k) {
+      return kSel ? __shfl_sync(KVC_FULL_MASK, w.e0, k & 31) : (tb + warp + kWarps * k) << 4;
+    };
+    auto issue = [&](int k, int base) {                // base: the first group of `cur`
+      if (k < count) {
+        const Window& w = k - base < 32 ? cur : nxt;
+        const int row = __shfl_sync(KVC_FULL_MASK, w.row, k & 31), e0 = entry(w, k);
+        if (row >= 0) {
+          const uint32_t dst = codes0 + (k % kStages) * WarpRing<D, kStages>::kStage;
+          const uint8_t* ks = x.K + (int64_t)row * D + lane * 16;
+          const uint8_t* vs = x.V + (int64_t)row * D + lane * 16;
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i) {          // rows past the last entry become 0
+            const bool there = e0 + crow + i * kPer < total;
+            cp_async16(dst + c_at[i], ks + i * 512, there);
+            cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at[i], vs + i * 512, there);
+          }
+          if (x.logm && lane < 16) cp_async4(lm0 + (k % kStages) * 64 + lane * 4, x.logm + row + lane, e0 + lane < total);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(k, 0);
     // ---- query rows: row nt*8 + g as the operand of this lane
     uint32_t qf[kQ][NT][kS][2];
     float fq[NT][2];
@@ -236,53 +350,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && sizeof(T) == 2 ? 3 : 2)
         see[nt][k] = row2 / a.tt < x.G && tok2 < r.n ? r.len + tok2 + 1 : 0;
       }
     }
-    const int total = r.len + r.n, all_see = r.len + t0 + 1;   // entries; those that every row sees
-    const int32_t* tab = x.table + r.gu * x.max_pages;
-    const int32_t* list = kSel ? a.sel + ((int64_t)u * x.T + t0) * a.n_sel : nullptr;
-    const int own = (r.len + t0) >> x.shift;
-    // first entry of a group, or -1 for none
-    auto entry_of = [&](int gi) {
-      if (gi >= groups) return -1;
-      if (!kSel) return gi << 4;
-      const int per = x.shift - 4, no = __ldg(list + (gi >> per));
-      return (unsigned)no <= (unsigned)own ? (no << x.shift) + ((gi & ((1 << per) - 1)) << 4) : -1;
-    };
-    auto page_of = [&](int e) {
-      const int page = e >= 0 ? __ldg(tab + (e >> x.shift)) : 0;
-      if ((unsigned)page < (unsigned)x.pages) return page;
-      bad = true;
-      return 0;
-    };
-    KFrag<D> kf[kGroups];
-    VFrag<D> vf[kGroups];
-    float ks[kGroups], vs[kGroups], lm[kGroups][2];
-    int e0[kGroups] = {}, page[kGroups] = {}, e0n[kGroups], pagen[kGroups];
-    const int inpage = (1 << x.shift) - 1;
-    auto load_k = [&](int i) {
-      const int64_t row = ((int64_t)page[i] << x.shift) + (e0[i] & inpage);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint8_t* p = x.K + (row + g + 8 * j) * D + 16 * c;
-#pragma unroll
-        for (int h = 0; h < kH; ++h)
-          kf[i].w[j][h] = e0[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(p + 64 * h)) : make_uint4(0, 0, 0, 0);
-        lm[i][j] = x.logm && e0[i] >= 0 ? __ldg(x.logm + row + g + 8 * j) : 0.f;
-      }
-      ks[i] = __ldg(x.k_scale + page[i]);
-    };
-    auto load_v = [&](int i) {
-      const int64_t row = ((int64_t)page[i] << x.shift) + (e0[i] & inpage);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* p = x.V + (row + 2 * c + (j & 1) + 8 * (j >> 1)) * D + kF * g;
-        if constexpr (D == 128) vf[i].w[j] = e0[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-        else vf[i].w[j] = e0[i] >= 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-      }
-      vs[i] = __ldg(x.v_scale + page[i]);
-    };
     float o[NT][kS][4], ref[NT][2], l[NT][2];
     int xo = 0;
-    bool any_v = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -292,112 +361,100 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && sizeof(T) == 2 ? 3 : 2)
       ref[nt][0] = ref[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
+    for (int k = 0, base = 0; k < count; ++k) {
+      if (k - base == 32) {
+        base = k;
+        cur = nxt;
+        nxt = window(k + 32);
+      }
+      const int e0 = entry(cur, k), exps = __shfl_sync(KVC_FULL_MASK, cur.exps, k & 31);
+      const bool here = !kSel || __shfl_sync(KVC_FULL_MASK, cur.row, k & 31) >= 0;
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      if (here) {
+        const uint32_t st = codes0 + (k % kStages) * WarpRing<D, kStages>::kStage;
+        float s[NT][4];
+        // ---- S^T = K Q^T
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      e0[i] = entry_of(tb * kGroups + i);
-      page[i] = page_of(e0[i]);
-      load_k(i);
-      load_v(i);
-      e0n[i] = tb + 1 < te ? entry_of((tb + 1) * kGroups + i) : -1;
-      pagen[i] = page_of(e0n[i]);
-    }
-    for (int tile = tb; tile < te; ++tile) {
-      float s[kGroups][NT][4];
-      // ---- S^T = K Q^T
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          const uint32_t wa[4] = {kf[i].w[0][h].x, kf[i].w[0][h].y, kf[i].w[0][h].z, kf[i].w[0][h].w};
-          const uint32_t wb[4] = {kf[i].w[1][h].x, kf[i].w[1][h].y, kf[i].w[1][h].z, kf[i].w[1][h].w};
+          const uint4 ka = lds128(st + k_at[h]), kb = lds128(st + k_at[h] + 8 * D);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t a0 = lo_codes(wa[w]), a1 = lo_codes(wb[w]), a2 = hi_codes(wa[w]), a3 = hi_codes(wb[w]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int k = kQ - 1; k >= 0; --k)
-                mma16816(s[i][nt], a0, a1, a2, a3, qf[k][nt][h * 4 + w][0], qf[k][nt][h * 4 + w][1]);
+              for (int i = kQ - 1; i >= 0; --i)
+                mma16816(s[nt], a0, a1, a2, a3, qf[i][nt][h * 4 + w][0], qf[i][nt][h * 4 + w][1]);
           }
         }
-      }
-      // ---- base-2 scores
-      int ecur[kGroups];
-      float vcur[kGroups];
-      bool rise = false;
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        ecur[i] = e0[i];
-        const bool cut = e0[i] < 0 || e0[i] + 16 > all_see;
+        // ---- base-2 scores
+        const float ks = kvcd::pow2i((exps & 255) - 64);
+        float lm[2] = {0.f, 0.f};
+        if (x.logm) {
+          lm[0] = ring.lm[k % kStages][pg] * kvcd::kLog2eC;
+          lm[1] = ring.lm[k % kStages][pg + 8] * kvcd::kLog2eC;
+        }
+        bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float f = fq[nt][k] * ks[i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float y = fmaf(s[i][nt][2 * j + k], f, lm[i][j] * kvcd::kLog2eC);
-              if (cut) y = e0[i] >= 0 && e0[i] + g + 8 * j < see[nt][k] ? y : -INFINITY;
-              s[i][nt][2 * j + k] = y;
-              mx[nt][k] = fmaxf(mx[nt][k], y);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const float f = fq[nt][i] * ks;
+            s[nt][i] = fmaf(s[nt][i], f, lm[0]);
+            s[nt][2 + i] = fmaf(s[nt][2 + i], f, lm[1]);
           }
-      }
-      // the next step's keys are on their way from here
+        if (e0 + 16 > all_see)
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        vcur[i] = vs[i];
-        e0[i] = e0n[i];
-        page[i] = pagen[i];
-        load_k(i);
-        e0n[i] = tile + 2 < te ? entry_of((tile + 2) * kGroups + i) : -1;
-        pagen[i] = page_of(e0n[i]);
-      }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) rise |= mx[nt][0] > ref[nt][0] + kRise || mx[nt][1] > ref[nt][1] + kRise;
-      if (__any_sync(KVC_FULL_MASK, rise)) {
+            for (int i = 0; i < 2; ++i) {
+              if (e0 + pg >= see[nt][i]) s[nt][i] = -INFINITY;
+              if (e0 + pg + 8 >= see[nt][i]) s[nt][2 + i] = -INFINITY;
+            }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float m = mx[nt][k];
-            m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 16));
-            if (m > ref[nt][k] + kRise) {
-              const float f = kvcd::ex2(ref[nt][k] - (m - kBelow));      // 0 at first
-              ref[nt][k] = m - kBelow;
-              l[nt][k] *= f;
+          for (int i = 0; i < 2; ++i) rise |= fmaxf(s[nt][i], s[nt][2 + i]) > ref[nt][i] + kRise;
+        if (__any_sync(KVC_FULL_MASK, rise)) {
 #pragma unroll
-              for (int j = 0; j < kS; ++j) {
-                o[nt][j][k] *= f;
-                o[nt][j][2 + k] *= f;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float m = fmaxf(s[nt][i], s[nt][2 + i]);
+              m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 16));
+              if (m > ref[nt][i] + kRise) {
+                const float f = kvcd::ex2(ref[nt][i] - (m - kBelow));    // 0 at first
+                ref[nt][i] = m - kBelow;
+                l[nt][i] *= f;
+#pragma unroll
+                for (int j = 0; j < kS; ++j) {
+                  o[nt][j][i] *= f;
+                  o[nt][j][2 + i] *= f;
+                }
               }
             }
-          }
-      }
-      // ---- numerators, and O^T += V^T P^T
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
+        }
+        // ---- numerators
         uint32_t pf[kP][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float b0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0], b1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float p0 = kvcd::ex2(s[i][nt][2 * j] - b0), p1 = kvcd::ex2(s[i][nt][2 * j + 1] - b1);
+            float p0 = kvcd::ex2(s[nt][2 * j] - b0), p1 = kvcd::ex2(s[nt][2 * j + 1] - b1);
             l[nt][0] += p0;
             l[nt][1] += p1;
 #pragma unroll
-            for (int k = 0; k < kP; ++k) {
+            for (int i = 0; i < kP; ++i) {
               const uint32_t w = f16x2(p0, p1);
-              pf[k][nt][j] = transpose8(w);
-              if (k + 1 < kP) {
+              pf[i][nt][j] = transpose8(w);
+              if (i + 1 < kP) {
                 float z0, z1;
                 kvcd::f16x2_f32(w, z0, z1);
                 p0 -= z0;
@@ -406,135 +463,178 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && sizeof(T) == 2 ? 3 : 2)
             }
           }
         }
-        if (ecur[i] >= 0) {
-          const int xv = kvcd::scale_exp(vcur[i]);
-          if (any_v && xv != xo) {                     // O's unit becomes this page's
-            const float f = kvcd::pow2i(xo - xv);
+        // ---- O^T += V^T P^T, in units of this page's scale
+        const int xv = (exps >> 8) - 64;
+        if (xv != xo) {
+          const float f = kvcd::pow2i(xo - xv);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int j = 0; j < kS; ++j)
+            for (int j = 0; j < kS; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[nt][j][k] *= f;
-          }
+              for (int i = 0; i < 4; ++i) o[nt][j][i] *= f;
           xo = xv;
-          any_v = true;
-          if (ecur[i] + 16 > total) {                  // rows past the last entry may hold anything
+        }
+        uint32_t vw[4][kF / 4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (ecur[i] + 2 * c + (j & 1) + 8 * (j >> 1) >= total) {
-                vf[i].w[j].x = vf[i].w[j].y = 0;
-                if constexpr (D == 128) vf[i].w[j].z = vf[i].w[j].w = 0;
-              }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t p = st + WarpRing<D, kStages>::kKeys + v_at[j & 1] + (j >> 1) * 8 * D;
+          if constexpr (D == 128) {
+            const uint4 v = lds128(p);
+            vw[j][0] = v.x; vw[j][1] = v.y; vw[j][2] = v.z; vw[j][3] = v.w;
+          } else {
+            const uint2 v = lds64(p);
+            vw[j][0] = v.x; vw[j][1] = v.y;
           }
         }
 #pragma unroll
-        for (int w = 0; w < kF / 4; ++w) {
-          auto word = [&](int j) {
-            if constexpr (D == 128) return w == 0 ? vf[i].w[j].x : w == 1 ? vf[i].w[j].y : w == 2 ? vf[i].w[j].z : vf[i].w[j].w;
-            else return w == 0 ? vf[i].w[j].x : vf[i].w[j].y;
-          };
+        for (int w = 0; w < kF / 4; ++w)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t ab = __byte_perm(word(0), word(1), hf ? 0x7362 : 0x5140);
-            const uint32_t cd = __byte_perm(word(2), word(3), hf ? 0x7362 : 0x5140);
+            const uint32_t ab = __byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140);
+            const uint32_t cd = __byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140);
             const uint32_t a0 = lo_codes(ab), a1 = hi_codes(ab), a2 = lo_codes(cd), a3 = hi_codes(cd);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int k = kP - 1; k >= 0; --k) mma16816(o[nt][2 * w + hf], a0, a1, a2, a3, pf[k][nt][0], pf[k][nt][1]);
+              for (int i = kP - 1; i >= 0; --i) mma16816(o[nt][2 * w + hf], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
           }
-        }
-        load_v(i);
       }
+      issue(k + kStages - 1, base);
     }
-    // ---- this piece's result
-    const bool whole = tb == 0 && te == tiles;
-    if (tb == 0 && te < tiles) {
-      left = item;
-      left_to = (int)((start + tiles - 1) / q);
-    }
-    const int64_t slot = ((int64_t)piece * 2 + (tb == 0 ? 1 : 0)) * kRows;
+    // ---- the warps' results joined: O in absolute units takes the ring's place
+    cp_wait<0>();
+    __syncwarp();
+    float* mine = reinterpret_cast<float*>(ring.codes);
     const float unit = kvcd::pow2i(xo);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float sum = l[nt][k];
+      for (int i = 0; i < 2; ++i) {
+        float sum = l[nt][i];
         sum += __shfl_xor_sync(KVC_FULL_MASK, sum, 4);
         sum += __shfl_xor_sync(KVC_FULL_MASK, sum, 8);
         sum += __shfl_xor_sync(KVC_FULL_MASK, sum, 16);
-        const int row = nt * 8 + 2 * c + k;
-        if (see[nt][k] == 0) continue;
-        const float f = whole ? (sum > 0.f ? unit / sum : 0.f) : unit;
-        const float m = sum > 0.f ? ref[nt][k] : -INFINITY;
-        float y[kF];
+        const int row = nt * 8 + 2 * c + i;
+        if (g == 0) sm.ml[warp][row] = make_float2(sum > 0.f ? ref[nt][i] : -INFINITY, sum);
+        if (see[nt][i] == 0 || count == 0) continue;
+        float* to = mine + row * D + kF * g;
 #pragma unroll
-        for (int j = 0; j < kS; ++j) {
-          y[2 * j] = o[nt][j][k] * f;
-          y[2 * j + 1] = o[nt][j][2 + k] * f;
-        }
-        if (whole) {
-          const int64_t orow = ((int64_t)u * x.G + row / a.tt) * x.T + t0 + row % a.tt;
-          T* to = static_cast<T*>(a.out) + orow * D + kF * g;
-#pragma unroll
-          for (int i = 0; i < kF; i += 8) {
-            if constexpr (kF32) {
-              *reinterpret_cast<float4*>(to + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-              *reinterpret_cast<float4*>(to + i + 4) = make_float4(y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
-            } else {
-              uint4 w;
-              w.x = __bfloat16_as_ushort(__float2bfloat16_rn(y[i])) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[i + 1])) << 16;
-              w.y = __bfloat16_as_ushort(__float2bfloat16_rn(y[i + 2])) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[i + 3])) << 16;
-              w.z = __bfloat16_as_ushort(__float2bfloat16_rn(y[i + 4])) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[i + 5])) << 16;
-              w.w = __bfloat16_as_ushort(__float2bfloat16_rn(y[i + 6])) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[i + 7])) << 16;
-              *reinterpret_cast<uint4*>(to + i) = w;
-            }
-          }
-          if (a.lse && g == 0) a.lse[orow] = sum > 0.f ? m + log2f(sum) : -INFINITY;
-        } else {
-          float* to = a.part + (slot + row) * D + kF * g;
-#pragma unroll
-          for (int i = 0; i < kF; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-          if (g == 0) a.part_ml[slot + row] = make_float2(m, sum);
-        }
+        for (int j = 0; j < kS; j += 2)
+          *reinterpret_cast<float4*>(to + 2 * j) = make_float4(o[nt][j][i] * unit, o[nt][j][2 + i] * unit,
+                                                               o[nt][j + 1][i] * unit, o[nt][j + 1][2 + i] * unit);
       }
+    __syncthreads();
+    const bool whole = tb == 0 && te == groups;
+    if (tb == 0 && te < groups) {
+      left = item;
+      left_to = (int)((start + groups - 1) / q);
+    }
+    const int64_t slot = ((int64_t)blockIdx.x * 2 + (tb == 0 ? 1 : 0)) * kRows;
+    constexpr int kVec = D / 4;
+    for (int i = threadIdx.x; i < x.G * a.tt * kVec; i += kThreads) {
+      const int row = i / kVec, f4 = i % kVec, tok = t0 + row % a.tt;
+      if (tok >= r.n) continue;
+      float M = -INFINITY, sum = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][row].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = sm.ml[w][row];
+        if (ml.x == -INFINITY) continue;               // saw nothing
+        const float f = kvcd::ex2(ml.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w].codes) + row * D + 4 * f4);
+        sum = fmaf(ml.y, f, sum);
+        y.x = fmaf(v.x, f, y.x);
+        y.y = fmaf(v.y, f, y.y);
+        y.z = fmaf(v.z, f, y.z);
+        y.w = fmaf(v.w, f, y.w);
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(a.part + (slot + row) * D + 4 * f4) = y;
+        if (f4 == 0) a.part_ml[slot + row] = make_float2(M, sum);
+        continue;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int64_t orow = ((int64_t)u * x.G + row / a.tt) * x.T + tok;
+      T* to = static_cast<T*>(a.out) + orow * D + 4 * f4;
+      if constexpr (kF32) {
+        *reinterpret_cast<float4*>(to) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      } else {
+        *reinterpret_cast<uint2*>(to) = make_uint2(kvctc::bf16x2(y.x * inv, y.y * inv), kvctc::bf16x2(y.z * inv, y.w * inv));
+      }
+      if (a.lse && f4 == 0) a.lse[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+    }
+    __syncthreads();                                   // the ring is free again
   }
-  if (lane == 0) a.tail[piece] = make_int2(left, left_to);
-  if (bad && lane == 0) kvcd::record_error(x.err, KVC_EDEVICE);
+  if (threadIdx.x == 0) a.tail[blockIdx.x] = make_int2(left, left_to);
+  // The next kernel's CTAs may come in from here: any earlier and they take registers that
+  // this kernel's or its successor's CTAs need (70 us instead of 53 for one token, all layers).
+  kvcd::pdl_trigger();
+  if (bad) kvcd::record_error(x.err, KVC_EDEVICE);
 }
 
 // Joins the partial results of the item that piece blockIdx.x leaves unfinished: the head in
-// its slot 1, the others in slot 0 of the pieces up to the last.  A warp a row.
+// its slot 1, the others in slot 0 of the pieces up to the last.  blockIdx.y takes 8 rows;
+// where an item has fewer, several warps share a row's pieces.
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(256) q8_combine_kernel(const __grid_constant__ Q8Attn a) {
   constexpr int C = D / 32;
-  kvcd::pdl_trigger();
+  __shared__ float sm_o[8][D];
+  __shared__ float2 sm_ml[8];
   kvcd::pdl_wait();
   const int2 tail = a.tail[blockIdx.x];
   if (tail.x < 0) return;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = min(8, a.x.G * a.tt - (int)blockIdx.y * 8);   // of this block
+  if (rows <= 0) return;
+  const int share = 8 / rows, row = blockIdx.y * 8 + warp % rows, part = warp / rows;
   const int u = tail.x / a.rp, t0 = (tail.x - u * a.rp) * a.tt;
   const int head = row / a.tt, tok = t0 + row % a.tt;
-  const Unit r = load_unit(a.x, u);
-  if (head >= a.x.G || tok >= r.n) return;
   float M = -INFINITY, l = 0.f, o[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int p = blockIdx.x; p <= tail.y; ++p) {
-    const int64_t slot = ((int64_t)p * 2 + (p == (int)blockIdx.x ? 1 : 0)) * kRows + row;
-    const float2 ml = a.part_ml[slot];
-    float v[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = a.part[slot * D + lane * C + i];
-    if (ml.x == -INFINITY) continue;
+  auto add = [&](float2 ml, const float (&v)[C]) {
+    if (ml.x == -INFINITY) return;
     const float Mn = fmaxf(M, ml.x), f0 = kvcd::ex2(M - Mn), f1 = kvcd::ex2(ml.x - Mn);
     l = fmaf(l, f0, ml.y * f1);
 #pragma unroll
     for (int i = 0; i < C; ++i) o[i] = fmaf(o[i], f0, v[i] * f1);
     M = Mn;
+  };
+  const Unit r = load_unit(a.x, u);
+  const bool live = part < share && tok < r.n;
+  if (live)
+    for (int p0 = blockIdx.x + part; p0 <= tail.y; p0 += 4 * share) {
+      float2 ml[4];
+      float v[4][C];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {                    // four pieces on their way at a time
+        const int p = p0 + k * share;
+        const int64_t slot = ((int64_t)min(p, tail.y) * 2 + (p == (int)blockIdx.x ? 1 : 0)) * kRows + row;
+        ml[k] = a.part_ml[slot];
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[k][i] = a.part[slot * D + lane * C + i];
+        if (p > tail.y) ml[k].x = -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add(ml[k], v[k]);
+    }
+  if (share > 1) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) sm_o[warp][lane * C + i] = o[i];
+    if (lane == 0) sm_ml[warp] = make_float2(M, l);
+    __syncthreads();
+    if (part > 0) return;
+    for (int k = 1; k < share; ++k) {
+      float v[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = sm_o[warp + k * rows][lane * C + i];
+      add(sm_ml[warp + k * rows], v);
+    }
   }
+  if (!live) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int64_t orow = ((int64_t)u * a.x.G + head) * a.x.T + tok;
   T* to = static_cast<T*>(a.out) + orow * D + lane * C;
@@ -548,15 +648,15 @@ struct Layout {
   size_t part, ml, tail, total;
 };
 
-// Row tiles of 8 rows and the CTAs per SM: one tile for picked pages, fp32, and up to 8 rows.
+// Row tiles of 8 rows: one for picked pages and fp32, else as many as the rows of a unit take, up to 4.
 int row_tiles(const kvc_params* p, const kvc_chunk* c, int n_sel) {
-  return p->dtype == KVC_F32 || n_sel > 0 || p->G * c->T <= 8 ? 1 : 2;
+  return p->dtype == KVC_F32 || n_sel > 0 ? 1 : std::min(4, (p->G * std::min(c->T, 32) + 7) / 8);
 }
-int ctas_per_sm(const kvc_params* p, int nt) { return nt == 1 && p->dtype == KVC_BF16 ? 3 : 2; }
+int ctas_per_sm(const kvc_params* p, int nt) { return p->dtype == KVC_F32 || nt > 2 ? 2 : 3; }
 
 Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   const int nt = row_tiles(p, c, n_sel);
-  const size_t pieces = (size_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, nt) * kWarps, rows = pieces * 2 * nt * 8;
+  const size_t pieces = (size_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, nt), rows = pieces * 2 * nt * 8;
   Layout w;
   w.part = 0;
   w.ml = kvc::align256(rows * p->d * sizeof(float));
@@ -565,22 +665,26 @@ Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   return w;
 }
 
-template <typename T, int D, int NT, int kGroups, bool kSel>
-cudaError_t launch(const Q8Attn& a, int grid, cudaStream_t s) {
+template <typename T, int D, int NT, bool kSel>
+cudaError_t launch(const Q8Attn& a, int sms, cudaStream_t s) {
+  const size_t smem = sizeof(AttnSmem<D, NT, Shape<T, NT>::kStages>);
+  cudaError_t e = kvc::chunk_allow_smem<q8_attn_kernel<T, D, NT, kSel>>(smem);
+  if (e != cudaSuccess) return e;
+  const int grid = sms * Shape<T, NT>::kCtas;
   kvc::count_launch();
-  cudaError_t e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kGroups, kSel>, dim3(grid), dim3(kThreads), 0, s, a);
+  e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel>, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(grid * kWarps, NT), dim3(256), 0, s, a);
+  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(grid, NT), dim3(256), 0, s, a);
 }
 
 template <int D>
-cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, int grid, cudaStream_t s) {
-  if (p->dtype == KVC_F32)
-    return a.sel ? launch<float, D, 1, 1, true>(a, grid, s) : launch<float, D, 1, 1, false>(a, grid, s);
-  if (a.sel) return launch<__nv_bfloat16, D, 1, 2, true>(a, grid, s);
-  if (nt == 1) return launch<__nv_bfloat16, D, 1, 2, false>(a, grid, s);
-  return launch<__nv_bfloat16, D, 2, 1, false>(a, grid, s);
+cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, int sms, cudaStream_t s) {
+  using B = __nv_bfloat16;
+  if (p->dtype == KVC_F32) return a.sel ? launch<float, D, 1, true>(a, sms, s) : launch<float, D, 1, false>(a, sms, s);
+  if (a.sel) return launch<B, D, 1, true>(a, sms, s);
+  return nt == 1 ? launch<B, D, 1, false>(a, sms, s) : nt == 2 ? launch<B, D, 2, false>(a, sms, s)
+       : nt == 3 ? launch<B, D, 3, false>(a, sms, s) : launch<B, D, 4, false>(a, sms, s);
 }
 
 }  // namespace
@@ -619,7 +723,6 @@ extern "C" int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8
   a.tt = n_sel > 0 ? 1 : std::min(nt * 8 / p->G, c->T);
   a.rp = (c->T + a.tt - 1) / a.tt;
   if (a.x.units * a.rp >= (1LL << 31)) return KVC_EINVAL;
-  const int grid = sms * ctas_per_sm(p, nt);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, grid, s) : launch_d<64>(p, a, nt, grid, s));
+  return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, sms, s) : launch_d<64>(p, a, nt, sms, s));
 }

@@ -44,7 +44,6 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
   extern __shared__ uint32_t keys[];                   // order codes of the scores, a page each
   __shared__ SelectSmem sm;
   const Q8Args& x = a.x;
-  kvcd::pdl_trigger();
   kvcd::pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t u = blockIdx.x / x.T;
