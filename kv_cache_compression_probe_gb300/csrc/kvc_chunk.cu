@@ -515,8 +515,7 @@ struct ChunkLayout {
 // 128 entries); the fp32 kernels two, with up to 64 rows (64 entries).
 constexpr int kMaxRowsTc = 256, kCtasTc = 1, kMaxRowsSimt = 64, kCtasSimt = 2;
 
-ChunkLayout chunk_layout(const kvc_params* p, const kvc_chunk* c) {
-  const size_t units = (size_t)p->B * p->H * (c->layer_end - c->layer_begin);
+ChunkLayout chunk_layout(const kvc_params* p, size_t units) {
   const bool tc = p->dtype == KVC_BF16;
   const size_t ctas = (size_t)(tc ? kCtasTc : kCtasSimt) * std::max(kvc::sm_count(), 1);
   const size_t rows = ctas * 2 * (tc ? kMaxRowsTc : kMaxRowsSimt);
@@ -528,6 +527,9 @@ ChunkLayout chunk_layout(const kvc_params* p, const kvc_chunk* c) {
   w.ml = w.part + kvc::align256(rows * p->d * sizeof(float));
   w.total = w.ml + kvc::align256(rows * 2 * sizeof(float));
   return w;
+}
+ChunkLayout chunk_layout(const kvc_params* p, const kvc_chunk* c) {
+  return chunk_layout(p, (size_t)p->B * p->H * (c->layer_end - c->layer_begin));
 }
 
 bool misaligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) != 0; }
@@ -568,12 +570,18 @@ cudaError_t launch_attn_simt(ChunkArgs& a, int sms, cudaStream_t s) {
   return launch_combine<float, D, MR>(a, grid, s);
 }
 
+// Attention and the joining of its pieces; the units' records and the entries are there.
 template <int D>
-cudaError_t launch_attn_bf16(ChunkArgs& a, int sms, int page_rows, cudaStream_t s) {
-  cudaError_t e = launch_prepare<__nv_bfloat16, D>(a, s);
-  if (e == cudaSuccess) e = kvc::chunk_attn_tc_launch(a, D, sms, page_rows, s);
+cudaError_t launch_attn_prepared(ChunkArgs& a, int sms, int page_rows, cudaStream_t s) {
+  const cudaError_t e = kvc::chunk_attn_tc_launch(a, D, sms, page_rows, s);
   if (e != cudaSuccess) return e;
   return a.T > a.tt ? launch_combine<__nv_bfloat16, D, 256>(a, sms, s) : launch_combine<__nv_bfloat16, D, 128>(a, sms, s);
+}
+
+template <int D>
+cudaError_t launch_attn_bf16(ChunkArgs& a, int sms, int page_rows, cudaStream_t s) {
+  const cudaError_t e = launch_prepare<__nv_bfloat16, D>(a, s);
+  return e != cudaSuccess ? e : launch_attn_prepared<D>(a, sms, page_rows, s);
 }
 
 template <int D>
@@ -665,15 +673,25 @@ void chunk_fill(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c) {
   a.withhold = withhold_copies();
 }
 
-static int chunk_workspace(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c, void* workspace, size_t ws_bytes) {
-  const ChunkLayout w = chunk_layout(p, c);
-  if (!workspace || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return KVC_EWORKSPACE;
+size_t chunk_rows_bytes(const kvc_params* p, int64_t units) { return chunk_layout(p, (size_t)units).total; }
+
+void chunk_rows_workspace(ChunkArgs& a, const kvc_params* p, int64_t units, void* workspace) {
+  const ChunkLayout w = chunk_layout(p, (size_t)units);
   char* ws = static_cast<char*>(workspace);
   a.rec = reinterpret_cast<int4*>(ws + w.rec);
   a.first = reinterpret_cast<int32_t*>(ws + w.first);
   a.seg = reinterpret_cast<ChunkSeg*>(ws + w.seg);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float*>(ws + w.ml);
+}
+
+cudaError_t chunk_attn_rows(ChunkArgs& a, int d, int sms, cudaStream_t s) {
+  return d == 128 ? launch_attn_prepared<128>(a, sms, 0, s) : launch_attn_prepared<64>(a, sms, 0, s);
+}
+
+static int chunk_workspace(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c, void* workspace, size_t ws_bytes) {
+  if (!workspace || ws_bytes < chunk_layout(p, c).total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return KVC_EWORKSPACE;
+  chunk_rows_workspace(a, p, (int64_t)p->B * p->H * (c->layer_end - c->layer_begin), workspace);
   return KVC_OK;
 }
 

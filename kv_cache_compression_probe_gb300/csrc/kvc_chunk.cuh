@@ -320,4 +320,11 @@ cudaError_t chunk_allow_smem(size_t bytes) {
 int chunk_check(const kvc_params* p, const kvc_chunk* c);
 void chunk_fill(ChunkArgs& a, const kvc_params* p, const kvc_chunk* c);
 
+// kvc_chunk_attn in bf16 without its first kernel, for callers that have written the units' records and
+// contiguous rows of entries themselves: the workspace for `units` of them, its
+// members in the argument block, and the launches.
+size_t chunk_rows_bytes(const kvc_params* p, int64_t units);
+void chunk_rows_workspace(ChunkArgs& a, const kvc_params* p, int64_t units, void* workspace);
+cudaError_t chunk_attn_rows(ChunkArgs& a, int d, int sms, cudaStream_t s);
+
 }  // namespace kvc

@@ -30,6 +30,10 @@ struct Q8Args {
 // Argument checks of the calls, and the fields that come from the blocks.
 int q8_check(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x);
 void q8_fill(Q8Args& a, const kvc_params* p, const kvc_chunk* c, const kvc_q8* x);
+// kvc_q8_attn for many rows (kvc_q8_chunk.cu): its workspace and launches.
+size_t q8_chunk_bytes(const kvc_params* p, const kvc_chunk* c);
+cudaError_t q8_chunk_launch(const kvc_params* p, const kvc_chunk* c, const Q8Args& x, const void* q, void* out,
+                            float* lse, void* workspace, cudaStream_t s);
 inline bool q8_misaligned(const void* x, int to) { return (reinterpret_cast<uintptr_t>(x) & (to - 1)) != 0; }
 
 }  // namespace kvc

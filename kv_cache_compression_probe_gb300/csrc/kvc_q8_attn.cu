@@ -654,6 +654,13 @@ int row_tiles(const kvc_params* p, const kvc_chunk* c, int n_sel) {
 }
 int ctas_per_sm(const kvc_params* p, int nt) { return p->dtype == KVC_F32 || nt > 2 ? 2 : 3; }
 
+// Whether the rows go to the kernel of kvc_chunk_attn (kvc_q8_chunk.cu).  Here and there: 64 rows
+// over 16384 entries (8 KV heads) 46 and 39 us, 128 rows 63 and 43, 8192 rows 2360 and 378.
+constexpr int kManyRows = 64;
+bool many_rows(const kvc_params* p, const kvc_chunk* c, int n_sel) {
+  return p->dtype == KVC_BF16 && n_sel == 0 && p->G * c->T > kManyRows;
+}
+
 Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   const int nt = row_tiles(p, c, n_sel);
   const size_t pieces = (size_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, nt), rows = pieces * 2 * nt * 8;
@@ -691,7 +698,7 @@ cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, int sms, cuda
 
 extern "C" size_t kvc_q8_workspace_bytes(const kvc_params* p, const kvc_chunk* c, int32_t n_sel) {
   if (kvc::chunk_check(p, c) != KVC_OK || c->page_rows < 16 || c->page_rows > 128 || n_sel < 0) return 0;
-  return layout(p, c, n_sel).total;
+  return many_rows(p, c, n_sel) ? kvc::q8_chunk_bytes(p, c) : layout(p, c, n_sel).total;
 }
 
 extern "C" int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const void* q,
@@ -701,14 +708,22 @@ extern "C" int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8
   if (st != KVC_OK) return st;
   if (!q || !len_lh || !len_new || !out || n_sel < 0 || (sel != nullptr) != (n_sel > 0)) return KVC_EINVAL;
   if (kvc::q8_misaligned(q, 16) || kvc::q8_misaligned(out, 32)) return KVC_EINVAL;
+  const bool many = many_rows(p, c, n_sel);
   const Layout w = layout(p, c, n_sel);
-  if (!workspace || ws_bytes < w.total || kvc::q8_misaligned(workspace, 256)) return KVC_EWORKSPACE;
+  if (!workspace || ws_bytes < (many ? kvc::q8_chunk_bytes(p, c) : w.total) || kvc::q8_misaligned(workspace, 256))
+    return KVC_EWORKSPACE;
   Q8Attn a = {};
   kvc::q8_fill(a.x, p, c, x);
   const int sms = kvc::sm_count();
   if (!a.x.err || sms <= 0) return KVC_ECUDA;
   a.x.len_lh = len_lh;
   a.x.len_new = len_new;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (many) {
+    if (a.x.units * c->max_pages >= (1LL << 31)) return KVC_EINVAL;
+    if (!kvc::chunk_tc_available()) return KVC_ECUDA;
+    return kvc::cuda_status(kvc::q8_chunk_launch(p, c, a.x, q, out, lse, workspace, s));
+  }
   a.q = q;
   a.out = out;
   a.lse = lse;
@@ -723,6 +738,5 @@ extern "C" int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8
   a.tt = n_sel > 0 ? 1 : std::min(nt * 8 / p->G, c->T);
   a.rp = (c->T + a.tt - 1) / a.tt;
   if (a.x.units * a.rp >= (1LL << 31)) return KVC_EINVAL;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, sms, s) : launch_d<64>(p, a, nt, sms, s));
 }
