@@ -267,12 +267,12 @@ class Q8:
             assert not bad.any(), (what, u, "lse", gl[bad][:4], ls[bad][:4])
             # out: every numerator is off by its score's error, 2^x (2^-22) and half a step of
             # 11 bits (fp32: of 22; more than 64 rows in bf16: of 8), or, when subnormal in fp16, by
-            # 2^-32 of the largest; then the fp32 sums and the rounding of the result
+            # 2^-25 where the largest is 2^7 over 8 at least: 2^-29 of it; then the fp32 sums and the rounding of the result
             many = pages is None and self.G * self.T > 64
             half = 2.0 ** -22 if self.dtype != "bf16" else 2.0 ** -8 if many else 2.0 ** -11
             pn = half + 2.0 ** -21 + N * 2.0 ** -23
             pm = p.max(-1, keepdims=True)
-            tol = (np.einsum("gtn,nd->gtd", p * (de + pn) + 2.0 ** -32 * pm * (p > 0), np.abs(V))
+            tol = (np.einsum("gtn,nd->gtd", p * (de + pn) + 2.0 ** -29 * pm * (p > 0), np.abs(V))
                    + (dbar + N * 2.0 ** -24 + 2.0 ** -21)[..., None] * np.abs(o) + 1.01 * e * np.abs(o) + 1e-30)
             go = out[b, lr, hs, :n]
             err = np.abs(go - o)
