@@ -1,19 +1,23 @@
 // kvc_q8_append and kvc_q8_pack: rows into the 8-bit cache.
 //
-// One CTA per (unit, page that the call writes): four warps for the keys and four for the
-// values.  The page's new rows are read twice (the second time from L1): once for their
-// largest magnitude, which with the page's old scale gives the new one, and once for the
-// codes.  Only when the scale grows are the page's old codes read and moved to it.
+// A task is the keys, or the values, that go into one page of a unit: one warp's for up to 8
+// tokens, a CTA's (8 warps) for more.  D / 16 lanes hold a row, 8 elements of each half a lane, so
+// that a rotation's pairs meet in a lane and loads and stores are 16 and 8 bytes.  The largest magnitude of the new
+// rows and the page's old scale give the new one; rows stay in registers until
+// then (beyond 8 a warp they are read again).  Only when the scale grows are the page's old
+// codes read and moved to it.
 #include <algorithm>
 
+#include "kvc_chunk_tc.cuh"
 #include "kvc_q8.cuh"
 
 namespace {
 
 using kvc::Q8Args;
 
-constexpr int kThreads = 256;
-constexpr int kQRows = 4;              // query rows of a warp
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kFew = 8;                // tokens up to which a task is one warp's
+constexpr int kQPasses = 2;            // query rows of a lane
 
 struct Q8Append {
   Q8Args x;
@@ -26,22 +30,27 @@ struct Q8Append {
   void* q_out;
   const int32_t* cap_lh;
   int32_t* len_out;
-  int64_t n_half, page_ctas;
-  int per_unit;                        // CTAs of a unit
+  int64_t n_half, page_ctas, tasks;
+  int per_unit;                        // pages of a unit that a call can touch
 };
 
-// A row of D elements over a warp: lane i has elements i*kP .. of the first half in v[0 .. kP)
-// and the same of the second half in v[kP ..), which the rotation pairs.
+// Lane i of a row's D / 16: elements 8i .. 8i + 7 of each half.
 template <typename T, int D>
-__device__ __forceinline__ void load_row(const T* row, int lane, float (&v)[D / 32]) {
-  constexpr int kP = D / 64;
+__device__ __forceinline__ void load_row(const T* row, int i, float (&v)[16]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const T* p = row + h * (D / 2) + lane * kP;
-    if constexpr (kP == 2) {
-      kvcd::VecLoad<T, 2>::ld(p, v + h * kP);
+    const T* p = row + h * (D / 2) + 8 * i;
+    if constexpr (sizeof(T) == 2) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[8 * h + 2 * k] = __uint_as_float(u[k] << 16);
+        v[8 * h + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+      }
     } else {
-      v[h] = kvcd::to_f(*p);
+      kvcd::VecLoad<T, 4>::ld(p, v + 8 * h);
+      kvcd::VecLoad<T, 4>::ld(p + 4, v + 8 * h + 4);
     }
   }
 }
@@ -49,15 +58,20 @@ __device__ __forceinline__ void load_row(const T* row, int lane, float (&v)[D / 
 // The rotation by table row e; every product and sum is rounded by itself, so that the codes
 // can be reproduced bit for bit.
 template <int D>
-__device__ __forceinline__ void rotate(float (&v)[D / 32], const float* cos_tab, const float* sin_tab, int64_t e,
-                                       int lane) {
-  constexpr int kP = D / 64;
+__device__ __forceinline__ void load_angles(const Q8Append& a, int64_t e, int i, float (&c)[8], float (&s)[8]) {
+  const int64_t at = e * (D / 2) + 8 * i;
 #pragma unroll
-  for (int i = 0; i < kP; ++i) {
-    const float c = __ldg(cos_tab + e * (D / 2) + lane * kP + i), s = __ldg(sin_tab + e * (D / 2) + lane * kP + i);
-    const float a = v[i], b = v[kP + i];
-    v[i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-    v[kP + i] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  for (int k = 0; k < 8; k += 4) {
+    kvcd::VecLoad<float, 4>::ld(a.cos_tab + at + k, c + k);
+    kvcd::VecLoad<float, 4>::ld(a.sin_tab + at + k, s + k);
+  }
+}
+__device__ __forceinline__ void rotate(float (&v)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float x = v[k], y = v[8 + k];
+    v[k] = __fsub_rn(__fmul_rn(x, c[k]), __fmul_rn(y, s[k]));
+    v[8 + k] = __fadd_rn(__fmul_rn(y, c[k]), __fmul_rn(x, s[k]));
   }
 }
 
@@ -68,52 +82,280 @@ __device__ __forceinline__ int64_t table_row(float pos, int n, int64_t n_half) {
   return e + 2 * (int64_t)(n - 1) < n_half ? e : -1;
 }
 
+// Bounds of four features, a byte each.
+struct Bounds4 {
+  uint32_t lo, hi;
+};
+constexpr uint32_t kNoLo = 0x7f7f7f7fu, kNoHi = 0x81818181u;      // 127, -127
+__device__ __forceinline__ void join(Bounds4& a, uint32_t lo, uint32_t hi) {
+  a.lo = __vmins4(a.lo, lo);
+  a.hi = __vmaxs4(a.hi, hi);
+}
+// Codes as signed bytes in the order of their values.
+__device__ __forceinline__ uint32_t in_order(uint32_t codes) {
+  const uint32_t s = codes & 0x80808080u;
+  return codes ^ (s - (s >> 7));
+}
+// rint(value / 4) of four codes in that order.
+__device__ __forceinline__ uint32_t bounds_of(uint32_t ordered) {
+  const uint32_t c = in_order(ordered);                // its own inverse
+  float v[4];
+  kvcd::e4m3_f32((uint16_t)c, v[0], v[1]);
+  kvcd::e4m3_f32((uint16_t)(c >> 16), v[2], v[3]);
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w |= (uint32_t)(kvcd::bound_of(v[k]) & 255) << (8 * k);
+  return w;
+}
+
+template <int D>
+struct TaskSmem {
+  float top[kWarps];
+  Bounds4 b[kWarps][D / 16][4];
+};
+
+// A page's part of a task, by kW warps (w: this one's number among them).  page_of() checks the unit's
+// pages and gives the task's, or -1; it comes after the first rows' loads, which need not wait
+// for the page table.
+template <typename T, int D, int kW, bool kKeys, class Page>
+__device__ __forceinline__ void append_page(const Q8Append& a, int64_t u, int old, int t0, int count, int64_t e0, int w,
+                                            TaskSmem<D>& sm, const Page& page_of) {
+  constexpr int kL = D / 16, kG = 32 / kL, kStep = kW * kG, kHold = kW > 1 && kG < 8 ? 2 : 1;
+  const Q8Args& x = a.x;
+  const int lane = threadIdx.x & 31, i = lane % kL, r0 = w * kG + lane / kL;   // first row of this lane
+  const T* rows = static_cast<const T*>(kKeys ? a.k_new : a.v_new) + (u * x.T + t0) * D;
+  const bool turn = kKeys && a.cos_tab, bounds = kKeys && x.bounds;
+  auto row = [&](int r, float (&v)[16]) {
+    load_row<T, D>(rows + (int64_t)r * D, i, v);
+    if (turn) {
+      float c[8], s[8];
+      load_angles<D>(a, e0 + 2 * (int64_t)(t0 + r), i, c, s);
+      rotate(v, c, s);
+    }
+  };
+  float held[kHold][16], top = 0.f;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k)
+    if (r0 + k * kStep < count) row(r0 + k * kStep, held[k]);
+  const int64_t page = page_of();
+  if (page < 0) return;
+  float* scale = (kKeys ? x.k_scale : x.v_scale) + page;
+  const int x_old = old > 0 ? kvcd::scale_exp(*scale) : kvc::kQ8MinExp;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k)
+    if (r0 + k * kStep < count)
+#pragma unroll
+      for (int f = 0; f < 16; ++f) top = fmaxf(top, fabsf(held[k][f]));
+  for (int r = r0 + kHold * kStep; r < count; r += kStep) {
+    float v[16];
+    row(r, v);
+#pragma unroll
+    for (int f = 0; f < 16; ++f) top = fmaxf(top, fabsf(v[f]));
+  }
+  top = kvcd::warp_max(top);
+  if constexpr (kW > 1) {
+    if (lane == 0) sm.top[w] = top;
+    __syncthreads();                                   // and every thread has read the old scale
+#pragma unroll
+    for (int k = 0; k < kW; ++k) top = fmaxf(top, sm.top[k]);
+  }
+  const int xs = max(x_old, kvcd::scale_for(top));
+  const bool grow = old > 0 && xs > x_old;
+  uint8_t* codes = (kKeys ? x.K : x.V) + (page << x.shift) * D + 8 * i;
+  Bounds4 b[4];                                        // of this lane's features, codes in order
+#pragma unroll
+  for (int k = 0; k < 4; ++k) b[k] = Bounds4{kNoLo, kNoHi};
+  if (grow) {                                          // the old codes move to the new scale
+    const float f = kvcd::pow2i(x_old - xs);
+    for (int r = r0; r < old; r += kStep)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2* p = reinterpret_cast<uint2*>(codes + r * D + h * (D / 2));
+        const uint2 was = *p;
+        uint32_t c[2] = {was.x, was.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float y[4];
+          kvcd::e4m3_f32((uint16_t)c[k], y[0], y[1]);
+          kvcd::e4m3_f32((uint16_t)(c[k] >> 16), y[2], y[3]);
+          c[k] = kvcd::f32_e4m3x2(y[0] * f, y[1] * f) | (uint32_t)kvcd::f32_e4m3x2(y[2] * f, y[3] * f) << 16;
+          if (bounds) join(b[2 * h + k], in_order(c[k]), in_order(c[k]));
+        }
+        *p = make_uint2(c[0], c[1]);
+      }
+  }
+  const float f = kvcd::pow2i(-xs);
+  auto put = [&](int r, const float (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t c[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float* y = v + 8 * h + 4 * k;
+        c[k] = kvcd::f32_e4m3x2(y[0] * f, y[1] * f) | (uint32_t)kvcd::f32_e4m3x2(y[2] * f, y[3] * f) << 16;
+        if (bounds) join(b[2 * h + k], in_order(c[k]), in_order(c[k]));
+      }
+      *reinterpret_cast<uint2*>(codes + (old + r) * D + h * (D / 2)) = make_uint2(c[0], c[1]);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kHold; ++k)
+    if (r0 + k * kStep < count) put(r0 + k * kStep, held[k]);
+  for (int r = r0 + kHold * kStep; r < count; r += kStep) {
+    float v[16];
+    row(r, v);
+    put(r, v);
+  }
+  if (w == 0 && lane == 0) *scale = kvcd::pow2i(xs);
+  if (kKeys && x.logm)
+    for (int r = w * 32 + lane; r < count; r += 32 * kW) x.logm[(page << x.shift) + old + r] = 0.f;
+  if (!bounds) return;
+#pragma unroll
+  for (int o = kL; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      join(b[k], __shfl_xor_sync(KVC_FULL_MASK, b[k].lo, o), __shfl_xor_sync(KVC_FULL_MASK, b[k].hi, o));
+  if constexpr (kW > 1) {
+    if (lane < kL)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sm.b[w][lane][k] = b[k];
+    __syncthreads();
+    if (w > 0) return;
+    for (int v = 1; v < kWarps; ++v)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) join(b[k], sm.b[v][i][k].lo, sm.b[v][i][k].hi);
+  }
+  if (lane >= kL) return;
+  int8_t* to = x.bounds + page * 2 * D + 8 * i;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint2* lo = reinterpret_cast<uint2*>(to + h * (D / 2));
+    uint2* hi = reinterpret_cast<uint2*>(to + D + h * (D / 2));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      b[2 * h + k].lo = bounds_of(b[2 * h + k].lo);
+      b[2 * h + k].hi = bounds_of(b[2 * h + k].hi);
+    }
+    if (old > 0 && !grow) {
+      const uint2 l = *lo, m = *hi;
+      join(b[2 * h], l.x, m.x);
+      join(b[2 * h + 1], l.y, m.y);
+    }
+    *lo = make_uint2(b[2 * h].lo, b[2 * h + 1].lo);
+    *hi = make_uint2(b[2 * h].hi, b[2 * h + 1].hi);
+  }
+}
+
+// Query rows: a lane has the same 8 + 8 elements of kQPasses rows.
+template <typename T, int D>
+__device__ __forceinline__ void rotate_queries(const Q8Append& a, int64_t warp) {
+  constexpr int kL = D / 16, kG = 32 / kL;
+  const Q8Args& x = a.x;
+  const int lane = threadIdx.x & 31, i = lane % kL;
+  const int64_t r0 = warp * kG * kQPasses + lane / kL;
+  const uint32_t total = (uint32_t)(x.units * x.G * x.T), per_b = (uint32_t)(x.per_seq * x.G) * x.T;   // rows, below 2^32
+  float v[kQPasses][16];
+  int64_t e[kQPasses];
+#pragma unroll
+  for (int k = 0; k < kQPasses; ++k) {
+    e[k] = -1;
+    if (r0 + k * kG >= total) continue;
+    const uint32_t r = (uint32_t)(r0 + k * kG);
+    const int b = (int)(r / per_b), t = (int)(r % (uint32_t)x.T);
+    const int n = x.n_new ? __ldg(x.n_new + b) : x.T;
+    if (n > x.T || t >= n) continue;
+    e[k] = a.cos_tab ? table_row(__ldg(a.pos_new + b), n, a.n_half) : 0;
+    if (e[k] < 0) continue;
+    e[k] += 2 * (int64_t)t;
+    load_row<T, D>(static_cast<const T*>(a.q) + (int64_t)r * D, i, v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kQPasses; ++k) {
+    if (e[k] < 0) continue;
+    if (a.cos_tab) {
+      float c[8], s[8];
+      load_angles<D>(a, e[k], i, c, s);
+      rotate(v[k], c, s);
+    }
+    T* to = static_cast<T*>(a.q_out) + (r0 + k * kG) * D + 8 * i;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if constexpr (sizeof(T) == 2) {
+        uint32_t y[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) y[f] = kvctc::bf16x2(v[k][8 * h + 2 * f], v[k][8 * h + 2 * f + 1]);
+        *reinterpret_cast<uint4*>(to + h * (D / 2)) = make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 8; f += 4)
+          *reinterpret_cast<float4*>(to + h * (D / 2) + f) =
+              make_float4(v[k][8 * h + f], v[k][8 * h + f + 1], v[k][8 * h + f + 2], v[k][8 * h + f + 3]);
+      }
+  }
+}
+
+template <typename T, int D, int kW>
+__global__ void __launch_bounds__(kThreads, kW > 1 ? 3 : 4) q8_append_kernel(const __grid_constant__ Q8Append a) {
+  __shared__ TaskSmem<D> sm;                           // kW > 1: a CTA is one task
+  const Q8Args& x = a.x;
+  kvcd::pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= a.page_ctas) {
+    rotate_queries<T, D>(a, (blockIdx.x - a.page_ctas) * kWarps + warp);
+    kvcd::pdl_trigger();
+    return;
+  }
+  const uint32_t task = blockIdx.x * (uint32_t)(kWarps / kW) + warp / kW;
+  if (task >= a.tasks) return;
+  const uint32_t u = (task >> 1) / (uint32_t)a.per_unit;
+  const int j = (int)((task >> 1) - u * (uint32_t)a.per_unit);
+  const int b = (int)(u / (uint32_t)x.per_seq);
+  const int64_t gu = kvcd::q8_unit_global(x, u);
+  const int len = __ldg(x.len_lh + gu), n = x.n_new ? __ldg(x.n_new + b) : x.T, cap = __ldg(a.cap_lh + gu);
+  const int64_t e0 = a.cos_tab ? table_row(__ldg(a.pos_new + b), n, a.n_half) : 0;
+  int bad = KVC_OK;
+  if (len < 0 || n < 0 || n > x.T || (int64_t)len + n > (int64_t)x.max_pages << x.shift || (n > 0 && e0 < 0))
+    bad = KVC_EDEVICE;
+  else if ((int64_t)len + n > cap)
+    bad = KVC_ECAPACITY;
+  const int32_t* tab = x.table + gu * x.max_pages;
+  const int first = len >> x.shift, last = n > 0 ? (len + n - 1) >> x.shift : first - 1;
+  // Every warp looks at all the pages that the unit's tokens touch; the first one reports.
+  auto page_of = [&]() -> int64_t {
+    bool ok = true;
+    int mine = 0;
+    if (bad == KVC_OK)
+      for (int i = first + lane; i <= last; i += 32) {
+        const int page = __ldg(tab + i);
+        ok &= (unsigned)page < (unsigned)x.pages;
+        if (i == first + j) mine = page;
+      }
+    if (!__all_sync(KVC_FULL_MASK, ok) && bad == KVC_OK) bad = KVC_EDEVICE;
+    if (j == 0 && (task & 1) == 0 && warp % kW == 0 && lane == 0) {
+      if (bad != KVC_OK) kvcd::record_error(x.err, bad);
+      a.len_out[gu] = bad == KVC_OK ? len + n : len;
+    }
+    return bad == KVC_OK ? __shfl_sync(KVC_FULL_MASK, mine, j & 31) : -1;
+  };
+  if (bad == KVC_OK && first + j <= last) {
+    const int begin = (first + j) << x.shift;
+    const int old = max(0, len - begin), t0 = begin + old - len;
+    const int count = min(1 << x.shift, len + n - begin) - old;
+    if (task & 1) append_page<T, D, kW, false>(a, u, old, t0, count, e0, warp % kW, sm, page_of);
+    else append_page<T, D, kW, true>(a, u, old, t0, count, e0, warp % kW, sm, page_of);
+  } else if (j == 0) {
+    page_of();
+  }
+  kvcd::pdl_trigger();
+}
+
+// ---------------------------------------------------------------- pack
 __device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
 struct PageSmem {
   float top[2][4];
   int lo[128], hi[128];
 };
-
-// Moves a page's first `rows` codes to a scale 2^up times as large, and (kBounds) adds them to
-// the bounds.  By the 128 threads of a half.
-template <int D, bool kBounds>
-__device__ __forceinline__ void rescale(uint8_t* page, int rows, int up, int i, PageSmem& sm) {
-  constexpr int kC = D / 16;
-  const float f = kvcd::pow2i(-up);
-  const int c = i % kC;
-  int lo[16], hi[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) { lo[k] = 127; hi[k] = -127; }
-  for (int r = i / kC; r < rows; r += 128 / kC) {
-    uint4* p = reinterpret_cast<uint4*>(page + r * D + c * 16);
-    uint4 w = *p;
-    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int sh = (k & 1) * 16;
-      float a, b;
-      kvcd::e4m3_f32((uint16_t)(u[k >> 1] >> sh), a, b);
-      const uint16_t code = kvcd::f32_e4m3x2(a * f, b * f);
-      u[k >> 1] = (u[k >> 1] & ~(0xffffu << sh)) | ((uint32_t)code << sh);
-      if (kBounds) {
-        kvcd::e4m3_f32(code, a, b);
-        const int x = kvcd::bound_of(a), y = kvcd::bound_of(b);
-        lo[2 * k] = min(lo[2 * k], x);
-        hi[2 * k] = max(hi[2 * k], x);
-        lo[2 * k + 1] = min(lo[2 * k + 1], y);
-        hi[2 * k + 1] = max(hi[2 * k + 1], y);
-      }
-    }
-    *p = w;
-  }
-  if (kBounds && i / kC < rows)
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      atomicMin(&sm.lo[c * 16 + k], lo[k]);
-      atomicMax(&sm.hi[c * 16 + k], hi[k]);
-    }
-}
 
 // The page's bounds from shared memory, four bytes a thread.
 template <int D>
@@ -126,152 +368,6 @@ __device__ __forceinline__ void store_bounds(int8_t* out, int i, const PageSmem&
   }
 }
 
-template <typename T, int D, bool kKeys>
-__device__ __forceinline__ void append_page(const Q8Append& a, int64_t u, int64_t page, int old, int t0, int count,
-                                            int64_t e0, PageSmem& sm) {
-  constexpr int kP = D / 64;
-  const Q8Args& x = a.x;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, i = threadIdx.x & 127;
-  const T* rows = static_cast<const T*>(kKeys ? a.k_new : a.v_new) + (u * x.T + t0) * D;
-  const bool turn = kKeys && a.cos_tab, bounds = kKeys && x.bounds;
-  float v[D / 32], top = 0.f;
-  for (int r = w; r < count; r += 4) {
-    load_row<T, D>(rows + (int64_t)r * D, lane, v);
-    if (turn) rotate<D>(v, a.cos_tab, a.sin_tab, e0 + 2 * (int64_t)(t0 + r), lane);
-#pragma unroll
-    for (int k = 0; k < 2 * kP; ++k) top = fmaxf(top, fabsf(v[k]));
-  }
-  top = kvcd::warp_max(top);
-  if (lane == 0) sm.top[kKeys ? 0 : 1][w] = top;
-  float* scale = (kKeys ? x.k_scale : x.v_scale) + page;
-  const int x_old = old > 0 ? kvcd::scale_exp(*scale) : kvc::kQ8MinExp;
-  half_sync(!kKeys);
-  const float* tops = sm.top[kKeys ? 0 : 1];
-  const int xs = max(x_old, kvcd::scale_for(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))));
-  const bool grow = old > 0 && xs > x_old;
-  uint8_t* codes = (kKeys ? x.K : x.V) + (page << x.shift) * D;
-  if (bounds) {
-    const int8_t* was = x.bounds + page * 2 * D;
-    if (i < D) {
-      sm.lo[i] = old > 0 && !grow ? was[i] : 127;
-      sm.hi[i] = old > 0 && !grow ? was[D + i] : -127;
-    }
-    half_sync(!kKeys);
-  }
-  if (grow) {
-    if (bounds) rescale<D, true>(codes, old, xs - x_old, i, sm);
-    else rescale<D, false>(codes, old, xs - x_old, i, sm);
-  }
-  const float f = kvcd::pow2i(-xs);
-  int lo[2 * kP], hi[2 * kP];
-#pragma unroll
-  for (int k = 0; k < 2 * kP; ++k) { lo[k] = 127; hi[k] = -127; }
-  for (int r = w; r < count; r += 4) {
-    if (count > 4) {                                   // else v holds this warp's only row
-      load_row<T, D>(rows + (int64_t)r * D, lane, v);
-      if (turn) rotate<D>(v, a.cos_tab, a.sin_tab, e0 + 2 * (int64_t)(t0 + r), lane);
-    }
-    uint8_t* to = codes + (old + r) * D + lane * kP;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float y[2];
-      const uint16_t c = kvcd::f32_e4m3x2(v[h * kP] * f, kP == 2 ? v[h * kP + kP - 1] * f : 0.f);
-      if constexpr (kP == 2) *reinterpret_cast<uint16_t*>(to + h * (D / 2)) = c;
-      else to[h * (D / 2)] = (uint8_t)c;
-      if (bounds) {
-        kvcd::e4m3_f32(c, y[0], y[1]);
-#pragma unroll
-        for (int k = 0; k < kP; ++k) {
-          lo[h * kP + k] = min(lo[h * kP + k], kvcd::bound_of(y[k]));
-          hi[h * kP + k] = max(hi[h * kP + k], kvcd::bound_of(y[k]));
-        }
-      }
-    }
-  }
-  if (bounds && w < count)
-#pragma unroll
-    for (int k = 0; k < 2 * kP; ++k) {
-      const int at = (k / kP) * (D / 2) + lane * kP + k % kP;
-      atomicMin(&sm.lo[at], lo[k]);
-      atomicMax(&sm.hi[at], hi[k]);
-    }
-  half_sync(!kKeys);                                   // every thread has read the old scale and bounds
-  if (i == 0) *scale = kvcd::pow2i(xs);
-  if (bounds) store_bounds<D>(x.bounds + page * 2 * D, i, sm);
-  if (kKeys && x.logm)
-    for (int r = i; r < count; r += 128) x.logm[(page << x.shift) + old + r] = 0.f;
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_constant__ Q8Append a) {
-  __shared__ PageSmem sm;
-  const Q8Args& x = a.x;
-  kvcd::pdl_trigger();
-  kvcd::pdl_wait();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x >= a.page_ctas) {                     // query rows, a few per warp
-    const int64_t total = x.units * x.G * x.T;
-    const int64_t r0 = ((blockIdx.x - a.page_ctas) * (kThreads / 32) + (threadIdx.x >> 5)) * kQRows;
-    float v[kQRows][D / 32];
-    int64_t e[kQRows];
-#pragma unroll
-    for (int k = 0; k < kQRows; ++k) {
-      const int64_t r = r0 + k;
-      e[k] = -1;
-      if (r >= total) continue;
-      const int64_t u = r / ((int64_t)x.G * x.T);
-      const int t = (int)(r % x.T), b = (int)(u / x.per_seq);
-      const int n = x.n_new ? x.n_new[b] : x.T;
-      if (n > x.T || t >= n) continue;
-      e[k] = a.cos_tab ? table_row(a.pos_new[b], n, a.n_half) : 0;
-      if (e[k] < 0) continue;
-      e[k] += 2 * (int64_t)t;
-      load_row<T, D>(static_cast<const T*>(a.q) + r * D, lane, v[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kQRows; ++k) {
-      if (e[k] < 0) continue;
-      if (a.cos_tab) rotate<D>(v[k], a.cos_tab, a.sin_tab, e[k], lane);
-      T* to = static_cast<T*>(a.q_out) + (r0 + k) * D;
-      constexpr int kP = D / 64;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < kP; ++i) to[h * (D / 2) + lane * kP + i] = kvcd::from_f<T>(v[k][h * kP + i]);
-    }
-    return;
-  }
-  const int64_t u = blockIdx.x / a.per_unit;
-  const int j = (int)(blockIdx.x - u * a.per_unit);
-  const int b = (int)(u / x.per_seq);
-  const int64_t gu = kvcd::q8_unit_global(x, u);
-  const int len = x.len_lh[gu], n = x.n_new ? x.n_new[b] : x.T, cap = a.cap_lh[gu];
-  const int64_t e0 = a.cos_tab ? table_row(a.pos_new[b], n, a.n_half) : 0;
-  int bad = KVC_OK;
-  if (len < 0 || n < 0 || n > x.T || (int64_t)len + n > (int64_t)x.max_pages << x.shift || (n > 0 && e0 < 0))
-    bad = KVC_EDEVICE;
-  else if ((int64_t)len + n > cap)
-    bad = KVC_ECAPACITY;
-  const int32_t* tab = x.table + gu * x.max_pages;
-  const int first = len >> x.shift, last = n > 0 ? (len + n - 1) >> x.shift : first - 1;
-  bool ok = true;
-  if (bad == KVC_OK)
-    for (int i = first + threadIdx.x; i <= last; i += kThreads) ok &= (unsigned)__ldg(tab + i) < (unsigned)x.pages;
-  if (!__syncthreads_and(ok) && bad == KVC_OK) bad = KVC_EDEVICE;
-  if (j == 0 && threadIdx.x == 0) {
-    if (bad != KVC_OK) kvcd::record_error(x.err, bad);
-    a.len_out[gu] = bad == KVC_OK ? len + n : len;
-  }
-  if (bad != KVC_OK || first + j > last) return;
-  const int begin = (first + j) << x.shift;
-  const int old = max(0, len - begin), t0 = begin + old - len;
-  const int count = min(1 << x.shift, len + n - begin) - old;
-  const int64_t page = __ldg(tab + first + j);
-  if (threadIdx.x < 128) append_page<T, D, true>(a, u, page, old, t0, count, e0, sm);
-  else append_page<T, D, false>(a, u, page, old, t0, count, e0, sm);
-}
-
-// ---------------------------------------------------------------- pack
 struct Q8Pack {
   Q8Args x;
   const void* Kp;
@@ -433,13 +529,18 @@ extern "C" int kvc_q8_append(const kvc_params* p, const kvc_chunk* c, const kvc_
   a.cap_lh = cap_lh;
   a.len_out = len_out;
   const int R = c->page_rows;
+  const bool few = c->T <= kFew;
   a.per_unit = std::min((c->T + R - 2) / R + 1, c->max_pages);
-  a.page_ctas = a.x.units * a.per_unit;
-  const int64_t rows = q ? a.x.units * a.x.G * a.x.T : 0, per = (kThreads / 32) * kQRows;
+  a.tasks = 2 * a.x.units * a.per_unit;
+  a.page_ctas = few ? (a.tasks + kWarps - 1) / kWarps : a.tasks;
+  const int64_t rows = q ? a.x.units * a.x.G * a.x.T : 0, per = kWarps * kQPasses * (512 / p->d);
   const int64_t grid = a.page_ctas + (rows + per - 1) / per;
-  if (grid >= (1LL << 31)) return KVC_EINVAL;
-  auto kernel = p->dtype == KVC_BF16 ? (p->d == 128 ? q8_append_kernel<__nv_bfloat16, 128> : q8_append_kernel<__nv_bfloat16, 64>)
-                                     : (p->d == 128 ? q8_append_kernel<float, 128> : q8_append_kernel<float, 64>);
+  if (grid >= (1LL << 31) || rows >= (1LL << 32) - 4096 || a.tasks >= (1LL << 32)) return KVC_EINVAL;
+  using B = __nv_bfloat16;
+  auto kernel = p->dtype == KVC_BF16 ? (p->d == 128 ? (few ? q8_append_kernel<B, 128, 1> : q8_append_kernel<B, 128, kWarps>)
+                                                    : (few ? q8_append_kernel<B, 64, 1> : q8_append_kernel<B, 64, kWarps>))
+                                     : (p->d == 128 ? (few ? q8_append_kernel<float, 128, 1> : q8_append_kernel<float, 128, kWarps>)
+                                                    : (few ? q8_append_kernel<float, 64, 1> : q8_append_kernel<float, 64, kWarps>));
   kvc::count_launch();
   return kvc::cuda_status(kvc::chunk_launch(kernel, dim3((unsigned)grid), dim3(kThreads), 0,
                                             static_cast<cudaStream_t>(stream), a));
