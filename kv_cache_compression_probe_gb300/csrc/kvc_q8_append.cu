@@ -209,40 +209,42 @@ __device__ __forceinline__ void append_page(const Q8Append& a, int64_t u, int ol
   if (w == 0 && lane == 0) *scale = kvcd::pow2i(xs);
   if (kKeys && x.logm)
     for (int r = w * 32 + lane; r < count; r += 32 * kW) x.logm[(page << x.shift) + old + r] = 0.f;
-  if (!bounds) return;
+  if constexpr (kKeys) {
+    if (!bounds) return;
 #pragma unroll
-  for (int o = kL; o < 32; o <<= 1)
+    for (int o = kL; o < 32; o <<= 1)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      join(b[k], __shfl_xor_sync(KVC_FULL_MASK, b[k].lo, o), __shfl_xor_sync(KVC_FULL_MASK, b[k].hi, o));
-  if constexpr (kW > 1) {
-    if (lane < kL)
+      for (int k = 0; k < 4; ++k)
+        join(b[k], __shfl_xor_sync(KVC_FULL_MASK, b[k].lo, o), __shfl_xor_sync(KVC_FULL_MASK, b[k].hi, o));
+    if constexpr (kW > 1) {
+      if (lane < kL)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sm.b[w][lane][k] = b[k];
-    __syncthreads();
-    if (w > 0) return;
-    for (int v = 1; v < kWarps; ++v)
+        for (int k = 0; k < 4; ++k) sm.b[w][lane][k] = b[k];
+      __syncthreads();
+      if (w > 0) return;
+      for (int v = 1; v < kWarps; ++v)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) join(b[k], sm.b[v][i][k].lo, sm.b[v][i][k].hi);
-  }
-  if (lane >= kL) return;
-  int8_t* to = x.bounds + page * 2 * D + 8 * i;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint2* lo = reinterpret_cast<uint2*>(to + h * (D / 2));
-    uint2* hi = reinterpret_cast<uint2*>(to + D + h * (D / 2));
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      b[2 * h + k].lo = bounds_of(b[2 * h + k].lo);
-      b[2 * h + k].hi = bounds_of(b[2 * h + k].hi);
+        for (int k = 0; k < 4; ++k) join(b[k], sm.b[v][i][k].lo, sm.b[v][i][k].hi);
     }
-    if (old > 0 && !grow) {
-      const uint2 l = *lo, m = *hi;
-      join(b[2 * h], l.x, m.x);
-      join(b[2 * h + 1], l.y, m.y);
+    if (lane >= kL) return;
+    int8_t* to = x.bounds + page * 2 * D + 8 * i;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint2* lo = reinterpret_cast<uint2*>(to + h * (D / 2));
+      uint2* hi = reinterpret_cast<uint2*>(to + D + h * (D / 2));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        b[2 * h + k].lo = bounds_of(b[2 * h + k].lo);
+        b[2 * h + k].hi = bounds_of(b[2 * h + k].hi);
+      }
+      if (old > 0 && !grow) {
+        const uint2 l = *lo, m = *hi;
+        join(b[2 * h], l.x, m.x);
+        join(b[2 * h + 1], l.y, m.y);
+      }
+      *lo = make_uint2(b[2 * h].lo, b[2 * h + 1].lo);
+      *hi = make_uint2(b[2 * h].hi, b[2 * h + 1].hi);
     }
-    *lo = make_uint2(b[2 * h].lo, b[2 * h + 1].lo);
-    *hi = make_uint2(b[2 * h].hi, b[2 * h + 1].hi);
   }
 }
 

@@ -5,6 +5,15 @@
 // for every key k of it (q+ and q- the positive and negative parts).  With q and the bounds as
 // 8-bit integers the sum is an integer below 2^24: exact, so a selection does not depend on the
 // order of a sum, and equal scores are equal.
+//
+// The sums are 8-bit integer products of the tensor cores, 16 pages x 8 query rows a time
+// (rows: G heads of one or more tokens), with the bounds as they lie in memory: a
+// product's 32 inner positions may stand for any features, as long as both operands agree, so
+// a lane takes whole 16-byte pieces.  The scores' order codes stay in shared
+// memory, where a warp per token (for a single token the whole CTA) looks for the n_sel-th largest bit by
+// bit.
+#include <algorithm>
+
 #include "kvc_q8.cuh"
 
 namespace {
@@ -18,125 +27,83 @@ struct Q8Select {
   const void* q;
   int32_t* sel;
   int n_sel, first, recent;
+  int tt, tiles;                       // tokens of a CTA, CTAs of a unit
 };
 
+template <int D, int NT>
 struct SelectSmem {
-  uint32_t pos[8][32], neg[8][32];     // q+ and q- of a head, four features a word
-  float top[8];                        // the head's largest |q|
+  uint2 q[NT][D / 16][32];             // the rows' q+ (first half) and q- as operands: a lane's words of a product
+  float top[NT * 8];                   // the rows' largest |q|
   int count[2][kWarps];
 };
 
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
 // Sum of v over the block; `turn` alternates between calls, so one barrier is enough.
-__device__ __forceinline__ int block_sum(int v, SelectSmem& sm, int& turn) {
+__device__ __forceinline__ int block_sum(int v, int (&count)[2][kWarps], int& turn) {
   v = __reduce_add_sync(KVC_FULL_MASK, v);
   turn ^= 1;
-  if ((threadIdx.x & 31) == 0) sm.count[turn][threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) count[turn][threadIdx.x >> 5] = v;
   __syncthreads();
   int t = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) t += sm.count[turn][i];
+  for (int i = 0; i < kWarps; ++i) t += count[turn][i];
   return t;
 }
 
-// One CTA per (unit, token).
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_constant__ Q8Select a) {
-  extern __shared__ uint32_t keys[];                   // order codes of the scores, a page each
-  __shared__ SelectSmem sm;
-  const Q8Args& x = a.x;
-  kvcd::pdl_wait();
+// The n_sel pages of largest code, by one warp, in ascending order.
+__device__ __forceinline__ void pick_by_warp(const uint32_t* keys, int nb, int n_sel, int32_t* out) {
+  const int lane = threadIdx.x & 31;
+  uint32_t cut = 0;                                    // the largest code that n_sel pages reach
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t trial = cut | 1u << bit;
+    int mine = 0;
+    for (int b = lane; b < nb; b += 32) mine += keys[b] >= trial;
+    mine = __reduce_add_sync(KVC_FULL_MASK, mine);
+    if (mine >= n_sel) cut = trial;
+    if (mine == n_sel) break;
+  }
+  int above = 0;
+  for (int b = lane; b < nb; b += 32) above += keys[b] > cut;
+  int quota = n_sel - __reduce_add_sync(KVC_FULL_MASK, above), at = 0;   // of those equal to it: the first ones
+  for (int b0 = 0; b0 < nb; b0 += 32) {
+    const uint32_t key = b0 + lane < nb ? keys[b0 + lane] : 0;
+    const bool in = b0 + lane < nb;
+    const uint32_t eq = __ballot_sync(KVC_FULL_MASK, in && key == cut), before = (1u << lane) - 1;
+    const bool take = in && (key > cut || (key == cut && __popc(eq & before) < quota));
+    const uint32_t taken = __ballot_sync(KVC_FULL_MASK, take);
+    if (take) out[at + __popc(taken & before)] = b0 + lane;
+    at += __popc(taken);
+    quota -= min(quota, __popc(eq));
+  }
+}
+
+// The same by the whole block; thread i looks at a run of pages.
+__device__ __forceinline__ void pick_by_block(const uint32_t* keys, int nb, int n_sel, int32_t* out,
+                                              int (&count)[2][kWarps]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t u = blockIdx.x / x.T;
-  const int t = (int)(blockIdx.x - u * x.T);
-  const int64_t gu = kvcd::q8_unit_global(x, u);
-  const int len = x.len_lh[gu], n = x.len_new[gu] - len;
-  if (len < 0 || n < 0 || n > x.T || (int64_t)len + n > (int64_t)x.max_pages << x.shift) {
-    if (t == 0 && tid == 0) kvcd::record_error(x.err, KVC_EDEVICE);
-    return;
-  }
-  if (t >= n) return;
-  int32_t* out = a.sel + blockIdx.x * (int64_t)a.n_sel;
-  const int nb = ((len + t) >> x.shift) + 1;           // pages the token sees, its own the last
-  if (nb <= a.n_sel) {
-    for (int i = tid; i < a.n_sel; i += kThreads) out[i] = i < nb ? i : -1;
-    return;
-  }
-  if (warp < G) {                                      // a head's row in 8-bit integers
-    const T* q = static_cast<const T*>(a.q) + ((u * G + warp) * x.T + t) * D;
-    float v[4], top = 0.f;
-    if (lane < D / 4) {
-      kvcd::VecLoad<T, 4>::ld(q + 4 * lane, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]));
-    }
-    top = kvcd::warp_max(top);
-    const float inv = top > 0.f ? __fmul_rn(127.f, __frcp_rn(top)) : 0.f;
-    uint32_t p = 0, m = 0;
-    if (lane < D / 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = min(max(__float2int_rn(__fmul_rn(v[i], inv)), -127), 127);
-        p |= (uint32_t)(max(c, 0) & 255) << (8 * i);
-        m |= (uint32_t)(min(c, 0) & 255) << (8 * i);
-      }
-      sm.pos[warp][lane] = p;
-      sm.neg[warp][lane] = m;
-    }
-    if (lane == 0) sm.top[warp] = top;
-  }
-  __syncthreads();
-  const int32_t* tab = x.table + gu * x.max_pages;
-  bool bad = false;
-  for (int b = tid; b < nb; b += kThreads) {
-    if (b < a.first || b > nb - 1 - a.recent) {
-      keys[b] = 0xffffffffu;
-      continue;
-    }
-    const int page = __ldg(tab + b);
-    if ((unsigned)page >= (unsigned)x.pages) {
-      bad = true;
-      keys[b] = 0;
-      continue;
-    }
-    const uint4* bd = reinterpret_cast<const uint4*>(x.bounds + (int64_t)page * 2 * D);
-    int acc[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) acc[g] = 0;
-#pragma unroll 4
-    for (int c = 0; c < D / 16; ++c) {
-      const uint4 lo = __ldg(bd + c), hi = __ldg(bd + D / 16 + c);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint4 p = *reinterpret_cast<const uint4*>(&sm.pos[g][4 * c]);
-        const uint4 m = *reinterpret_cast<const uint4*>(&sm.neg[g][4 * c]);
-        acc[g] = __dp4a((int)p.x, (int)hi.x, __dp4a((int)p.y, (int)hi.y, __dp4a((int)p.z, (int)hi.z, __dp4a((int)p.w, (int)hi.w, acc[g]))));
-        acc[g] = __dp4a((int)m.x, (int)lo.x, __dp4a((int)m.y, (int)lo.y, __dp4a((int)m.z, (int)lo.z, __dp4a((int)m.w, (int)lo.w, acc[g]))));
-      }
-    }
-    const float s = __ldg(x.k_scale + page);
-    float best = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < G; ++g) best = fmaxf(best, __fmul_rn(__fmul_rn((float)acc[g], s), sm.top[g]));
-    keys[b] = kvcd::float_key(best + 0.f);             // -0 counts as 0
-  }
-  if (__syncthreads_or(bad) && tid == 0) kvcd::record_error(x.err, KVC_EDEVICE);
-  // The largest code that at least n_sel pages reach, bit by bit.
   int turn = 0;
   uint32_t cut = 0;
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t trial = cut | 1u << bit;
     int mine = 0;
     for (int b = tid; b < nb; b += kThreads) mine += keys[b] >= trial;
-    if (block_sum(mine, sm, turn) >= a.n_sel) cut = trial;
+    mine = block_sum(mine, count, turn);
+    if (mine >= n_sel) cut = trial;
+    if (mine == n_sel) break;
   }
-  // Pages above it, and of those equal the first ones; thread i looks at a run of pages.
   const int per = (nb + kThreads - 1) / kThreads, b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
   int above = 0, equal = 0;
   for (int b = b0; b < b1; ++b) {
     above += keys[b] > cut;
     equal += keys[b] == cut;
   }
-  const int quota = a.n_sel - block_sum(above, sm, turn);   // of the equal ones
+  const int quota = n_sel - block_sum(above, count, turn);    // of the equal ones
   int s1 = above, s2 = equal;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -144,11 +111,11 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
     if (lane >= o) { s1 += v1; s2 += v2; }
   }
   __syncthreads();
-  if (lane == 31) { sm.count[0][warp] = s1; sm.count[1][warp] = s2; }
+  if (lane == 31) { count[0][warp] = s1; count[1][warp] = s2; }
   __syncthreads();
   s1 -= above;
   s2 -= equal;
-  for (int w = 0; w < warp; ++w) { s1 += sm.count[0][w]; s2 += sm.count[1][w]; }
+  for (int w = 0; w < warp; ++w) { s1 += count[0][w]; s2 += count[1][w]; }
   for (int b = b0; b < b1; ++b) {
     const bool gt = keys[b] > cut, eq = keys[b] == cut;
     if (gt || (eq && s2 < quota)) out[s1 + min(s2, quota)] = b;
@@ -157,13 +124,149 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
   }
 }
 
-template <typename T, int D>
+// One CTA per (unit, tt tokens); query row r is head r % G of token r / G.
+template <typename T, int D, int G, int NT>
+__global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_constant__ Q8Select a) {
+  constexpr int kH = D / 64, kS = D / 32;              // 16-byte pieces of a row per lane, products for lo (and for hi)
+  extern __shared__ uint32_t keys[];                   // [tt][max_pages] order codes of the scores
+  __shared__ SelectSmem<D, NT> sm;
+  const Q8Args& x = a.x;
+  kvcd::pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int64_t u = blockIdx.x / a.tiles;
+  const int t0 = (int)(blockIdx.x - u * a.tiles) * a.tt;
+  const int64_t gu = kvcd::q8_unit_global(x, u);
+  const int len = x.len_lh[gu], n = x.len_new[gu] - len;
+  if (len < 0 || n < 0 || n > x.T || (int64_t)len + n > (int64_t)x.max_pages << x.shift) {
+    if (t0 == 0 && tid == 0) kvcd::record_error(x.err, KVC_EDEVICE);
+    return;
+  }
+  const int tokens = min(a.tt, n - t0);
+  if (tokens <= 0) return;
+  int32_t* out = a.sel + (u * x.T + t0) * a.n_sel;
+  const int most = ((len + t0 + tokens - 1) >> x.shift) + 1;   // pages that the last token sees
+  if (most > a.n_sel) {
+    const int32_t* tab = x.table + gu * x.max_pages;
+    // ---- the first pages' bounds are on their way while the rows become integers
+    uint4 lo[2][kH], hi[2][kH];
+    float scale[2];
+    bool bad = false;
+    auto fetch = [&](int p0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = p0 + g + 8 * j;
+        int page = b < most ? __ldg(tab + b) : 0;
+        if ((unsigned)page >= (unsigned)x.pages) {
+          bad = true;
+          page = 0;
+        }
+        const uint4* p = reinterpret_cast<const uint4*>(x.bounds + (int64_t)page * 2 * D) + c;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          lo[j][h] = __ldg(p + 4 * h);
+          hi[j][h] = __ldg(p + D / 16 + 4 * h);
+        }
+        scale[j] = __ldg(x.k_scale + page);
+      }
+    };
+    fetch(warp * 16);
+    for (int r = warp; r < NT * 8; r += kWarps) {
+      const int tok = r / G;
+      float v[4] = {0.f, 0.f, 0.f, 0.f}, top = 0.f;
+      if (tok < tokens && lane < D / 4) {
+        kvcd::VecLoad<T, 4>::ld(static_cast<const T*>(a.q) + ((u * G + r % G) * x.T + t0 + tok) * D + 4 * lane, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]));
+      }
+      top = kvcd::warp_max(top);
+      const float inv = top > 0.f ? __fmul_rn(127.f, __frcp_rn(top)) : 0.f;
+      uint32_t p = 0, m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = min(max(__float2int_rn(__fmul_rn(v[i], inv)), -127), 127);
+        p |= (uint32_t)(max(k, 0) & 255) << (8 * i);
+        m |= (uint32_t)(min(k, 0) & 255) << (8 * i);
+      }
+      if (lane < D / 4) {                              // word `lane`: piece h, lane c of the operand, word i of it
+        const int h = lane / 16, cc = (lane % 16) / 4, i = lane % 4, s = 2 * h + i / 2;
+        uint32_t* to = reinterpret_cast<uint32_t*>(&sm.q[r / 8][s][(r % 8) * 4 + cc]) + (i & 1);
+        to[0] = p;
+        to[kS * 64] = m;                               // kS products later
+      }
+      if (lane == 0) sm.top[r] = top;
+    }
+    __syncthreads();
+    for (int p0 = warp * 16; p0 < most; p0 += kWarps * 16) {
+      if (p0 > warp * 16) fetch(p0);
+      int acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0;
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const uint4 r0 = v ? lo[0][h] : hi[0][h], r1 = v ? lo[1][h] : hi[1][h];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_s8(acc[nt], r0.x, r1.x, r0.y, r1.y, sm.q[nt][v * kS + 2 * h][lane]);
+            mma_s8(acc[nt], r0.z, r1.z, r0.w, r1.w, sm.q[nt][v * kS + 2 * h + 1][lane]);
+          }
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int b = p0 + g + 8 * j;
+          float s0 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j], scale[j]), sm.top[nt * 8 + 2 * c]);
+          float s1 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j + 1], scale[j]), sm.top[nt * 8 + 2 * c + 1]);
+          if (G > 1) s0 = fmaxf(s0, s1);
+          if (G > 2) s0 = fmaxf(s0, __shfl_xor_sync(KVC_FULL_MASK, s0, 1));
+          if (G > 4) s0 = fmaxf(s0, __shfl_xor_sync(KVC_FULL_MASK, s0, 2));
+          auto put = [&](int tok, float s) {
+            const int own = (len + t0 + tok) >> x.shift;
+            if (tok < tokens && b <= own)
+              keys[tok * x.max_pages + b] = b < a.first || b > own - a.recent ? 0xffffffffu : kvcd::float_key(s + 0.f);   // -0 counts as 0
+          };
+          const int tok = (nt * 8 + 2 * c) / G;
+          if (G == 1) {
+            put(tok, s0);
+            put(tok + 1, s1);
+          } else if (2 * c % G == 0) {
+            put(tok, s0);
+          }
+        }
+    }
+    if (bad) kvcd::record_error(x.err, KVC_EDEVICE);
+    __syncthreads();
+  }
+  if (tokens == 1 && most > a.n_sel) {
+    pick_by_block(keys, most, a.n_sel, out, sm.count);
+  } else {
+    for (int tok = warp; tok < tokens; tok += kWarps) {
+      const int nb = ((len + t0 + tok) >> x.shift) + 1;
+      int32_t* to = out + tok * (int64_t)a.n_sel;
+      if (nb > a.n_sel) pick_by_warp(keys + tok * x.max_pages, nb, a.n_sel, to);
+      else
+        for (int i = lane; i < a.n_sel; i += 32) to[i] = i < nb ? i : -1;
+    }
+  }
+  kvcd::pdl_trigger();
+}
+
+template <typename T, int D, int NT>
 auto select_kernel(int G) {
-  return G == 1 ? q8_select_kernel<T, D, 1> : G == 2 ? q8_select_kernel<T, D, 2>
-       : G == 4 ? q8_select_kernel<T, D, 4> : q8_select_kernel<T, D, 8>;
+  return G == 1 ? q8_select_kernel<T, D, 1, NT> : G == 2 ? q8_select_kernel<T, D, 2, NT>
+       : G == 4 ? q8_select_kernel<T, D, 4, NT> : q8_select_kernel<T, D, 8, NT>;
+}
+template <int NT>
+auto select_kernel(const kvc_params* p) {
+  const bool bf = p->dtype == KVC_BF16;
+  return p->d == 128 ? (bf ? select_kernel<__nv_bfloat16, 128, NT>(p->G) : select_kernel<float, 128, NT>(p->G))
+                     : (bf ? select_kernel<__nv_bfloat16, 64, NT>(p->G) : select_kernel<float, 64, NT>(p->G));
 }
 
 constexpr int kMaxPages = 32768;       // their order codes fit a CTA's shared memory
+constexpr int kKeyBytes = 64 << 10;    // and what several tokens' codes may take of it
 
 }  // namespace
 
@@ -185,13 +288,16 @@ extern "C" int kvc_q8_select(const kvc_params* p, const kvc_chunk* c, const kvc_
   a.n_sel = n_sel;
   a.first = first;
   a.recent = recent;
-  const int64_t grid = a.x.units * c->T;
+  // Tokens of a CTA: they share the reading of the bounds, and their codes share its memory.
+  const int fit = kKeyBytes / (c->max_pages * (int)sizeof(uint32_t));
+  const int nt = c->T * p->G > 8 && fit * p->G > 8 ? 4 : 1;
+  a.tt = std::max(1, std::min({c->T, nt * 8 / p->G, fit}));
+  a.tiles = (c->T + a.tt - 1) / a.tt;
+  const int64_t grid = a.x.units * a.tiles;
   if (grid >= (1LL << 31)) return KVC_EINVAL;
-  const bool bf = p->dtype == KVC_BF16;
-  auto kernel = p->d == 128 ? (bf ? select_kernel<__nv_bfloat16, 128>(p->G) : select_kernel<float, 128>(p->G))
-                            : (bf ? select_kernel<__nv_bfloat16, 64>(p->G) : select_kernel<float, 64>(p->G));
-  const size_t smem = (size_t)c->max_pages * sizeof(uint32_t);
-  if (smem > (40u << 10)) {
+  auto kernel = nt == 4 ? select_kernel<4>(p) : select_kernel<1>(p);
+  const size_t smem = (size_t)a.tt * c->max_pages * sizeof(uint32_t);
+  if (smem > (30u << 10)) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPages * 4);
     if (e != cudaSuccess) return kvc::cuda_status(e);
   }
