@@ -1,6 +1,6 @@
 // kvc_q8_attn: attention over the 8-bit cache, over all entries or over picked pages.
 //
-// A warp works by itself on every fourth 16-entry group of its CTA's part of an item: groups of codes come through a
+// A warp works by itself, as a rule on every fourth 16-entry group of its CTA's part of an item: groups of codes come through a
 // ring in shared memory that the warp fills itself (cp.async, three groups ahead), are turned into fp16 in registers (exact), and
 // multiplied with mma.sync in the transposed form, entries or features on the 16-wide side,
 // query rows on the 8-wide one:
@@ -28,7 +28,8 @@
 //
 // The groups of all items (row blocks of units, or picked pages of tokens) lie on one line that is
 // cut into equal pieces, one per CTA; a CTA's warps join their results in shared memory, and what a cut
-// splits is joined in order by a combine kernel.
+// splits is joined in order by a combine kernel.  Where there are many items (kSolo) a piece is a warp's, which
+// saves the joining and spreads an item's first and last steps over four times as many groups.
 #include <algorithm>
 
 #include "kvc_chunk_tc.cuh"
@@ -105,20 +106,21 @@ struct LocateSmem {
   long long total, start;
   int item;
 };
-// Block-wide: this CTA's piece [lo, hi) of the line (q groups a piece), and the item that holds
-// lo, with its first group.
-template <bool kSel>
+// Block-wide: this CTA's piece of the line (q groups; kSolo: this warp's), [lo, hi), and the item
+// that holds the CTA's first group, with its own first group.
+template <bool kSel, bool kSolo>
 __device__ __forceinline__ void locate(const Q8Attn& a, LocateSmem& sm, long long& q, long long& lo, long long& hi) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (int)a.x.units * a.rp;
   const int per = (n + kThreads - 1) / kThreads, i0 = min((long long)n, (long long)tid * per), i1 = min((long long)n, (long long)i0 + per);
+  int cu = -1;                                         // the unit looked at last
+  Unit cr;
   auto cost = [&](int i) {
     const int u = i / a.rp;
-    const Unit r = load_unit(a.x, u);
-    return item_groups<kSel>(a, r, (i - u * a.rp) * a.tt);
+    if (u != cu) cr = load_unit(a.x, cu = u);
+    return item_groups<kSel>(a, cr, (i - u * a.rp) * a.tt);
   };
   long long mine = 0;
-#pragma unroll 4
   for (int i = i0; i < i1; ++i) mine += cost(i);
   long long incl = mine;
 #pragma unroll
@@ -134,9 +136,11 @@ __device__ __forceinline__ void locate(const Q8Attn& a, LocateSmem& sm, long lon
     if (w < warp) before += sm.warp[w];
     total += sm.warp[w];
   }
-  q = max((total + gridDim.x - 1) / gridDim.x, (long long)kWarps);
-  lo = min(total, (long long)blockIdx.x * q);
-  hi = min(total, lo + q);
+  constexpr int kPieces = kSolo ? kWarps : 1;           // of a CTA
+  q = (total + gridDim.x * kPieces - 1) / (gridDim.x * kPieces);
+  if (!kSolo) q = max(q, (long long)kWarps);
+  lo = min(total, (long long)blockIdx.x * kPieces * q);
+  hi = min(total, lo + kPieces * q);
   long long at = before + incl - mine;
   if (lo < hi && at <= lo && lo < at + mine) {
     for (int i = i0; i < i1; ++i) {
@@ -150,6 +154,10 @@ __device__ __forceinline__ void locate(const Q8Attn& a, LocateSmem& sm, long lon
     }
   }
   __syncthreads();
+  if (kSolo) {
+    lo = min(hi, lo + warp * q);
+    hi = min(hi, lo + q);
+  }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -197,7 +205,7 @@ struct AttnSmem {
   LocateSmem loc;
 };
 
-template <typename T, int D, int NT, bool kSel>
+template <typename T, int D, int NT, bool kSel, bool kSolo>
 __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(const __grid_constant__ Q8Attn a) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kQ = kF32 ? 3 : 1, kP = kF32 ? 2 : 1;  // fp16 parts of a query row, of the numerators
@@ -213,7 +221,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
   kvcd::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   long long q, lo, hi;
-  locate<kSel>(a, sm.loc, q, lo, hi);
+  locate<kSel, kSolo>(a, sm.loc, q, lo, hi);
+  constexpr int kTeam = kSolo ? 1 : kWarps;            // warps that share an item's groups
+  const int me = kSolo ? 0 : warp, piece = kSolo ? blockIdx.x * kWarps + warp : blockIdx.x;
   long long start = sm.loc.start;
   int item = sm.loc.item, left = -1, left_to = 0;
   bool bad = false;
@@ -238,14 +248,15 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) c_at[i] = place(crow + i * kPer, cchunk);
 
+  int ru = -1;
+  Unit r;
   for (long long at = lo; at < hi;) {
     // the item that holds group `at`
-    Unit r;
     int u, t0, groups;
     while (true) {
       u = item / a.rp;
       t0 = (item - u * a.rp) * a.tt;
-      r = load_unit(x, u);
+      if (u != ru) r = load_unit(x, ru = u);
       groups = item_groups<kSel>(a, r, t0);
       if (at < start + groups) break;
       start += groups;
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     }
     const int tb = (int)(at - start), te = (int)min((long long)groups, hi - start);
     at = start + te;
-    const int count = max(0, (te - tb - warp + kWarps - 1) / kWarps);   // this warp's groups
+    const int count = max(0, (te - tb - me + kTeam - 1) / kTeam);   // this warp's groups
     const int total = r.len + r.n, all_see = r.len + t0 + 1;   // entries; those that every row sees
     const int32_t* tab = x.table + r.gu * x.max_pages;
     const int32_t* list = kSel ? a.sel + ((int64_t)u * x.T + t0) * a.n_sel : nullptr;
@@ -263,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     struct Window { int e0, row, exps; };
     auto window = [&](int k0) {
       Window w{0, -1, 0};
-      const int gi = tb + warp + kWarps * (k0 + lane);
+      const int gi = tb + me + kTeam * (k0 + lane);
       if (gi < te) {
         w.e0 = gi << 4;
         bool ok = true;
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     };
     Window cur = window(0), nxt = window(32);
     auto entry = [&](const Window& w, int k) {
-      return kSel ? __shfl_sync(KVC_FULL_MASK, w.e0, k & 31) : (tb + warp + kWarps * k) << 4;
+      return kSel ? __shfl_sync(KVC_FULL_MASK, w.e0, k & 31) : (tb + me + kTeam * k) << 4;
     };
     auto issue = [&](int k, int base) {                // base: the first group of `cur`
       if (k < count) {
@@ -545,23 +556,25 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
           *reinterpret_cast<float4*>(to + 2 * j) = make_float4(o[nt][j][i] * unit, o[nt][j][2 + i] * unit,
                                                                o[nt][j + 1][i] * unit, o[nt][j + 1][2 + i] * unit);
       }
-    __syncthreads();
+    if (kSolo) __syncwarp();
+    else __syncthreads();
     const bool whole = tb == 0 && te == groups;
     if (tb == 0 && te < groups) {
       left = item;
       left_to = (int)((start + groups - 1) / q);
     }
-    const int64_t slot = ((int64_t)blockIdx.x * 2 + (tb == 0 ? 1 : 0)) * kRows;
+    const int64_t slot = ((int64_t)piece * 2 + (tb == 0 ? 1 : 0)) * kRows;
     constexpr int kVec = D / 4;
-    for (int i = threadIdx.x; i < x.G * a.tt * kVec; i += kThreads) {
+    for (int i = kSolo ? lane : threadIdx.x; i < x.G * a.tt * kVec; i += 32 * kTeam) {
       const int row = i / kVec, f4 = i % kVec, tok = t0 + row % a.tt;
       if (tok >= r.n) continue;
       float M = -INFINITY, sum = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][row].x);
+      for (int j = 0; j < kTeam; ++j) M = fmaxf(M, sm.ml[kSolo ? warp : j][row].x);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int j = 0; j < kTeam; ++j) {
+        const int w = kSolo ? warp : j;
         const float2 ml = sm.ml[w][row];
         if (ml.x == -INFINITY) continue;               // saw nothing
         const float f = kvcd::ex2(ml.x - M);
@@ -587,9 +600,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
       }
       if (a.lse && f4 == 0) a.lse[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
     }
-    __syncthreads();                                   // the ring is free again
+    if (kSolo) __syncwarp();
+    else __syncthreads();                              // the ring is free again
   }
-  if (threadIdx.x == 0) a.tail[blockIdx.x] = make_int2(left, left_to);
+  if (kSolo ? lane == 0 : threadIdx.x == 0) a.tail[piece] = make_int2(left, left_to);
   // The next kernel's CTAs may come in from here: any earlier and they take registers that
   // this kernel's or its successor's CTAs need (70 us instead of 53 for one token, all layers).
   kvcd::pdl_trigger();
@@ -675,6 +689,14 @@ int row_tiles(const kvc_params* p, const kvc_chunk* c, int n_sel) {
 }
 int ctas_per_sm(const kvc_params* p, int nt) { return p->dtype == KVC_F32 || nt > 2 ? 2 : 3; }
 
+// Whether a warp takes an item by itself: one row tile, and more items than kSoloItems.
+constexpr int kSoloItems = 2400;
+bool solo(const kvc_params* p, const kvc_chunk* c, int n_sel) {
+  const int tt = n_sel > 0 ? 1 : std::min(8 / p->G, c->T);
+  return row_tiles(p, c, n_sel) == 1 &&
+         (int64_t)p->B * p->H * (c->layer_end - c->layer_begin) * ((c->T + tt - 1) / tt) >= kSoloItems;
+}
+
 // Whether the rows go to the kernel of kvc_chunk_attn (kvc_q8_chunk.cu).  Here and there: 64 rows
 // over 16384 entries (8 KV heads) 46 and 39 us, 128 rows 63 and 43, 8192 rows 2360 and 378.
 constexpr int kManyRows = 64;
@@ -684,7 +706,8 @@ bool many_rows(const kvc_params* p, const kvc_chunk* c, int n_sel) {
 
 Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   const int nt = row_tiles(p, c, n_sel);
-  const size_t pieces = (size_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, nt), rows = pieces * 2 * nt * 8;
+  const size_t pieces = (size_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, nt) * (solo(p, c, n_sel) ? kWarps : 1);
+  const size_t rows = pieces * 2 * nt * 8;
   Layout w;
   w.part = 0;
   w.ml = kvc::align256(rows * p->d * sizeof(float));
@@ -693,26 +716,31 @@ Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   return w;
 }
 
-template <typename T, int D, int NT, bool kSel>
+template <typename T, int D, int NT, bool kSel, bool kSolo>
 cudaError_t launch(const Q8Attn& a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<D, NT, Shape<T, NT>::kStages>);
-  cudaError_t e = kvc::chunk_allow_smem<q8_attn_kernel<T, D, NT, kSel>>(smem);
+  cudaError_t e = kvc::chunk_allow_smem<q8_attn_kernel<T, D, NT, kSel, kSolo>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = sms * Shape<T, NT>::kCtas;
   kvc::count_launch();
-  e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel>, dim3(grid), dim3(kThreads), smem, s, a);
+  e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel, kSolo>, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(grid, NT), dim3(256), 0, s, a);
+  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(kSolo ? grid * kWarps : grid, NT), dim3(256), 0, s, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_one_tile(const Q8Attn& a, bool solo, int sms, cudaStream_t s) {
+  if (a.sel) return solo ? launch<T, D, 1, true, true>(a, sms, s) : launch<T, D, 1, true, false>(a, sms, s);
+  return solo ? launch<T, D, 1, false, true>(a, sms, s) : launch<T, D, 1, false, false>(a, sms, s);
 }
 
 template <int D>
-cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, int sms, cudaStream_t s) {
+cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, bool solo, int sms, cudaStream_t s) {
   using B = __nv_bfloat16;
-  if (p->dtype == KVC_F32) return a.sel ? launch<float, D, 1, true>(a, sms, s) : launch<float, D, 1, false>(a, sms, s);
-  if (a.sel) return launch<B, D, 1, true>(a, sms, s);
-  return nt == 1 ? launch<B, D, 1, false>(a, sms, s) : nt == 2 ? launch<B, D, 2, false>(a, sms, s)
-       : nt == 3 ? launch<B, D, 3, false>(a, sms, s) : launch<B, D, 4, false>(a, sms, s);
+  if (p->dtype == KVC_F32) return launch_one_tile<float, D>(a, solo, sms, s);
+  return nt == 1 ? launch_one_tile<B, D>(a, solo, sms, s) : nt == 2 ? launch<B, D, 2, false, false>(a, sms, s)
+       : nt == 3 ? launch<B, D, 3, false, false>(a, sms, s) : launch<B, D, 4, false, false>(a, sms, s);
 }
 
 }  // namespace
@@ -756,8 +784,9 @@ extern "C" int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8
   a.tail = reinterpret_cast<int2*>(ws + w.tail);
   a.scale_log2 = kvcd::kLog2eC / sqrtf((float)p->d);
   const int nt = row_tiles(p, c, n_sel);
+  const bool lone = solo(p, c, n_sel);
   a.tt = n_sel > 0 ? 1 : std::min(nt * 8 / p->G, c->T);
   a.rp = (c->T + a.tt - 1) / a.tt;
   if (a.x.units * a.rp >= (1LL << 31)) return KVC_EINVAL;
-  return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, sms, s) : launch_d<64>(p, a, nt, sms, s));
+  return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, lone, sms, s) : launch_d<64>(p, a, nt, lone, sms, s));
 }

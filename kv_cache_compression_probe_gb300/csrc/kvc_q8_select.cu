@@ -10,8 +10,8 @@
 // (rows: G heads of one or more tokens), with the bounds as they lie in memory: a
 // product's 32 inner positions may stand for any features, as long as both operands agree, so
 // a lane takes whole 16-byte pieces.  The scores' order codes stay in shared
-// memory, where a warp per token (for a single token the whole CTA) looks for the n_sel-th largest bit by
-// bit.
+// memory, where a warp per token (for a single token the whole CTA) looks for the n_sel-th largest by
+// halving the range of codes; scores are spread over it, so about 10 steps are enough as a rule.
 #include <algorithm>
 
 #include "kvc_q8.cuh"
@@ -35,6 +35,7 @@ struct SelectSmem {
   uint2 q[NT][D / 16][32];             // the rows' q+ (first half) and q- as operands: a lane's words of a product
   float top[NT * 8];                   // the rows' largest |q|
   int count[2][kWarps];
+  uint32_t ends[2];
 };
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
@@ -59,13 +60,21 @@ __device__ __forceinline__ int block_sum(int v, int (&count)[2][kWarps], int& tu
 // The n_sel pages of largest code, by one warp, in ascending order.
 __device__ __forceinline__ void pick_by_warp(const uint32_t* keys, int nb, int n_sel, int32_t* out) {
   const int lane = threadIdx.x & 31;
-  uint32_t cut = 0;                                    // the largest code that n_sel pages reach
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t trial = cut | 1u << bit;
+  uint32_t cut = 0xffffffffu, top = 0;                 // least and largest code of the pages that need not be in
+  for (int b = lane; b < nb; b += 32) {
+    const uint32_t key = keys[b];
+    cut = min(cut, key);
+    top = max(top, key == 0xffffffffu ? 0 : key);
+  }
+  cut = __reduce_min_sync(KVC_FULL_MASK, cut);
+  top = max(cut, __reduce_max_sync(KVC_FULL_MASK, top));
+  while (cut < top) {                                  // cut: the largest code so far that n_sel pages reach; none above top is
+    const uint32_t trial = cut + (top - cut + 1) / 2;
     int mine = 0;
     for (int b = lane; b < nb; b += 32) mine += keys[b] >= trial;
     mine = __reduce_add_sync(KVC_FULL_MASK, mine);
     if (mine >= n_sel) cut = trial;
+    else top = trial - 1;
     if (mine == n_sel) break;
   }
   int above = 0;
@@ -85,16 +94,30 @@ __device__ __forceinline__ void pick_by_warp(const uint32_t* keys, int nb, int n
 
 // The same by the whole block; thread i looks at a run of pages.
 __device__ __forceinline__ void pick_by_block(const uint32_t* keys, int nb, int n_sel, int32_t* out,
-                                              int (&count)[2][kWarps]) {
+                                              int (&count)[2][kWarps], uint32_t (&ends)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int turn = 0;
-  uint32_t cut = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t trial = cut | 1u << bit;
+  uint32_t cut = 0xffffffffu, top = 0;
+  for (int b = tid; b < nb; b += kThreads) {
+    const uint32_t key = keys[b];
+    cut = min(cut, key);
+    top = max(top, key == 0xffffffffu ? 0 : key);
+  }
+  if (tid == 0) { ends[0] = 0xffffffffu; ends[1] = 0; }
+  __syncthreads();
+  cut = __reduce_min_sync(KVC_FULL_MASK, cut);
+  top = __reduce_max_sync(KVC_FULL_MASK, top);
+  if (lane == 0) { atomicMin(&ends[0], cut); atomicMax(&ends[1], top); }
+  __syncthreads();
+  cut = ends[0];
+  top = max(cut, ends[1]);
+  while (cut < top) {
+    const uint32_t trial = cut + (top - cut + 1) / 2;
     int mine = 0;
     for (int b = tid; b < nb; b += kThreads) mine += keys[b] >= trial;
     mine = block_sum(mine, count, turn);
     if (mine >= n_sel) cut = trial;
+    else top = trial - 1;
     if (mine == n_sel) break;
   }
   const int per = (nb + kThreads - 1) / kThreads, b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
@@ -148,10 +171,13 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
   if (most > a.n_sel) {
     const int32_t* tab = x.table + gu * x.max_pages;
     // ---- the first pages' bounds are on their way while the rows become integers
-    uint4 lo[2][kH], hi[2][kH];
-    float scale[2];
+    struct Fetched {
+      uint4 lo[2][kH], hi[2][kH];
+      float scale[2];
+    };
     bool bad = false;
     auto fetch = [&](int p0) {
+      Fetched f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int b = p0 + g + 8 * j;
@@ -163,13 +189,14 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
         const uint4* p = reinterpret_cast<const uint4*>(x.bounds + (int64_t)page * 2 * D) + c;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          lo[j][h] = __ldg(p + 4 * h);
-          hi[j][h] = __ldg(p + D / 16 + 4 * h);
+          f.lo[j][h] = __ldg(p + 4 * h);
+          f.hi[j][h] = __ldg(p + D / 16 + 4 * h);
         }
-        scale[j] = __ldg(x.k_scale + page);
+        f.scale[j] = __ldg(x.k_scale + page);
       }
+      return f;
     };
-    fetch(warp * 16);
+    Fetched next = fetch(warp * 16);
     for (int r = warp; r < NT * 8; r += kWarps) {
       const int tok = r / G;
       float v[4] = {0.f, 0.f, 0.f, 0.f}, top = 0.f;
@@ -197,7 +224,8 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
     }
     __syncthreads();
     for (int p0 = warp * 16; p0 < most; p0 += kWarps * 16) {
-      if (p0 > warp * 16) fetch(p0);
+      const Fetched f = next;
+      if (p0 + kWarps * 16 < most) next = fetch(p0 + kWarps * 16);
       int acc[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0;
@@ -205,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
       for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          const uint4 r0 = v ? lo[0][h] : hi[0][h], r1 = v ? lo[1][h] : hi[1][h];
+          const uint4 r0 = v ? f.lo[0][h] : f.hi[0][h], r1 = v ? f.lo[1][h] : f.hi[1][h];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_s8(acc[nt], r0.x, r1.x, r0.y, r1.y, sm.q[nt][v * kS + 2 * h][lane]);
@@ -217,8 +245,8 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int b = p0 + g + 8 * j;
-          float s0 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j], scale[j]), sm.top[nt * 8 + 2 * c]);
-          float s1 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j + 1], scale[j]), sm.top[nt * 8 + 2 * c + 1]);
+          float s0 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j], f.scale[j]), sm.top[nt * 8 + 2 * c]);
+          float s1 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j + 1], f.scale[j]), sm.top[nt * 8 + 2 * c + 1]);
           if (G > 1) s0 = fmaxf(s0, s1);
           if (G > 2) s0 = fmaxf(s0, __shfl_xor_sync(KVC_FULL_MASK, s0, 1));
           if (G > 4) s0 = fmaxf(s0, __shfl_xor_sync(KVC_FULL_MASK, s0, 2));
@@ -240,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
     __syncthreads();
   }
   if (tokens == 1 && most > a.n_sel) {
-    pick_by_block(keys, most, a.n_sel, out, sm.count);
+    pick_by_block(keys, most, a.n_sel, out, sm.count, sm.ends);
   } else {
     for (int tok = warp; tok < tokens; tok += kWarps) {
       const int nb = ((len + t0 + tok) >> x.shift) + 1;
