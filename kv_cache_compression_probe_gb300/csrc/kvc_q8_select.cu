@@ -6,10 +6,11 @@
 // 8-bit integers the sum is an integer below 2^24: exact, so a selection does not depend on the
 // order of a sum, and equal scores are equal.
 //
-// The sums are 8-bit integer products of the tensor cores, 16 pages x 8 query rows a time
-// (rows: G heads of one or more tokens), with the bounds as they lie in memory: a
-// product's 32 inner positions may stand for any features, as long as both operands agree, so
-// a lane takes whole 16-byte pieces.  The scores' order codes stay in shared
+// The sums are products of the tensor cores, 16 pages x 8 query rows a time (rows: G heads of one
+// or more tokens).  The integers go as fp16, which holds them exactly, and every partial sum is an integer
+// below 2^24, which fp32 holds: exact as well, and 8 times as fast here as the 8-bit integer form (8 cycles a 16 x 8 x 16
+// product and scheduler against 66 for 16 x 8 x 32).  A product's 16 inner positions may stand for any features, as long as
+// both operands agree, so a lane takes whole 16-byte pieces of the bounds.  The scores' order codes stay in shared
 // memory, where a warp per token (for a single token the whole CTA) looks for the n_sel-th largest by
 // halving the range of codes; scores are spread over it, so about 10 steps are enough as a rule.
 #include <algorithm>
@@ -32,17 +33,25 @@ struct Q8Select {
 
 template <int D, int NT>
 struct SelectSmem {
-  uint2 q[NT][D / 16][32];             // the rows' q+ (first half) and q- as operands: a lane's words of a product
+  uint2 q[NT][D / 8][32];              // the rows' q+ (first half) and q- as operands: a lane's words of a product
   float top[NT * 8];                   // the rows' largest |q|
   int count[2][kWarps];
   uint32_t ends[2];
 };
 
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+// Four signed bytes as fp16 pairs: with the sign bit turned over a byte is x + 128, the low bits of the fp16
+// number 1024 + 128 + x.
+__device__ __forceinline__ void bytes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
 // Sum of v over the block; `turn` alternates between calls, so one barrier is enough.
@@ -150,7 +159,7 @@ __device__ __forceinline__ void pick_by_block(const uint32_t* keys, int nb, int 
 // One CTA per (unit, tt tokens); query row r is head r % G of token r / G.
 template <typename T, int D, int G, int NT>
 __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_constant__ Q8Select a) {
-  constexpr int kH = D / 64, kS = D / 32;              // 16-byte pieces of a row per lane, products for lo (and for hi)
+  constexpr int kH = D / 64, kS = D / 16;              // 16-byte pieces of a row per lane, products for lo (and for hi)
   extern __shared__ uint32_t keys[];                   // [tt][max_pages] order codes of the scores
   __shared__ SelectSmem<D, NT> sm;
   const Q8Args& x = a.x;
@@ -215,10 +224,12 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
         m |= (uint32_t)(min(k, 0) & 255) << (8 * i);
       }
       if (lane < D / 4) {                              // word `lane`: piece h, lane c of the operand, word i of it
-        const int h = lane / 16, cc = (lane % 16) / 4, i = lane % 4, s = 2 * h + i / 2;
-        uint32_t* to = reinterpret_cast<uint32_t*>(&sm.q[r / 8][s][(r % 8) * 4 + cc]) + (i & 1);
-        to[0] = p;
-        to[kS * 64] = m;                               // kS products later
+        const int h = lane / 16, cc = (lane % 16) / 4, i = lane % 4;
+        uint2 y;
+        bytes_f16(p, y.x, y.y);
+        sm.q[r / 8][4 * h + i][(r % 8) * 4 + cc] = y;
+        bytes_f16(m, y.x, y.y);
+        sm.q[r / 8][kS + 4 * h + i][(r % 8) * 4 + cc] = y;
       }
       if (lane == 0) sm.top[r] = top;
     }
@@ -226,18 +237,22 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
     for (int p0 = warp * 16; p0 < most; p0 += kWarps * 16) {
       const Fetched f = next;
       if (p0 + kWarps * 16 < most) next = fetch(p0 + kWarps * 16);
-      int acc[NT][4];
+      float acc[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0;
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
       for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
           const uint4 r0 = v ? f.lo[0][h] : f.hi[0][h], r1 = v ? f.lo[1][h] : f.hi[1][h];
+          const uint32_t wa[4] = {r0.x, r0.y, r0.z, r0.w}, wb[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_s8(acc[nt], r0.x, r1.x, r0.y, r1.y, sm.q[nt][v * kS + 2 * h][lane]);
-            mma_s8(acc[nt], r0.z, r1.z, r0.w, r1.w, sm.q[nt][v * kS + 2 * h + 1][lane]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, a2, a3;
+            bytes_f16(wa[i], a0, a2);
+            bytes_f16(wb[i], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a0, a1, a2, a3, sm.q[nt][v * kS + 4 * h + i][lane]);
           }
         }
 #pragma unroll
@@ -245,8 +260,8 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int b = p0 + g + 8 * j;
-          float s0 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j], f.scale[j]), sm.top[nt * 8 + 2 * c]);
-          float s1 = __fmul_rn(__fmul_rn((float)acc[nt][2 * j + 1], f.scale[j]), sm.top[nt * 8 + 2 * c + 1]);
+          float s0 = __fmul_rn(__fmul_rn(acc[nt][2 * j], f.scale[j]), sm.top[nt * 8 + 2 * c]);
+          float s1 = __fmul_rn(__fmul_rn(acc[nt][2 * j + 1], f.scale[j]), sm.top[nt * 8 + 2 * c + 1]);
           if (G > 1) s0 = fmaxf(s0, s1);
           if (G > 2) s0 = fmaxf(s0, __shfl_xor_sync(KVC_FULL_MASK, s0, 1));
           if (G > 4) s0 = fmaxf(s0, __shfl_xor_sync(KVC_FULL_MASK, s0, 2));
