@@ -158,7 +158,7 @@ __device__ __forceinline__ void pick_by_block(const uint32_t* keys, int nb, int 
 
 // One CTA per (unit, tt tokens); query row r is head r % G of token r / G.
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_constant__ Q8Select a) {
+__global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_constant__ Q8Select a) {
   constexpr int kH = D / 64, kS = D / 16;              // 16-byte pieces of a row per lane, products for lo (and for hi)
   extern __shared__ uint32_t keys[];                   // [tt][max_pages] order codes of the scores
   __shared__ SelectSmem<D, NT> sm;
@@ -206,20 +206,26 @@ __global__ void __launch_bounds__(kThreads) q8_select_kernel(const __grid_consta
       return f;
     };
     Fetched next = fetch(warp * 16);
-    for (int r = warp; r < NT * 8; r += kWarps) {
-      const int tok = r / G;
-      float v[4] = {0.f, 0.f, 0.f, 0.f}, top = 0.f;
-      if (tok < tokens && lane < D / 4) {
-        kvcd::VecLoad<T, 4>::ld(static_cast<const T*>(a.q) + ((u * G + r % G) * x.T + t0 + tok) * D + 4 * lane, v);
+    float v[NT][4];                                    // this warp's rows warp, warp + 8, ..
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]));
-      }
+    for (int j = 0; j < NT; ++j) {
+      const int r = warp + j * kWarps, tok = r / G;
+      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.f;
+      if (tok < tokens && lane < D / 4)
+        kvcd::VecLoad<T, 4>::ld(static_cast<const T*>(a.q) + ((u * G + r % G) * x.T + t0 + tok) * D + 4 * lane, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = warp + j * kWarps;
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[j][i]));
       top = kvcd::warp_max(top);
       const float inv = top > 0.f ? __fmul_rn(127.f, __frcp_rn(top)) : 0.f;
       uint32_t p = 0, m = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k = min(max(__float2int_rn(__fmul_rn(v[i], inv)), -127), 127);
+        const int k = min(max(__float2int_rn(__fmul_rn(v[j][i], inv)), -127), 127);
         p |= (uint32_t)(max(k, 0) & 255) << (8 * i);
         m |= (uint32_t)(min(k, 0) & 255) << (8 * i);
       }
