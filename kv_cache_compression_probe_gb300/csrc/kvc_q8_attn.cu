@@ -198,9 +198,17 @@ struct WarpRing {
   alignas(128) unsigned char codes[kStages][kStage];             // later this warp's O
   float lm[kStages][16];
 };
+template <int D, int NT>
+struct SharedQ {                       // the query rows as operands, and what their products are in units of
+  uint2 words[NT][D / 16][32];
+  float units[NT * 8];
+};
+template <int D>
+struct SharedQ<D, 1> {};
 template <int D, int NT, int kStages>
 struct AttnSmem {
   WarpRing<D, kStages> ring[kWarps];
+  SharedQ<D, NT> q;
   float2 ml[kWarps][NT * 8];
   LocateSmem loc;
 };
@@ -210,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kQ = kF32 ? 3 : 1, kP = kF32 ? 2 : 1;  // fp16 parts of a query row, of the numerators
   constexpr int kH = D / 64, kS = D / 16;              // 16-byte pieces of a row per lane, products
+  constexpr bool kShareQ = NT > 1;
   constexpr int kRows = NT * 8;
   constexpr int kF = D / 8;                            // features of a lane's output
   constexpr int kStages = Shape<T, NT>::kStages;
@@ -328,12 +337,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     };
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) issue(k, 0);
-    // ---- query rows: row nt*8 + g as the operand of this lane
-    uint32_t qf[kQ][NT][kS][2];
+    // ---- query rows: row nt*8 + g as the operand of this lane, in registers; of several row tiles in
+    // shared memory, which the CTA's warps fill together
+    uint32_t qr[kQ][kShareQ ? 1 : NT][kS][2];
     float fq[NT][2];
     int see[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    auto query_tile = [&](int nt, uint32_t (&qf)[kQ][kS][2]) {   // its operand; returns what the row's products are in units of
       const int row = nt * 8 + g, head = row / a.tt, tok = t0 + row % a.tt;
       const bool live = head < x.G && tok < r.n;
       const T* src = static_cast<const T*>(a.q) + (((int64_t)u * x.G + head) * x.T + tok) * D + 16 * c;
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
 #pragma unroll
           for (int k = 0; k < kQ; ++k) {
             const uint32_t w = f16x2(y0, y1);
-            qf[k][nt][h * 4 + i / 4][(i >> 1) & 1] = w;
+            qf[k][h * 4 + i / 4][(i >> 1) & 1] = w;
             if (k + 1 < kQ) {
               float z0, z1;
               kvcd::f16x2_f32(w, z0, z1);
@@ -368,12 +377,35 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
             }
           }
         }
+      return kvcd::pow2i(e) * a.scale_log2;
+    };
+    if constexpr (kShareQ) {
+      for (int nt = warp; nt < NT; nt += kWarps) {
+        uint32_t qf[kQ][kS][2];
+        const float up = query_tile(nt, qf);
+#pragma unroll
+        for (int j = 0; j < kS; ++j) sm.q.words[nt][j][lane] = make_uint2(qf[0][j][0], qf[0][j][1]);
+        if (c == 0) sm.q.units[nt * 8 + g] = up;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float up = 0.f;
+      if constexpr (!kShareQ) {
+        uint32_t qf[kQ][kS][2];
+        up = query_tile(nt, qf);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i)
+#pragma unroll
+          for (int j = 0; j < kS; ++j) { qr[i][nt][j][0] = qf[i][j][0]; qr[i][nt][j][1] = qf[i][j][1]; }
+      }
       // what this lane needs of its result columns, rows nt*8 + 2c and + 1
-      const float up = kvcd::pow2i(e) * a.scale_log2;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        fq[nt][k] = __shfl_sync(KVC_FULL_MASK, up, 8 * c + 4 * k);
         const int row2 = nt * 8 + 2 * c + k, tok2 = t0 + row2 % a.tt;
+        if constexpr (kShareQ) fq[nt][k] = sm.q.units[row2];
+        else fq[nt][k] = __shfl_sync(KVC_FULL_MASK, up, 8 * c + 4 * k);
         see[nt][k] = row2 / a.tt < x.G && tok2 < r.n ? r.len + tok2 + 1 : 0;
       }
     }
@@ -415,7 +447,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = kQ - 1; i >= 0; --i)
-                mma16816(s[nt], a0, a1, a2, a3, qf[i][nt][h * 4 + w][0], qf[i][nt][h * 4 + w][1]);
+                if constexpr (kShareQ) {
+                  const uint2 b = sm.q.words[nt][h * 4 + w][lane];
+                  mma16816(s[nt], a0, a1, a2, a3, b.x, b.y);
+                } else {
+                  mma16816(s[nt], a0, a1, a2, a3, qr[i][nt][h * 4 + w][0], qr[i][nt][h * 4 + w][1]);
+                }
           }
         }
         // ---- base-2 scores
