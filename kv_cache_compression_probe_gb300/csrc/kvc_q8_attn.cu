@@ -59,8 +59,7 @@ struct Q8Attn {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -175,17 +174,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t p) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
-  return v;
-}
-
 // Shape of a kernel: CTAs per SM, and groups in a warp's ring.
 template <typename T, int NT>
 struct Shape {
@@ -431,14 +419,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
       cp_wait<kStages - 2>();
       __syncwarp();
       if (here) {
-        const uint32_t st = codes0 + (k % kStages) * WarpRing<D, kStages>::kStage;
+        const unsigned char* st = ring.codes[k % kStages];
         float s[NT][4];
         // ---- S^T = K Q^T
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          const uint4 ka = lds128(st + k_at[h]), kb = lds128(st + k_at[h] + 8 * D);
+          const uint4 ka = *reinterpret_cast<const uint4*>(st + k_at[h]), kb = *reinterpret_cast<const uint4*>(st + k_at[h] + 8 * D);
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -547,12 +535,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
         uint32_t vw[4][kF / 4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t p = st + WarpRing<D, kStages>::kKeys + v_at[j & 1] + (j >> 1) * 8 * D;
+          const unsigned char* p = st + WarpRing<D, kStages>::kKeys + v_at[j & 1] + (j >> 1) * 8 * D;
           if constexpr (D == 128) {
-            const uint4 v = lds128(p);
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
             vw[j][0] = v.x; vw[j][1] = v.y; vw[j][2] = v.z; vw[j][3] = v.w;
           } else {
-            const uint2 v = lds64(p);
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
             vw[j][0] = v.x; vw[j][1] = v.y;
           }
         }
