@@ -55,6 +55,7 @@ struct Q8Attn {
   int2* tail;                          // [CTAs]: the item a piece leaves unfinished, and its last piece
   float scale_log2;
   int n_sel, tt, rp;                   // tokens per row block, row blocks per unit
+  int team;                            // CTAs of an item (kTeam)
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -174,6 +175,29 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// How the groups are shared out: kLine and kSolo as above; kTeam: a cluster an item, whose CTAs join
+// their results through distributed shared memory, without a combine kernel.
+enum Mode { kLine, kSolo, kTeam };
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {     // of the same place in another CTA
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(kvcd::smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // Shape of a kernel: CTAs per SM, and groups in a warp's ring.
 template <typename T, int NT>
 struct Shape {
@@ -198,10 +222,11 @@ struct AttnSmem {
   WarpRing<D, kStages> ring[kWarps];
   SharedQ<D, NT> q;
   float2 ml[kWarps][NT * 8];
+  float2 joined[NT * 8];               // of the CTA's warps
   LocateSmem loc;
 };
 
-template <typename T, int D, int NT, bool kSel, bool kSolo>
+template <typename T, int D, int NT, bool kSel, Mode kMode>
 __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(const __grid_constant__ Q8Attn a) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kQ = kF32 ? 3 : 1, kP = kF32 ? 2 : 1;  // fp16 parts of a query row, of the numerators
@@ -217,12 +242,22 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
   const Q8Args& x = a.x;
   kvcd::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  long long q, lo, hi;
-  locate<kSel, kSolo>(a, sm.loc, q, lo, hi);
-  constexpr int kTeam = kSolo ? 1 : kWarps;            // warps that share an item's groups
-  const int me = kSolo ? 0 : warp, piece = kSolo ? blockIdx.x * kWarps + warp : blockIdx.x;
-  long long start = sm.loc.start;
-  int item = sm.loc.item, left = -1, left_to = 0;
+  constexpr int kShare = kMode == kSolo ? 1 : kWarps;  // warps that share an item's groups
+  const int me = kMode == kSolo ? 0 : warp, piece = kMode == kSolo ? blockIdx.x * kWarps + warp : blockIdx.x;
+  long long q = 0, lo = 0, hi = 0, start = 0;
+  int item = 0, left = -1, left_to = 0;
+  if constexpr (kMode == kTeam) {                      // this CTA's share of its cluster's item
+    item = blockIdx.x / a.team;
+    const int rank = blockIdx.x - item * a.team, u0 = item / a.rp;
+    const long long n = item_groups<kSel>(a, load_unit(x, u0), (item - u0 * a.rp) * a.tt);
+    if (n == 0) return;
+    lo = n * rank / a.team;                            // (no group of its own: it takes part in the joining all the same)
+    hi = n * (rank + 1) / a.team;
+  } else {
+    locate<kSel, kMode == kSolo>(a, sm.loc, q, lo, hi);
+    start = sm.loc.start;
+    item = sm.loc.item;
+  }
   bool bad = false;
   WarpRing<D, kStages>& ring = sm.ring[warp];
   const uint32_t codes0 = kvcd::smem_u32(ring.codes), lm0 = kvcd::smem_u32(ring.lm);
@@ -245,9 +280,19 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) c_at[i] = place(crow + i * kPer, cchunk);
 
+  // Four features of a finished row.
+  auto put_row = [&](int u, int t0, int row, int f4, float M, float sum, const float4& y) {
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t orow = ((int64_t)u * x.G + row / a.tt) * x.T + t0 + row % a.tt;
+    T* to = static_cast<T*>(a.out) + orow * D + 4 * f4;
+    if constexpr (kF32) *reinterpret_cast<float4*>(to) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    else *reinterpret_cast<uint2*>(to) = make_uint2(kvctc::bf16x2(y.x * inv, y.y * inv), kvctc::bf16x2(y.z * inv, y.w * inv));
+    if (a.lse && f4 == 0) a.lse[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+  };
+
   int ru = -1;
   Unit r;
-  for (long long at = lo; at < hi;) {
+  for (long long at = lo; kMode == kTeam || at < hi;) {
     // the item that holds group `at`
     int u, t0, groups;
     while (true) {
@@ -255,13 +300,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
       t0 = (item - u * a.rp) * a.tt;
       if (u != ru) r = load_unit(x, ru = u);
       groups = item_groups<kSel>(a, r, t0);
-      if (at < start + groups) break;
+      if (kMode == kTeam || at < start + groups) break;
       start += groups;
       ++item;
     }
     const int tb = (int)(at - start), te = (int)min((long long)groups, hi - start);
     at = start + te;
-    const int count = max(0, (te - tb - me + kTeam - 1) / kTeam);   // this warp's groups
+    const int count = max(0, (te - tb - me + kShare - 1) / kShare);   // this warp's groups
     const int total = r.len + r.n, all_see = r.len + t0 + 1;   // entries; those that every row sees
     const int32_t* tab = x.table + r.gu * x.max_pages;
     const int32_t* list = kSel ? a.sel + ((int64_t)u * x.T + t0) * a.n_sel : nullptr;
@@ -271,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     struct Window { int e0, row, exps; };
     auto window = [&](int k0) {
       Window w{0, -1, 0};
-      const int gi = tb + me + kTeam * (k0 + lane);
+      const int gi = tb + me + kShare * (k0 + lane);
       if (gi < te) {
         w.e0 = gi << 4;
         bool ok = true;
@@ -294,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     };
     Window cur = window(0), nxt = window(32);
     auto entry = [&](const Window& w, int k) {
-      return kSel ? __shfl_sync(KVC_FULL_MASK, w.e0, k & 31) : (tb + me + kTeam * k) << 4;
+      return kSel ? __shfl_sync(KVC_FULL_MASK, w.e0, k & 31) : (tb + me + kShare * k) << 4;
     };
     auto issue = [&](int k, int base) {                // base: the first group of `cur`
       if (k < count) {
@@ -581,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
           *reinterpret_cast<float4*>(to + 2 * j) = make_float4(o[nt][j][i] * unit, o[nt][j][2 + i] * unit,
                                                                o[nt][j + 1][i] * unit, o[nt][j + 1][2 + i] * unit);
       }
-    if (kSolo) __syncwarp();
+    if (kMode == kSolo) __syncwarp();
     else __syncthreads();
     const bool whole = tb == 0 && te == groups;
     if (tb == 0 && te < groups) {
@@ -590,16 +635,16 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     }
     const int64_t slot = ((int64_t)piece * 2 + (tb == 0 ? 1 : 0)) * kRows;
     constexpr int kVec = D / 4;
-    for (int i = kSolo ? lane : threadIdx.x; i < x.G * a.tt * kVec; i += 32 * kTeam) {
+    for (int i = kMode == kSolo ? lane : threadIdx.x; i < x.G * a.tt * kVec; i += 32 * kShare) {
       const int row = i / kVec, f4 = i % kVec, tok = t0 + row % a.tt;
       if (tok >= r.n) continue;
       float M = -INFINITY, sum = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < kTeam; ++j) M = fmaxf(M, sm.ml[kSolo ? warp : j][row].x);
+      for (int j = 0; j < kShare; ++j) M = fmaxf(M, sm.ml[kMode == kSolo ? warp : j][row].x);
 #pragma unroll
-      for (int j = 0; j < kTeam; ++j) {
-        const int w = kSolo ? warp : j;
+      for (int j = 0; j < kShare; ++j) {
+        const int w = kMode == kSolo ? warp : j;
         const float2 ml = sm.ml[w][row];
         if (ml.x == -INFINITY) continue;               // saw nothing
         const float f = kvcd::ex2(ml.x - M);
@@ -610,25 +655,45 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
         y.z = fmaf(v.z, f, y.z);
         y.w = fmaf(v.w, f, y.w);
       }
-      if (!whole) {
+      if constexpr (kMode == kTeam) {                  // in place: only this thread uses these
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(sm.ring[0].codes) + row * D + 4 * f4) = y;
+        if (f4 == 0) sm.joined[row] = make_float2(M, sum);
+      } else if (whole) {
+        put_row(u, t0, row, f4, M, sum, y);
+      } else {
         *reinterpret_cast<float4*>(a.part + (slot + row) * D + 4 * f4) = y;
         if (f4 == 0) a.part_ml[slot + row] = make_float2(M, sum);
-        continue;
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int64_t orow = ((int64_t)u * x.G + row / a.tt) * x.T + tok;
-      T* to = static_cast<T*>(a.out) + orow * D + 4 * f4;
-      if constexpr (kF32) {
-        *reinterpret_cast<float4*>(to) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-      } else {
-        *reinterpret_cast<uint2*>(to) = make_uint2(kvctc::bf16x2(y.x * inv, y.y * inv), kvctc::bf16x2(y.z * inv, y.w * inv));
-      }
-      if (a.lse && f4 == 0) a.lse[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
     }
-    if (kSolo) __syncwarp();
+    if constexpr (kMode == kTeam) {
+      cluster_sync();
+      const int rank = blockIdx.x - item * a.team;
+      for (int i = rank * kThreads + threadIdx.x; i < x.G * a.tt * kVec; i += a.team * kThreads) {
+        const int row = i / kVec, f4 = i % kVec;
+        if (t0 + row % a.tt >= r.n) continue;
+        float M = -INFINITY, sum = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < a.team; ++w) {
+          const float2 ml = cluster_load2(cluster_addr(&sm.joined[row], w));
+          const float4 v = cluster_load4(cluster_addr(reinterpret_cast<const float*>(sm.ring[0].codes) + row * D + 4 * f4, w));
+          if (ml.x == -INFINITY) continue;             // saw nothing
+          const float Mn = fmaxf(M, ml.x), f0 = kvcd::ex2(M - Mn), f1 = kvcd::ex2(ml.x - Mn);
+          sum = fmaf(sum, f0, ml.y * f1);
+          y.x = fmaf(y.x, f0, v.x * f1);
+          y.y = fmaf(y.y, f0, v.y * f1);
+          y.z = fmaf(y.z, f0, v.z * f1);
+          y.w = fmaf(y.w, f0, v.w * f1);
+          M = Mn;
+        }
+        put_row(u, t0, row, f4, M, sum, y);
+      }
+      cluster_sync();                                  // nobody leaves while others read from it
+      break;
+    }
+    if (kMode == kSolo) __syncwarp();
     else __syncthreads();                              // the ring is free again
   }
-  if (kSolo ? lane == 0 : threadIdx.x == 0) a.tail[piece] = make_int2(left, left_to);
+  if (kMode == kSolo ? lane == 0 : kMode == kLine && threadIdx.x == 0) a.tail[piece] = make_int2(left, left_to);
   // The next kernel's CTAs may come in from here: any earlier and they take registers that
   // this kernel's or its successor's CTAs need (70 us instead of 53 for one token, all layers).
   kvcd::pdl_trigger();
@@ -714,12 +779,34 @@ int row_tiles(const kvc_params* p, const kvc_chunk* c, int n_sel) {
 }
 int ctas_per_sm(const kvc_params* p, int nt) { return p->dtype == KVC_F32 || nt > 2 ? 2 : 3; }
 
+// Tokens of a row block, and items of a call.
+int block_tokens(const kvc_params* p, const kvc_chunk* c, int n_sel) {
+  return n_sel > 0 ? 1 : std::min(row_tiles(p, c, n_sel) * 8 / p->G, c->T);
+}
+int64_t item_count(const kvc_params* p, const kvc_chunk* c, int n_sel) {
+  const int tt = block_tokens(p, c, n_sel);
+  return (int64_t)p->B * p->H * (c->layer_end - c->layer_begin) * ((c->T + tt - 1) / tt);
+}
+
 // Whether a warp takes an item by itself: one row tile, and more items than kSoloItems.
 constexpr int kSoloItems = 2400;
 bool solo(const kvc_params* p, const kvc_chunk* c, int n_sel) {
-  const int tt = n_sel > 0 ? 1 : std::min(8 / p->G, c->T);
-  return row_tiles(p, c, n_sel) == 1 &&
-         (int64_t)p->B * p->H * (c->layer_end - c->layer_begin) * ((c->T + tt - 1) / tt) >= kSoloItems;
+  return row_tiles(p, c, n_sel) == 1 && item_count(p, c, n_sel) >= kSoloItems;
+}
+
+// CTAs that take an item as a cluster, or 0: where the items are few, and short by what the pages (picked, or of
+// the table) hold at most.  A warp then has kTeamGroups groups to do at most; a longer
+// item wants more CTAs than a cluster has.
+constexpr int kTeamGroups = 16;
+int team_size(const kvc_params* p, const kvc_chunk* c, int n_sel) {
+  const int64_t items = item_count(p, c, n_sel);
+  const int64_t groups = (int64_t)(n_sel > 0 ? std::min(n_sel, c->max_pages) : c->max_pages) * (c->page_rows / 16);
+  const int64_t room = (int64_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, row_tiles(p, c, n_sel));
+  int team = 8;
+  while (team > 1 && items * team > room) team /= 2;
+  if (items * team > room || groups > (int64_t)team * kWarps * kTeamGroups) return 0;
+  while (team > 1 && groups <= team / 2 * kWarps) team /= 2;   // no more than there are groups for
+  return team;
 }
 
 // Whether the rows go to the kernel of kvc_chunk_attn (kvc_q8_chunk.cu).  Here and there: 64 rows
@@ -741,31 +828,50 @@ Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   return w;
 }
 
-template <typename T, int D, int NT, bool kSel, bool kSolo>
-cudaError_t launch(const Q8Attn& a, int sms, cudaStream_t s) {
+template <typename T, int D, int NT, bool kSel, Mode kMode>
+cudaError_t launch_mode(const Q8Attn& a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<D, NT, Shape<T, NT>::kStages>);
-  cudaError_t e = kvc::chunk_allow_smem<q8_attn_kernel<T, D, NT, kSel, kSolo>>(smem);
+  cudaError_t e = kvc::chunk_allow_smem<q8_attn_kernel<T, D, NT, kSel, kMode>>(smem);
   if (e != cudaSuccess) return e;
+  kvc::count_launch();
+  if (kMode == kTeam) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.x.units * a.rp * a.team));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)a.team;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, q8_attn_kernel<T, D, NT, kSel, kMode>, a);
+  }
   const int grid = sms * Shape<T, NT>::kCtas;
-  kvc::count_launch();
-  e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel, kSolo>, dim3(grid), dim3(kThreads), smem, s, a);
+  e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel, kMode>, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(kSolo ? grid * kWarps : grid, NT), dim3(256), 0, s, a);
+  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(kMode == kSolo ? grid * kWarps : grid, NT), dim3(256), 0, s, a);
 }
 
-template <typename T, int D>
-cudaError_t launch_one_tile(const Q8Attn& a, bool solo, int sms, cudaStream_t s) {
-  if (a.sel) return solo ? launch<T, D, 1, true, true>(a, sms, s) : launch<T, D, 1, true, false>(a, sms, s);
-  return solo ? launch<T, D, 1, false, true>(a, sms, s) : launch<T, D, 1, false, false>(a, sms, s);
+template <typename T, int D, int NT, bool kSel>
+cudaError_t launch(const Q8Attn& a, bool alone, int sms, cudaStream_t s) {
+  if (a.team > 0) return launch_mode<T, D, NT, kSel, kTeam>(a, sms, s);
+  if constexpr (NT == 1)
+    if (alone) return launch_mode<T, D, NT, kSel, kSolo>(a, sms, s);
+  return launch_mode<T, D, NT, kSel, kLine>(a, sms, s);
 }
 
 template <int D>
-cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, bool solo, int sms, cudaStream_t s) {
+cudaError_t launch_d(const kvc_params* p, const Q8Attn& a, int nt, bool alone, int sms, cudaStream_t s) {
   using B = __nv_bfloat16;
-  if (p->dtype == KVC_F32) return launch_one_tile<float, D>(a, solo, sms, s);
-  return nt == 1 ? launch_one_tile<B, D>(a, solo, sms, s) : nt == 2 ? launch<B, D, 2, false, false>(a, sms, s)
-       : nt == 3 ? launch<B, D, 3, false, false>(a, sms, s) : launch<B, D, 4, false, false>(a, sms, s);
+  if (p->dtype == KVC_F32) return a.sel ? launch<float, D, 1, true>(a, alone, sms, s) : launch<float, D, 1, false>(a, alone, sms, s);
+  if (a.sel) return launch<B, D, 1, true>(a, alone, sms, s);
+  return nt == 1 ? launch<B, D, 1, false>(a, alone, sms, s) : nt == 2 ? launch<B, D, 2, false>(a, alone, sms, s)
+       : nt == 3 ? launch<B, D, 3, false>(a, alone, sms, s) : launch<B, D, 4, false>(a, alone, sms, s);
 }
 
 }  // namespace
@@ -809,9 +915,10 @@ extern "C" int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8
   a.tail = reinterpret_cast<int2*>(ws + w.tail);
   a.scale_log2 = kvcd::kLog2eC / sqrtf((float)p->d);
   const int nt = row_tiles(p, c, n_sel);
-  const bool lone = solo(p, c, n_sel);
-  a.tt = n_sel > 0 ? 1 : std::min(nt * 8 / p->G, c->T);
+  const bool alone = solo(p, c, n_sel);
+  a.team = team_size(p, c, n_sel);
+  a.tt = block_tokens(p, c, n_sel);
   a.rp = (c->T + a.tt - 1) / a.tt;
   if (a.x.units * a.rp >= (1LL << 31)) return KVC_EINVAL;
-  return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, lone, sms, s) : launch_d<64>(p, a, nt, lone, sms, s));
+  return kvc::cuda_status(p->d == 128 ? launch_d<128>(p, a, nt, alone, sms, s) : launch_d<64>(p, a, nt, alone, sms, s));
 }

@@ -40,6 +40,15 @@ CASES = {
     "many units": dict(lens=np.arange(7 * 3 * 16) * 3 % 211, n_new=[1, 2, 3, 4, 5, 6, 7], B=7, L=3, H=16, G=2),
     "runs of short units": dict(lens=np.where(np.arange(600) % 7 == 3, 300, np.arange(600) % 50), n_new=[1], L=50,
                                 H=12, G=1, d=64),
+    # tables wider than the cache needs (then an item's groups are not known to be few), by row tiles
+    "wide table": dict(lens=[300, 50, 700, 129], n_new=[1], H=4, max_pages=700),
+    "wide table, two tiles": dict(lens=[300, 50, 700, 129], n_new=[4], H=4, max_pages=700),
+    "wide table, three tiles": dict(lens=[300, 50, 700, 129], n_new=[5, 3], B=2, H=2, page=32, max_pages=300),
+    "wide table, four tiles": dict(lens=[300, 50, 700, 129], n_new=[7, 8], B=2, H=2, max_pages=700),
+    "wide table, G 8, d 64": dict(lens=[300, 50, 700, 129], n_new=[2, 1], B=2, H=2, G=8, d=64, page=64, max_pages=200),
+    # more items than warps
+    "many items": dict(lens=np.arange(2500) % 37, n_new=[1], L=125, H=20, d=64),
+    "many tokens": dict(lens=np.arange(32) * 7 % 150, n_new=[80, 79, 80, 70], B=4, H=8, G=2, d=64),
     "layer range": dict(lens=[5, 70, 200, 130, 64, 9, 1, 300], n_new=[9, 20], B=2, L=4, layers=(1, 3)),
     "layer range, long": dict(lens=[5, 70, 200, 130, 64, 9], n_new=[90, 61], B=2, L=3, layers=(1, 3), page=64),
     "no n_new": dict(lens=[5, 70], n_new=[9, 9], B=2, pass_n_new=False),
@@ -50,7 +59,8 @@ CASES = {
     "sharp, one token": dict(lens=[300, 700], n_new=[1], H=2, qscale=20.0, page=64),
 }
 F32 = ("one token", "one token, page 128, d 64", "ragged chunks", "drafts, G 8", "long chunk", "layer range",
-       "scales of all sizes", "dead entries", "sharp", "no new tokens anywhere", "empty cache")
+       "scales of all sizes", "dead entries", "sharp", "no new tokens anywhere", "empty cache", "wide table",
+       "wide table, four tiles", "wide table, G 8, d 64", "many items", "many tokens")
 ALL = [(n, "bf16") for n in CASES] + [(n, "f32") for n in F32]
 IDS = [f"{n}-{t}" for n, t in ALL]
 
