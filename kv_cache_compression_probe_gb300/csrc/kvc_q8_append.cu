@@ -316,10 +316,9 @@ __global__ void __launch_bounds__(kThreads, kW > 1 ? 3 : 4) q8_append_kernel(con
   const int len = __ldg(x.len_lh + gu), n = x.n_new ? __ldg(x.n_new + b) : x.T, cap = __ldg(a.cap_lh + gu);
   const int64_t e0 = a.cos_tab ? table_row(__ldg(a.pos_new + b), n, a.n_half) : 0;
   int bad = KVC_OK;
-  if (len < 0 || n < 0 || n > x.T || (int64_t)len + n > (int64_t)x.max_pages << x.shift || (n > 0 && e0 < 0))
-    bad = KVC_EDEVICE;
-  else if ((int64_t)len + n > cap)
-    bad = KVC_ECAPACITY;
+  if (len < 0 || n < 0 || n > x.T || (n > 0 && e0 < 0)) bad = KVC_EDEVICE;
+  else if ((int64_t)len + n > cap) bad = KVC_ECAPACITY;
+  else if ((int64_t)len + n > (int64_t)x.max_pages << x.shift) bad = KVC_EDEVICE;
   const int32_t* tab = x.table + gu * x.max_pages;
   const int first = len >> x.shift, last = n > 0 ? (len + n - 1) >> x.shift : first - 1;
   // Every warp looks at all the pages that the unit's tokens touch; the first one reports.
@@ -395,8 +394,9 @@ __global__ void __launch_bounds__(kThreads) q8_pack_kernel(const __grid_constant
   const int len = x.len_lh[gu], cap = a.cap_lh[gu], R = 1 << x.shift;
   const int32_t* tab = x.table + gu * x.max_pages;
   int bad = KVC_OK;
-  if (len < 0 || len > (int64_t)x.max_pages << x.shift || off < 0 || off + len > a.rows) bad = KVC_EDEVICE;
+  if (len < 0 || off < 0 || off + len > a.rows) bad = KVC_EDEVICE;
   else if (len > cap) bad = KVC_ECAPACITY;
+  else if (len > (int64_t)x.max_pages << x.shift) bad = KVC_EDEVICE;
   bool ok = true;
   const int need = bad == KVC_OK ? (int)(((int64_t)len + R - 1) >> x.shift) : 0;
   for (int i = threadIdx.x; i < need; i += kThreads) ok &= (unsigned)__ldg(tab + i) < (unsigned)x.pages;

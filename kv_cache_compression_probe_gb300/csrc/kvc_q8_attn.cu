@@ -797,7 +797,7 @@ bool solo(const kvc_params* p, const kvc_chunk* c, int n_sel) {
 // CTAs that take an item as a cluster, or 0: where the items are few, and short by what the pages (picked, or of
 // the table) hold at most.  A warp then has kTeamGroups groups to do at most; a longer
 // item wants more CTAs than a cluster has.
-constexpr int kTeamGroups = 16;
+constexpr int kTeamGroups = 32;
 int team_size(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   const int64_t items = item_count(p, c, n_sel);
   const int64_t groups = (int64_t)(n_sel > 0 ? std::min(n_sel, c->max_pages) : c->max_pages) * (c->page_rows / 16);

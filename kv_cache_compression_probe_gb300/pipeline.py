@@ -325,6 +325,17 @@ class Compressor:
                            self.len_lh, self.cap_lh, self.off_lh, out, lse, self.len_lh,
                            self._ws_chunk, stream)
 
+    def to_q8(self, reserve: int, pos_next, T: int = 1, **kw):
+        """The packed cache in 8 bits (kvc_q8_pack), as a QuantizedCache with room for `reserve`
+        more tokens per (b, l, h), in calls of up to T.  pos_next [B]: the position of each sequence's next token
+        (n_max at most, unless n_pos says otherwise); further arguments as QuantizedCache's.
+        Waits for the device once, for the largest length."""
+        kw.setdefault("n_pos", self.p.n_max + int(reserve))
+        cache = QuantizedCache(self.p, int(self.len_lh.max()) + int(reserve), T, logm=True,
+                               device=self.device, **kw)
+        cache.pack(self.Kp, self.Vp, self.logm, self.len_lh, self.off_lh, pos_next)
+        return cache
+
     def decode_many(self, q_all, kn_all, vn_all, out_all, pos_all=None, graph=True):
         """T = q_all.shape[0] decode steps back to back (step t reads q_all[t],
         kn_all[t], vn_all[t] and writes out_all[t]).  With graph=True the T calls
@@ -599,6 +610,115 @@ class ChunkedCache:
         n = int(self.len_lh[b, l, h])
         o = ((b * self.p.L + l) * self.p.H + h) * self.cap
         return tuple(t[o:o + n].float().cpu().numpy() for t in (self.K, self.V, self.pos, self.mass))
+
+
+class QuantizedCache:
+    """A paged cache of e4m3 codes with a power-of-two scale for every page and head
+    (kvc_q8_*): half the bytes of a bf16 cache, empty at first or a compressed cache in 8
+    bits (Compressor.to_q8).
+
+    A step rotates and appends the new tokens (kvc_q8_append) and attends (kvc_q8_attn); with
+    n_sel, every token of every KV head attends over n_sel pages only (kvc_q8_select): the `first`
+    pages, the last `recent` ones, and of the others those of largest score.  Every (b, l, h) owns pages
+    for `tokens` entries; positions go up to n_pos.  Nothing waits for the device or allocates, so
+    steps can be captured into a CUDA graph.  The class only allocates and marshals.
+    """
+
+    def __init__(self, p: kvc.kvc_params, tokens: int, T: int = 1, page_rows: int = 64,
+                 n_pos: Optional[int] = None, n_sel: int = 0, first: int = 1, recent: int = 2,
+                 logm: bool = False, rotate: bool = True, device="cuda"):
+        if n_sel and not (first >= 0 and recent >= 1 and first + recent <= n_sel):
+            raise ValueError("the first and recent pages must fit n_sel")
+        B, L, H = p.B, p.L, p.H
+        per = -(-int(tokens) // page_rows)
+        self.T, self.cap, self.page_rows = int(T), per * page_rows, int(page_rows)
+        self.n_sel, self.first, self.recent = int(n_sel), int(first), int(recent)
+        pages = B * L * H * per
+        self.p = kvc.kvc_params.from_buffer_copy(p)
+        self.p.packed_rows = pages * page_rows
+        z = dict(device=device)
+        f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+        self.K = torch.zeros((pages * page_rows, p.d), dtype=u8, **z)
+        self.V = torch.zeros((pages * page_rows, p.d), dtype=u8, **z)
+        self.k_scale = torch.ones((pages,), dtype=f32, **z)
+        self.v_scale = torch.ones((pages,), dtype=f32, **z)
+        self.bounds = torch.zeros((pages, 2, p.d), dtype=torch.int8, **z) if n_sel else None
+        self.logm = torch.zeros((pages * page_rows,), dtype=f32, **z) if logm else None
+        self.x = kvc.make_q8(self.K, self.V, self.k_scale, self.v_scale, self.bounds, self.logm)
+        self.table = torch.arange(pages, dtype=i32, **z).view(B, L, H, per)
+        self.len_lh = torch.zeros((B, L, H), dtype=i32, **z)
+        self.len_new = torch.zeros((B, L, H), dtype=i32, **z)
+        self.cap_lh = torch.full((B, L, H), self.cap, dtype=i32, **z)
+        self.pos_next = torch.zeros((B,), dtype=f32, **z)
+        self.n_new = torch.zeros((B,), dtype=i32, **z)
+        self.rope_cos = self.rope_sin = None
+        if rotate:
+            n_half = 2 * int(n_pos if n_pos is not None else max(p.n_max, self.cap))
+            self.rope_cos = torch.empty((n_half, p.d // 2), dtype=f32, **z)
+            self.rope_sin = torch.empty((n_half, p.d // 2), dtype=f32, **z)
+            kvc.kvc_rope_table(p.d, p.rope_base, n_half, self.rope_cos, self.rope_sin)
+        self.q = torch.empty((B * L * H * p.G * self.T * p.d,), dtype=TORCH_DT[p.dtype], **z)
+        self.sel = torch.empty((B * L * H * self.T * max(1, n_sel),), dtype=i32, **z)
+        # (what a call needs depends on its tokens: a few row tiles, or expanded rows)
+        few = min(self.T, 64 // p.G + 1)
+        self.ws = torch.empty(max(kvc.kvc_q8_workspace_bytes(self.p, self._chunk(t), self.n_sel)
+                                  for t in {self.T, *range(1, few + 1)}), dtype=u8, **z)
+
+    def _chunk(self, T):
+        return kvc.make_chunk(T, 0, self.p.L, page_rows=self.page_rows, page_table=self.table, n_new=self.n_new)
+
+    def pack(self, Kp, Vp, logm, len_lh, off_lh, pos_next, stream=None):
+        """Replaces the cache by a packed one (its keys are rotated already); pos_next [B]:
+        the position of each sequence's next token.  With a `stream`, it must be torch's
+        current one."""
+        _current_stream_only(stream)
+        kvc.kvc_q8_pack(self.p, self._chunk(1), self.x, Kp, Vp, logm, len_lh, off_lh, self.cap_lh, self.len_new,
+                        stream)
+        self.len_lh.copy_(self.len_new)
+        self.pos_next.copy_(pos_next)
+
+    def step(self, q, k_new, v_new, out, n_new=None, lse=None, stream=None):
+        """q.shape[3] <= T new tokens per sequence (n_new [B] int32 on the device when not
+        every sequence has that many): q, out [B, L, H*G, T', d], k_new, v_new
+        [B, L, H, T', d], not rotated yet; lse [B, L, H*G, T'] or None.  With a `stream`, it must be torch's
+        current one.  A (b, l, h) without room is skipped: it takes no token, its rows of out
+        stay, and kvc_device_error reports it (as it does a count above T', or positions beyond n_pos)."""
+        p, T = self.p, q.shape[3] if q.dim() == 5 else 0
+        _check_chunk(p, p.L, q, k_new, v_new, out, n_new=(n_new, (p.B,), torch.int32),
+                     lse=(lse, (p.B, p.L, p.H * p.G, T), torch.float32))
+        _current_stream_only(stream)
+        if T > self.T:
+            raise ValueError(f"{T} tokens, the cache was built for {self.T}")
+        if n_new is None:
+            self.n_new.fill_(T)
+        else:
+            self.n_new.copy_(n_new)
+        c = self._chunk(T)
+        turned = self.q[:q.numel()].view(q.shape)
+        kvc.kvc_q8_append(p, c, self.x, self.rope_cos, self.rope_sin, q, k_new, v_new, self.pos_next, turned,
+                          self.len_lh, self.cap_lh, self.len_new, stream)
+        sel = None
+        if self.n_sel:
+            sel = self.sel[:p.B * p.L * p.H * T * self.n_sel].view(p.B, p.L, p.H, T, self.n_sel)
+            kvc.kvc_q8_select(p, c, self.x, turned, self.len_lh, self.len_new, self.first, self.recent, sel, stream)
+        kvc.kvc_q8_attn(p, c, self.x, turned, self.len_lh, self.len_new, sel, out, lse, self.ws, stream)
+        # what was taken, not what was asked for: (b, l, h) that the device skipped keep their length
+        self.pos_next.add_((self.len_new - self.len_lh).flatten(1).amax(1))
+        self.len_lh.copy_(self.len_new)
+
+    def entries(self, b: int, l: int, h: int):
+        """(K, V, log m or None) the (b, l, h) holds, in entry order (host copies)."""
+        n = int(self.len_lh[b, l, h])
+        o = ((b * self.p.L + l) * self.p.H + h) * self.cap
+        page = torch.arange(o, o + n, device=self.K.device) // self.page_rows
+        K, V = (t[o:o + n].view(torch.float8_e4m3fn).float() * s[page][:, None]
+                for t, s in ((self.K, self.k_scale), (self.V, self.v_scale)))
+        return K.cpu().numpy(), V.cpu().numpy(), None if self.logm is None else self.logm[o:o + n].cpu().numpy()
+
+
+def _current_stream_only(stream):
+    if stream is not None and kvc._raw_stream(stream) != kvc._raw_stream(None):
+        raise ValueError("the stream must be torch's current one")
 
 
 def pad_bounds(bounds_list, S_max: int) -> np.ndarray:
