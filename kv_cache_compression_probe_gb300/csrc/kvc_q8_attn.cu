@@ -276,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
   }
   constexpr int kPer = 32 / (D / 16), kCopies = 16 / kPer;       // rows of one copy instruction, copies
   const int crow = lane / (D / 16), cchunk = lane % (D / 16);
-  uint32_t c_at[kCopies];
-#pragma unroll
-  for (int i = 0; i < kCopies; ++i) c_at[i] = place(crow + i * kPer, cchunk);
+  // (the pieces' places repeat every 8 rows)
+  const uint32_t c_first[2] = {(uint32_t)place(crow, cchunk), (uint32_t)place(crow + kPer, cchunk)};
+  auto c_at = [&](int i) { return c_first[i * kPer / 4 % 2 * (kPer < 8)] + (i * kPer / 8) * 8 * D; };
 
   // Four features of a finished row.
   auto put_row = [&](int u, int t0, int row, int f4, float M, float sum, const float4& y) {
@@ -352,15 +352,15 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
           if (e0 + 16 <= total) {
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-              cp_async16(dst + c_at[i], ks + i * 512);
-              cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at[i], vs + i * 512);
+              cp_async16(dst + c_at(i), ks + i * 512);
+              cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at(i), vs + i * 512);
             }
           } else {                                     // rows past the last entry become 0
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
               const bool there = e0 + crow + i * kPer < total;
-              cp_async16(dst + c_at[i], ks + i * 512, there);
-              cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at[i], vs + i * 512, there);
+              cp_async16(dst + c_at(i), ks + i * 512, there);
+              cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at(i), vs + i * 512, there);
             }
           }
           if (x.logm && lane < 16) cp_async4(lm0 + (k % kStages) * 64 + lane * 4, x.logm + row + lane, e0 + lane < total);
@@ -374,7 +374,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
     // shared memory, which the CTA's warps fill together
     uint32_t qr[kQ][kShareQ ? 1 : NT][kS][2];
     float fq[NT][2];
-    int see[NT][2];
+    // Entries that the row of this lane's result column sees (0: a row of no token).
+    auto see = [&](int nt, int k) {
+      const int row = nt * 8 + 2 * c + k, tok = t0 + row % a.tt;
+      return row / a.tt < x.G && tok < r.n ? r.len + tok + 1 : 0;
+    };
     auto query_tile = [&](int nt, uint32_t (&qf)[kQ][kS][2]) {   // its operand; returns what the row's products are in units of
       const int row = nt * 8 + g, head = row / a.tt, tok = t0 + row % a.tt;
       const bool live = head < x.G && tok < r.n;
@@ -436,10 +440,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
       // what this lane needs of its result columns, rows nt*8 + 2c and + 1
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int row2 = nt * 8 + 2 * c + k, tok2 = t0 + row2 % a.tt;
-        if constexpr (kShareQ) fq[nt][k] = sm.q.units[row2];
+        if constexpr (kShareQ) fq[nt][k] = sm.q.units[nt * 8 + 2 * c + k];
         else fq[nt][k] = __shfl_sync(KVC_FULL_MASK, up, 8 * c + 4 * k);
-        see[nt][k] = row2 / a.tt < x.G && tok2 < r.n ? r.len + tok2 + 1 : 0;
       }
     }
     float o[NT][kS][4], ref[NT][2], l[NT][2];
@@ -509,8 +511,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (e0 + pg >= see[nt][i]) s[nt][i] = -INFINITY;
-              if (e0 + pg + 8 >= see[nt][i]) s[nt][2 + i] = -INFINITY;
+              const int lim = see(nt, i) - e0 - pg;
+              if (lim <= 0) s[nt][i] = -INFINITY;
+              if (lim <= 8) s[nt][2 + i] = -INFINITY;
             }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -619,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
         sum += __shfl_xor_sync(KVC_FULL_MASK, sum, 16);
         const int row = nt * 8 + 2 * c + i;
         if (g == 0) sm.ml[warp][row] = make_float2(sum > 0.f ? ref[nt][i] : -INFINITY, sum);
-        if (see[nt][i] == 0 || count == 0) continue;
+        if (see(nt, i) == 0 || count == 0) continue;
         float* to = mine + row * D + kF * g;
 #pragma unroll
         for (int j = 0; j < kS; j += 2)
