@@ -812,11 +812,16 @@ int team_size(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   return team;
 }
 
-// Whether the rows go to the kernel of kvc_chunk_attn (kvc_q8_chunk.cu).  Here and there: 64 rows
-// over 16384 entries (8 KV heads) 46 and 39 us, 128 rows 63 and 43, 8192 rows 2360 and 378.
+// Whether the rows go to the kernel of kvc_chunk_attn (kvc_q8_chunk.cu): more than kManyRows of a unit, and more
+// than kShortWork groups to do here, by what the table's pages hold at most.  Here and there (8 KV heads, G 4): 64 rows over
+// 16384 entries 40 and 39 us, 128 rows 63 and 43, 8192 rows 2360 and 378; by groups: 256 rows over 2000
+// entries (8.3 K groups) 22 and 30, 128 rows of 8 sequences over 500 (8.7 K) 24 and 30, 256 rows (18 K) 51 and 38,
+// 68 rows of 8 sequences over 2000 (24 K) 47 and 41, 96 rows over 14000 (21 K) 43 and 40.
 constexpr int kManyRows = 64;
+constexpr int64_t kShortWork = 12288;
 bool many_rows(const kvc_params* p, const kvc_chunk* c, int n_sel) {
-  return p->dtype == KVC_BF16 && n_sel == 0 && p->G * c->T > kManyRows;
+  return p->dtype == KVC_BF16 && n_sel == 0 && p->G * c->T > kManyRows &&
+         item_count(p, c, n_sel) * c->max_pages * (c->page_rows / 16) > kShortWork;
 }
 
 Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {

@@ -46,6 +46,17 @@ CASES = {
     "wide table, three tiles": dict(lens=[300, 50, 700, 129], n_new=[5, 3], B=2, H=2, page=32, max_pages=300),
     "wide table, four tiles": dict(lens=[300, 50, 700, 129], n_new=[7, 8], B=2, H=2, max_pages=700),
     "wide table, G 8, d 64": dict(lens=[300, 50, 700, 129], n_new=[2, 1], B=2, H=2, G=8, d=64, page=64, max_pages=200),
+    # many rows and wide tables: expanded rows
+    "expanded": dict(lens=[600, 129], n_new=[333], H=2, page=128, max_pages=40),
+    "expanded, G 1": dict(lens=[100], n_new=[700], G=1, page=64, max_pages=300),
+    "expanded, G 2, d 64": dict(lens=[100, 0], n_new=[300], H=2, G=2, d=64, max_pages=400),
+    "expanded, G 8": dict(lens=[100, 333], n_new=[130], H=2, G=8, page=32, max_pages=100),
+    "expanded, layer range": dict(lens=[5, 70, 200, 130, 64, 9, 0, 31, 77], n_new=[90, 61, 0], B=3, L=3, layers=(1, 3),
+                                  page=64, max_pages=100),
+    "expanded, scales of all sizes": dict(lens=[300, 50, 129], n_new=[40], H=3, spread=6.0, max_pages=900),
+    "expanded, dead entries": dict(lens=[300, 129], n_new=[40], H=2, dead=0.7, logm=True, max_pages=1300),
+    "expanded, no log m": dict(lens=[300, 129], n_new=[40], H=2, logm=False, max_pages=1300),
+    "expanded, unit by unit": dict(lens=[70, 300, 0], n_new=[20], H=3, page=128, max_pages=16384),
     # more items than warps
     "many items": dict(lens=np.arange(2500) % 37, n_new=[1], L=125, H=20, d=64),
     "many tokens": dict(lens=np.arange(32) * 7 % 150, n_new=[80, 79, 80, 70], B=4, H=8, G=2, d=64),

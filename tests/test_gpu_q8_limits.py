@@ -26,11 +26,14 @@ def _done(kvc, code=0):
 
 
 # ------------------------------------------------------------------ attention
-@pytest.mark.parametrize("n_new,T", [(1, 1), (7, 7), (40, 40)])
+WIDE = 4000                                            # table columns with which many rows are expanded
+
+
+@pytest.mark.parametrize("n_new,wide", [(1, None), (7, None), (40, None), (40, WIDE)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_rows_that_see_nothing(kvc, dtype, n_new, T):
+def test_rows_that_see_nothing(kvc, dtype, n_new, wide):
     """All of ln m is -inf: out 0, lse -inf; the other unit's rows as ever."""
-    c = Q8(kvc, [200, 129], [n_new], H=2, dtype=dtype, page=32)
+    c = Q8(kvc, [200, 129], [n_new], H=2, dtype=dtype, page=32, max_pages=wide)
     c.fill_new()
     dead = c.table[0][:-(-(200 + n_new) // 32)]
     for p in dead:
@@ -47,11 +50,11 @@ def test_rows_that_see_nothing(kvc, dtype, n_new, T):
         c.check_attn(s, picks)
 
 
-@pytest.mark.parametrize("T", [1, 3, 30])
-def test_masked_and_unused_places_may_hold_anything(kvc, T):
+@pytest.mark.parametrize("T,wide", [(1, None), (3, None), (30, None), (30, WIDE)])
+def test_masked_and_unused_places_may_hold_anything(kvc, T, wide):
     """Codes that are no numbers behind the last entry and in pages of nobody, NaN ln m and
     scales there, +-inf queries and NaN in rows of no token."""
-    c = Q8(kvc, [77, 130, 16], [T], H=3, T=T + 2, page=64)
+    c = Q8(kvc, [77, 130, 16], [T], H=3, T=T + 2, page=64, max_pages=wide)
     c.fill_new()
     s = c.upload()
     assert (s["K"] == UNUSED).any() and torch.isnan(s["logm"]).any() and torch.isnan(s["k_scale"]).any()
@@ -62,11 +65,11 @@ def test_masked_and_unused_places_may_hold_anything(kvc, T):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n", [1, 6, 50])
-def test_scales_at_their_ends(kvc, dtype, n):
+@pytest.mark.parametrize("n,wide", [(1, None), (6, None), (50, None), (50, WIDE)])
+def test_scales_at_their_ends(kvc, dtype, n, wide):
     """Pages whose values' scales are 2^-40 .. 2^40 side by side, keys likewise with queries that
     bring the scores back."""
-    c = Q8(kvc, [200], [n], dtype=dtype, page=16, logm=False)
+    c = Q8(kvc, [200], [n], dtype=dtype, page=16, logm=False, max_pages=wide)
     c.fill_new()
     used = c.used.any(1)
     pages = np.flatnonzero(used)
@@ -81,8 +84,8 @@ def test_scales_at_their_ends(kvc, dtype, n):
 
 def test_scores_that_rise_and_leap(kvc):
     """Scores of thousands, rising from page to page: the reference moves again and again."""
-    for G, n in ((4, 1), (2, 9), (8, 4), (4, 33)):
-        c = Q8(kvc, [400, 65], [n], H=2, G=G, page=16, logm=False, seed=G)
+    for G, n, wide in ((4, 1, None), (2, 9, None), (8, 4, None), (4, 33, None), (4, 33, WIDE)):
+        c = Q8(kvc, [400, 65], [n], H=2, G=G, page=16, logm=False, seed=G, max_pages=wide)
         c.fill_new()
         for j in range(c.table.shape[1]):
             for u in range(2):
@@ -96,8 +99,8 @@ def test_scores_that_rise_and_leap(kvc):
 
 def test_optional_outputs_and_repeats(kvc):
     """lse may be left out; the same call gives the same bits, whatever the workspace held."""
-    for n_new in ([1, 1], [3, 5], [40, 33]):
-        c = Q8(kvc, [100, 0, 300, 64], n_new, B=2, H=2, page=32)
+    for n_new, wide in (([1, 1], None), ([3, 5], None), ([40, 33], None), ([40, 33], WIDE)):
+        c = Q8(kvc, [100, 0, 300, 64], n_new, B=2, H=2, page=32, max_pages=wide)
         c.fill_new()
         a, b = c.upload(), c.upload()
         c.attn(a)
@@ -132,8 +135,8 @@ def test_picked_pages_that_are_none(kvc):
 def test_units_out_of_range_are_skipped(kvc):
     """Lengths that are negative, shrink, grow by more than T or pass the table: reported, rows and
     lists left alone; the other units' results as ever."""
-    for n in (1, 40):
-        c = Q8(kvc, [50, 60, 70, 80, 90], [n], H=5, page=16)
+    for n, wide in ((1, None), (40, None), (40, WIDE)):
+        c = Q8(kvc, [50, 60, 70, 80, 90], [n], H=5, page=16, max_pages=wide)
         c.fill_new()
         s = c.upload()
         good = c.upload()
@@ -153,8 +156,8 @@ def test_units_out_of_range_are_skipped(kvc):
 
 def test_pages_outside_the_extent_are_reported(kvc):
     """A page number out of range: no access outside the cache; the other unit as ever."""
-    for n in (1, 40):
-        c = Q8(kvc, [100, 100], [n], H=2, page=16)
+    for n, wide in ((1, None), (40, None), (40, WIDE)):
+        c = Q8(kvc, [100, 100], [n], H=2, page=16, max_pages=wide)
         c.fill_new()
         for bad in (-1, c.n_pages, 1 << 30):
             s = c.upload()
