@@ -211,11 +211,13 @@ __device__ __forceinline__ void append_page(const Q8Append& a, int64_t u, int ol
     for (int r = w * 32 + lane; r < count; r += 32 * kW) x.logm[(page << x.shift) + old + r] = 0.f;
   if constexpr (kKeys) {
     if (!bounds) return;
+    const bool one = kW == 1 && count == 1 && !grow;   // a single row, which the first lanes hold: lo is hi
+    if (!one)
 #pragma unroll
-    for (int o = kL; o < 32; o <<= 1)
+      for (int o = kL; o < 32; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        join(b[k], __shfl_xor_sync(KVC_FULL_MASK, b[k].lo, o), __shfl_xor_sync(KVC_FULL_MASK, b[k].hi, o));
+        for (int k = 0; k < 4; ++k)
+          join(b[k], __shfl_xor_sync(KVC_FULL_MASK, b[k].lo, o), __shfl_xor_sync(KVC_FULL_MASK, b[k].hi, o));
     if constexpr (kW > 1) {
       if (lane < kL)
 #pragma unroll
@@ -235,7 +237,7 @@ __device__ __forceinline__ void append_page(const Q8Append& a, int64_t u, int ol
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         b[2 * h + k].lo = bounds_of(b[2 * h + k].lo);
-        b[2 * h + k].hi = bounds_of(b[2 * h + k].hi);
+        b[2 * h + k].hi = one ? b[2 * h + k].lo : bounds_of(b[2 * h + k].hi);
       }
       if (old > 0 && !grow) {
         const uint2 l = *lo, m = *hi;

@@ -704,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(
 }
 
 // Joins the partial results of the item that piece blockIdx.x leaves unfinished: the head in
-// its slot 1, the others in slot 0 of the pieces up to the last.  blockIdx.y takes 8 rows;
-// where an item has fewer, several warps share a row's pieces.
+// its slot 1, the others in slot 0 of the pieces up to the last.  blockIdx.y takes as many rows as
+// the block has warps; where an item has fewer, several warps share a row's pieces.
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(256) q8_combine_kernel(const __grid_constant__ Q8Attn a) {
   constexpr int C = D / 32;
@@ -715,9 +715,9 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const __grid_constant__
   const int2 tail = a.tail[blockIdx.x];
   if (tail.x < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = min(8, a.x.G * a.tt - (int)blockIdx.y * 8);   // of this block
+  const int warps = blockDim.x >> 5, rows = min(warps, a.x.G * a.tt - (int)blockIdx.y * warps);   // of this block
   if (rows <= 0) return;
-  const int share = 8 / rows, row = blockIdx.y * 8 + warp % rows, part = warp / rows;
+  const int share = warps / rows, row = blockIdx.y * warps + warp % rows, part = warp / rows;
   const int u = tail.x / a.rp, t0 = (tail.x - u * a.rp) * a.tt;
   const int head = row / a.tt, tok = t0 + row % a.tt;
   float M = -INFINITY, l = 0.f, o[C];
@@ -862,7 +862,10 @@ cudaError_t launch_mode(const Q8Attn& a, int sms, cudaStream_t s) {
   e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel, kMode>, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
-  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(kMode == kSolo ? grid * kWarps : grid, NT), dim3(256), 0, s, a);
+  // (kSolo: many items of few pieces, so a warp a row)
+  const int warps = kMode == kSolo ? 4 : 8;
+  return kvc::chunk_launch(q8_combine_kernel<T, D, NT * 8>, dim3(kMode == kSolo ? grid * kWarps : grid, NT * 8 / warps),
+                           dim3(32 * warps), 0, s, a);
 }
 
 template <typename T, int D, int NT, bool kSel>
