@@ -66,39 +66,65 @@ __device__ __forceinline__ int block_sum(int v, int (&count)[2][kWarps], int& tu
   return t;
 }
 
+// The codes of a warp's pages, lane i those of pages i, i + 32, ..: in registers where they are at most 32 kRegs
+// (0: in shared memory).  Pages beyond nb count as code 0.
+template <int kRegs>
+struct WarpKeys {
+  uint32_t reg[kRegs];
+  __device__ __forceinline__ WarpKeys(const uint32_t* keys, int nb) {
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) reg[i] = (int)(threadIdx.x & 31) + 32 * i < nb ? keys[(threadIdx.x & 31) + 32 * i] : 0;
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) f((int)(threadIdx.x & 31) + 32 * i, reg[i]);
+  }
+};
+template <>
+struct WarpKeys<0> {
+  const uint32_t* keys;
+  int nb;
+  __device__ __forceinline__ WarpKeys(const uint32_t* k, int n) : keys(k), nb(n) {}
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int b = threadIdx.x & 31; b < (nb + 31 & ~31); b += 32) f(b, b < nb ? keys[b] : 0);
+  }
+};
+
 // The n_sel pages of largest code, by one warp, in ascending order.
+template <int kRegs>
 __device__ __forceinline__ void pick_by_warp(const uint32_t* keys, int nb, int n_sel, int32_t* out) {
   const int lane = threadIdx.x & 31;
+  const WarpKeys<kRegs> mine(keys, nb);
   uint32_t cut = 0xffffffffu, top = 0;                 // least and largest code of the pages that need not be in
-  for (int b = lane; b < nb; b += 32) {
-    const uint32_t key = keys[b];
-    cut = min(cut, key);
+  mine.each([&](int b, uint32_t key) {
+    cut = min(cut, b < nb ? key : 0xffffffffu);
     top = max(top, key == 0xffffffffu ? 0 : key);
-  }
+  });
   cut = __reduce_min_sync(KVC_FULL_MASK, cut);
   top = max(cut, __reduce_max_sync(KVC_FULL_MASK, top));
   while (cut < top) {                                  // cut: the largest code so far that n_sel pages reach; none above top is
     const uint32_t trial = cut + (top - cut + 1) / 2;
-    int mine = 0;
-    for (int b = lane; b < nb; b += 32) mine += keys[b] >= trial;
-    mine = __reduce_add_sync(KVC_FULL_MASK, mine);
-    if (mine >= n_sel) cut = trial;
+    int reach = 0;
+    mine.each([&](int b, uint32_t key) { reach += key >= trial; });
+    reach = __reduce_add_sync(KVC_FULL_MASK, reach);
+    if (reach >= n_sel) cut = trial;
     else top = trial - 1;
-    if (mine == n_sel) break;
+    if (reach == n_sel) break;
   }
   int above = 0;
-  for (int b = lane; b < nb; b += 32) above += keys[b] > cut;
+  mine.each([&](int b, uint32_t key) { above += b < nb && key > cut; });
   int quota = n_sel - __reduce_add_sync(KVC_FULL_MASK, above), at = 0;   // of those equal to it: the first ones
-  for (int b0 = 0; b0 < nb; b0 += 32) {
-    const uint32_t key = b0 + lane < nb ? keys[b0 + lane] : 0;
-    const bool in = b0 + lane < nb;
-    const uint32_t eq = __ballot_sync(KVC_FULL_MASK, in && key == cut), before = (1u << lane) - 1;
-    const bool take = in && (key > cut || (key == cut && __popc(eq & before) < quota));
+  const uint32_t before = (1u << lane) - 1;
+  mine.each([&](int b, uint32_t key) {
+    const uint32_t eq = __ballot_sync(KVC_FULL_MASK, b < nb && key == cut);
+    const bool take = b < nb && (key > cut || (key == cut && __popc(eq & before) < quota));
     const uint32_t taken = __ballot_sync(KVC_FULL_MASK, take);
-    if (take) out[at + __popc(taken & before)] = b0 + lane;
+    if (take) out[at + __popc(taken & before)] = b;
     at += __popc(taken);
     quota -= min(quota, __popc(eq));
-  }
+  });
 }
 
 // The same by the whole block; thread i looks at a run of pages.
@@ -294,7 +320,10 @@ __global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_con
     for (int tok = warp; tok < tokens; tok += kWarps) {
       const int nb = ((len + t0 + tok) >> x.shift) + 1;
       int32_t* to = out + tok * (int64_t)a.n_sel;
-      if (nb > a.n_sel) pick_by_warp(keys + tok * x.max_pages, nb, a.n_sel, to);
+      const uint32_t* mine = keys + tok * x.max_pages;
+      if (nb > a.n_sel && nb <= 256) pick_by_warp<8>(mine, nb, a.n_sel, to);
+      else if (nb > a.n_sel && nb <= 640) pick_by_warp<20>(mine, nb, a.n_sel, to);
+      else if (nb > a.n_sel) pick_by_warp<0>(mine, nb, a.n_sel, to);
       else
         for (int i = lane; i < a.n_sel; i += 32) to[i] = i < nb ? i : -1;
     }
