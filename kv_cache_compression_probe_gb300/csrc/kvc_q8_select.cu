@@ -11,7 +11,7 @@
 // below 2^24, which fp32 holds: exact as well, and 8 times as fast here as the 8-bit integer form (8 cycles a 16 x 8 x 16
 // product and scheduler against 66 for 16 x 8 x 32).  A product's 16 inner positions may stand for any features, as long as
 // both operands agree, so a lane takes whole 16-byte pieces of the bounds.  The scores' order codes stay in shared
-// memory, where a warp per token (for a single token the whole CTA) looks for the n_sel-th largest by
+// memory, where a warp per token (for a single token over many pages the whole CTA) looks for the n_sel-th largest by
 // halving the range of codes; scores are spread over it, so about 10 steps are enough as a rule.
 #include <algorithm>
 
@@ -22,6 +22,9 @@ namespace {
 using kvc::Q8Args;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+constexpr int kWarpPages = 640;        // pages whose codes a warp keeps in registers; a single token over more is the whole CTA's
+                                       // (512 pages: a warp 11.7 us, the CTA 13.8)
 
 struct Q8Select {
   Q8Args x;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_con
     if (bad) kvcd::record_error(x.err, KVC_EDEVICE);
     __syncthreads();
   }
-  if (tokens == 1 && most > a.n_sel) {
+  if (tokens == 1 && most > max(a.n_sel, kWarpPages)) {
     pick_by_block(keys, most, a.n_sel, out, sm.count, sm.ends);
   } else {
     for (int tok = warp; tok < tokens; tok += kWarps) {
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_con
       int32_t* to = out + tok * (int64_t)a.n_sel;
       const uint32_t* mine = keys + tok * x.max_pages;
       if (nb > a.n_sel && nb <= 256) pick_by_warp<8>(mine, nb, a.n_sel, to);
-      else if (nb > a.n_sel && nb <= 640) pick_by_warp<20>(mine, nb, a.n_sel, to);
+      else if (nb > a.n_sel && nb <= kWarpPages) pick_by_warp<kWarpPages / 32>(mine, nb, a.n_sel, to);
       else if (nb > a.n_sel) pick_by_warp<0>(mine, nb, a.n_sel, to);
       else
         for (int i = lane; i < a.n_sel; i += 32) to[i] = i < nb ? i : -1;
