@@ -199,10 +199,10 @@ __device__ __forceinline__ float2 cluster_load2(uint32_t a) {
 }
 
 // Shape of a kernel: CTAs per SM, and groups in a warp's ring.
-template <typename T, int NT>
+template <typename T, int NT, Mode kMode>
 struct Shape {
-  static constexpr int kCtas = NT <= 2 && sizeof(T) == 2 ? 3 : 2;
-  static constexpr int kStages = kCtas == 3 ? 4 : 6;
+  static constexpr int kCtas = sizeof(T) != 2 || NT > 2 ? 2 : NT == 1 && kMode == kTeam ? 4 : 3;
+  static constexpr int kStages = kCtas == 4 ? 3 : kCtas == 3 ? 4 : 6;
 };
 template <int D, int kStages>
 struct WarpRing {
@@ -227,14 +227,14 @@ struct AttnSmem {
 };
 
 template <typename T, int D, int NT, bool kSel, Mode kMode>
-__global__ void __launch_bounds__(kThreads, Shape<T, NT>::kCtas) q8_attn_kernel(const __grid_constant__ Q8Attn a) {
+__global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_kernel(const __grid_constant__ Q8Attn a) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kQ = kF32 ? 3 : 1, kP = kF32 ? 2 : 1;  // fp16 parts of a query row, of the numerators
   constexpr int kH = D / 64, kS = D / 16;              // 16-byte pieces of a row per lane, products
   constexpr bool kShareQ = NT > 1;
   constexpr int kRows = NT * 8;
   constexpr int kF = D / 8;                            // features of a lane's output
-  constexpr int kStages = Shape<T, NT>::kStages;
+  constexpr int kStages = Shape<T, NT, kMode>::kStages;
   using Smem = AttnSmem<D, NT, kStages>;
   static_assert(kRows * D * 4 <= kStages * WarpRing<D, kStages>::kStage, "O takes the ring's place");
   extern __shared__ __align__(128) unsigned char attn_raw[];
@@ -780,7 +780,7 @@ struct Layout {
 int row_tiles(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   return p->dtype == KVC_F32 || n_sel > 0 ? 1 : std::min(4, (p->G * std::min(c->T, 32) + 7) / 8);
 }
-int ctas_per_sm(const kvc_params* p, int nt) { return p->dtype == KVC_F32 || nt > 2 ? 2 : 3; }
+int ctas_per_sm(const kvc_params* p, int nt, bool team = false) { return p->dtype == KVC_F32 || nt > 2 ? 2 : nt == 1 && team ? 4 : 3; }
 
 // Tokens of a row block, and items of a call.
 int block_tokens(const kvc_params* p, const kvc_chunk* c, int n_sel) {
@@ -804,7 +804,7 @@ constexpr int kTeamGroups = 32;
 int team_size(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   const int64_t items = item_count(p, c, n_sel);
   const int64_t groups = (int64_t)(n_sel > 0 ? std::min(n_sel, c->max_pages) : c->max_pages) * (c->page_rows / 16);
-  const int64_t room = (int64_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, row_tiles(p, c, n_sel));
+  const int64_t room = (int64_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, row_tiles(p, c, n_sel), true);
   int team = 8;
   while (team > 1 && items * team > room) team /= 2;
   if (items * team > room || groups > (int64_t)team * kWarps * kTeamGroups) return 0;
@@ -838,7 +838,7 @@ Layout layout(const kvc_params* p, const kvc_chunk* c, int n_sel) {
 
 template <typename T, int D, int NT, bool kSel, Mode kMode>
 cudaError_t launch_mode(const Q8Attn& a, int sms, cudaStream_t s) {
-  const size_t smem = sizeof(AttnSmem<D, NT, Shape<T, NT>::kStages>);
+  const size_t smem = sizeof(AttnSmem<D, NT, Shape<T, NT, kMode>::kStages>);
   cudaError_t e = kvc::chunk_allow_smem<q8_attn_kernel<T, D, NT, kSel, kMode>>(smem);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
@@ -858,7 +858,7 @@ cudaError_t launch_mode(const Q8Attn& a, int sms, cudaStream_t s) {
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, q8_attn_kernel<T, D, NT, kSel, kMode>, a);
   }
-  const int grid = sms * Shape<T, NT>::kCtas;
+  const int grid = sms * Shape<T, NT, kMode>::kCtas;
   e = kvc::chunk_launch(q8_attn_kernel<T, D, NT, kSel, kMode>, dim3(grid), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   kvc::count_launch();
