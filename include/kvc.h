@@ -199,7 +199,8 @@ int64_t kvc_launch_count(void);
 /* Bounded device waits (no counterpart on the pages: error handling of this
  * library).  Kernels that pipeline copies and tensor-core products through
  * mbarriers (the tensor-core passes of kvc_score, both decode kernels of the
- * kvc_decode_attn family, the bf16 kernels of kvc_chunk_attn and kvc_chunk_mass)
+ * kvc_decode_attn family, the bf16 kernels of kvc_chunk_attn and kvc_chunk_mass, which
+ * kvc_q8_attn uses for many rows)
  * give up a wait after first_wait_ns nanoseconds of
  * global time: the CTA then stops issuing work, waits (with its own fixed
  * limits: 2 s for copies and products already issued, 0.1 s in the probe
@@ -627,7 +628,8 @@ int kvc_q8_select(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, cons
  * the n = len_new - len_lh of an (l,h) attends over the entries e <= len_lh + t, with sel
  * only over those in its pages:
  *   s_e = q_t . k_e / sqrt(d) + logm_e,  out = sum_e softmax_e(s) v_e,  lse = log2 sum_e 2^(s_e log2 e)
- * with fp32 statistics (bf16: the softmax's numerators are rounded to 11 bits).  A row whose
+ * with fp32 statistics (bf16: the softmax's numerators are rounded to 11 bits, or to 8 where
+ * many rows go through expanded rows).  A row whose
  * scores are all -inf gets out = 0 and lse = -inf.  sel, n_sel as kvc_q8_select leaves them (each page once;
  * numbers that are no page the token sees are passed over), NULL and 0 = all entries.
  * lse [B, Lr, H*G, T] may be NULL.  Rows t >= n of out and lse stay as they were.  Query values
@@ -640,7 +642,8 @@ int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const 
                 void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of kvc_q8_attn for this n_sel (0: all entries); 0 for invalid
- * arguments. */
+ * arguments.  It depends on c->T too: many rows (more than 64 of an (l,h), unless the tables are
+ * short) need room for expanded rows, up to 1 GB or one (l,h)'s table if that is more. */
 size_t kvc_q8_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk* c /* host */,
                               int32_t n_sel);
 

@@ -6,6 +6,8 @@
 // rows and the page's old scale give the new one; rows stay in registers until
 // then (beyond 8 a warp they are read again).  Only when the scale grows are the page's old
 // codes read and moved to it.
+// Bound by latency: one token of 4096 (b,l,h) with 16384 query rows 8.9 us (with a CTA of 8 warps a page 28, most of them
+// idle), a 2048-token chunk of 8 KV heads, 47 MB, 11.8 us (with 4 loads of 4 bytes a lane and row 26).
 #include <algorithm>
 
 #include "kvc_chunk_tc.cuh"

