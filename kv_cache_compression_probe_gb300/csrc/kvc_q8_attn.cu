@@ -318,11 +318,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
     const int32_t* tab = x.table + r.gu * x.max_pages;
     const int32_t* list = kSel ? a.sel + ((int64_t)u * x.T + t0) * a.n_sel : nullptr;
     const int own = (r.len + t0) >> x.shift, inpage = (1 << x.shift) - 1;
-    // A window: lane i knows of the warp's group k0 + i its first entry and row (-1: none) and
-    // the exponents of its scales.
+    // A window: lane i knows of the warp's group k0 + i its first entry, its first row (a multiple of 16)
+    // and the exponents of its scales; with the latter two whether there is such a group (kThere), and whether every row
+    // of the block sees all of it (kFull).
+    constexpr int kThere = 1, kFull = 2;
     struct Window { int e0, row, exps; };
     auto window = [&](int k0) {
-      Window w{0, -1, 0};
+      Window w{0, 0, 0};
       const int gi = tb + me + kShare * (k0 + lane);
       if (gi < te) {
         w.e0 = gi << 4;
@@ -335,8 +337,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
         if (ok) {
           const int page = __ldg(tab + (w.e0 >> x.shift));
           if ((unsigned)page < (unsigned)x.pages) {
-            w.row = (page << x.shift) + (w.e0 & inpage);
-            w.exps = (kvcd::scale_exp(__ldg(x.k_scale + page)) + 64) | (kvcd::scale_exp(__ldg(x.v_scale + page)) + 64) << 8;
+            const int flags = kThere | (w.e0 + 16 <= all_see ? kFull : 0);
+            w.row = ((page << x.shift) + (w.e0 & inpage)) | flags;
+            w.exps = (kvcd::scale_exp(__ldg(x.k_scale + page)) + 64) | (kvcd::scale_exp(__ldg(x.v_scale + page)) + 64) << 8 | flags << 16;
           } else {
             bad = true;
           }
@@ -351,26 +354,26 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
     auto issue = [&](int k, int base) {                // base: the first group of `cur`
       if (k < count) {
         const Window& w = k - base < 32 ? cur : nxt;
-        const int row = __shfl_sync(KVC_FULL_MASK, w.row, k & 31), e0 = entry(w, k);
-        if (row >= 0) {
-          const uint32_t dst = codes0 + (k % kStages) * WarpRing<D, kStages>::kStage;
-          const uint8_t* ks = x.K + (int64_t)row * D + lane * 16;
-          const uint8_t* vs = x.V + (int64_t)row * D + lane * 16;
-          if (e0 + 16 <= total) {
+        const int got = __shfl_sync(KVC_FULL_MASK, w.row, k & 31), row = got & ~15;
+        const uint32_t dst = codes0 + (k % kStages) * WarpRing<D, kStages>::kStage, to_lm = lm0 + (k % kStages) * 64 + lane * 4;
+        const uint8_t* ks = x.K + (int64_t)row * D + lane * 16;
+        const uint8_t* vs = x.V + (int64_t)row * D + lane * 16;
+        if (got & kFull) {
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-              cp_async16(dst + c_at(i), ks + i * 512);
-              cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at(i), vs + i * 512);
-            }
-          } else {                                     // rows past the last entry become 0
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-              const bool there = e0 + crow + i * kPer < total;
-              cp_async16(dst + c_at(i), ks + i * 512, there);
-              cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at(i), vs + i * 512, there);
-            }
+          for (int i = 0; i < kCopies; ++i) {
+            cp_async16(dst + c_at(i), ks + i * 512);
+            cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at(i), vs + i * 512);
           }
-          if (x.logm && lane < 16) cp_async4(lm0 + (k % kStages) * 64 + lane * 4, x.logm + row + lane, e0 + lane < total);
+          if (x.logm && lane < 16) cp_async4(to_lm, x.logm + row + lane, true);
+        } else if (got & kThere) {                     // rows past the last entry become 0
+          const int e0 = entry(w, k);
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i) {
+            const bool there = e0 + crow + i * kPer < total;
+            cp_async16(dst + c_at(i), ks + i * 512, there);
+            cp_async16(dst + WarpRing<D, kStages>::kKeys + c_at(i), vs + i * 512, there);
+          }
+          if (x.logm && lane < 16) cp_async4(to_lm, x.logm + row + lane, e0 + lane < total);
         }
       }
       cp_commit();
@@ -468,11 +471,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
         cur = nxt;
         nxt = window(k + 32);
       }
-      const int e0 = entry(cur, k), exps = __shfl_sync(KVC_FULL_MASK, cur.exps, k & 31);
-      const bool here = !kSel || __shfl_sync(KVC_FULL_MASK, cur.row, k & 31) >= 0;
+      const int exps = __shfl_sync(KVC_FULL_MASK, cur.exps, k & 31);
       cp_wait<kStages - 2>();
       __syncwarp();
-      if (here) {
+      if (exps & kThere << 16) {
         const unsigned char* st = ring.codes[k % kStages];
         float s[NT][4];
         // ---- S^T = K Q^T
@@ -513,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
             s[nt][i] = fmaf(s[nt][i], f, lm[0]);
             s[nt][2 + i] = fmaf(s[nt][2 + i], f, lm[1]);
           }
-        if (e0 + 16 > all_see)
+        if (!(exps & kFull << 16)) {
+          const int e0 = entry(cur, k);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
               if (lim <= 0) s[nt][i] = -INFINITY;
               if (lim <= 8) s[nt][2 + i] = -INFINITY;
             }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -548,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
             }
         }
         // ---- numerators, in units of this page's scale over O's
-        const int xv = (exps >> 8) - 64;
+        const int xv = (exps >> 8 & 255) - 64;
         if (xv > xo || xv < xo - kNear) {              // O's unit becomes this page's
           const float f = kvcd::pow2i(xo - xv);
 #pragma unroll
