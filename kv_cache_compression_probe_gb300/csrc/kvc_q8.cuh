@@ -75,6 +75,18 @@ __device__ __forceinline__ void f16x2_f32(uint32_t v, float& lo, float& hi) {
 }
 __device__ __forceinline__ void e4m3_f32(uint16_t c, float& lo, float& hi) { f16x2_f32(e4m3_f16x2(c), lo, hi); }
 
+// Four elements as floats.  (What an earlier call may have written is read by plain loads, or copied by cp.async, in
+// these kernels, not through the read-only path: they may be launched before that call has ended.)
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* o) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  o[0] = __uint_as_float(u.x << 16); o[1] = __uint_as_float(u.x & 0xffff0000u);
+  o[2] = __uint_as_float(u.y << 16); o[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float* o) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+}
+
 // What a page's bounds hold of a code.
 __device__ __forceinline__ int bound_of(float code_value) { return __float2int_rn(code_value * 0.25f); }
 

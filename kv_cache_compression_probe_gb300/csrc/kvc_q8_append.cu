@@ -43,7 +43,7 @@ __device__ __forceinline__ void load_row(const T* row, int i, float (&v)[16]) {
   for (int h = 0; h < 2; ++h) {
     const T* p = row + h * (D / 2) + 8 * i;
     if constexpr (sizeof(T) == 2) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 w = *reinterpret_cast<const uint4*>(p);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -51,8 +51,8 @@ __device__ __forceinline__ void load_row(const T* row, int i, float (&v)[16]) {
         v[8 * h + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
       }
     } else {
-      kvcd::VecLoad<T, 4>::ld(p, v + 8 * h);
-      kvcd::VecLoad<T, 4>::ld(p + 4, v + 8 * h + 4);
+      kvcd::load4(p, v + 8 * h);
+      kvcd::load4(p + 4, v + 8 * h + 4);
     }
   }
 }
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, kW > 1 ? 3 : 4) q8_append_kernel(con
   const int j = (int)((task >> 1) - u * (uint32_t)a.per_unit);
   const int b = (int)(u / (uint32_t)x.per_seq);
   const int64_t gu = kvcd::q8_unit_global(x, u);
-  const int len = __ldg(x.len_lh + gu), n = x.n_new ? __ldg(x.n_new + b) : x.T, cap = __ldg(a.cap_lh + gu);
+  const int len = x.len_lh[gu], n = x.n_new ? __ldg(x.n_new + b) : x.T, cap = __ldg(a.cap_lh + gu);
   const int64_t e0 = a.cos_tab ? table_row(__ldg(a.pos_new + b), n, a.n_half) : 0;
   int bad = KVC_OK;
   if (len < 0 || n < 0 || n > x.T || (n > 0 && e0 < 0)) bad = KVC_EDEVICE;
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads) q8_pack_kernel(const __grid_constant
   const T* rows = static_cast<const T*>(half ? a.Vp : a.Kp) + from * D + c * 8;
   float top = 0.f, v[8];
   for (int r = i / kC; r < count; r += 128 / kC) {
-    kvcd::VecLoad<T, 4>::ld(rows + (int64_t)r * D, v);
-    kvcd::VecLoad<T, 4>::ld(rows + (int64_t)r * D + 4, v + 4);
+    kvcd::load4(rows + (int64_t)r * D, v);
+    kvcd::load4(rows + (int64_t)r * D + 4, v + 4);
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
   }
@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(kThreads) q8_pack_kernel(const __grid_constant
   for (int k = 0; k < 8; ++k) { lo[k] = 127; hi[k] = -127; }
   uint8_t* codes = (half ? x.V : x.K) + (page << x.shift) * D + c * 8;
   for (int r = i / kC; r < count; r += 128 / kC) {
-    kvcd::VecLoad<T, 4>::ld(rows + (int64_t)r * D, v);
-    kvcd::VecLoad<T, 4>::ld(rows + (int64_t)r * D + 4, v + 4);
+    kvcd::load4(rows + (int64_t)r * D, v);
+    kvcd::load4(rows + (int64_t)r * D + 4, v + 4);
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

@@ -91,8 +91,8 @@ struct Unit {
 __device__ __forceinline__ Unit load_unit(const Q8Args& x, int64_t u) {
   Unit r;
   r.gu = kvcd::q8_unit_global(x, u);
-  r.len = __ldg(x.len_lh + r.gu);
-  r.n = __ldg(x.len_new + r.gu) - r.len;
+  r.len = x.len_lh[r.gu];
+  r.n = x.len_new[r.gu] - r.len;
   if (r.len < 0 || r.n < 0 || r.n > x.T || (int64_t)r.len + r.n > (int64_t)x.max_pages << x.shift) {
     r.n = 0;
     if (blockIdx.x == 0) kvcd::record_error(x.err, KVC_EDEVICE);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
         w.e0 = gi << 4;
         bool ok = true;
         if (kSel) {
-          const int per = x.shift - 4, no = __ldg(list + (gi >> per));
+          const int per = x.shift - 4, no = list[gi >> per];
           ok = (unsigned)no <= (unsigned)own;
           w.e0 = (no << x.shift) + ((gi & ((1 << per) - 1)) << 4);
         }
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
           if ((unsigned)page < (unsigned)x.pages) {
             const int flags = kThere | (w.e0 + 16 <= all_see ? kFull : 0);
             w.row = ((page << x.shift) + (w.e0 & inpage)) | flags;
-            w.exps = (kvcd::scale_exp(__ldg(x.k_scale + page)) + 64) | (kvcd::scale_exp(__ldg(x.v_scale + page)) + 64) << 8 | flags << 16;
+            w.exps = (kvcd::scale_exp(x.k_scale[page]) + 64) | (kvcd::scale_exp(x.v_scale[page]) + 64) << 8 | flags << 16;
           } else {
             bad = true;
           }
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
       for (int h = 0; h < kH; ++h)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          if (live) kvcd::VecLoad<T, 4>::ld(src + h * 64 + i, v[h] + i);
+          if (live) kvcd::load4(src + h * 64 + i, v[h] + i);
           else v[h][i] = v[h][i + 1] = v[h][i + 2] = v[h][i + 3] = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(v[h][i + k]));

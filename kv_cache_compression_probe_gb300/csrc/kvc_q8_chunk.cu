@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(kThreads) q8_expand_kernel(const __grid_consta
     const int64_t from = (int64_t)(there ? page : 0) << x.shift, to = u * a.rows + (j << x.shift);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const float s = __ldg((v ? x.v_scale : x.k_scale) + (there ? page : 0));
+      const float s = (v ? x.v_scale : x.k_scale)[there ? page : 0];
       const uint4* src = reinterpret_cast<const uint4*>((v ? x.V : x.K) + from * D);
       __nv_bfloat16* dst = (v ? a.V : a.K) + to * D;
 #pragma unroll 2
       for (int i = threadIdx.x; i < count * kC; i += kThreads) {
-        const uint4 w = __ldg(src + i);
+        const uint4 w = src[i];
         const uint32_t c[4] = {w.x, w.y, w.z, w.w};
         uint32_t o[8];
 #pragma unroll

@@ -59,6 +59,11 @@ __device__ __forceinline__ void bytes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
+// Order code of a score: -0 counts as 0, and what is no number as the least, so that kAlways is the code of the
+// pages that are always in alone (the search relies on there being n_sel of them at most).
+constexpr uint32_t kAlways = 0xffffffffu;
+__device__ __forceinline__ uint32_t order_of(float s) { return s == s ? kvcd::float_key(s + 0.f) : 0; }
+
 // Sum of v over the block; `turn` alternates between calls, so one barrier is enough.
 __device__ __forceinline__ int block_sum(int v, int (&count)[2][kWarps], int& turn) {
   v = __reduce_add_sync(KVC_FULL_MASK, v);
@@ -105,7 +110,7 @@ __device__ __forceinline__ void pick_by_warp(const uint32_t* keys, int nb, int n
   uint32_t cut = 0xffffffffu, top = 0;                 // least and largest code of the pages that need not be in
   mine.each([&](int b, uint32_t key) {
     cut = min(cut, b < nb ? key : 0xffffffffu);
-    top = max(top, key == 0xffffffffu ? 0 : key);
+    top = max(top, key == kAlways ? 0 : key);
   });
   cut = __reduce_min_sync(KVC_FULL_MASK, cut);
   top = max(cut, __reduce_max_sync(KVC_FULL_MASK, top));
@@ -141,7 +146,7 @@ __device__ __forceinline__ void pick_by_block(const uint32_t* keys, int nb, int 
   for (int b = tid; b < nb; b += kThreads) {
     const uint32_t key = keys[b];
     cut = min(cut, key);
-    top = max(top, key == 0xffffffffu ? 0 : key);
+    top = max(top, key == kAlways ? 0 : key);
   }
   if (tid == 0) { ends[0] = 0xffffffffu; ends[1] = 0; }
   __syncthreads();
@@ -229,10 +234,10 @@ __global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_con
         const uint4* p = reinterpret_cast<const uint4*>(x.bounds + (int64_t)page * 2 * D) + c;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          f.lo[j][h] = __ldg(p + 4 * h);
-          f.hi[j][h] = __ldg(p + D / 16 + 4 * h);
+          f.lo[j][h] = p[4 * h];
+          f.hi[j][h] = p[D / 16 + 4 * h];
         }
-        f.scale[j] = __ldg(x.k_scale + page);
+        f.scale[j] = x.k_scale[page];
       }
       return f;
     };
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_con
       const int r = warp + j * kWarps, tok = r / G;
       v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.f;
       if (tok < tokens && lane < D / 4)
-        kvcd::VecLoad<T, 4>::ld(static_cast<const T*>(a.q) + ((u * G + r % G) * x.T + t0 + tok) * D + 4 * lane, v[j]);
+        kvcd::load4(static_cast<const T*>(a.q) + ((u * G + r % G) * x.T + t0 + tok) * D + 4 * lane, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_select_kernel(const __grid_con
           auto put = [&](int tok, float s) {
             const int own = (len + t0 + tok) >> x.shift;
             if (tok < tokens && b <= own)
-              keys[tok * x.max_pages + b] = b < a.first || b > own - a.recent ? 0xffffffffu : kvcd::float_key(s + 0.f);   // -0 counts as 0
+              keys[tok * x.max_pages + b] = b < a.first || b > own - a.recent ? kAlways : order_of(s);
           };
           const int tok = (nt * 8 + 2 * c) / G;
           if (G == 1) {

@@ -131,6 +131,28 @@ def test_picked_pages_that_are_none(kvc):
     assert (s["out"][0, 0, :4, 1] == 0).all()
 
 
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("what", ["inf", "nan", "scale", "all scales"])
+def test_a_choice_among_scores_that_are_no_numbers(kvc, n, what):
+    """Infinite or NaN queries and scales of one (l, h): its rows hold distinct pages that it sees,
+    the first and last ones among them; nothing beyond its rows is written, the others choose as ever."""
+    c = Q8(kvc, [400, 500, 300], [n], H=3, page=16)
+    c.fill_new()
+    s, good = c.upload(), c.upload()
+    pages = s["c"]._keep[0].view(3, -1)[1, :500 // 16].long()
+    if what in ("inf", "nan"):
+        s["q"].view(1, 1, 3, 4, n, 128)[:, :, 1] = float(what)
+    else:
+        s["k_scale"][pages[::2] if what == "scale" else pages] = float("nan")
+    c.select(s, 6, 1, 2)
+    c.select(good, 6, 1, 2)
+    _done(kvc)
+    assert torch.equal(s["sel"][0, 0, [0, 2]], good["sel"][0, 0, [0, 2]])
+    for t, row in enumerate(s["sel"][0, 0, 1].cpu().numpy()):
+        own = (500 + t) // 16
+        assert (np.diff(row) > 0).all() and row[0] == 0 and row[-1] == own and own - 1 in row
+
+
 # ------------------------------------------------------------------ invalid and full units
 def test_units_out_of_range_are_skipped(kvc):
     """Lengths that are negative, shrink, grow by more than T or pass the table: reported, rows and
