@@ -42,7 +42,7 @@ namespace kvcd {
 
 // unit_global of kvc_chunk.cuh for this block.
 __device__ __forceinline__ int64_t q8_unit_global(const kvc::Q8Args& a, int64_t u) {
-  return u + (u / a.lh_span) * a.lh_gap + a.lh_base;
+  return a.lh_gap ? u + (uint32_t)u / (uint32_t)a.lh_span * a.lh_gap + a.lh_base : u + a.lh_base;   // units are below 2^24
 }
 
 __device__ __forceinline__ float pow2i(int x) { return __int_as_float((x + 127) << 23); }

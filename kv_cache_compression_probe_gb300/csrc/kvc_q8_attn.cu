@@ -128,7 +128,20 @@ __device__ __forceinline__ void locate(const Q8Attn& a, LocateSmem& sm, long lon
     return item_groups<kSel>(a, cr, (i - u * a.rp) * a.tt);
   };
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += cost(i);
+  long long part[8] = {};                              // of this thread's items in eighths
+  const int eighth = (per + 7) / 8;
+  if (a.rp == 1) {                                     // an item a unit: eight units' lengths on their way at a time
+    for (int k = 0; k < eighth; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * eighth + k;
+        if (i < i1) part[j] += item_groups<kSel>(a, load_unit(a.x, i), 0);
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine += part[j];
+  } else {
+    for (int i = i0; i < i1; ++i) mine += cost(i);
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -144,13 +157,23 @@ __device__ __forceinline__ void locate(const Q8Attn& a, LocateSmem& sm, long lon
     total += sm.warp[w];
   }
   constexpr int kPieces = kSolo ? kWarps : 1;           // of a CTA
-  q = (total + gridDim.x * kPieces - 1) / (gridDim.x * kPieces);
+  const long long all = total + gridDim.x * kPieces - 1;
+  q = all >> 31 ? all / (gridDim.x * kPieces) : (long long)((unsigned)all / (gridDim.x * kPieces));
   if (!kSolo) q = max(q, (long long)kWarps);
   lo = min(total, (long long)blockIdx.x * kPieces * q);
   hi = min(total, lo + kPieces * q);
   long long at = before + incl - mine;
   if (lo < hi && at <= lo && lo < at + mine) {
-    for (int i = i0; i < i1; ++i) {
+    int i = i0;
+    if (a.rp == 1) {                                   // the eighth that holds it
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (i == i0 + j * eighth && lo >= at + part[j]) {
+          at += part[j];
+          i += eighth;
+        }
+    }
+    for (; i < i1; ++i) {
       const int c = cost(i);
       if (lo < at + c) {
         sm.item = i;
