@@ -43,6 +43,7 @@ using namespace kvctc;
 constexpr int kThreads = 640;
 constexpr int kBias = 4;               // bias tiles in flight
 constexpr float kFar = 0x1p30f;        // half a tile's sum of numerators may be this large or (at first) its inverse
+constexpr float kCoarse = 0x1p26f;     // references beyond have steps of 8 and more
 constexpr float kLeap = 16.f;          // and then its largest of 64 is above the reference by 24 at least
 constexpr int kCols = 512;             // TMEM columns
 
@@ -167,11 +168,14 @@ __device__ __forceinline__ void scores4(const RowScore& r, const uint32_t* s, co
 // numerators add as much error as that of the result (0.0023 instead of 0.0017 against 64 bits, for any
 // number of entries).  A second bf16 part of P would cost the exponentials twice, because 64 numerators
 // and their products do not fit this thread's 96 registers, and half as many products again.  The products come from TMEM in blocks of 16, the next
-// block on its way while one is worked on.
-template <int kMode, bool kMask>
+// block on its way while one is worked on.  kApart: the base is
+// taken off scores already rounded, as score_max rounds them, so that the largest gives 1 even beyond
+// kCoarse (nearer bases come off in the same step as elsewhere, and 0 after it).
+template <int kMode, bool kMask, bool kApart = false>
 __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, const float* lm, const float* rel,
                                             float base, int lim, uint32_t (&p)[32]) {
-  const float sh = cap_base<kMode>(r) - (base + r.shift);
+  const float later = kApart && fabsf(base) > kCoarse ? base : 0.f;
+  const float sh = cap_base<kMode>(r) - (base - later + r.shift);
   const uint64_t mb = pk(sh, sh);
   uint64_t s0 = 0, s1 = 0;
   uint32_t s[2][16];
@@ -185,7 +189,7 @@ __device__ __forceinline__ float numerators(const RowScore& r, uint32_t ts, cons
       float f[4];
       scores4<kMode, kMask>(r, s[q & 1] + e, lm, rel, q * 16 + e, mb, lim, f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = kvcd::ex2(f[i]);
+      for (int i = 0; i < 4; ++i) f[i] = kvcd::ex2(kApart ? f[i] - later : f[i]);
       s0 = add2(s0, pk(f[0], f[1]));
       s1 = add2(s1, pk(f[2], f[3]));
       p[q * 8 + e / 2] = bf16x2(f[0], f[1]);
@@ -690,7 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (move) m = t;
             settled = any_seen || t > -INFINITY;
-            sum = numerators<kMode, true>(rs, ts, lm, rel, m, lim, p);
+            // from 2^26 on, half a step of a score (4 and more) is no longer small against kFar: without
+            // the rounding in between the largest could come out as 2^256, or as 0
+            sum = numerators<kMode, true, true>(rs, ts, lm, rel, m, lim, p);
             named_or(pair, 64, false);                 // xtop and xl may be written again
           }
           if (kMode != kSums && lane == 0) kvcd::mbar_arrive(&sm.bias_empty[b]);

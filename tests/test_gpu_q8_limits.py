@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import q8_oracle as Q
-from tests.chunk_cases import DT
+from tests.chunk_cases import DT, EPS
 from tests.q8_cases import UNUSED, Q8
 
 pytestmark = pytest.mark.gpu
@@ -493,3 +493,33 @@ def test_choice_of_many_pages(kvc):
         kvc.kvc_q8_select(p, c, x, q, lens, lens + T, 2, 3, sel)
         _done(kvc)
         assert sel[0, 0, 0, 0].tolist() == list(range(497)) + [(n - T) // page - 2 + i for i in range(3)]
+
+
+# ------------------------------------------------------------------ scores whose steps are large
+@pytest.mark.parametrize("n, dtype", [(1, "bf16"), (9, "bf16"), (9, "f32"), (70, "bf16"), (70, "f32")])
+@pytest.mark.parametrize("power", [24, 28, 34])
+def test_scores_with_steps_far_above_one(kvc, n, dtype, power):
+    """Scores around 2^power (in fp32 a step is 1 to 1024 there): the row's one largest still gives 1.
+    A score is off by at most d 2^-23 of the sum of its products' magnitudes, so a row whose largest score leads by
+    more than twice that and 60 has the output of that entry alone, to the roundings of its numerator and of the result."""
+    c = Q8(kvc, [1300, 700, 90, 3000], [n] * 2, B=2, H=2, T=n, dtype=dtype, max_pages=700, logm=False, seed=31 + power)
+    c.fill_new()
+    c.q *= 2.0 ** power / 4
+    s = c.upload()
+    c.attn(s)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    c.check_attn(s)
+    out, alone = s["out"].double().cpu().numpy(), 0
+    rtol = EPS[dtype] + (2.0 ** -22 if dtype == "f32" else 2.0 ** -8 if n == 70 else 2.0 ** -11) + 2.0 ** -21
+    for u in c.units:
+        b, lr, h, hs, n_b, n0 = c.where(u)
+        K, V, lm = c.entries(u)
+        q = c.q[b, lr, hs].double().numpy()
+        x = Q.q8_scores(q, K, lm, n0, c.page)
+        off = c.d * 2.0 ** -23 * (np.abs(q) @ np.abs(K).T / np.sqrt(c.d)).max(-1)
+        best, rest = x.argmax(-1), np.sort(x, -1)[..., -2]
+        clear = x.max(-1) - rest > 2 * off + 60
+        alone += clear.sum()
+        np.testing.assert_allclose(out[b, lr, hs][clear], V[best][clear], rtol=rtol, atol=1e-12)
+    assert alone > 0
