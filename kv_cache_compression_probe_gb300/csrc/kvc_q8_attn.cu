@@ -522,7 +522,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
                 }
           }
         }
-        // ---- base-2 scores
+        // ---- base-2 scores.  The reference comes off them first, exactly for scores near it: where a step of fp32
+        // is 2 and more (scores beyond 2^24), reference + 15 would round to a numerator of 2^16, which fp16 does
+        // not hold, and reference - `down` to the reference.
         const float ks = kvcd::pow2i((exps & 255) - 64);
         float lm[2] = {0.f, 0.f};
         if (x.logm) {
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) rise |= fmaxf(s[nt][i], s[nt][2 + i]) > ref[nt][i] + kRise;
+          for (int i = 0; i < 2; ++i) rise |= fmaxf(s[nt][i], s[nt][2 + i]) - ref[nt][i] > kRise;
         if (__any_sync(KVC_FULL_MASK, rise)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
               m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 4));
               m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 8));
               m = fmaxf(m, __shfl_xor_sync(KVC_FULL_MASK, m, 16));
-              if (m > ref[nt][i] + kRise) {
+              if (m - ref[nt][i] > kRise) {
                 const float f = kvcd::ex2(ref[nt][i] - (m - kBelow));    // 0 at first
                 ref[nt][i] = m - kBelow;
                 l[nt][i] *= f;
@@ -590,13 +592,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
         uint32_t pf[kP][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float b0 = down - ref[nt][0], b1 = down - ref[nt][1];
           float p[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            p[2 * j] = kvcd::ex2(s[nt][2 * j] + b0);
-            p[2 * j + 1] = kvcd::ex2(s[nt][2 * j + 1] + b1);
-          }
+          for (int j = 0; j < 4; ++j) p[j] = kvcd::ex2((s[nt][j] - ref[nt][j & 1]) + down);
           l[nt][0] = fmaf(p[0] + p[2], back, l[nt][0]);
           l[nt][1] = fmaf(p[1] + p[3], back, l[nt][1]);
 #pragma unroll
