@@ -38,6 +38,7 @@
 // rows (16 sequences, up to 5 tokens) 34 us: bound by instructions' latency, since the results of 24 rows leave registers for
 // 8 warps an SM.
 #include <algorithm>
+#include <cfloat>
 
 #include "kvc_chunk_tc.cuh"
 #include "kvc_q8.cuh"
@@ -48,7 +49,7 @@ using kvc::Q8Args;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kBelow = 7.f, kRise = 15.f;            // the reference, and when it moves
-constexpr float kNone = -1e30f;                        // the reference of a row that has seen nothing
+constexpr float kNone = -FLT_MAX;                      // the reference of a row that has seen nothing: below every score but -inf
 constexpr int kNear = 3;                               // how far below O's unit a page's scale may lie
 
 struct Q8Attn {

@@ -123,3 +123,18 @@ def test_ln_m_steps_on_large_scores(kvc, form, dtype, power, step):
         V = c.entries(u)[1]
         room = (2.0 * EPS[dtype] + len(V) * 2.0 ** -22 + 2.0 ** -10) * np.abs(V).max(0)
         assert (out[b, lr, hs, :n] <= V.max(0) + room).all() and (out[b, lr, hs, :n] >= V.min(0) - room).all()
+
+
+# ------------------------------------------------------------------ scores of the largest sizes
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("form,dtype", ALL)
+def test_scores_of_all_sizes_there_are(kvc, form, dtype, sign):
+    """Queries around 2^62 and keys around 2^40, all products of a row's of one sign: scores near 2^107, which
+    a row that has seen nothing is not to be taken for."""
+    c, pick = _same_keys(kvc, form, dtype, 9, 62, 40, v_exps=(0, 0, -1))
+    key = torch.from_numpy(np.sign(c.val["K"][c.used][0]))
+    c.q = (c.q.double().abs().clamp(2.0 ** 58, 2.0 ** 64) * sign * key).to(c.q.dtype)
+    s, picks = _run(c, pick)
+    scores = s["lse"][s["lse"] != 7.0]
+    assert (scores.abs() > 1e30).all() and ((scores < 0) == (sign < 0)).all()
+    _check_averages(c, s, picks)
