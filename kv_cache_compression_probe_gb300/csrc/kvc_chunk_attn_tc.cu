@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the sum tells whether the reference was near enough: above 2^30 (or not a number)
           // it was too low; a row's first sum below 2^-30 may have lost entries
           settled |= l > 0.f;
-          const bool far = live && lim > 0 && (!(sum < kFar) || (!settled && !(sum > 1.f / kFar)));
+          // (beyond kCoarse every tile is done again: see there)
+          const bool far = live && lim > 0 && (!(sum < kFar) || (!settled && !(sum > 1.f / kFar)) || fabsf(m) > kCoarse);
           if (named_or(pair, 64, far)) {
             const float top = score_max<kMode>(rs, ts, lm, rel, lim);
             sm.xtop[st][half][row] = top;
@@ -695,7 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (move) m = t;
             settled = any_seen || t > -INFINITY;
             // from 2^26 on, half a step of a score (4 and more) is no longer small against kFar: without
-            // the rounding in between the largest could come out as 2^256, or as 0
+            // the rounding in between the largest could come out as 2^256, or as 0.  All further tiles take the
+            // rounded scores as well, or equal ones would weigh up to half a step apart
             sum = numerators<kMode, true, true>(rs, ts, lm, rel, m, lim, p);
             named_or(pair, 64, false);                 // xtop and xl may be written again
           }

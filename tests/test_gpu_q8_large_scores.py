@@ -22,16 +22,20 @@ def kvc():
 
 
 LENS = [1300, 700, 90, 3000]
+LONG = np.linspace(2500, 4500, 32)                         # several groups a warp where the line is cut into pieces
 FORMS = {
     "cluster": dict(lens=LENS, n_new=[1], H=4),
-    "pieces": dict(lens=LENS, n_new=[1], H=4, max_pages=1500),
+    "cluster, two row tiles": dict(lens=LENS, n_new=[3], H=4),
+    "cluster, four row tiles": dict(lens=LENS, n_new=[9, 7], B=2, H=2),
+    "cluster, picked pages": dict(lens=LENS, n_new=[3], H=4, pick=(60, 1, 2)),
+    "pieces": dict(lens=LONG, n_new=[1], H=32, page=128),
+    "pieces, three row tiles": dict(lens=LONG, n_new=[5], H=32, page=128),
     "a warp an item": dict(lens=60 + np.arange(2500) % 70, n_new=[1], L=125, H=20, d=64),
-    "two row tiles": dict(lens=LENS, n_new=[3], H=4, max_pages=1500),
-    "four row tiles": dict(lens=LENS, n_new=[9, 7], B=2, H=2, max_pages=1500),
-    "picked pages": dict(lens=LENS, n_new=[3], H=4, pick=(9, 1, 2)),
-    "expanded": dict(lens=LENS, n_new=[40], H=4, max_pages=1500),
+    "expanded": dict(lens=LONG[:24], n_new=[40], H=24, page=64, max_pages=400),
 }
+LARGE = ("pieces", "pieces, three row tiles", "a warp an item", "expanded")     # a few powers of these
 ALL = [(f, "bf16") for f in FORMS] + [(f, "f32") for f in FORMS if f != "expanded"]
+STREAMED = [(f, t) for f, t in ALL if f != "expanded"]
 
 
 def _same_keys(kvc, form, dtype, seed, q_power, k_power=0, v_exps=(0,)):
@@ -74,7 +78,7 @@ def _check_averages(c, s, picks, numerator=0.0):
         b, lr, h, hs, n, n0 = c.where(u)
         K, V, _ = c.entries(u)
         q = c.q[b, lr, hs, :n].double().numpy()
-        for t in range(n):
+        for t in sorted({0, 1, n // 2, n - 1} & set(range(n))):
             see = np.arange(len(V)) <= n0 + t
             if picks is not None:
                 see &= np.isin(np.arange(len(V)) // c.page, picks[u][t])
@@ -90,11 +94,8 @@ def _check_averages(c, s, picks, numerator=0.0):
 
 
 # ------------------------------------------------------------------ steps of 1 to 1024
-MANY = "a warp an item"                                  # thousands of units: a few powers
-
-
-@pytest.mark.parametrize("form,dtype,power", [(f, t, x) for f, t in ALL if f != "expanded"
-                                              for x in ((25, 28) if f == MANY else (24, 25, 26, 27, 28, 34))])
+@pytest.mark.parametrize("form,dtype,power", [(f, t, x) for f, t in STREAMED
+                                              for x in ((25, 28) if f in LARGE else (24, 25, 26, 27, 28, 34))])
 def test_equal_scores_over_pages_of_other_value_scales(kvc, form, dtype, power):
     """Neighbouring pages' value scales differ by 2 to 8: equal scores keep equal weights."""
     c, pick = _same_keys(kvc, form, dtype, 5 + power, power, v_exps=(0, -1, -3, -2, 0, 2, 1, -1))
@@ -102,8 +103,8 @@ def test_equal_scores_over_pages_of_other_value_scales(kvc, form, dtype, power):
 
 
 @pytest.mark.parametrize("form,dtype,power,step",
-                         [(f, t, x, y) for f, t in ALL if f != "expanded"
-                          for x, y in (((25, 8), (27, 16)) if f == MANY else
+                         [(f, t, x, y) for f, t in STREAMED
+                          for x, y in (((25, 8), (27, 16)) if f in LARGE else
                                        ((24, 8), (24, 16), (25, 8), (25, 16), (26, 8), (26, 16), (27, 16), (28, 32)))])
 def test_ln_m_steps_on_large_scores(kvc, form, dtype, power, step):
     """ln m of 0 and step ln 2 in turn: a score may stand 16 above the reference exactly, where its numerator
