@@ -89,14 +89,16 @@ struct Unit {
   int len, n;                          // entries before the chunk, new tokens (0: nothing to do)
   int64_t gu;
 };
-__device__ __forceinline__ Unit load_unit(const Q8Args& x, int64_t u) {
+// report: whether lengths out of range are this CTA's to report: block 0's, which looks at all units to find its
+// piece; of a cluster, which looks at its own unit alone, the first CTA's.
+__device__ __forceinline__ Unit load_unit(const Q8Args& x, int64_t u, bool report = blockIdx.x == 0) {
   Unit r;
   r.gu = kvcd::q8_unit_global(x, u);
   r.len = x.len_lh[r.gu];
   r.n = x.len_new[r.gu] - r.len;
   if (r.len < 0 || r.n < 0 || r.n > x.T || (int64_t)r.len + r.n > (int64_t)x.max_pages << x.shift) {
     r.n = 0;
-    if (blockIdx.x == 0) kvcd::record_error(x.err, KVC_EDEVICE);
+    if (report) kvcd::record_error(x.err, KVC_EDEVICE);
   }
   return r;
 }
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
   if constexpr (kMode == kTeam) {                      // this CTA's share of its cluster's item
     item = blockIdx.x / a.team;
     const int rank = blockIdx.x - item * a.team, u0 = item / a.rp;
-    const long long n = item_groups<kSel>(a, load_unit(x, u0), (item - u0 * a.rp) * a.tt);
+    const long long n = item_groups<kSel>(a, load_unit(x, u0, rank == 0), (item - u0 * a.rp) * a.tt);
     if (n == 0) return;
     lo = n * rank / a.team;                            // (no group of its own: it takes part in the joining all the same)
     hi = n * (rank + 1) / a.team;

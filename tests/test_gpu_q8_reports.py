@@ -1,0 +1,86 @@
+"""kvc_q8_select and kvc_q8_attn report every (b, l, h) with lengths or pages out of range, whichever
+it is and in each form of the kernel, and skip that one alone."""
+import numpy as np
+import pytest
+import torch
+
+from tests.q8_cases import Q8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvc():
+    from kv_cache_compression_probe_gb300 import build, kvc as K
+    build.build()
+    yield K
+    torch.cuda.empty_cache()
+
+
+FORMS = {
+    "cluster": dict(n=1), "cluster, two row blocks": dict(n=40), "cluster, fp32": dict(n=3, dtype="f32"),
+    "pieces": dict(n=1, wide=1500), "four row tiles": dict(n=7, wide=700), "expanded": dict(n=40, wide=4000),
+    "picked pages": dict(n=2, pick=(3, 1, 1)),
+}
+BAD = {                                                    # (length before, length after) of a unit with n tokens
+    "a length below 0": lambda n: (-1, n - 1),
+    "fewer after than before": lambda n: (60, 59),
+    "more than T tokens": lambda n: (60, 60 + n + 1),
+    "past the table": lambda n: (1 << 30, (1 << 30) + n),
+}
+
+
+@pytest.mark.parametrize("what", list(BAD))
+@pytest.mark.parametrize("form", list(FORMS))
+def test_lengths_out_of_range_of_any_unit(kvc, form, what):
+    f = dict(FORMS[form])
+    n, wide, pick, dtype = f["n"], f.get("wide"), f.get("pick"), f.get("dtype", "bf16")
+    c = Q8(kvc, [50, 60, 70, 80, 90], [n], H=5, page=16, dtype=dtype, max_pages=wide)
+    c.fill_new()
+    good = c.upload()
+    if pick:
+        c.select(good, *pick)
+    c.attn(good, good.get("sel"))
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    for u in (1, 2, 4):
+        s = c.upload()
+        s["len"].view(-1)[u], s["new"].view(-1)[u] = BAD[what](n)
+        if pick:
+            c.select(s, *pick)
+            torch.cuda.synchronize()
+            assert kvc.kvc_device_error() == kvc.KVC_EDEVICE, u
+            assert (s["sel"][0, 0, u] == -9).all()
+            s["sel"][0, 0, u] = 0
+        c.attn(s, s.get("sel"))
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_error() == kvc.KVC_EDEVICE, u
+        others = [h for h in range(20) if h // 4 != u]
+        assert (s["out"][0, 0, 4 * u:4 * u + 4] == 7.0).all() and (s["lse"][0, 0, 4 * u:4 * u + 4] == 7.0).all()
+        for k in ("out", "lse"):
+            assert torch.equal(s[k][0, 0, others], good[k][0, 0, others]), (u, k)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+def test_pages_out_of_range_of_any_unit(kvc, form):
+    f = dict(FORMS[form])
+    n, wide, pick, dtype = f["n"], f.get("wide"), f.get("pick"), f.get("dtype", "bf16")
+    c = Q8(kvc, [50, 60, 70, 80, 90], [n], H=5, page=16, dtype=dtype, max_pages=wide)
+    c.fill_new()
+    good = c.upload()
+    if pick:
+        c.select(good, *pick)
+    c.attn(good, good.get("sel"))
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == 0
+    for u in (1, 4):
+        s = c.upload()
+        if pick:
+            s["sel"] = good["sel"].clone()
+        s["c"]._keep[0].view(5, -1)[u, 0] = c.n_pages
+        c.attn(s, s.get("sel"))
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_error() == kvc.KVC_EDEVICE, u
+        others = [h for h in range(20) if h // 4 != u]
+        for k in ("out", "lse"):
+            assert torch.equal(s[k][0, 0, others], good[k][0, 0, others]), (u, k)
