@@ -12,6 +12,7 @@
 
 #include "kvc_chunk_tc.cuh"
 #include "kvc_q8.cuh"
+#include "kvc_rows.h"
 
 namespace {
 
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) q8_pack_kernel(const __grid_constant
   const int len = x.len_lh[gu], cap = a.cap_lh[gu], R = 1 << x.shift;
   const int32_t* tab = x.table + gu * x.max_pages;
   int bad = KVC_OK;
-  if (len < 0 || off < 0 || off + len > a.rows) bad = KVC_EDEVICE;
+  if (!kvc::rows_fit(off, len, a.rows)) bad = KVC_EDEVICE;
   else if (len > cap) bad = KVC_ECAPACITY;
   else if (len > (int64_t)x.max_pages << x.shift) bad = KVC_EDEVICE;
   bool ok = true;

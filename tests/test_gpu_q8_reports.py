@@ -84,3 +84,22 @@ def test_pages_out_of_range_of_any_unit(kvc, form):
         others = [h for h in range(20) if h // 4 != u]
         for k in ("out", "lse"):
             assert torch.equal(s[k][0, 0, others], good[k][0, 0, others]), (u, k)
+
+
+@pytest.mark.parametrize("off", [2 ** 63 - 1, 2 ** 63 - 90, 2 ** 62, -2 ** 63, -1])
+def test_pack_skips_offsets_of_any_size(kvc, off):
+    """An offset near 2^63 is out of range, whatever it and the length add up to."""
+    c = Q8(kvc, [90, 40], [0], H=2, page=16, T=1)
+    s = c.upload()
+    rows = 200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Kp, Vp = (torch.randn((rows, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    lm = torch.zeros(rows, device="cuda")
+    offs = torch.tensor([off, 150], device="cuda")
+    old = s["K"].clone()
+    kvc.kvc_q8_pack(s["p"], s["c"], s["x"], Kp, Vp, lm, s["len"], offs, s["cap"], s["len_out"])
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error() == kvc.KVC_EDEVICE
+    assert s["len_out"].view(-1).tolist() == [0, 40]
+    for p in c.table[0][c.table[0] >= 0]:
+        assert torch.equal(s["K"][p * 16:(p + 1) * 16], old[p * 16:(p + 1) * 16])
