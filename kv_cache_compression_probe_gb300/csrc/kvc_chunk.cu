@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) chunk_prepare_kernel(ChunkArg
   const float pos0 = kAppend ? a.pos_new[b] : 0.f;
   int bad = KVC_OK;
   if (len < 0 || n < 0 || n > a.T || off < 0 || (int64_t)len + n > a.packed_rows) bad = KVC_EDEVICE;
-  else if (!a.page_table && off + len + n > a.packed_rows) bad = KVC_EDEVICE;
+  else if (!a.page_table && !kvc::rows_fit(off, (int64_t)len + n, a.packed_rows)) bad = KVC_EDEVICE;
   else if ((int64_t)len + n > cap) bad = KVC_ECAPACITY;
   else if (next_off > off && off + len + n > next_off && next_has > 0) bad = KVC_ECAPACITY;
   else if (a.page_table) {

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/kvc.h"
+#include "kvc_rows.h"
 
 #define KVC_FULL_MASK 0xffffffffu
 

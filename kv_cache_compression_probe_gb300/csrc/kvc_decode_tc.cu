@@ -126,7 +126,7 @@ __device__ __forceinline__ int chunks_of(const kvc::DecodeTcArgs& a, int64_t i) 
   const int64_t gi = kvc::lh_global(i, a.lh_span, a.lh_gap, a.lh_base);
   const int len = a.len_lh[gi];
   const int64_t off = a.off_lh[gi];
-  if (len < 0 || off < 0 || off + len > a.packed_rows ||
+  if (!kvc::rows_fit(off, len, a.packed_rows) ||
       (len + kChunkTc) / kChunkTc > a.n_chunk_max)
     return -1;
   return len > 0 ? (len + kChunkTc - 1) / kChunkTc : 1;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(128 * G) decode_merge_kernel(kvc::DecodeTcArgs
   const int64_t gblh = kvc::lh_global(blh, a.lh_span, a.lh_gap, a.lh_base);
   const int len = a.len_lh[gblh];
   const int64_t off = a.off_lh[gblh];
-  if (len < 0 || off < 0 || off + len > a.packed_rows || (len + kChunkTc) / kChunkTc > a.n_chunk_max)
+  if (!kvc::rows_fit(off, len, a.packed_rows) || (len + kChunkTc) / kChunkTc > a.n_chunk_max)
     return;                                          // reported by the plan
   const int nch = len > 0 ? (len + kChunkTc - 1) / kChunkTc : 1;
   const int h = blh % a.H;

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(const __grid_co
   const int64_t off = a.page_table ? 0 : a.off_lh[gu];
   const float safe_from = ea.pos_next[u / a.per_seq] - ea.recent;
   bool ok = len >= 0 && len <= ea.max_len && len <= a.packed_rows && off >= 0 &&
-            (a.page_table || off + len <= a.packed_rows);
+            (a.page_table || kvc::rows_fit(off, len, a.packed_rows));
   if (ok && a.page_table) {
     const int need = (int)(((int64_t)len + (1 << a.page_shift) - 1) >> a.page_shift);
     ok = need <= a.max_pages;

@@ -12,7 +12,6 @@
 
 #include "kvc_chunk_tc.cuh"
 #include "kvc_q8.cuh"
-#include "kvc_rows.h"
 
 namespace {
 
