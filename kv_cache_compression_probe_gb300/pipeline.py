@@ -629,15 +629,32 @@ class QuantizedCache:
                  logm: bool = False, rotate: bool = True, device="cuda"):
         if n_sel and not (first >= 0 and recent >= 1 and first + recent <= n_sel):
             raise ValueError("the first and recent pages must fit n_sel")
+        # what a call of a step would refuse, before there is anything to lose
+        if page_rows not in (16, 32, 64, 128):
+            raise ValueError("page_rows must be 16, 32, 64 or 128")
+        if tokens < 1 or not 1 <= T <= 65536:
+            raise ValueError("a cache holds at least one token and takes 1 to 65536 at a time")
         B, L, H = p.B, p.L, p.H
         per = -(-int(tokens) // page_rows)
         self.T, self.cap, self.page_rows = int(T), per * page_rows, int(page_rows)
         self.n_sel, self.first, self.recent = int(n_sel), int(first), int(recent)
         pages = B * L * H * per
+        if pages * page_rows >= 1 << 31 or self.cap > 1 << 27:
+            raise ValueError("a cache has fewer than 2^31 rows, and 2^27 at most of one (b, l, h)")
+        if n_sel and (n_sel > 32768 or per > 32768):
+            raise ValueError("pages are picked from 32768 of a (b, l, h) at most")
         self.p = kvc.kvc_params.from_buffer_copy(p)
         self.p.packed_rows = pages * page_rows
         z = dict(device=device)
         f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+        self.table = torch.arange(pages, dtype=i32, **z).view(B, L, H, per)
+        self.n_new = torch.zeros((B,), dtype=i32, **z)
+        # (what a call needs depends on its tokens: a few row tiles, or expanded rows)
+        few = min(self.T, 64 // p.G + 1)
+        need = [kvc.kvc_q8_workspace_bytes(self.p, self._chunk(t), self.n_sel) for t in {self.T, *range(1, few + 1)}]
+        if min(need) == 0:
+            raise ValueError("the library takes no cache of these sizes")
+        self.ws = torch.empty(max(need), dtype=u8, **z)
         self.K = torch.zeros((pages * page_rows, p.d), dtype=u8, **z)
         self.V = torch.zeros((pages * page_rows, p.d), dtype=u8, **z)
         self.k_scale = torch.ones((pages,), dtype=f32, **z)
@@ -645,12 +662,10 @@ class QuantizedCache:
         self.bounds = torch.zeros((pages, 2, p.d), dtype=torch.int8, **z) if n_sel else None
         self.logm = torch.zeros((pages * page_rows,), dtype=f32, **z) if logm else None
         self.x = kvc.make_q8(self.K, self.V, self.k_scale, self.v_scale, self.bounds, self.logm)
-        self.table = torch.arange(pages, dtype=i32, **z).view(B, L, H, per)
         self.len_lh = torch.zeros((B, L, H), dtype=i32, **z)
         self.len_new = torch.zeros((B, L, H), dtype=i32, **z)
         self.cap_lh = torch.full((B, L, H), self.cap, dtype=i32, **z)
         self.pos_next = torch.zeros((B,), dtype=f32, **z)
-        self.n_new = torch.zeros((B,), dtype=i32, **z)
         self.rope_cos = self.rope_sin = None
         if rotate:
             n_half = 2 * int(n_pos if n_pos is not None else max(p.n_max, self.cap))
@@ -659,10 +674,6 @@ class QuantizedCache:
             kvc.kvc_rope_table(p.d, p.rope_base, n_half, self.rope_cos, self.rope_sin)
         self.q = torch.empty((B * L * H * p.G * self.T * p.d,), dtype=TORCH_DT[p.dtype], **z)
         self.sel = torch.empty((B * L * H * self.T * max(1, n_sel),), dtype=i32, **z)
-        # (what a call needs depends on its tokens: a few row tiles, or expanded rows)
-        few = min(self.T, 64 // p.G + 1)
-        self.ws = torch.empty(max(kvc.kvc_q8_workspace_bytes(self.p, self._chunk(t), self.n_sel)
-                                  for t in {self.T, *range(1, few + 1)}), dtype=u8, **z)
 
     def _chunk(self, T):
         return kvc.make_chunk(T, 0, self.p.L, page_rows=self.page_rows, page_table=self.table, n_new=self.n_new)
@@ -672,6 +683,8 @@ class QuantizedCache:
         the position of each sequence's next token.  With a `stream`, it must be torch's
         current one."""
         _current_stream_only(stream)
+        if tuple(pos_next.shape) != (self.p.B,):
+            raise ValueError(f"pos_next must be [{self.p.B}]")
         kvc.kvc_q8_pack(self.p, self._chunk(1), self.x, Kp, Vp, logm, len_lh, off_lh, self.cap_lh, self.len_new,
                         stream)
         self.len_lh.copy_(self.len_new)
@@ -689,11 +702,15 @@ class QuantizedCache:
         _current_stream_only(stream)
         if T > self.T:
             raise ValueError(f"{T} tokens, the cache was built for {self.T}")
+        c = self._chunk(T)
+        # the attention would refuse these only after the tokens are in the cache
+        kvc._q8_ptrs(c, self.x, out, lse)
+        if out.data_ptr() % 32:
+            raise ValueError("out must begin on a 32-byte boundary")
         if n_new is None:
             self.n_new.fill_(T)
         else:
             self.n_new.copy_(n_new)
-        c = self._chunk(T)
         turned = self.q[:q.numel()].view(q.shape)
         kvc.kvc_q8_append(p, c, self.x, self.rope_cos, self.rope_sin, q, k_new, v_new, self.pos_next, turned,
                           self.len_lh, self.cap_lh, self.len_new, stream)
