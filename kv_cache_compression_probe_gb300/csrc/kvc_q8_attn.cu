@@ -28,7 +28,7 @@
 //
 // The groups of all items (row blocks of units, or picked pages of tokens) lie on one line that is
 // cut into equal pieces, one per CTA; a CTA's warps join their results in shared memory, and what a cut
-// splits is joined in order by a combine kernel.  Where there are many items (kSolo) a piece is a warp's, which
+// splits is joined in order by a combine kernel.  Where there is an item for every warp (kSolo) a piece is a warp's, which
 // saves the joining and spreads an item's first and last steps over four times as many groups (300 tokens with
 // 1024 picked entries each, 8 KV heads: 85 us, with a piece a CTA 101 before later steps).  Few short items are a cluster's each
 // (kTeam), which joins through distributed shared memory and needs no second kernel (one token of one layer
@@ -826,15 +826,21 @@ int64_t item_count(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   return (int64_t)p->B * p->H * (c->layer_end - c->layer_begin) * ((c->T + tt - 1) / tt);
 }
 
-// Whether a warp takes an item by itself: one row tile, and more items than kSoloItems.
-constexpr int kSoloItems = 2400;
+// Whether a piece is a warp's: one row tile, and an item at least for every warp of the grid (bf16: 1824 on 152 SMs).
+// A CTA's piece and a warp's, us: 1024 picked entries a token, 1840 items 75 and 67, 3200 items 117 and 107; 256 picked
+// entries, 1840 items 39 and 33; one token over 2048 caches of 100..150 entries 36 and 30, of 400..600 63 and 62, of
+// 1000..3000 169 and 178 (the lengths are not known here); fp32, 1200 items of 500..1000 entries 81 and 71.  Below, with
+// fewer items than warps, the two come closer (480 items of 1024 picked entries 21.7 and 21.8).
 bool solo(const kvc_params* p, const kvc_chunk* c, int n_sel) {
-  return row_tiles(p, c, n_sel) == 1 && item_count(p, c, n_sel) >= kSoloItems;
+  const int nt = row_tiles(p, c, n_sel);
+  return nt == 1 && item_count(p, c, n_sel) >= (int64_t)std::max(kvc::sm_count(), 1) * ctas_per_sm(p, nt) * kWarps;
 }
 
 // CTAs that take an item as a cluster, or 0: where the items are few, and short by what the pages (picked, or of
 // the table) hold at most.  A warp then has kTeamGroups groups to do at most; a longer
-// item wants more CTAs than a cluster has.
+// item wants more CTAs than a cluster has.  Pieces with a combine kernel and clusters, us, one token of one layer, by groups a
+// warp: 8 (4000 entries) 16.8 and 10.4, 16 18.3 and 14.1, 23 18.6 and 18.0, 31 20.8 and 21.4, 47 21.8 and 29.3; with 2 KV
+// heads 31 28.3 and 21.5, 47 30.0 and 29.1; 5 tokens, 31 31.2 and 30.7; fp32 16 18.1 and 18.0, 31 21.1 and 29.1.
 constexpr int kTeamGroups = 32;
 int team_size(const kvc_params* p, const kvc_chunk* c, int n_sel) {
   const int64_t items = item_count(p, c, n_sel);
