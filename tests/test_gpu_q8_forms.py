@@ -1,4 +1,5 @@
-"""kvc_q8_attn on both sides of the sizes where its form changes."""
+"""kvc_q8_attn on both sides of the sizes where its form changes, and its streaming forms to the rounding
+of their own numerators (11 bits in bf16)."""
 import numpy as np
 import pytest
 import torch
@@ -16,6 +17,13 @@ def kvc():
     build.build()
     yield K
     torch.cuda.empty_cache()
+
+
+def _expands(c):
+    """Whether a bf16 call goes through expanded rows: more than 64 rows of a (b, l, h), and more than 12288 groups
+    of 16 entries to do in blocks of 32 rows, by what the table's pages hold."""
+    blocks = -(-c.T // (32 // c.G))
+    return c.G * c.T > 64 and len(c.units) * blocks * c.table.shape[1] * c.page // 16 > 12288
 
 
 def _check_numerators(c, s, pages=None):
@@ -74,3 +82,24 @@ def test_picked_pages_around_the_number_of_warps(kvc, T):
     c.check_select(s, picks)
     c.check_attn(s, picks)
     _check_numerators(c, s, picks)
+
+
+# ------------------------------------------------------------------ precision of the streaming forms
+STREAMED = {
+    "four row tiles, 333 tokens": dict(lens=[600, 129], n_new=[333], H=2, page=128),
+    "four row tiles, G 8": dict(lens=[100, 333], n_new=[130], H=2, G=8, page=32),
+    "four row tiles, layer range": dict(lens=[5, 70, 200, 130, 64, 9], n_new=[90, 61], B=2, L=3, layers=(1, 3), page=64),
+    "four row tiles, sharp": dict(lens=[300, 700], n_new=[60], H=2, qscale=20.0, page=64),
+    "three row tiles, pieces": dict(lens=[9000, 20011], n_new=[5], H=2, page=64),
+    "two row tiles, pieces": dict(lens=[9000, 20011], n_new=[3], H=2, page=128),
+    "one row tile, pieces": dict(lens=[9000, 20011], n_new=[1], H=2, page=64),
+    "a table wider than its entries": dict(lens=[300, 50], n_new=[7], H=2, max_pages=1500),
+}
+
+
+@pytest.mark.parametrize("name", list(STREAMED))
+def test_numerators_keep_11_bits(kvc, name):
+    c = Q8(kvc, seed=list(STREAMED).index(name), **STREAMED[name])
+    s = _attn(kvc, c)
+    assert not _expands(c)
+    _check_numerators(c, s)
