@@ -329,9 +329,9 @@ class Compressor:
         """The packed cache in 8 bits (kvc_q8_pack), as a QuantizedCache with room for `reserve`
         more tokens per (b, l, h), in calls of up to T.  pos_next [B]: the position of each sequence's next token
         (n_max at most, unless n_pos says otherwise); further arguments as QuantizedCache's.
-        Waits for the device once, for the largest length."""
+        Waits for the device once, for the lengths."""
         kw.setdefault("n_pos", self.p.n_max + int(reserve))
-        cache = QuantizedCache(self.p, int(self.len_lh.max()) + int(reserve), T, logm=True,
+        cache = QuantizedCache(self.p, self.len_lh.cpu() + int(reserve), T, logm=True,
                                device=self.device, **kw)
         cache.pack(self.Kp, self.Vp, self.logm, self.len_lh, self.off_lh, pos_next)
         return cache
@@ -620,11 +620,11 @@ class QuantizedCache:
     A step rotates and appends the new tokens (kvc_q8_append) and attends (kvc_q8_attn); with
     n_sel, every token of every KV head attends over n_sel pages only (kvc_q8_select): the `first`
     pages, the last `recent` ones, and of the others those of largest score.  Every (b, l, h) owns pages
-    for `tokens` entries; positions go up to n_pos.  Nothing waits for the device or allocates, so
+    for `tokens` entries (a number, or [B, L, H] of them in host memory); positions go up to n_pos.  Nothing waits for the device or allocates, so
     steps can be captured into a CUDA graph.  The class only allocates and marshals.
     """
 
-    def __init__(self, p: kvc.kvc_params, tokens: int, T: int = 1, page_rows: int = 64,
+    def __init__(self, p: kvc.kvc_params, tokens, T: int = 1, page_rows: int = 64,
                  n_pos: Optional[int] = None, n_sel: int = 0, first: int = 1, recent: int = 2,
                  logm: bool = False, rotate: bool = True, device="cuda"):
         if n_sel and not (first >= 0 and recent >= 1 and first + recent <= n_sel):
@@ -632,13 +632,16 @@ class QuantizedCache:
         # what a call of a step would refuse, before there is anything to lose
         if page_rows not in (16, 32, 64, 128):
             raise ValueError("page_rows must be 16, 32, 64 or 128")
-        if tokens < 1 or not 1 <= T <= 65536:
-            raise ValueError("a cache holds at least one token and takes 1 to 65536 at a time")
         B, L, H = p.B, p.L, p.H
-        per = -(-int(tokens) // page_rows)
+        room = torch.as_tensor(tokens, dtype=torch.int64, device="cpu")
+        if room.dim() and tuple(room.shape) != (B, L, H):
+            raise ValueError(f"tokens must be a number or {[B, L, H]}")
+        if int(room.min()) < 1 or not 1 <= T <= 65536:
+            raise ValueError("a cache holds at least one token and takes 1 to 65536 at a time")
+        owned = torch.div(room + (page_rows - 1), page_rows, rounding_mode="floor").expand(B, L, H)   # pages
+        per, pages = int(owned.max()), int(owned.sum())
         self.T, self.cap, self.page_rows = int(T), per * page_rows, int(page_rows)
         self.n_sel, self.first, self.recent = int(n_sel), int(first), int(recent)
-        pages = B * L * H * per
         if pages * page_rows >= 1 << 31 or self.cap > 1 << 27:
             raise ValueError("a cache has fewer than 2^31 rows, and 2^27 at most of one (b, l, h)")
         if n_sel and (n_sel > 32768 or per > 32768):
@@ -647,7 +650,9 @@ class QuantizedCache:
         self.p.packed_rows = pages * page_rows
         z = dict(device=device)
         f32, i32, u8 = torch.float32, torch.int32, torch.uint8
-        self.table = torch.arange(pages, dtype=i32, **z).view(B, L, H, per)
+        self._first = owned.flatten().cumsum(0).view(B, L, H) - owned     # pages before a (b, l, h)'s own
+        column = torch.arange(per)
+        self.table = torch.where(column < owned[..., None], self._first[..., None] + column, -1).to(dtype=i32, **z)
         self.n_new = torch.zeros((B,), dtype=i32, **z)
         # (what a call needs depends on its tokens: a few row tiles, or expanded rows)
         few = min(self.T, 64 // p.G + 1)
@@ -664,7 +669,7 @@ class QuantizedCache:
         self.x = kvc.make_q8(self.K, self.V, self.k_scale, self.v_scale, self.bounds, self.logm)
         self.len_lh = torch.zeros((B, L, H), dtype=i32, **z)
         self.len_new = torch.zeros((B, L, H), dtype=i32, **z)
-        self.cap_lh = torch.full((B, L, H), self.cap, dtype=i32, **z)
+        self.cap_lh = (owned * page_rows).to(dtype=i32, **z)
         self.pos_next = torch.zeros((B,), dtype=f32, **z)
         self.rope_cos = self.rope_sin = None
         if rotate:
@@ -726,7 +731,7 @@ class QuantizedCache:
     def entries(self, b: int, l: int, h: int):
         """(K, V, log m or None) the (b, l, h) holds, in entry order (host copies)."""
         n = int(self.len_lh[b, l, h])
-        o = ((b * self.p.L + l) * self.p.H + h) * self.cap
+        o = int(self._first[b, l, h]) * self.page_rows
         page = torch.arange(o, o + n, device=self.K.device) // self.page_rows
         K, V = (t[o:o + n].view(torch.float8_e4m3fn).float() * s[page][:, None]
                 for t, s in ((self.K, self.k_scale), (self.V, self.v_scale)))
