@@ -630,8 +630,9 @@ int kvc_q8_select(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, cons
  *   s_e = q_t . k_e / sqrt(d) + logm_e,  out = sum_e softmax_e(s) v_e,  lse = log2 sum_e 2^(s_e log2 e)
  * with fp32 statistics (bf16: the softmax's numerators are rounded to 11 bits, or to 8 where
  * many rows go through expanded rows).  A row whose
- * scores are all -inf gets out = 0 and lse = -inf.  sel, n_sel as kvc_q8_select leaves them (each page once;
- * numbers that are no page the token sees are passed over), NULL and 0 = all entries.
+ * scores are all -inf gets out = 0 and lse = -inf.  sel, n_sel as kvc_q8_select leaves them: a token that
+ * sees own + 1 pages has its pages, each once, in the first min(n_sel, own + 1) places (numbers there that are no
+ * page it sees are passed over; a page behind them is left out and reported as KVC_EDEVICE); NULL and 0 = all entries.
  * lse [B, Lr, H*G, T] may be NULL.  Rows t >= n of out and lse stay as they were.  Query values
  * up to 2^64.  An (l,h) with lengths out of range is skipped; with a page
  * outside the extent its rows are unspecified; both report KVC_EDEVICE.  Workspace:

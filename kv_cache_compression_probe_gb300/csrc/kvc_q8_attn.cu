@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, NT, kMode>::kCtas) q8_attn_
     const int32_t* tab = x.table + r.gu * x.max_pages;
     const int32_t* list = kSel ? a.sel + ((int64_t)u * x.T + t0) * a.n_sel : nullptr;
     const int own = (r.len + t0) >> x.shift, inpage = (1 << x.shift) - 1;
+    if (kSel && tb == 0 && me == 0)                    // places that no group stands for must hold no page
+      for (int i = own + 1 + lane; i < a.n_sel; i += 32) bad |= (unsigned)list[i] <= (unsigned)own;
     // A window: lane i knows of the warp's group k0 + i its first entry, its first row (a multiple of 16)
     // and the exponents of its scales; with the latter two whether there is such a group (kThere), and whether every row
     // of the block sees all of it (kFull).

@@ -103,3 +103,22 @@ def test_pack_skips_offsets_of_any_size(kvc, off):
     assert s["len_out"].view(-1).tolist() == [0, 40]
     for p in c.table[0][c.table[0] >= 0]:
         assert torch.equal(s["K"][p * 16:(p + 1) * 16], old[p * 16:(p + 1) * 16])
+
+
+@pytest.mark.parametrize("units", [1, 250])
+def test_picked_pages_behind_their_places(kvc, units):
+    """A token that sees two pages has its list in the first two places; a page further on is reported."""
+    U = 8 * units
+    c = Q8(kvc, [20] * U, [1], L=units, H=8, page=16, logm=False)
+    c.fill_new()
+    s = c.upload()
+    for places, code in (([1, 0, -1, -1], 0), ([-1, 1, 5, -7], 0), ([0, -1, 1 << 30, 2], 0), ([-1, 0, 1, -1], kvc.KVC_EDEVICE),
+                         ([0, 9, -1, 1], kvc.KVC_EDEVICE)):
+        lists = np.tile(np.array([0, 1, -1, -1], np.int32), (U, 1))
+        lists[U - 1] = places
+        s["sel"] = torch.from_numpy(lists).cuda().view(1, units, 8, 1, 4)
+        s["out"].fill_(7.0), s["lse"].fill_(7.0)
+        c.attn(s, s["sel"])
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_error() == code, places
+        c.check_attn(s, {u: [[j for j in lists[u][:2] if 0 <= j <= 1]] for u in range(U)})
