@@ -611,7 +611,8 @@ int kvc_q8_pack(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const 
  * than n_sel, it picks the pages j < first, j > own - recent, and of the others those of
  * largest score (ties to the lower page) up to n_sel in all:
  *   score_j = max_g fl(fl(D_gj k_scale_j) a_g),  D_gj = sum_f max(i_gf lo_jf, i_gf hi_jf),
- *   a_g = max_f |q_gf|,  i_gf = rint(fl(q_gf fl(127 fl(1 / a_g))))   (0 for a_g = 0)
+ *   a_g = max_f |q_gf|,  i_gf = rint(fl(q_gf fl(127 fl(1 / a_g))))   (0 for a_g = 0; held to -127 .. 127,
+ *   and 0 for q_gf = 0, where a_g is so small, below 2^-121, that the factor overflows)
  * an upper bound of the products with the page's keys, up to the rounding to 8 bits.  log m does
  * not enter.  Call after kvc_q8_append of the same tokens (q is its q_out); len_lh are the
  * lengths before it, len_new after it (its len_out), both [B, L, H]; n = len_new - len_lh.
@@ -629,7 +630,7 @@ int kvc_q8_select(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, cons
  * only over those in its pages:
  *   s_e = q_t . k_e / sqrt(d) + logm_e,  out = sum_e softmax_e(s) v_e,  lse = log2 sum_e 2^(s_e log2 e)
  * with fp32 statistics (bf16: the softmax's numerators are rounded to 11 bits, or to 8 where
- * many rows go through expanded rows).  A row whose
+ * many rows go through expanded rows, see kvc_q8_workspace_bytes).  A row whose
  * scores are all -inf gets out = 0 and lse = -inf.  sel, n_sel as kvc_q8_select leaves them: a token that
  * sees own + 1 pages has its pages, each once, in the first min(n_sel, own + 1) places (numbers there that are no
  * page it sees are passed over; a page behind them is left out and reported as KVC_EDEVICE); NULL and 0 = all entries.
@@ -643,8 +644,9 @@ int kvc_q8_attn(const kvc_params* p, const kvc_chunk* c, const kvc_q8* x, const 
                 void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of kvc_q8_attn for this n_sel (0: all entries); 0 for invalid
- * arguments.  It depends on c->T too: many rows (more than 64 of an (l,h), unless the tables are
- * short) need room for expanded rows, up to 1 GB or one (l,h)'s table if that is more. */
+ * arguments.  It depends on c->T too: many rows (more than 64 of an (l,h), and more than 12288 groups of 16
+ * entries over all (l,h) and blocks of 32 rows, by what c->max_pages hold; bf16, all entries) need room for
+ * expanded rows, up to 1 GB or one (l,h)'s table if that is more. */
 size_t kvc_q8_workspace_bytes(const kvc_params* p /* host */, const kvc_chunk* c /* host */,
                               int32_t n_sel);
 

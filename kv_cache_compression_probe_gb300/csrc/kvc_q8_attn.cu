@@ -30,11 +30,11 @@
 // cut into equal pieces, one per CTA; a CTA's warps join their results in shared memory, and what a cut
 // splits is joined in order by a combine kernel.  Where there is an item for every warp (kSolo) a piece is a warp's, which
 // saves the joining and spreads an item's first and last steps over four times as many groups (300 tokens with
-// 1024 picked entries each, 8 KV heads: 85 us, with a piece a CTA 101 before later steps).  Few short items are a cluster's each
+// 1024 picked entries each, 8 KV heads: 86 us, with a piece a CTA 91).  Few short items are a cluster's each
 // (kTeam), which joins through distributed shared memory and needs no second kernel (one token of one layer
 // over 200..512 entries 6.9 us, with pieces and combine 10.6).
 // Measured: one token over 256 caches of 3200..5000 entries, d 128, G 4: 53 us, 5.1 TB/s (48.8 without the
-// arithmetic, 4 of it the combine kernel); over 4096 caches of 1000..3000: 6.1 TB/s, 91% of the copy rate.  With 20
+// arithmetic, 4 of it the combine kernel); over 4096 caches of 1000..3000: 6.0 TB/s, 90% of the copy rate.  With 20
 // rows (16 sequences, up to 5 tokens) 34 us: bound by instructions' latency, since the results of 24 rows leave registers for
 // 8 warps an SM.
 #include <algorithm>

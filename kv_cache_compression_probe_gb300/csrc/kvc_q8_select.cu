@@ -13,8 +13,8 @@
 // both operands agree, so a lane takes whole 16-byte pieces of the bounds.  The scores' order codes stay in shared
 // memory, where a warp per token (for a single token over many pages the whole CTA) looks for the n_sel-th largest by
 // halving the range of codes; scores are spread over it, so about 10 steps are enough as a rule.
-// Measured (d 128, G 4): one token over 256 caches of 512 pages 11.8 us (34 MB of bounds, 3 TB/s: a chain of loads, the
-// scores, the search), 300 tokens over 8 caches of 512 pages 20.1 us (instructions: issue slots 48%).
+// Measured (d 128, G 4): one token over 256 caches of 512 pages 10.9 us (34 MB of bounds, 3 TB/s: a chain of loads, the
+// scores, the search), 300 tokens over 8 caches of 512 pages 19.5 us (instructions: issue slots 48%).
 #include <algorithm>
 
 #include "kvc_q8.cuh"
