@@ -697,7 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             settled = any_seen || t > -INFINITY;
             // from 2^26 on, half a step of a score (4 and more) is no longer small against kFar: without
             // the rounding in between the largest could come out as 2^256, or as 0.  All further tiles take the
-            // rounded scores as well, or equal ones would weigh up to half a step apart
+            // rounded scores as well, or equal ones would weigh up to half a step apart (which is left where a row's
+            // reference passes 2^26 by a few: 2^4)
             sum = numerators<kMode, true, true>(rs, ts, lm, rel, m, lim, p);
             named_or(pair, 64, false);                 // xtop and xl may be written again
           }
