@@ -571,7 +571,8 @@ size_t kvc_mass_evict_workspace_bytes(const kvc_params* p /* host */,
  * page_table is needed) and T; softcap, window and slopes must be off.  p->dtype is
  * the type of q, k_new, v_new and out; p->packed_rows the extent of the cache's rows.
  * Layouts as in kvc_chunk_attn.  Each call is one or a few kernels without allocation, so it can
- * be captured.  Every value must be finite, but log m may be -inf.  Errors:
+ * be captured.  Every value must be finite, but log m may be -inf (and may count as -inf
+ * below -2^124, as the types' lowest values do).  Errors:
  * KVC_EINVAL (also K, V, bounds, q, k_new or v_new off a 16-byte boundary, out off a
  * 32-byte one), KVC_EWORKSPACE, KVC_ECUDA. */
 
